@@ -111,8 +111,9 @@ def _quantize_rows_plain(x):
     """Symmetric int8 with one scale per row: s = max(|x|, 2^-100) / 127, q = rint(x (127 / max))."""
     x = x.float()
     top = x.abs().amax(dim=1, keepdim=True).clamp(min=2.0 ** -100)
-    q = torch.round(x * (127.0 / top)).clamp(-127.0, 127.0)
-    return q.to(torch.int8), (top / 127.0).squeeze(1)
+    most = torch.full_like(top, 127.0)  # tensor by tensor: a division each (a scalar's is done by its reciprocal)
+    q = torch.round(x * (most / top)).clamp(-127.0, 127.0)
+    return q.to(torch.int8), (top / most).squeeze(1)
 
 
 def prepare(case, seed):
@@ -320,7 +321,7 @@ def exact(case, seed):
                 # the codes are whole numbers with no 64-bit value of their own: those of the 32-bit definition
                 x = s["x"][rows].float()
                 top = torch.clamp(x.abs().max(dim=1)[0], min=2.0 ** -100)
-                q = torch.clamp(torch.round(x * (127.0 / top)[:, None]), -127, 127)
+                q = torch.clamp(torch.round(x * torch.div(torch.full_like(top, 127.0), top)[:, None]), -127, 127)
                 v = torch.einsum("mk,nk->mn", q.double(), s["wq"][e].double())
                 v = v * (top.double()[:, None] / 127.0) * s["ws"][e].double()[None, :]
             if op in ("fprop", "int8") and s["bias"] is not None:
