@@ -95,7 +95,8 @@ enum {
     MXQ_ERR_LAUNCH = -6,       /* a CUDA call failed (see mxq_last_cuda_error) */
     MXQ_ERR_FLAGS = -7,        /* unknown or inconsistent flags */
     MXQ_ERR_ALIGN = -8,        /* a pointer is not 16-byte aligned */
-    MXQ_ERR_SCRATCH_LIMIT = -9 /* problem larger than mxq_grouped_dbias_noalloc's fixed scratch */
+    MXQ_ERR_SCRATCH_LIMIT = -9, /* problem larger than mxq_grouped_dbias_noalloc's fixed scratch */
+    MXQ_ERR_VALUE = -10        /* a scalar argument is outside its range */
 };
 
 /* device status word bits (sticky; OR-ed by the kernels) */
@@ -116,8 +117,10 @@ enum {
                              paths: also write the bf16 values that were quantized */
     MXQ_ACCUMULATE = 16,  /* wgrad: dW += product (else dW = product) */
     MXQ_OUT_BF16 = 32,    /* wgrad: dW in bf16 (else fp32) */
-    MXQ_PAD_EXPERTS = 64  /* group_quantize / requant: expert counts need not be
+    MXQ_PAD_EXPERTS = 64, /* group_quantize / requant: expert counts need not be
                              multiples of 128; see "Padded grouping" below */
+    MXQ_OUT_F32 = 128     /* ragged fprop / dgrad, int8: fp32 output (else bf16);
+                             dropout: x, residual and out are fp32 (else bf16) */
 };
 
 /* operation ids for mxq_workspace_bytes */
@@ -379,6 +382,85 @@ MXQ_API int mxq_swiglu_bwd_quantize(const void* dh_bf16, const void* y_bf16, int
                                     void* col_data, void* col_scale, float* dbias_out, void* dy_bf16_out,
                                     const int32_t* d_noop, int32_t* d_status, void* ws, size_t ws_bytes,
                                     mxq_stream_t stream);
+
+/* ---- Ragged grouped products in bf16 -------------------------------------
+ *
+ * The three products of an expert layer on bf16 operands, for expert counts
+ * that are multiples of nothing: any m_e >= 0 with sum(m_e) == M (device
+ * memory; a negative count or a wrong sum sets the status word and writes
+ * nothing). N and K are multiples of 8, at most 2^20. x and dy may be slices
+ * of wider rows: ldx, lddy are row strides in elements, multiples of 8 and at
+ * least the row's width. W is one contiguous (E, N, K) tensor. Sums are fp32
+ * and rounded once. An expert without rows reads nothing and, in wgrad, gets a
+ * zero dW (untouched with MXQ_ACCUMULATE). Infinities and NaN stay in the
+ * rows (fprop, dgrad) or the expert (wgrad) that they belong to. Outputs are
+ * the same bits from run to run. No workspace. */
+
+/* y[m,:] = x[m,:] . w[e(m)]^T (+ bias[e(m)]); y (M, N) bf16, or fp32 with
+ * MXQ_OUT_F32; bias (E, N) bf16 or NULL. */
+MXQ_API int mxq_ragged_gemm_fprop(const void* x_bf16, int64_t ldx, const void* w_bf16, const void* bias_bf16,
+                                  int64_t M, int64_t N, int64_t K, int E, const int64_t* d_m_splits, int flags,
+                                  void* y, int32_t* d_status, mxq_stream_t stream);
+
+/* dx[m,:] = dy[m,:] . w[e(m)]; dx (M, K) bf16, or fp32 with MXQ_OUT_F32. */
+MXQ_API int mxq_ragged_gemm_dgrad(const void* dy_bf16, int64_t lddy, const void* w_bf16, int64_t M, int64_t N,
+                                  int64_t K, int E, const int64_t* d_m_splits, int flags, void* dx,
+                                  int32_t* d_status, mxq_stream_t stream);
+
+/* dw[e] = dy_e^T . x_e; dw (E, N, K) fp32, or bf16 with MXQ_OUT_BF16; added to
+ * what dw holds with MXQ_ACCUMULATE. */
+MXQ_API int mxq_ragged_gemm_wgrad(const void* dy_bf16, int64_t lddy, const void* x_bf16, int64_t ldx, int64_t M,
+                                  int64_t N, int64_t K, int E, const int64_t* d_m_splits, int flags, void* dw,
+                                  int32_t* d_status, mxq_stream_t stream);
+
+/* ---- Ragged grouped products in int8 -------------------------------------
+ *
+ * Symmetric int8 with one fp32 scale per token and per output channel, for
+ * serving quantized experts. */
+
+/* Quantizes the rows of x (M, K), row stride ldx: scale[m] = a / 127 and
+ * q[m,k] = rint(x[m,k] * (127 / a)) with a = max(max_k |x[m,k]|, 2^-100), each
+ * step one IEEE fp32 rounding, ties to even. A row that holds an infinity or
+ * NaN gets scale NaN and codes 0. K % 16 == 0, K <= 2^20. A weight (E, N, K) is
+ * quantized per output channel by the same call on its E*N rows. */
+MXQ_API int mxq_int8_quantize_rows(const void* x_bf16, int64_t ldx, int64_t M, int64_t K, void* q, float* scale,
+                                   mxq_stream_t stream);
+
+/* y[m,n] = (sum_k xq[m,k] wq[e,n,k]) x_scale[m] w_scale[e,n] (+ bias[e,n]);
+ * xq (M, K) and wq (E, N, K) int8, scales fp32 (M) and (E, N), bias (E, N) bf16
+ * or NULL, y (M, N) bf16 or, with MXQ_OUT_F32, fp32. The sum is fp32 over whole
+ * numbers. Grouping as in the bf16 products; K % 16 == 0, N % 8 == 0. */
+MXQ_API int mxq_int8_gemm_fprop(const void* xq, const float* x_scale, const void* wq, const float* w_scale,
+                                const void* bias_bf16, int64_t M, int64_t N, int64_t K, int E,
+                                const int64_t* d_m_splits, int flags, void* y, int32_t* d_status,
+                                mxq_stream_t stream);
+
+/* ---- Dropout from a counter ----------------------------------------------
+ *
+ * D(v) drops element i (its row-major index) of v when word (i mod 8) of
+ * Philox 4x32-10 at the counter (i div 8, offset) under the key seed is below
+ * t = rint(65536 p), words being 16-bit halves, low half first; what is kept
+ * is scaled by 65536 / (65536 - t). d_rng is {seed, offset}, two int64 in
+ * device memory, so that a captured graph can be replayed with new ones (the
+ * caller advances the offset). The mask is made again wherever it is needed
+ * and never stored. 0 <= p <= 1 (MXQ_ERR_VALUE otherwise); p = 1 drops all.
+ * Dropped elements come out as 0 whatever they held. */
+
+/* h = D(silu(g) * u) for the rows [g | u] of y (M, 2F); h (M, F). F % 8 == 0.
+ * fp32 steps of mxq_swiglu_fwd, one rounding to bf16; p = 0 gives its bits. */
+MXQ_API int mxq_swiglu_dropout_fwd(const void* y_bf16, int64_t M, int64_t F, const int64_t* d_rng, double p,
+                                   void* h_bf16, mxq_stream_t stream);
+
+/* The gradient [dg | du] (M, 2F) of y from dh (M, F), with the mask of the
+ * forward call that had the same d_rng and p. */
+MXQ_API int mxq_swiglu_dropout_bwd(const void* dh_bf16, const void* y_bf16, int64_t M, int64_t F,
+                                   const int64_t* d_rng, double p, void* dy_bf16, mxq_stream_t stream);
+
+/* out[i] = D(x)[i] (+ residual[i]) over n elements; residual NULL for none.
+ * Without a residual it is its own gradient: dx = D(dout). out may be x or
+ * residual. */
+MXQ_API int mxq_dropout(const void* x, const void* residual, int64_t n, const int64_t* d_rng, double p, int flags,
+                        void* out, mxq_stream_t stream);
 
 /* Measurement utility beside the MXFP8 path: the tensor-pipe ceiling that
  * bounds the grouped GEMMs on this GPU. Launches one CTA per SM on `stream`;

@@ -7,6 +7,7 @@ built in-tree for sm_103a by :func:`moe_expert_grouped_group_gb300.build.build`.
 from . import mxq  # noqa: F401
 from .mxq import (  # noqa: F401
     MXQError,
+    dropout,
     group_quantize,
     group_quantize_scaled_bias,
     grouped_dbias,
@@ -15,8 +16,13 @@ from .mxq import (  # noqa: F401
     grouped_gemm_fprop,
     grouped_gemm_fprop_swiglu,
     grouped_gemm_wgrad,
+    int8_gemm_fprop,
+    int8_quantize_rows,
     new_status,
     probe_mma_stream,
+    ragged_gemm_dgrad,
+    ragged_gemm_fprop,
+    ragged_gemm_wgrad,
     requant_colwise,
     requant_colwise_scaled_bias,
     scale_bytes,
@@ -24,6 +30,8 @@ from .mxq import (  # noqa: F401
     status_read,
     swiglu_bwd,
     swiglu_bwd_quantize,
+    swiglu_dropout_bwd,
+    swiglu_dropout_fwd,
     swiglu_fwd,
     swiglu_quantize,
     workspace_bytes,

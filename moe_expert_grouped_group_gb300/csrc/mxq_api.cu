@@ -567,6 +567,7 @@ const char* mxq_error_string(int code) {
         case MXQ_ERR_ALIGN: return "a pointer is not 16-byte aligned";
         case MXQ_ERR_SCRATCH_LIMIT:
             return "(M/128)*N exceeds the 2,097,152-float scratch of mxq_grouped_dbias_noalloc";
+        case MXQ_ERR_VALUE: return "a scalar argument is outside its range";
         default: return "unknown error";
     }
 }

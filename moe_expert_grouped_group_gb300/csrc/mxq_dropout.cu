@@ -1,0 +1,194 @@
+// mxq_dropout.cu -- dropout whose mask is made from a counter and never
+// stored: the same {seed, offset} gives the same mask in the forward pass, in
+// the backward pass and on any launch shape.
+//
+// Element i (row-major index of the (M, F) tensor that is dropped) is dropped
+// when its 16-bit word is below t = round(65536 p), and scaled by
+// 65536 / (65536 - t) otherwise, so that the expectation is kept exactly for
+// the probability t / 65536 that is used. Its word is the (i mod 8)-th, low
+// half first, of Philox 4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel
+// random numbers: as easy as 1, 2, 3", SC 2011) at the counter
+// (i div 8, offset) under the key `seed`, all 64-bit, low word first. 16 bits
+// an element halve the generator's work against 32.
+//
+// A dropped element is selected away, not multiplied by 0: an infinity or NaN
+// in it does not reach the output or the gradient.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "mxq_common.cuh"
+#include "mxq_ragged.h"
+
+namespace mxq {
+namespace ragged {
+
+// The eight 16-bit words of counter `block`, two per 32-bit word.
+__device__ __forceinline__ uint4 philox(uint64_t block, uint64_t offset, uint64_t seed) {
+    uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c1 = (uint32_t)b;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c3 = (uint32_t)a;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return make_uint4(c0, c1, c2, c3);
+}
+__device__ __forceinline__ bool kept(const uint4& w, int j, uint32_t t) {
+    const uint32_t x = j < 2 ? w.x : j < 4 ? w.y : j < 6 ? w.z : w.w;
+    return ((j & 1) ? x >> 16 : x & 0xFFFFu) >= t;
+}
+
+struct Rng {
+    uint64_t seed, offset;
+};
+__device__ __forceinline__ Rng load_rng(const int64_t* rng) {
+    return Rng{(uint64_t)__ldg(rng), (uint64_t)__ldg(rng + 1)};
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = bf16lo(ws[j]);
+        f[2 * j + 1] = bf16hi(ws[j]);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+        o[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__global__ void __launch_bounds__(256) swiglu_dropout_fwd_kernel(const uint16_t* y, int64_t M, int64_t F,
+                                                                 const int64_t* rng, uint32_t t, float scale,
+                                                                 uint16_t* h) {
+    const Rng r = load_rng(rng);
+    const int64_t per = F / 8, vecs = M * per;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < vecs; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t m = i / per, f = (i - m * per) * 8;
+        float g[8], u[8], o[8];
+        unpack8(*reinterpret_cast<const uint4*>(y + m * 2 * F + f), g);
+        unpack8(*reinterpret_cast<const uint4*>(y + m * 2 * F + F + f), u);
+        const uint4 w = philox((uint64_t)i, r.offset, r.seed);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = kept(w, j, t) ? __fmul_rn(swiglu_h(g[j], u[j]), scale) : 0.0f;
+        *reinterpret_cast<uint4*>(h + i * 8) = pack8(o);
+    }
+}
+
+__global__ void __launch_bounds__(256) swiglu_dropout_bwd_kernel(const uint16_t* dh, const uint16_t* y, int64_t M,
+                                                                 int64_t F, const int64_t* rng, uint32_t t,
+                                                                 float scale, uint16_t* dy) {
+    const Rng r = load_rng(rng);
+    const int64_t per = F / 8, vecs = M * per;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < vecs; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t m = i / per, f = (i - m * per) * 8;
+        float d[8], g[8], u[8], dg[8], du[8];
+        unpack8(*reinterpret_cast<const uint4*>(dh + i * 8), d);
+        unpack8(*reinterpret_cast<const uint4*>(y + m * 2 * F + f), g);
+        unpack8(*reinterpret_cast<const uint4*>(y + m * 2 * F + F + f), u);
+        const uint4 w = philox((uint64_t)i, r.offset, r.seed);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            swiglu_grads(__fmul_rn(d[j], scale), g[j], u[j], dg[j], du[j]);
+            if (!kept(w, j, t)) dg[j] = du[j] = 0.0f;
+        }
+        *reinterpret_cast<uint4*>(dy + m * 2 * F + f) = pack8(dg);
+        *reinterpret_cast<uint4*>(dy + m * 2 * F + F + f) = pack8(du);
+    }
+}
+
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
+    unpack8(*reinterpret_cast<const uint4*>(p), f);
+}
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
+    *reinterpret_cast<uint4*>(p) = pack8(f);
+}
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f32(float* p, float v) { *p = v; }
+__device__ __forceinline__ void from_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// out may be x or residual: a thread reads its elements before it writes them.
+template <typename T>
+__global__ void __launch_bounds__(256) dropout_kernel(const T* x, const T* residual, int64_t n, const int64_t* rng,
+                                                      uint32_t t, float scale, T* out) {
+    const Rng r = load_rng(rng);
+    const int64_t vecs = (n + 7) / 8;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < vecs; i += (int64_t)gridDim.x * blockDim.x) {
+        const uint4 w = philox((uint64_t)i, r.offset, r.seed);
+        if (8 * i + 8 <= n) {
+            float v[8], a[8];
+            load8(x + 8 * i, v);
+            if (residual) load8(residual + 8 * i, a);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = kept(w, j, t) ? __fmul_rn(v[j], scale) : 0.0f;
+                if (residual) v[j] = __fadd_rn(v[j], a[j]);
+            }
+            store8(out + 8 * i, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (8 * i + j < n) {
+                    float v = kept(w, j, t) ? __fmul_rn(to_f32(x[8 * i + j]), scale) : 0.0f;
+                    if (residual) v = __fadd_rn(v, to_f32(residual[8 * i + j]));
+                    from_f32(out + 8 * i + j, v);
+                }
+        }
+    }
+}
+
+static unsigned grid_for(int64_t vecs) {
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>((vecs + 255) / 256, (int64_t)sm_count() * 8));
+}
+static float scale_of(uint32_t t) { return t >= 65536u ? 0.0f : (float)(65536.0 / (65536 - (int)t)); }
+
+cudaError_t run_swiglu_dropout_fwd(const void* y, int64_t M, int64_t F, const int64_t* rng, uint32_t t, void* h,
+                                   cudaStream_t s) {
+    if (M == 0) return cudaSuccess;
+    swiglu_dropout_fwd_kernel<<<grid_for(M * (F / 8)), 256, 0, s>>>((const uint16_t*)y, M, F, rng, t, scale_of(t),
+                                                                    (uint16_t*)h);
+    return cudaGetLastError();
+}
+cudaError_t run_swiglu_dropout_bwd(const void* dh, const void* y, int64_t M, int64_t F, const int64_t* rng, uint32_t t,
+                                   void* dy, cudaStream_t s) {
+    if (M == 0) return cudaSuccess;
+    swiglu_dropout_bwd_kernel<<<grid_for(M * (F / 8)), 256, 0, s>>>((const uint16_t*)dh, (const uint16_t*)y, M, F, rng,
+                                                                    t, scale_of(t), (uint16_t*)dy);
+    return cudaGetLastError();
+}
+cudaError_t run_dropout(const void* x, const void* residual, int64_t n, int f32, const int64_t* rng, uint32_t t,
+                        void* out, cudaStream_t s) {
+    if (n == 0) return cudaSuccess;
+    const unsigned grid = grid_for((n + 7) / 8);
+    if (f32)
+        dropout_kernel<float><<<grid, 256, 0, s>>>((const float*)x, (const float*)residual, n, rng, t, scale_of(t),
+                                                   (float*)out);
+    else
+        dropout_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>((const __nv_bfloat16*)x, (const __nv_bfloat16*)residual, n,
+                                                           rng, t, scale_of(t), (__nv_bfloat16*)out);
+    return cudaGetLastError();
+}
+
+}  // namespace ragged
+}  // namespace mxq

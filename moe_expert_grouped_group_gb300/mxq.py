@@ -18,7 +18,7 @@ import torch
 
 from .build import LIB
 
-ROWWISE, COLWISE, SWIZZLE, DEQUANT_OUT, ACCUMULATE, OUT_BF16, PAD_EXPERTS = 1, 2, 4, 8, 16, 32, 64
+ROWWISE, COLWISE, SWIZZLE, DEQUANT_OUT, ACCUMULATE, OUT_BF16, PAD_EXPERTS, OUT_F32 = 1, 2, 4, 8, 16, 32, 64, 128
 OP_GROUP_QUANTIZE, OP_REQUANT_COLWISE, OP_GROUPED_DBIAS = 1, 2, 3
 OP_GEMM_FPROP, OP_GEMM_DGRAD, OP_GEMM_WGRAD, OP_SWIGLU_BWD_QUANTIZE, OP_SCALED_BIAS = 4, 5, 6, 7, 8
 OP_GEMM_DGRAD_SWIGLU = 9
@@ -32,7 +32,9 @@ SYMBOLS = [
     "mxq_grouped_dbias_noalloc", "mxq_swiglu_quantize", "mxq_swiglu_bwd_quantize", "mxq_group_quantize_scaled_bias",
     "mxq_requant_colwise_scaled_bias", "mxq_grouped_gemm_fprop_swiglu", "mxq_grouped_gemm_dgrad_swiglu",
     "mxq_scale_bytes_grouped", "mxq_grouped_gemm_fprop_ex", "mxq_grouped_gemm_dgrad_ex", "mxq_probe_mma_stream",
-    "mxq_probe_mma_stream_ex", "mxq_selftest_wait_timeout",
+    "mxq_probe_mma_stream_ex", "mxq_selftest_wait_timeout", "mxq_ragged_gemm_fprop", "mxq_ragged_gemm_dgrad",
+    "mxq_ragged_gemm_wgrad", "mxq_int8_quantize_rows", "mxq_int8_gemm_fprop", "mxq_swiglu_dropout_fwd",
+    "mxq_swiglu_dropout_bwd", "mxq_dropout",
 ]
 
 
@@ -42,6 +44,7 @@ class MXQError(RuntimeError):
 
 _lib = None
 _P, _I64, _INT, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_F64 = ctypes.c_double
 
 
 def load(path: str = LIB) -> ctypes.CDLL:
@@ -79,6 +82,14 @@ def load(path: str = LIB) -> ctypes.CDLL:
                                                  _P, _P, _P, _SZ, _P]
     L.mxq_requant_colwise_scaled_bias.argtypes = [_P, _P, _I64, _I64, _INT, _P, _INT, _P, _P, _P, _P, _P, _P, _P,
                                                   _P, _P, _P, _P, _SZ, _P]
+    L.mxq_ragged_gemm_fprop.argtypes = [_P, _I64, _P, _P, _I64, _I64, _I64, _INT, _P, _INT, _P, _P, _P]
+    L.mxq_ragged_gemm_dgrad.argtypes = [_P, _I64, _P, _I64, _I64, _I64, _INT, _P, _INT, _P, _P, _P]
+    L.mxq_ragged_gemm_wgrad.argtypes = [_P, _I64, _P, _I64, _I64, _I64, _I64, _INT, _P, _INT, _P, _P, _P]
+    L.mxq_int8_quantize_rows.argtypes = [_P, _I64, _I64, _I64, _P, _P, _P]
+    L.mxq_int8_gemm_fprop.argtypes = [_P, _P, _P, _P, _P, _I64, _I64, _I64, _INT, _P, _INT, _P, _P, _P]
+    L.mxq_swiglu_dropout_fwd.argtypes = [_P, _I64, _I64, _P, _F64, _P, _P]
+    L.mxq_swiglu_dropout_bwd.argtypes = [_P, _P, _I64, _I64, _P, _F64, _P, _P]
+    L.mxq_dropout.argtypes = [_P, _P, _I64, _P, _F64, _INT, _P, _P]
     L.mxq_status_read.argtypes = [_P, _P, _P]
     L.mxq_probe_mma_stream.argtypes = [_I64, _P, _P]
     L.mxq_probe_mma_stream.restype = _INT
@@ -91,7 +102,9 @@ def load(path: str = LIB) -> ctypes.CDLL:
     L.mxq_last_cuda_error.restype = _INT
     for a in ("mxq_group_quantize", "mxq_requant_colwise", "mxq_grouped_dbias", "mxq_grouped_gemm_fprop",
               "mxq_grouped_gemm_dgrad", "mxq_grouped_gemm_wgrad", "mxq_swiglu_fwd", "mxq_swiglu_bwd",
-              "mxq_status_read"):
+              "mxq_status_read", "mxq_ragged_gemm_fprop", "mxq_ragged_gemm_dgrad", "mxq_ragged_gemm_wgrad",
+              "mxq_int8_quantize_rows", "mxq_int8_gemm_fprop", "mxq_swiglu_dropout_fwd", "mxq_swiglu_dropout_bwd",
+              "mxq_dropout"):
         getattr(L, a).restype = _INT
     return L
 
@@ -645,3 +658,173 @@ def swiglu_bwd_quantize(dh, y, m_splits, rowwise=True, colwise=True, swizzle=Tru
                                        0 if ws is None else ws.numel() * ws.element_size(), _stream())
     _check(rc, "mxq_swiglu_bwd_quantize")
     return o
+
+
+# ------------------------------------------------ ragged bf16 and int8 products, dropout
+_I8 = (torch.int8,)
+_I64T = (torch.int64,)
+
+
+def _rows_ptr(t, name, dtypes):
+    """Pointer and row stride of a 2-D CUDA tensor whose rows are contiguous (the tensor may be a
+    slice of wider rows). The stride of a tensor with fewer than two rows is never used."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise MXQError(f"{name}: tensor arguments must be CUDA tensors")
+    if t.dtype not in dtypes:
+        raise MXQError(f"{name}: dtype {t.dtype}, expected one of {[str(d) for d in dtypes]}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise MXQError(f"{name}: expected a 2-D tensor with contiguous rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _shape(t, name, want):
+    if tuple(t.shape) != tuple(want):
+        raise MXQError(f"{name}: shape {tuple(t.shape)}, expected {tuple(want)}")
+
+
+def _out_flag(out, out_dtype, shape, dev, default, other, flag):
+    """The output tensor of a product and the flag for its element type."""
+    if out is None:
+        dt = default if out_dtype is None else out_dtype
+        if dt not in (default, other):
+            raise MXQError(f"out_dtype: {dt}, expected {default} or {other}")
+        out = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise MXQError(f"out: dtype {out.dtype}, out_dtype is {out_dtype}")
+        _shape(out, "out", shape)
+        _need(out, "out", 0, (default, other))
+    return out, (flag if out.dtype == other else 0)
+
+
+def _grouping(m_splits, E):
+    m_splits = _splits(m_splits)
+    if m_splits is None:
+        raise MXQError("m_splits is required")
+    if m_splits.numel() != E:
+        raise MXQError(f"m_splits: {m_splits.numel()} counts for {E} experts")
+    return _ptr(m_splits)
+
+
+def ragged_gemm_fprop(x, w, m_splits, bias=None, out_dtype=None, status=None, out=None):
+    """Y = X W_e^T (+ b_e) on bf16, any expert counts. x (M, K), its rows possibly a slice of wider
+    ones; w (E, N, K); bias (E, N); Y (M, N) in bf16 (default) or fp32."""
+    xp, ldx = _rows_ptr(x, "x", _BF16)
+    M, K = x.shape
+    E, N, Kw = w.shape
+    _shape(w, "w", (E, N, K))
+    _need(w, "w", E * N * K * 2, _BF16)
+    _need(bias, "bias", E * N * 2, _BF16)
+    _need_flags(None, status)
+    out, flag = _out_flag(out, out_dtype, (M, N), x.device, torch.bfloat16, torch.float32, OUT_F32)
+    rc = lib().mxq_ragged_gemm_fprop(xp, ldx, _ptr(w), _ptr(bias), M, N, K, E, _grouping(m_splits, E), flag,
+                                     _ptr(out), _ptr(status), _stream())
+    _check(rc, "mxq_ragged_gemm_fprop")
+    return out
+
+
+def ragged_gemm_dgrad(dy, w, m_splits, out_dtype=None, status=None, out=None):
+    """dX = dY W_e on bf16, any expert counts. dy (M, N), w (E, N, K); dX (M, K) in bf16 (default) or fp32."""
+    dyp, lddy = _rows_ptr(dy, "dy", _BF16)
+    M, N = dy.shape
+    E, Nw, K = w.shape
+    _shape(w, "w", (E, N, K))
+    _need(w, "w", E * N * K * 2, _BF16)
+    _need_flags(None, status)
+    out, flag = _out_flag(out, out_dtype, (M, K), dy.device, torch.bfloat16, torch.float32, OUT_F32)
+    rc = lib().mxq_ragged_gemm_dgrad(dyp, lddy, _ptr(w), M, N, K, E, _grouping(m_splits, E), flag, _ptr(out),
+                                     _ptr(status), _stream())
+    _check(rc, "mxq_ragged_gemm_dgrad")
+    return out
+
+
+def ragged_gemm_wgrad(dy, x, m_splits, accumulate=False, out_dtype=None, status=None, out=None):
+    """dW_e = dY_e^T X_e on bf16, any expert counts. dy (M, N), x (M, K); dW (E, N, K) in fp32 (default)
+    or bf16, added to `out` with accumulate."""
+    dyp, lddy = _rows_ptr(dy, "dy", _BF16)
+    xp, ldx = _rows_ptr(x, "x", _BF16)
+    M, N = dy.shape
+    K = x.shape[1]
+    _shape(x, "x", (M, K))
+    if accumulate and out is None:
+        raise MXQError("accumulate needs out")
+    if _splits(m_splits) is None:
+        raise MXQError("m_splits is required")
+    E = m_splits.numel()
+    _need_flags(None, status)
+    out, flag = _out_flag(out, out_dtype, (E, N, K), dy.device, torch.float32, torch.bfloat16, OUT_BF16)
+    rc = lib().mxq_ragged_gemm_wgrad(dyp, lddy, xp, ldx, M, N, K, E, _grouping(m_splits, E),
+                                     flag | (ACCUMULATE if accumulate else 0), _ptr(out), _ptr(status), _stream())
+    _check(rc, "mxq_ragged_gemm_wgrad")
+    return out
+
+
+def int8_quantize_rows(x, out=None):
+    """bf16 rows (M, K) -> (int8 codes (M, K), fp32 scales (M,)), x ~ q * scale."""
+    xp, ldx = _rows_ptr(x, "x", _BF16)
+    M, K = x.shape
+    q, scale = out if out is not None else (torch.empty((M, K), dtype=torch.int8, device=x.device),
+                                            torch.empty((M,), dtype=torch.float32, device=x.device))
+    _need(q, "q", M * K, _I8)
+    _need(scale, "scale", M * 4, _F32)
+    _check(lib().mxq_int8_quantize_rows(xp, ldx, M, K, _ptr(q), _ptr(scale), _stream()), "mxq_int8_quantize_rows")
+    return q, scale
+
+
+def int8_gemm_fprop(xq, x_scale, wq, w_scale, m_splits, bias=None, out_dtype=None, status=None, out=None):
+    """Y = (Xq Wq_e^T) x_scale w_scale_e (+ b_e). xq (M, K) int8, x_scale (M,), wq (E, N, K) int8,
+    w_scale (E, N); Y (M, N) in bf16 (default) or fp32."""
+    M, K = xq.shape
+    E, N, Kw = wq.shape
+    _shape(wq, "wq", (E, N, K))
+    _need(xq, "xq", M * K, _I8)
+    _need(x_scale, "x_scale", M * 4, _F32)
+    _need(wq, "wq", E * N * K, _I8)
+    _need(w_scale, "w_scale", E * N * 4, _F32)
+    _need(bias, "bias", E * N * 2, _BF16)
+    _need_flags(None, status)
+    out, flag = _out_flag(out, out_dtype, (M, N), xq.device, torch.bfloat16, torch.float32, OUT_F32)
+    rc = lib().mxq_int8_gemm_fprop(_ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(bias), M, N, K, E,
+                                   _grouping(m_splits, E), flag, _ptr(out), _ptr(status), _stream())
+    _check(rc, "mxq_int8_gemm_fprop")
+    return out
+
+
+def swiglu_dropout_fwd(y, rng, p, out=None):
+    """h = D(silu(g) * u) of FC1's output y = [g | u] (M, 2F). rng: CUDA int64 {seed, offset}."""
+    M, F2 = y.shape
+    out = out if out is not None else torch.empty((M, F2 // 2), dtype=torch.bfloat16, device=y.device)
+    _need(y, "y", M * F2 * 2, _BF16)
+    _need(rng, "rng", 16, _I64T)
+    _need(out, "out", M * (F2 // 2) * 2, _BF16)
+    _check(lib().mxq_swiglu_dropout_fwd(_ptr(y), M, F2 // 2, _ptr(rng), p, _ptr(out), _stream()),
+           "mxq_swiglu_dropout_fwd")
+    return out
+
+
+def swiglu_dropout_bwd(dh, y, rng, p, out=None):
+    """The gradient [dg | du] (M, 2F) of y from dh (M, F); rng and p those of the forward call."""
+    M, F2 = y.shape
+    out = out if out is not None else torch.empty((M, F2), dtype=torch.bfloat16, device=y.device)
+    _need(dh, "dh", M * (F2 // 2) * 2, _BF16)
+    _need(y, "y", M * F2 * 2, _BF16)
+    _need(rng, "rng", 16, _I64T)
+    _need(out, "out", M * F2 * 2, _BF16)
+    _check(lib().mxq_swiglu_dropout_bwd(_ptr(dh), _ptr(y), M, F2 // 2, _ptr(rng), p, _ptr(out), _stream()),
+           "mxq_swiglu_dropout_bwd")
+    return out
+
+
+def dropout(x, rng, p, residual=None, out=None):
+    """D(x) (+ residual), bf16 or fp32; its own gradient when residual is None. out may be x or residual."""
+    _need(x, "x", 0, _BF16 + _F32)
+    out = out if out is not None else torch.empty_like(x)
+    n, size = x.numel(), x.element_size()
+    _need(residual, "residual", n * size, (x.dtype,))
+    _need(rng, "rng", 16, _I64T)
+    _need(out, "out", n * size, (x.dtype,))
+    _check(lib().mxq_dropout(_ptr(x), _ptr(residual), n, _ptr(rng), p, OUT_F32 if x.dtype == torch.float32 else 0,
+                             _ptr(out), _stream()), "mxq_dropout")
+    return out
