@@ -3,14 +3,13 @@
 //   fprop  Y[m,:]  = X[m,:]  . W[e(m)]^T (+ b[e(m)])
 //   dgrad  dX[m,:] = dY[m,:] . W[e(m)]
 //   wgrad  dW[e]   = dY_e^T . X_e
-// fp32 accumulation in TMEM, one rounding to bf16 (or none, fp32 outputs).
+// fp32 sums, one rounding to bf16 (or none, fp32 outputs).
 //
-// Which operand is which. fprop and dgrad put the weight's features on the
-// MMA's M (128 TMEM lanes) and the tokens on its N, because N is a field of
-// the instruction descriptor that may differ from tile to tile: a slice of an
-// expert's rows costs MMA work in steps of 16 rows, not 128. The accumulator
-// is the transpose of the output tile: lane = feature, column = token. wgrad
-// puts dY's features on M, X's on N, and sums over the expert's rows.
+// Which operand is which. The output's contiguous dimension is put on the
+// MMA's M (TMEM lanes), its rows on the MMA's N (accumulator columns): W and
+// the tokens in fprop and dgrad, X and dY in wgrad. N is a field of the
+// instruction descriptor that may differ from tile to tile, so a slice of an
+// expert's rows costs MMA work in steps of 32 rows (16 on one SM), not 128.
 //
 // Majorness. X and dY of fprop / dgrad and W of fprop are K-major; W of dgrad
 // and both operands of wgrad are MN-major. All are staged as 128-byte-wide
@@ -24,10 +23,23 @@
 // from m_e on are zeroed in shared memory, in the last block of an expert,
 // before its MMAs (zeroing one operand would not do: 0 * inf is not 0).
 //
-// One persistent CTA per SM, warp-specialised: warp 0 issues TMA loads into a
-// ring of 64-deep stages, warp 1 owns TMEM and issues the MMAs from one lane,
-// warps 2..9 drain one of two accumulators while the MMAs fill the other.
-// Every wait is bounded (about 2 s); on expiry MXQ_STATUS_WAIT_TIMEOUT is set.
+// fp32 results. The tensor core truncates as it adds to its fp32 accumulator:
+// over 2048 rows a wgrad entry came out 2.1e-6 off (relative 2-norm; an fp32
+// matrix product 3.9e-7). Outputs that are not rounded to bf16 are therefore
+// summed in registers, one accumulator of FLUSH stages at a time (kRegs).
+//
+// Two shapes of the one kernel. Pairs of SMs (kCG = 2) share a tile of 256
+// features by up to 256 rows, each staging half of both operands: 32 KB a
+// stage and SM for the MMA work that costs one SM alone 48 KB. One SM
+// (kCG = 1) takes 128 features by up to 32 rows: what is left of the product
+// when experts have few rows is reading W, and its stages are small enough to
+// keep nine in flight.
+//
+// Persistent and warp-specialised: warp 0 issues TMA loads into a ring of
+// 64-deep stages, warp 1 owns TMEM and issues the MMAs (rank 0 of a pair; rank
+// 1's only zeroes its share of an expert's last rows), warps 2..9 drain one of
+// two accumulators while the MMAs fill the other. Every wait is bounded (about
+// 2 s); on expiry MXQ_STATUS_WAIT_TIMEOUT is set.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -42,19 +54,27 @@
 namespace mxq {
 namespace ragged {
 
-constexpr int BK = 64;   // reduction depth of a stage: 128 bytes of bf16
-constexpr int BN = 256;  // widest MMA N
-constexpr int STAGES = 4;
-constexpr int A_BYTES = kFM * BK * 2;
-constexpr int B_BYTES = BN * BK * 2;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int BK = 64;    // reduction depth of a stage: 128 bytes of bf16
+constexpr int FLUSH = 8;  // stages an accumulator holds before it is added to the registers (kRegs)
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
-constexpr int TMEM_COLS = 512;
-constexpr int BAR_REGION = STAGES * STAGE_BYTES;
-constexpr int TABLE_REGION = BAR_REGION + 256;
-__host__ __device__ constexpr int smem_bytes(int E) { return 1024 + TABLE_REGION + 8 * (E + 1); }
-static_assert(smem_bytes(MXQ_MAX_EXPERTS) <= 232448, "shared memory over the per-block limit");
+
+template <int kCG>
+struct Shape {
+    static constexpr int kFeat = kFM * kCG;                   // features of a tile
+    static constexpr int kWide = kCG == 2 ? 256 : 32;         // widest MMA N
+    static constexpr int kStep = 16 * kCG;                    // its granularity
+    static constexpr int kBox = kCG == 2 ? 64 : 32;           // token rows of a K-major box
+    static constexpr int kStages = kCG == 2 ? 6 : 9;
+    static constexpr int kA = kFM * BK * 2, kStage = kA + kWide / kCG * BK * 2;
+    static constexpr int kTmem = 2 * kWide;
+    static constexpr int kEpi = kStages * kStage;             // staging of the bf16 epilogue, two groups
+    static constexpr int kBars = kEpi + 2 * kEpiBytes;
+    static constexpr int kTables = kBars + 512;
+    __host__ __device__ static constexpr int smem(int E) { return 1024 + kTables + 12 * (E + 1); }
+    static_assert(1024 + kTables + 12 * (MXQ_MAX_EXPERTS + 1) <= 232448, "shared memory over the per-block limit");
+    static_assert(kBars % 8 == 0 && 8 * (3 * kStages + 4) <= 512, "barrier region");
+};
 
 struct Params {
     int64_t M, N, K;
@@ -66,63 +86,76 @@ struct Params {
     int32_t* status;
 };
 
-// Store one value, or add it to what is there.
-__device__ __forceinline__ void put(void* out, int64_t i, float v, bool f32, bool add) {
-    if (f32) {
-        float* o = static_cast<float*>(out) + i;
-        *o = add ? *o + v : v;
-    } else {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + i;
-        *o = __float2bfloat16_rn(add ? __bfloat162float(*o) + v : v);
-    }
-}
-
-template <int kMode>
+template <int kMode, int kCG, bool kRegs>
 __global__ void __launch_bounds__(THREADS, 1)
     ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Params p) {
+    using S = Shape<kCG>;
+    constexpr int STAGES = S::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align<1024>(smem_raw);
-    int32_t* s_off = reinterpret_cast<int32_t*>(smem + TABLE_REGION);
+    int32_t* s_off = reinterpret_cast<int32_t*>(smem + S::kTables);
     int32_t* s_slices = s_off + p.E + 1;
+    int32_t* s_order = s_slices + p.E + 1;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = kCG == 2 ? cta_rank() : 0;
 
-    const int bad = load_ragged(p.m_splits, p.E, p.M, BN, s_off, s_slices);
+    // both CTAs of a pair find the same fault and stop before any cluster-wide step
+    const int bad = load_ragged(p.m_splits, p.E, p.M, S::kWide, s_off, s_slices);
     if (bad) {
         report_status(p.status, bad);
         return;
     }
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_REGION);
-    const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
-    const uint32_t accf0 = smem_u32(bars + 2 * STAGES), acce0 = smem_u32(bars + 2 * STAGES + 2);
+    if (kMode == kWgrad) {
+        for (int e = threadIdx.x; e < p.E; e += THREADS) {
+            const int m = s_off[e + 1] - s_off[e];
+            int before = 0;
+            for (int f = 0; f < p.E; ++f) {
+                const int o = s_off[f + 1] - s_off[f];
+                before += o > m || (o == m && f < e);
+            }
+            s_order[before] = e;
+        }
+    }
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, fix0 = empty0 + 8 * STAGES;
+    const uint32_t accf0 = fix0 + 8 * STAGES, acce0 = accf0 + 16;
     volatile int* abort_flag = &s_abort;
     if (threadIdx.x == 0) {
         s_abort = 0;
         for (int st = 0; st < STAGES; ++st) {
             mbar_init(full0 + 8 * st, 1);
             mbar_init(empty0 + 8 * st, 1);
+            mbar_init(fix0 + 8 * st, 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf0 + 8 * b, 1);
-            mbar_init(acce0 + 8 * b, EPI_WARPS);
+            mbar_init(acce0 + 8 * b, kCG * EPI_WARPS);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmA) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmB) : "memory");
     }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
-                     "r"(TMEM_COLS)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    if (warp == 1) tmem_alloc<kCG>(smem_u32(&s_tmem), S::kTmem);
     fence_before();
     __syncthreads();
+    if (kCG == 2) cluster_sync();  // both CTAs' barriers exist before any load completes on rank 0's
     fence_after();
     const uint32_t tmem = s_tmem;
-    const Walk<kMode, BN> W(p.N, p.K, p.E, s_off, s_slices);
+    const Walk<kMode, S::kFeat, S::kWide, S::kStep> W(p.N, p.K, p.E, s_off, s_slices, s_order);
+    const int64_t first = blockIdx.x / kCG, stride = gridDim.x / kCG;
     constexpr bool a_mn = kMode != kFprop, b_mn = kMode == kWgrad;
+    // rows of an expert's last block that are zeroed: left .. up to the next multiple of 16
+    auto ragged_end = [](const Tile& T, int r) { return kMode == kWgrad && T.red - r < BK && ((T.red - r) & 15) != 0; };
+    auto zero_rows = [&](const Tile& T, int r, int stage) {
+        const int left = T.red - r, per = (16 - (left & 15)) * 8, boxes = 2 + (T.n / kCG + 63) / 64;
+        uint8_t* s = smem + stage * S::kStage + left * 128;
+        for (int i = lane; i < per * boxes; i += 32)
+            *reinterpret_cast<uint4*>(s + i / per * 8192 + i % per * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_async_smem();
+        __syncwarp();
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
@@ -130,28 +163,36 @@ __global__ void __launch_bounds__(THREADS, 1)
             int stage = 0;
             uint32_t phase = 0;
             int64_t fills = 0;
-            for (int64_t t = blockIdx.x; t < W.total; t += gridDim.x) {
+            for (int64_t t = first; t < W.total; t += stride) {
                 const Tile T = W.get(t);
-                const int boxes = (T.n + 63) / 64;
+                const int half = T.n / kCG;  // this CTA's columns of the tile: [rank * half, + half)
+                const int boxes = (half + S::kBox - 1) / S::kBox;
+                const int f = T.f0 + rank * kFM, c = T.c0 + rank * half;
+                const uint32_t bytes = S::kA + boxes * S::kBox * BK * 2;
                 for (int r = 0; r < T.red; r += BK) {
                     if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag)) {
-                        drain_ring(full0, STAGES, fills);
+                        if (rank == 0) drain_ring(full0, STAGES, fills);  // rank 1's copies complete there too
                         goto done_producer;
                     }
-                    const uint32_t fb = full0 + 8 * stage, a = smem_u32(smem + stage * STAGE_BYTES), b = a + A_BYTES;
-                    mbar_expect_tx(fb, A_BYTES + boxes * 8192);
+                    const uint32_t own = full0 + 8 * stage, a = smem_u32(smem + stage * S::kStage), b = a + S::kA;
+                    // a pair's loads complete on rank 0's barrier, but where each CTA has to zero rows on its own
+                    const bool local = kCG == 1 || ragged_end(T, r);
+                    if (local) mbar_expect_tx(own, bytes);
+                    else if (rank == 0) mbar_expect_tx(own, 2 * bytes);
+                    const uint32_t fb = local ? (kCG == 2 ? mapa(own, rank) : own) : mapa(own, 0);
                     if (kMode == kFprop) {
-                        tma_load_3d(a, &tmA, fb, r, T.f0, T.e);
+                        load_3d<kCG>(a, &tmA, fb, r, f, T.e);
                     } else if (kMode == kDgrad) {
-                        tma_load_3d(a, &tmA, fb, T.f0, r, T.e);
-                        tma_load_3d(a + 8192, &tmA, fb, T.f0 + 64, r, T.e);
+                        load_3d<kCG>(a, &tmA, fb, f, r, T.e);
+                        load_3d<kCG>(a + 8192, &tmA, fb, f + 64, r, T.e);
                     } else {
-                        tma_load_2d(a, &tmA, fb, T.f0, T.red0 + r);
-                        tma_load_2d(a + 8192, &tmA, fb, T.f0 + 64, T.red0 + r);
+                        load_2d<kCG>(a, &tmA, fb, f, T.red0 + r);
+                        load_2d<kCG>(a + 8192, &tmA, fb, f + 64, T.red0 + r);
                     }
                     for (int i = 0; i < boxes; ++i) {
-                        if (kMode == kWgrad) tma_load_2d(b + 8192 * i, &tmB, fb, T.c0 + 64 * i, T.red0 + r);
-                        else tma_load_2d(b + 8192 * i, &tmB, fb, r, T.c0 + 64 * i);
+                        const uint32_t dst = b + S::kBox * BK * 2 * i;
+                        if (kMode == kWgrad) load_2d<kCG>(dst, &tmB, fb, c + S::kBox * i, T.red0 + r);
+                        else load_2d<kCG>(dst, &tmB, fb, r, c + S::kBox * i);
                     }
                     ++fills;
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
@@ -159,98 +200,183 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         done_producer:;
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------ MMA issuer
         int stage = 0, buf = 0;
-        uint32_t phase = 0, aphase = 0;
+        uint32_t phase = 0, aphase = 0, fixed = 0;  // fixed: bit st = parity of fix[st]
         const uint32_t base = smem_u32(smem);
         // MN-major: 64-element chunks 8192 bytes apart, 8-row groups of the reduction 1024 apart
         const uint64_t ad0 = smem_desc(base, a_mn ? 8192 : 16, 1024);
-        const uint64_t bd0 = smem_desc(base + A_BYTES, b_mn ? 8192 : 16, 1024);
+        const uint64_t bd0 = smem_desc(base + S::kA, b_mn ? 8192 : 16, 1024);
         constexpr uint32_t a_step = (a_mn ? 2048 : 32) / 16, b_step = (b_mn ? 2048 : 32) / 16;  // 16 of the reduction
         bool ok = true;
-        for (int64_t t = blockIdx.x; t < W.total && ok; t += gridDim.x) {
+        for (int64_t t = first; t < W.total && ok; t += stride) {
             const Tile T = W.get(t);
-            if (T.red == 0) continue;  // wgrad of an empty expert: the epilogue writes zeros
-            const uint32_t id = idesc_f16(1, a_mn, b_mn, kFM, T.n);
-            ok = mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag);
-            for (int r = 0; r < T.red && ok; r += BK) {
-                ok = mbar_wait(full0 + 8 * stage, phase, abort_flag);
-                if (!ok) break;
-                const int left = min(BK, T.red - r), steps = (left + 15) / 16;
-                if (kMode == kWgrad && (left & 15)) {
-                    // rows left .. 16 * steps of every box belong to the next expert
-                    const int per = (16 * steps - left) * 8, boxes = 2 + (T.n + 63) / 64;
-                    uint8_t* s = smem + stage * STAGE_BYTES + left * 128;
-                    for (int i = lane; i < per * boxes; i += 32)
-                        *reinterpret_cast<uint4*>(s + i / per * 8192 + i % per * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    fence_async_smem();
+            const uint32_t id = idesc_f16(1, a_mn, b_mn, S::kFeat, T.n);
+            for (int r0 = 0; r0 < T.red && ok; r0 += kRegs ? FLUSH * BK : T.red) {
+                const int r1 = kRegs ? min(T.red, r0 + FLUSH * BK) : T.red;
+                ok = mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag);
+                for (int r = r0; r < r1 && ok; r += BK) {
+                    ok = mbar_wait(full0 + 8 * stage, phase, abort_flag);
+                    if (!ok) break;
+                    const int steps = (min(BK, T.red - r) + 15) / 16;
+                    if (ragged_end(T, r)) {
+                        zero_rows(T, r, stage);
+                        if (kCG == 2) {
+                            ok = mbar_wait(fix0 + 8 * stage, fixed >> stage & 1, abort_flag);
+                            if (!ok) break;
+                            fixed ^= 1u << stage;
+                            fence_cluster();
+                        }
+                    }
+                    fence_after();
+                    if (lane == 0) {
+                        const uint64_t so = (uint64_t)(stage * (S::kStage / 16));
+                        for (int k = 0; k < steps; ++k)
+                            mma_f16<kCG>(tmem + buf * S::kWide, ad0 + so + k * a_step, bd0 + so + k * b_step, id,
+                                         r > r0 || k > 0);
+                        mma_commit<kCG>(empty0 + 8 * stage);
+                    }
                     __syncwarp();
+                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
-                fence_after();
-                if (lane == 0) {
-                    const uint64_t so = (uint64_t)(stage * (STAGE_BYTES / 16));
-                    for (int k = 0; k < steps; ++k)
-                        mma_f16(tmem + buf * BN, ad0 + so + k * a_step, bd0 + so + k * b_step, id, (r | k) != 0);
-                    mma_commit(empty0 + 8 * stage);
-                }
+                if (ok && lane == 0) mma_commit<kCG>(accf0 + 8 * buf);
                 __syncwarp();
-                if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                buf ^= 1;
+                aphase ^= buf == 0;
             }
-            if (ok && lane == 0) mma_commit(accf0 + 8 * buf);
-            __syncwarp();
-            buf ^= 1;
-            aphase ^= buf == 0;
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------ rank 1: its rows of a ragged end
+        if (kMode == kWgrad) {
+            int stage = 0;
+            uint32_t loaded = 0;  // bit st = parity of this CTA's own full[st], used by ragged ends only
+            bool ok = true;
+            for (int64_t t = first; t < W.total && ok; t += stride) {
+                const Tile T = W.get(t);
+                if (T.red == 0) continue;
+                const int last = (T.red - 1) / BK;
+                const int at = (stage + last) % STAGES;
+                if (ragged_end(T, last * BK)) {
+                    ok = mbar_wait(full0 + 8 * at, loaded >> at & 1, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    loaded ^= 1u << at;
+                    zero_rows(T, last * BK, at);
+                    if (lane == 0) arrive_remote_release(mapa(fix0 + 8 * at, 0));
+                }
+                stage = (at + 1) % STAGES;
+            }
         }
     } else {
         // ------------------------------------------------------ epilogue
-        const int q = warp & 3, half = (warp - 2) >> 2;
+        const int q = warp & 3, group = (warp - 2) >> 2;  // two groups of four warps share the columns
+        uint8_t* stage = smem + S::kEpi + group * kEpiBytes;
+        const int64_t ld = kMode == kFprop ? p.N : p.K;  // features
         int buf = 0;
         uint32_t aphase = 0;
-        for (int64_t t = blockIdx.x; t < W.total; t += gridDim.x) {
-            const Tile T = W.get(t);
-            const int f = T.f0 + q * 32 + lane;
-            const bool live = f < (kMode == kDgrad ? p.K : p.N);
-            const bool add = kMode == kWgrad && p.accumulate;
-            if (T.red == 0) {
-                if (!add && live)
-                    for (int j = half; j < T.cols; j += 2)
-                        put(p.out, ((int64_t)T.e * p.N + f) * p.K + T.c0 + j, 0.0f, p.out_f32, false);
-                continue;
-            }
-            const bool ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
-            __syncwarp();
-            if (!ok || *abort_flag) break;
-            fence_after();
-            const float b =
-                kMode == kFprop && p.bias && live ? __bfloat162float(p.bias[(int64_t)T.e * p.N + f]) : 0.0f;
-            for (int c = 32 * half; c < T.cols; c += 64) {
-                uint32_t v[32];
-                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * BN + c, v);
-                tmem_wait_ld();
-                if (live) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (c + j >= T.cols) break;
-                        const int64_t i = kMode == kWgrad ? ((int64_t)T.e * p.N + f) * p.K + T.c0 + c + j
-                                                          : (int64_t)(T.c0 + c + j) * (kMode == kDgrad ? p.K : p.N) + f;
-                        put(p.out, i, __uint_as_float(v[j]) + b, p.out_f32, add);
-                    }
-                }
-            }
+        auto drained = [&] {
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acce0 + 8 * buf);
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive(acce0 + 8 * buf);
+                else arrive_remote_relaxed(mapa(acce0 + 8 * buf, 0));
+            }
             buf ^= 1;
             aphase ^= buf == 0;
+        };
+        for (int64_t t = first; t < W.total; t += stride) {
+            const Tile T = W.get(t);
+            const int f0 = T.f0 + rank * kFM;
+            const int live = (int)min((int64_t)kFM, ld - f0);  // may be negative: nothing to store
+            if (kMode == kWgrad && T.red == 0) {
+                // an empty expert: 16-byte stores of zero, a row piece of 128 features at a time
+                if (!p.accumulate) {
+                    const int size = p.out_f32 ? 4 : 2, per = live * size / 16;
+                    for (int c = q + 4 * group; c < T.cols; c += 8)
+                        for (int i = lane; i < per; i += 32)
+                            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + ((T.row0 + c) * ld + f0) * size +
+                                                      16 * i) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                continue;
+            }
+            if constexpr (kRegs) {
+                constexpr int kChunks = (S::kWide + 63) / 64;  // 32-column chunks of a group
+                float acc[kChunks][32];
+                bool ok = true;
+                for (int r0 = 0; r0 < T.red && ok; r0 += FLUSH * BK) {
+                    ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
+                    __syncwarp();
+                    ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+                    if (!ok) break;
+                    fence_after();
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i) {
+                        const int c = 64 * i + 32 * group;
+                        if (c < T.cols) {
+#pragma unroll
+                            for (int h = 0; h < 32; h += 16) {
+                                uint32_t v[16];
+                                tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + buf * S::kWide + c + h, v);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    acc[i][h + j] = r0 == 0 ? __uint_as_float(v[j])
+                                                            : __fadd_rn(acc[i][h + j], __uint_as_float(v[j]));
+                            }
+                        }
+                    }
+                    drained();
+                }
+                if (!ok) break;
+                const int l = q * 32 + lane;
+                if (l < live) {
+                    const float b =
+                        kMode == kFprop && p.bias ? __bfloat162float(p.bias[(int64_t)T.e * p.N + f0 + l]) : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int c = 64 * i + 32 * group + j;
+                            if (c >= T.cols) break;
+                            const int64_t at = (T.row0 + c) * ld + f0 + l;
+                            const float v = __fadd_rn(acc[i][j], b);
+                            if (p.out_f32) {
+                                float* o = static_cast<float*>(p.out) + at;
+                                *o = p.accumulate ? *o + v : v;
+                            } else {  // bf16 with accumulation
+                                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
+                                *o = __float2bfloat16_rn(__bfloat162float(*o) + v);
+                            }
+                        }
+                }
+            } else {
+                const bool ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
+                // the groups' warps meet at barriers below: all of a group stop, or none
+                if (group_any(1 + group, kEpiGroup, !ok || *abort_flag)) break;
+                fence_after();
+                float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (kMode == kFprop && p.bias) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int l = q * 32 + (lane >> 2) + 8 * g;
+                        if (l < live) b[g] = __bfloat162float(p.bias[(int64_t)T.e * p.N + f0 + l]);
+                    }
+                }
+                for (int c = 32 * group; c < T.cols; c += 64)
+                    store_columns_bf16(tmem + buf * S::kWide + c, q, lane, 1 + group, stage,
+                                       static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * ld + f0, ld, live, T.cols - c,
+                                       [&](float v, int l, int) { return v + b[(l >> 3) & 3]; });
+                drained();
+            }
         }
     }
     fence_before();
     __syncthreads();
     if (s_abort && threadIdx.x == 0 && p.status) atomicOr(p.status, MXQ_STATUS_WAIT_TIMEOUT);
+    if (kCG == 2) cluster_sync();  // rank 0's MMAs have read this CTA's shared memory for the last time
     if (warp == 1) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+        tmem_dealloc<kCG>(tmem, S::kTmem);
     }
 }
 
@@ -295,41 +421,85 @@ int sm_count() {
     return v;
 }
 
-template <int kMode>
-static cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const Params& p, int64_t tiles, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(ragged_gemm_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes(MXQ_MAX_EXPERTS));
-    if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, sm_count()));
-    ragged_gemm_kernel<kMode><<<grid, THREADS, smem_bytes(p.E), s>>>(a, b, p);
-    return cudaGetLastError();
+// Co-resident CTA pairs of the pair kernel on the current device.
+template <int kMode, bool kRegs>
+static int max_pairs() {
+    static std::atomic<int> cache[64];
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && (n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * (sm_count() / 2));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = Shape<2>::smem(MXQ_MAX_EXPERTS);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, (void*)ragged_gemm_kernel<kMode, 2, kRegs>, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        n = sm_count() / 2;
+    }
+    if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
-cudaError_t run_gemm(const GemmCall& c, cudaStream_t s) {
-    Params p{c.M, c.N, c.K, c.E, c.m_splits, static_cast<const __nv_bfloat16*>(c.bias), c.out, c.out_f32, c.accumulate,
-             c.status};
+template <int kMode, int kCG, bool kRegs>
+static cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const Params& p, int64_t tiles, cudaStream_t s) {
+    using S = Shape<kCG>;
+    cudaError_t e = cudaFuncSetAttribute(ragged_gemm_kernel<kMode, kCG, kRegs>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem(MXQ_MAX_EXPERTS));
+    if (e != cudaSuccess) return e;
+    const int64_t most = kCG == 2 ? max_pairs<kMode, kRegs>() : sm_count();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(kCG * std::max<int64_t>(1, std::min(tiles, most))));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = S::smem(p.E);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCG;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, ragged_gemm_kernel<kMode, kCG, kRegs>, a, b, p);
+}
+
+template <int kMode, int kCG>
+static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
+    using S = Shape<kCG>;
+    const Params p{c.M, c.N, c.K, c.E, c.m_splits, static_cast<const __nv_bfloat16*>(c.bias), c.out, c.out_f32,
+                   c.accumulate, c.status};
     CUtensorMap a, b;
     bool ok;
-    const int64_t feats = ((c.mode == kDgrad ? c.K : c.N) + kFM - 1) / kFM;
-    int64_t tiles = (c.M / BN + std::min<int64_t>(c.E, c.M)) * feats;  // no fewer than the device counts
-    if (c.mode == kWgrad) {
-        tiles = feats * ((c.K + BN - 1) / BN) * c.E;
+    const int64_t feats = ((kMode == kFprop ? c.N : c.K) + S::kFeat - 1) / S::kFeat;
+    int64_t tiles = (c.M / S::kWide + std::min<int64_t>(c.E, c.M)) * feats;  // no fewer than the device counts
+    if (kMode == kWgrad) {
+        tiles = feats * ((c.N + S::kWide - 1) / S::kWide) * c.E;
         // with M == 0 nothing is loaded: any valid address does
         const int64_t rows = std::max<int64_t>(c.M, 1);
-        const int64_t da[2] = {c.N, rows}, sa[1] = {2 * c.ld_mat}, db[2] = {c.K, rows}, sb[1] = {2 * c.ld_tok};
-        const int box[2] = {64, BK};
-        ok = encode_tmap(&a, c.M ? c.mat : c.out, 2, 2, da, sa, box, 128) &&
-             encode_tmap(&b, c.M ? c.tok : c.out, 2, 2, db, sb, box, 128);
+        const int64_t da[2] = {c.K, rows}, sa[1] = {2 * c.ld_tok}, db[2] = {c.N, rows}, sb[1] = {2 * c.ld_mat};
+        const int boxa[2] = {64, BK}, boxb[2] = {S::kBox, BK};
+        ok = encode_tmap(&a, c.M ? c.tok : c.out, 2, 2, da, sa, boxa, 128) &&
+             encode_tmap(&b, c.M ? c.mat : c.out, 2, 2, db, sb, boxb, 128);
     } else {
         const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {2 * c.K, 2 * c.K * c.N};
-        const int64_t db[2] = {c.mode == kDgrad ? c.N : c.K, c.M}, sb[1] = {2 * c.ld_tok};
-        const int boxa[3] = {64, c.mode == kDgrad ? BK : kFM, 1}, boxb[2] = {64, 64};
+        const int64_t db[2] = {kMode == kDgrad ? c.N : c.K, c.M}, sb[1] = {2 * c.ld_tok};
+        const int boxa[3] = {64, kMode == kDgrad ? BK : kFM, 1}, boxb[2] = {BK, S::kBox};
         ok = encode_tmap(&a, c.mat, 2, 3, da, sa, boxa, 128) && encode_tmap(&b, c.tok, 2, 2, db, sb, boxb, 128);
     }
     if (!ok) return cudaErrorInvalidValue;
-    if (c.mode == kFprop) return launch<kFprop>(a, b, p, tiles, s);
-    if (c.mode == kDgrad) return launch<kDgrad>(a, b, p, tiles, s);
-    return launch<kWgrad>(a, b, p, tiles, s);
+    return c.out_f32 || c.accumulate ? launch<kMode, kCG, true>(a, b, p, tiles, s)
+                                     : launch<kMode, kCG, false>(a, b, p, tiles, s);
+}
+
+cudaError_t run_gemm(const GemmCall& c, cudaStream_t s) {
+    if (c.mode == kWgrad) return run_mode<kWgrad, 2>(c, s);
+    const bool few = c.M <= (int64_t)Shape<1>::kWide * c.E;
+    if (c.mode == kFprop) return few ? run_mode<kFprop, 1>(c, s) : run_mode<kFprop, 2>(c, s);
+    return few ? run_mode<kDgrad, 1>(c, s) : run_mode<kDgrad, 2>(c, s);
 }
 
 }  // namespace ragged

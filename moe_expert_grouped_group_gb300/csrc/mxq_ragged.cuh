@@ -35,24 +35,129 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
 __device__ __forceinline__ uint32_t idesc_f16(uint32_t fmt, uint32_t a_mn, uint32_t b_mn, uint32_t m, uint32_t n) {
     return (1u << 4) | (fmt << 7) | (fmt << 10) | (a_mn << 15) | (b_mn << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
+// kCG = 1: one SM's tile; 2: a tile of a pair of SMs (a cluster of two CTAs), issued by its rank 0.
+template <int kCG>
 __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t accum) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(id), "r"(accum)
-        : "memory");
+    if constexpr (kCG == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a), "l"(b), "r"(id), "r"(accum)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a), "l"(b), "r"(id), "r"(accum)
+            : "memory");
 }
+// Arrive on `bar` (in both CTAs of a pair) when the MMAs issued so far have completed.
+template <int kCG>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if constexpr (kCG == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                bar),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                     : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+template <int kCG>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
+    if constexpr (kCG == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+}
+template <int kCG>
+__device__ __forceinline__ void tmem_dealloc(uint32_t tmem, uint32_t cols) {
+    if constexpr (kCG == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+}
+// TMA loads into this CTA's shared memory; `bar` may be the pair's rank 0's (a cluster address) when kCG = 2.
+template <int kCG>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    if constexpr (kCG == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+            "%4}], [%2];" ::"r"(dst),
+            "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y)
+            : "memory");
+    else
+        tma_load_2d(dst, map, bar, x, y);
+}
+template <int kCG>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+    if constexpr (kCG == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+            "%4, %5}], [%2];" ::"r"(dst),
+            "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "r"(z)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+            "%5}], [%2];" ::"r"(dst),
+            "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "r"(z)
+            : "memory");
+}
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// shared::cluster address of the variable at shared::cta address `a` in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t mapa(uint32_t a, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+// Remote arrive after a completed tcgen05.ld: nothing of this CTA's memory is handed over, so no release.
+__device__ __forceinline__ void arrive_remote_relaxed(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// Remote arrive that hands this thread's earlier writes to the waiter.
+__device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// Order what other CTAs of the cluster released to this thread's completed waits before its later accesses.
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
+// Barrier `id` of `threads` threads; true in all of them when `v` is true in any.
+__device__ __forceinline__ bool group_any(int id, int threads, bool v) {
+    uint32_t r;
+    __syncwarp();
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-        "[%2];" ::"r"(dst),
-        "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id), "r"(threads)
         : "memory");
+    __syncwarp();
+    return r != 0;
 }
+__device__ __forceinline__ void group_sync(int id, int threads) {
+    __syncwarp();
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+    __syncwarp();
+}
+
 // 32 consecutive accumulator columns of this warp's 32 TMEM lanes
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
@@ -64,11 +169,75 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
+// 16 consecutive accumulator columns of this warp's 32 TMEM lanes
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// 32 consecutive accumulator columns of 16 TMEM lanes, as a matrix fragment: registers 4i .. 4i+3 of
+// thread t hold lanes t/4 (first two) and t/4 + 8 at columns 8i + 2(t mod 4) and the next.
+__device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// ------------------------------------------------------------ bf16 epilogue
+// The accumulator is the transpose of the output tile (lane = feature, column =
+// output row), so 32 columns x 128 lanes go through a staging buffer: matrix
+// fragments out of TMEM, two columns rounded and packed at a time, transposed
+// on the way into shared memory (stmatrix .trans), then whole 256-byte row
+// pieces in 16-byte stores. Rows are 272 bytes apart: eight consecutive rows
+// start in different banks.
+constexpr int kEpiRow = 272, kEpiBytes = 32 * kEpiRow, kEpiGroup = 128;
+
+// Columns c0 .. c0 + 31 of TMEM lanes 32 q + ... of the group's four warps, each value passed through
+// f(value, lane in 0..127, column in 0..31), to out + column * ld + lane for lanes < live and
+// columns < cols. Called by the four warps (q = 0..3) of barrier `id`.
+template <class F>
+__device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int q, int lane, int id, uint8_t* stage,
+                                                   __nv_bfloat16* out, int64_t ld, int live, int cols, F f) {
+    uint32_t v[2][16];
+    tmem_ld16x32(tmem + ((uint32_t)(q * 32) << 16), v[0]);
+    tmem_ld16x32(tmem + ((uint32_t)(q * 32 + 16) << 16), v[1]);
+    tmem_wait_ld();
+    uint32_t w[4][4];  // [8-column block][8-lane block]
+    const int fl = q * 32 + (lane >> 2), fc = 2 * (lane & 3);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int r = 4 * b + 2 * (g & 1), l = fl + 8 * g, col = 8 * b + fc;
+            w[b][g] = bf16x2_bits(f(__uint_as_float(v[g >> 1][r]), l, col), f(__uint_as_float(v[g >> 1][r + 1]), l, col + 1));
+        }
+    group_sync(id, kEpiGroup);  // the stage's last readers are done
+    const uint32_t at = smem_u32(stage) + (lane & 7) * kEpiRow + (q * 32 + (lane >> 3) * 8) * 2;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at + 8 * b * kEpiRow),
+                     "r"(w[b][0]), "r"(w[b][1]), "r"(w[b][2]), "r"(w[b][3])
+                     : "memory");
+    group_sync(id, kEpiGroup);
+    const int piece = lane & 15;
+    if (piece * 8 < live)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = q * 8 + i * 2 + (lane >> 4);
+            if (j < cols)
+                *reinterpret_cast<uint4*>(out + j * ld + piece * 8) =
+                    *reinterpret_cast<const uint4*>(stage + j * kEpiRow + piece * 16);
+        }
 }
 
 // ------------------------------------------------------------ ragged grouping
@@ -133,71 +302,76 @@ __device__ __forceinline__ int owner_of(const int32_t* table, int E, int32_t i) 
     return lo;
 }
 
-// A slice of an expert's rows: the expert's m rows are cut evenly into
-// ceil(m / width) slices, each a multiple of `step` rows wide (the MMA's N
-// granularity) but the last, so a remainder of a few rows costs a few columns
-// of MMA work spread over all slices and never a near-empty full tile.
+// A slice of an expert's rows: the expert's m rows, in units of `step` rows
+// (the MMA's N granularity), are dealt evenly to ceil(m / width) slices, so a
+// remainder of a few rows costs a few columns of MMA work and never a
+// near-empty full tile.
 struct Slice {
     int row, rows, n;  // first token row, rows of the expert in it, MMA N
 };
 __device__ __forceinline__ Slice slice_of(int off, int m, int count, int i, int step) {
-    const int even = (m + count - 1) / count;
+    const int64_t units = (m + step - 1) / step;
+    const int u0 = (int)(units * i / count), u1 = (int)(units * (i + 1) / count);
     Slice s;
-    s.n = (even + step - 1) / step * step;
-    s.row = off + i * s.n;
-    s.rows = min(s.n, m - i * s.n);
+    s.n = (u1 - u0) * step;
+    s.row = off + u0 * step;
+    s.rows = min(s.n, m - u0 * step);
     return s;
 }
 
-// One output tile.
+// One output tile: out[row0 + c][f0 + l] for accumulator column c, lane l.
 struct Tile {
     int e;
-    int f0;    // first feature on the MMA's M
-    int c0;    // fprop, dgrad: first token row; wgrad: first column of dW
-    int cols;  // columns to store
-    int n;     // MMA N
-    int red0;  // wgrad: first token row of the sum
-    int red;   // length of the sum
+    int f0;        // first output column (feature), on the MMA's M
+    int c0;        // first row of the other operand: fprop, dgrad: a token row; wgrad: a row of dW[e]
+    int cols;      // accumulator columns to store
+    int n;         // MMA N
+    int red0;      // wgrad: first token row of the sum
+    int red;       // length of the sum
+    int64_t row0;  // first output row
 };
 
-// The tiles of a product in the order in which a grid takes them, kWide the
-// widest MMA N.
-template <int kMode, int kWide>
+// The tiles of a product in the order in which a grid takes them: kFeat
+// features by at most kWide columns, kWide's granularity kStep. `order` (wgrad)
+// lists the experts, heaviest first.
+template <int kMode, int kFeat, int kWide, int kStep>
 struct Walk {
     int64_t N, K, total;
     int E, feats;  // tiles along the MMA's M
     int wide;      // wgrad: tiles along its N
-    const int32_t *off, *slices;
+    const int32_t *off, *slices, *order;
 
-    __device__ Walk(int64_t N_, int64_t K_, int E_, const int32_t* off_, const int32_t* slices_)
-        : N(N_), K(K_), E(E_), off(off_), slices(slices_) {
-        feats = (int)(((kMode == kDgrad ? K : N) + kFM - 1) / kFM);
-        wide = (int)((K + kWide - 1) / kWide);
+    __device__ Walk(int64_t N_, int64_t K_, int E_, const int32_t* off_, const int32_t* slices_, const int32_t* order_)
+        : N(N_), K(K_), E(E_), off(off_), slices(slices_), order(order_) {
+        feats = (int)(((kMode == kFprop ? N : K) + kFeat - 1) / kFeat);
+        wide = (int)((N + kWide - 1) / kWide);
         total = kMode == kWgrad ? (int64_t)E * feats * wide : (int64_t)slices[E] * feats;
     }
     __device__ Tile get(int64_t t) const {
         Tile T;
         if (kMode == kWgrad) {
             const int per = feats * wide, r = (int)(t % per);
-            T.e = (int)(t / per);
-            T.f0 = r / wide * kFM;
+            T.e = order[t / per];
+            T.f0 = r / wide * kFeat;
             T.c0 = r % wide * kWide;
-            T.cols = (int)min((int64_t)kWide, K - T.c0);
-            T.n = (T.cols + 15) / 16 * 16;
+            T.cols = (int)min((int64_t)kWide, N - T.c0);
+            T.n = (T.cols + kStep - 1) / kStep * kStep;
             T.red0 = off[T.e];
             T.red = off[T.e + 1] - T.red0;
+            T.row0 = T.e * N + T.c0;
         } else {
             // slices of an expert run fastest, so that the CTAs of one wave share its weight rows
             T.e = owner_of(slices, E, (int32_t)(t / feats));
             const int count = slices[T.e + 1] - slices[T.e];
             const int64_t r = t - (int64_t)slices[T.e] * feats;
-            const Slice s = slice_of(off[T.e], off[T.e + 1] - off[T.e], count, (int)(r % count), 16);
-            T.f0 = (int)(r / count) * kFM;
+            const Slice s = slice_of(off[T.e], off[T.e + 1] - off[T.e], count, (int)(r % count), kStep);
+            T.f0 = (int)(r / count) * kFeat;
             T.c0 = s.row;
             T.cols = s.rows;
             T.n = s.n;
             T.red0 = 0;
             T.red = (int)(kMode == kDgrad ? N : K);
+            T.row0 = s.row;
         }
         return T;
     }

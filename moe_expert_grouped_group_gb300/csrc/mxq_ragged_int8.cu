@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = s_tmem;
-    const Walk<kFprop, BN> W(p.N, p.K, p.E, s_off, s_slices);
+    const Walk<kFprop, kFM, BN, 16> W(p.N, p.K, p.E, s_off, s_slices, nullptr);
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     const uint32_t fb = rawf0 + 8 * stage, a = smem_u32(smem + RAW_REGION + stage * RAW_BYTES);
                     mbar_expect_tx(fb, RAW_A + boxes * 64 * BK);
-                    tma_load_3d(a, &tmA, fb, r, T.f0, T.e);
+                    load_3d<1>(a, &tmA, fb, r, T.f0, T.e);
                     for (int i = 0; i < boxes; ++i)
                         tma_load_2d(a + RAW_A + i * 64 * BK, &tmB, fb, r, T.c0 + 64 * i);
                     ++fills;
@@ -158,11 +158,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int steps = (min(BK, T.red - r) + 15) / 16;
                     const uint64_t so = (uint64_t)(stage * (STAGE_BYTES / 16));
                     for (int k = 0; k < steps; ++k)
-                        mma_f16(tmem + buf * BN, ad0 + so + 2 * k, bd0 + so + 2 * k, id, (r | k) != 0);
-                    mma_commit(empty0 + 8 * stage);
+                        mma_f16<1>(tmem + buf * BN, ad0 + so + 2 * k, bd0 + so + 2 * k, id, (r | k) != 0);
+                    mma_commit<1>(empty0 + 8 * stage);
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
-                if (ok) mma_commit(accf0 + 8 * buf);
+                if (ok) mma_commit<1>(accf0 + 8 * buf);
                 buf ^= 1;
                 aphase ^= buf == 0;
             }
