@@ -36,9 +36,9 @@
 // keep nine in flight.
 //
 // Persistent and warp-specialised: warp 0 issues TMA loads into a ring of
-// 64-deep stages, warp 1 owns TMEM and issues the MMAs (rank 0 of a pair; rank
-// 1's only zeroes its share of an expert's last rows), warps 2..9 drain one of
-// two accumulators while the MMAs fill the other. Every wait is bounded (about
+// 64-deep stages, warp 1 owns TMEM and issues the MMAs (rank 0 of a pair),
+// warps 2..9 drain one of two accumulators while the MMAs fill the other, warp
+// 10 zeroes its CTA's share of an expert's last rows (wgrad). Every wait is bounded (about
 // 2 s); on expiry MXQ_STATUS_WAIT_TIMEOUT is set.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -57,7 +57,7 @@ namespace ragged {
 constexpr int BK = 64;    // reduction depth of a stage: 128 bytes of bf16
 constexpr int FLUSH = 8;  // stages an accumulator holds before it is added to the registers (kRegs)
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int THREADS = 96 + 32 * EPI_WARPS;
 
 template <int kCG>
 struct Shape {
@@ -73,7 +73,7 @@ struct Shape {
     static constexpr int kTables = kBars + 512;
     __host__ __device__ static constexpr int smem(int E) { return 1024 + kTables + 12 * (E + 1); }
     static_assert(1024 + kTables + 12 * (MXQ_MAX_EXPERTS + 1) <= 232448, "shared memory over the per-block limit");
-    static_assert(kBars % 8 == 0 && 8 * (3 * kStages + 4) <= 512, "barrier region");
+    static_assert(kBars % 8 == 0 && 8 * (4 * kStages + 4) <= 512, "barrier region");
 };
 
 struct Params {
@@ -119,15 +119,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     }
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
-    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, fix0 = empty0 + 8 * STAGES;
-    const uint32_t accf0 = fix0 + 8 * STAGES, acce0 = accf0 + 16;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, tail0 = empty0 + 8 * STAGES;
+    const uint32_t fix0 = tail0 + 8 * STAGES, accf0 = fix0 + 8 * STAGES, acce0 = accf0 + 16;
     volatile int* abort_flag = &s_abort;
     if (threadIdx.x == 0) {
         s_abort = 0;
         for (int st = 0; st < STAGES; ++st) {
             mbar_init(full0 + 8 * st, 1);
             mbar_init(empty0 + 8 * st, 1);
-            mbar_init(fix0 + 8 * st, 1);
+            mbar_init(tail0 + 8 * st, 1);
+            mbar_init(fix0 + 8 * st, kCG);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf0 + 8 * b, 1);
@@ -146,7 +147,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const Walk<kMode, S::kFeat, S::kWide, S::kStep> W(p.N, p.K, p.E, s_off, s_slices, s_order);
     const int64_t first = blockIdx.x / kCG, stride = gridDim.x / kCG;
     constexpr bool a_mn = kMode != kFprop, b_mn = kMode == kWgrad;
-    // rows of an expert's last block that are zeroed: left .. up to the next multiple of 16
+    // An expert's last block of rows in wgrad, when it ends inside a step of 16: its loads complete on each
+    // CTA's own tail[st], warp 10 of both CTAs zeroes the rows up to the next multiple of 16 and arrives on
+    // rank 0's fix[st], and the MMAs wait for that instead of full[st]. The parities of full, tail and fix
+    // of a stage therefore follow their own uses, not the ring's laps.
     auto ragged_end = [](const Tile& T, int r) { return kMode == kWgrad && T.red - r < BK && ((T.red - r) & 15) != 0; };
     auto zero_rows = [&](const Tile& T, int r, int stage) {
         const int left = T.red - r, per = (16 - (left & 15)) * 8, boxes = 2 + (T.n / kCG + 63) / 64;
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            int64_t fills = 0;
+            uint32_t used = 0, full_uses = 0, tail_uses = 0, tail_last = 0;  // bits of stages
             for (int64_t t = first; t < W.total; t += stride) {
                 const Tile T = W.get(t);
                 const int half = T.n / kCG;  // this CTA's columns of the tile: [rank * half, + half)
@@ -171,15 +175,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint32_t bytes = S::kA + boxes * S::kBox * BK * 2;
                 for (int r = 0; r < T.red; r += BK) {
                     if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag)) {
-                        if (rank == 0) drain_ring(full0, STAGES, fills);  // rank 1's copies complete there too
+                        // a bounded wait expired: no copy may be in flight when the block ends
+                        volatile int unused = 0;
+                        for (int st = 0; st < STAGES; ++st) {
+                            const bool tail = tail_last >> st & 1;
+                            if ((used >> st & 1) && (tail || rank == 0))  // rank 1's full loads complete on rank 0's
+                                mbar_wait((tail ? tail0 : full0) + 8 * st,
+                                          ((tail ? tail_uses : full_uses) >> st & 1) ^ 1, &unused);
+                        }
                         goto done_producer;
                     }
-                    const uint32_t own = full0 + 8 * stage, a = smem_u32(smem + stage * S::kStage), b = a + S::kA;
-                    // a pair's loads complete on rank 0's barrier, but where each CTA has to zero rows on its own
-                    const bool local = kCG == 1 || ragged_end(T, r);
-                    if (local) mbar_expect_tx(own, bytes);
-                    else if (rank == 0) mbar_expect_tx(own, 2 * bytes);
-                    const uint32_t fb = local ? (kCG == 2 ? mapa(own, rank) : own) : mapa(own, 0);
+                    const bool tail = ragged_end(T, r);
+                    const uint32_t own = (tail ? tail0 : full0) + 8 * stage, bit = 1u << stage;
+                    if (tail) mbar_expect_tx(own, bytes);
+                    else if (rank == 0) mbar_expect_tx(own, kCG * bytes);
+                    const uint32_t fb = kCG == 2 ? mapa(own, tail ? rank : 0) : own;
+                    const uint32_t a = smem_u32(smem + stage * S::kStage), b = a + S::kA;
                     if (kMode == kFprop) {
                         load_3d<kCG>(a, &tmA, fb, r, f, T.e);
                     } else if (kMode == kDgrad) {
@@ -194,75 +205,84 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (kMode == kWgrad) load_2d<kCG>(dst, &tmB, fb, c + S::kBox * i, T.red0 + r);
                         else load_2d<kCG>(dst, &tmB, fb, r, c + S::kBox * i);
                     }
-                    ++fills;
+                    used |= bit;
+                    if (tail) {
+                        tail_uses ^= bit;
+                        tail_last |= bit;
+                    } else {
+                        full_uses ^= bit;
+                        tail_last &= ~bit;
+                    }
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
             }
         done_producer:;
         }
-    } else if (warp == 1 && rank == 0) {
-        // ------------------------------------------------------ MMA issuer
-        int stage = 0, buf = 0;
-        uint32_t phase = 0, aphase = 0, fixed = 0;  // fixed: bit st = parity of fix[st]
-        const uint32_t base = smem_u32(smem);
-        // MN-major: 64-element chunks 8192 bytes apart, 8-row groups of the reduction 1024 apart
-        const uint64_t ad0 = smem_desc(base, a_mn ? 8192 : 16, 1024);
-        const uint64_t bd0 = smem_desc(base + S::kA, b_mn ? 8192 : 16, 1024);
-        constexpr uint32_t a_step = (a_mn ? 2048 : 32) / 16, b_step = (b_mn ? 2048 : 32) / 16;  // 16 of the reduction
-        bool ok = true;
-        for (int64_t t = first; t < W.total && ok; t += stride) {
-            const Tile T = W.get(t);
-            const uint32_t id = idesc_f16(1, a_mn, b_mn, S::kFeat, T.n);
-            for (int r0 = 0; r0 < T.red && ok; r0 += kRegs ? FLUSH * BK : T.red) {
-                const int r1 = kRegs ? min(T.red, r0 + FLUSH * BK) : T.red;
-                ok = mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag);
-                for (int r = r0; r < r1 && ok; r += BK) {
-                    ok = mbar_wait(full0 + 8 * stage, phase, abort_flag);
-                    if (!ok) break;
-                    const int steps = (min(BK, T.red - r) + 15) / 16;
-                    if (ragged_end(T, r)) {
-                        zero_rows(T, r, stage);
-                        if (kCG == 2) {
-                            ok = mbar_wait(fix0 + 8 * stage, fixed >> stage & 1, abort_flag);
-                            if (!ok) break;
-                            fixed ^= 1u << stage;
-                            fence_cluster();
-                        }
-                    }
-                    fence_after();
-                    if (lane == 0) {
-                        const uint64_t so = (uint64_t)(stage * (S::kStage / 16));
-                        for (int k = 0; k < steps; ++k)
-                            mma_f16<kCG>(tmem + buf * S::kWide, ad0 + so + k * a_step, bd0 + so + k * b_step, id,
-                                         r > r0 || k > 0);
-                        mma_commit<kCG>(empty0 + 8 * stage);
-                    }
-                    __syncwarp();
-                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
-                }
-                if (ok && lane == 0) mma_commit<kCG>(accf0 + 8 * buf);
-                __syncwarp();
-                buf ^= 1;
-                aphase ^= buf == 0;
-            }
-        }
     } else if (warp == 1) {
-        // ------------------------------------------------------ rank 1: its rows of a ragged end
+        // ------------------------------------------------------ MMA issuer (rank 0)
+        // One thread from here to the end of the loop: with the MMAs of each stage behind a branch of a
+        // converged warp, a stage took 764 cycles to issue, whatever its N.
+        if (rank == 0 && lane == 0) {
+            int stage = 0, buf = 0;
+            uint32_t aphase = 0, full_uses = 0, fix_uses = 0;  // bits of stages: parities
+            const uint32_t base = smem_u32(smem);
+            // MN-major: 64-element chunks 8192 bytes apart, 8-row groups of the reduction 1024 apart
+            const uint64_t ad0 = smem_desc(base, a_mn ? 8192 : 16, 1024);
+            const uint64_t bd0 = smem_desc(base + S::kA, b_mn ? 8192 : 16, 1024);
+            constexpr uint32_t a_step = (a_mn ? 2048 : 32) / 16, b_step = (b_mn ? 2048 : 32) / 16;  // 16 of the sum
+            for (int64_t t = first; t < W.total; t += stride) {
+                const Tile T = W.get(t);
+                const uint32_t id = idesc_f16(1, a_mn, b_mn, S::kFeat, T.n);
+                for (int r0 = 0; r0 < T.red; r0 += kRegs ? FLUSH * BK : T.red) {
+                    const int r1 = kRegs ? min(T.red, r0 + FLUSH * BK) : T.red;
+                    const uint32_t d = tmem + buf * S::kWide;
+                    if (!mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag)) goto done_mma;
+                    for (int r = r0; r < r1; r += BK) {
+                        const uint64_t so = (uint64_t)(stage * (S::kStage / 16));
+                        if (ragged_end(T, r)) {
+                            if (!mbar_wait(fix0 + 8 * stage, fix_uses >> stage & 1, abort_flag)) goto done_mma;
+                            fix_uses ^= 1u << stage;
+                            if (kCG == 2) fence_cluster();
+                        } else {
+                            if (!mbar_wait(full0 + 8 * stage, full_uses >> stage & 1, abort_flag)) goto done_mma;
+                            full_uses ^= 1u << stage;
+                        }
+                        fence_after();
+                        if (T.red - r >= BK) {
+#pragma unroll
+                            for (int k = 0; k < BK / 16; ++k)
+                                mma_f16<kCG>(d, ad0 + so + k * a_step, bd0 + so + k * b_step, id, r > r0 || k > 0);
+                        } else {
+                            for (int k = 0; k < (T.red - r + 15) / 16; ++k)
+                                mma_f16<kCG>(d, ad0 + so + k * a_step, bd0 + so + k * b_step, id, r > r0 || k > 0);
+                        }
+                        mma_commit<kCG>(empty0 + 8 * stage);
+                        if (++stage == STAGES) stage = 0;
+                    }
+                    mma_commit<kCG>(accf0 + 8 * buf);
+                    buf ^= 1;
+                    aphase ^= buf == 0;
+                }
+            }
+        done_mma:;
+        }
+    } else if (warp == 2 + EPI_WARPS) {
+        // ------------------------------------------------------ rows of the next expert (wgrad)
         if (kMode == kWgrad) {
             int stage = 0;
-            uint32_t loaded = 0;  // bit st = parity of this CTA's own full[st], used by ragged ends only
-            bool ok = true;
-            for (int64_t t = first; t < W.total && ok; t += stride) {
+            uint32_t uses = 0;  // bits of stages: parity of tail[st]
+            for (int64_t t = first; t < W.total; t += stride) {
                 const Tile T = W.get(t);
                 if (T.red == 0) continue;
-                const int last = (T.red - 1) / BK;
-                const int at = (stage + last) % STAGES;
+                const int last = (T.red - 1) / BK, at = (stage + last) % STAGES;
                 if (ragged_end(T, last * BK)) {
-                    ok = mbar_wait(full0 + 8 * at, loaded >> at & 1, abort_flag);
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    loaded ^= 1u << at;
+                    if (!__all_sync(0xffffffffu, mbar_wait(tail0 + 8 * at, uses >> at & 1, abort_flag))) break;
+                    uses ^= 1u << at;
                     zero_rows(T, last * BK, at);
-                    if (lane == 0) arrive_remote_release(mapa(fix0 + 8 * at, 0));
+                    if (lane == 0) {
+                        if (rank == 0) mbar_arrive(fix0 + 8 * at);
+                        else arrive_remote_release(mapa(fix0 + 8 * at, 0));
+                    }
                 }
                 stage = (at + 1) % STAGES;
             }
