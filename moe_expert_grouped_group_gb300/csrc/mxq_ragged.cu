@@ -163,34 +163,35 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            uint32_t used = 0, full_uses = 0, tail_uses = 0, tail_last = 0;  // bits of stages
-            for (int64_t t = first; t < W.total; t += stride) {
-                const Tile T = W.get(t);
-                const int half = T.n / kCG;  // this CTA's columns of the tile: [rank * half, + half)
-                const int boxes = (half + S::kBox - 1) / S::kBox;
-                const int f = T.f0 + rank * kFM, c = T.c0 + rank * half;
-                const uint32_t bytes = S::kA + boxes * S::kBox * BK * 2;
-                for (int r = 0; r < T.red; r += BK) {
-                    if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag)) {
-                        // a bounded wait expired: no copy may be in flight when the block ends
-                        volatile int unused = 0;
-                        for (int st = 0; st < STAGES; ++st) {
-                            const bool tail = tail_last >> st & 1;
-                            if ((used >> st & 1) && (tail || rank == 0))  // rank 1's full loads complete on rank 0's
-                                mbar_wait((tail ? tail0 : full0) + 8 * st,
-                                          ((tail ? tail_uses : full_uses) >> st & 1) ^ 1, &unused);
-                        }
-                        goto done_producer;
+        int stage = 0;
+        uint32_t phase = 0;
+        uint32_t used = 0, full_uses = 0, tail_uses = 0, tail_last = 0;  // bits of stages
+        for (int64_t t = first; t < W.total; t += stride) {
+            const Tile T = W.get(t);
+            const int half = T.n / kCG;  // this CTA's columns of the tile: [rank * half, + half)
+            const int boxes = (half + S::kBox - 1) / S::kBox;
+            const int f = T.f0 + rank * kFM, c = T.c0 + rank * half;
+            const uint32_t bytes = S::kA + boxes * S::kBox * BK * 2;
+            for (int r = 0; r < T.red; r += BK) {
+                if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag)) {
+                    // a bounded wait expired: no copy may be in flight when the block ends
+                    volatile int unused = 0;
+                    for (int st = 0; st < STAGES; ++st) {
+                        const bool tail = tail_last >> st & 1;
+                        if ((used >> st & 1) && (tail || rank == 0))  // rank 1's full loads complete on rank 0's
+                            mbar_wait((tail ? tail0 : full0) + 8 * st, ((tail ? tail_uses : full_uses) >> st & 1) ^ 1,
+                                      &unused);
                     }
-                    const bool tail = ragged_end(T, r);
-                    const uint32_t own = (tail ? tail0 : full0) + 8 * stage, bit = 1u << stage;
+                    goto done_producer;
+                }
+                __syncwarp();
+                const bool tail = ragged_end(T, r);
+                const uint32_t own = (tail ? tail0 : full0) + 8 * stage, bit = 1u << stage;
+                const uint32_t fb = kCG == 2 ? mapa(own, tail ? rank : 0) : own;
+                const uint32_t a = smem_u32(smem) + stage * S::kStage, b = a + S::kA;
+                if (elect_one()) {
                     if (tail) mbar_expect_tx(own, bytes);
                     else if (rank == 0) mbar_expect_tx(own, kCG * bytes);
-                    const uint32_t fb = kCG == 2 ? mapa(own, tail ? rank : 0) : own;
-                    const uint32_t a = smem_u32(smem + stage * S::kStage), b = a + S::kA;
                     if (kMode == kFprop) {
                         load_3d<kCG>(a, &tmA, fb, r, f, T.e);
                     } else if (kMode == kDgrad) {
@@ -200,29 +201,31 @@ __global__ void __launch_bounds__(THREADS, 1)
                         load_2d<kCG>(a, &tmA, fb, f, T.red0 + r);
                         load_2d<kCG>(a + 8192, &tmA, fb, f + 64, T.red0 + r);
                     }
-                    for (int i = 0; i < boxes; ++i) {
+#pragma unroll
+                    for (int i = 0; i < S::kWide / kCG / S::kBox; ++i) {
                         const uint32_t dst = b + S::kBox * BK * 2 * i;
-                        if (kMode == kWgrad) load_2d<kCG>(dst, &tmB, fb, c + S::kBox * i, T.red0 + r);
-                        else load_2d<kCG>(dst, &tmB, fb, r, c + S::kBox * i);
+                        if (i < boxes) {
+                            if (kMode == kWgrad) load_2d<kCG>(dst, &tmB, fb, c + S::kBox * i, T.red0 + r);
+                            else load_2d<kCG>(dst, &tmB, fb, r, c + S::kBox * i);
+                        }
                     }
-                    used |= bit;
-                    if (tail) {
-                        tail_uses ^= bit;
-                        tail_last |= bit;
-                    } else {
-                        full_uses ^= bit;
-                        tail_last &= ~bit;
-                    }
-                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
+                __syncwarp();
+                used |= bit;
+                if (tail) {
+                    tail_uses ^= bit;
+                    tail_last |= bit;
+                } else {
+                    full_uses ^= bit;
+                    tail_last &= ~bit;
+                }
+                if (++stage == STAGES) { stage = 0; phase ^= 1; }
             }
-        done_producer:;
         }
+    done_producer:;
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer (rank 0)
-        // One thread from here to the end of the loop: with the MMAs of each stage behind a branch of a
-        // converged warp, a stage took 764 cycles to issue, whatever its N.
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             int stage = 0, buf = 0;
             uint32_t aphase = 0, full_uses = 0, fix_uses = 0;  // bits of stages: parities
             const uint32_t base = smem_u32(smem);
@@ -237,8 +240,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int r1 = kRegs ? min(T.red, r0 + FLUSH * BK) : T.red;
                     const uint32_t d = tmem + buf * S::kWide;
                     if (!mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag)) goto done_mma;
+                    __syncwarp();
                     for (int r = r0; r < r1; r += BK) {
-                        const uint64_t so = (uint64_t)(stage * (S::kStage / 16));
+                        const uint64_t ad = ad0 + (uint64_t)(stage * (S::kStage / 16));
+                        const uint64_t bd = bd0 + (uint64_t)(stage * (S::kStage / 16));
                         if (ragged_end(T, r)) {
                             if (!mbar_wait(fix0 + 8 * stage, fix_uses >> stage & 1, abort_flag)) goto done_mma;
                             fix_uses ^= 1u << stage;
@@ -247,19 +252,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                             if (!mbar_wait(full0 + 8 * stage, full_uses >> stage & 1, abort_flag)) goto done_mma;
                             full_uses ^= 1u << stage;
                         }
+                        __syncwarp();
                         fence_after();
-                        if (T.red - r >= BK) {
+                        const int steps = T.red - r >= BK ? BK / 16 : (T.red - r + 15) / 16;
+                        if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < BK / 16; ++k)
-                                mma_f16<kCG>(d, ad0 + so + k * a_step, bd0 + so + k * b_step, id, r > r0 || k > 0);
-                        } else {
-                            for (int k = 0; k < (T.red - r + 15) / 16; ++k)
-                                mma_f16<kCG>(d, ad0 + so + k * a_step, bd0 + so + k * b_step, id, r > r0 || k > 0);
+                                if (k < steps) mma_f16<kCG>(d, ad + k * a_step, bd + k * b_step, id, r > r0 || k > 0);
+                            mma_commit<kCG>(empty0 + 8 * stage);
+                            if (r + BK >= r1) mma_commit<kCG>(accf0 + 8 * buf);
                         }
-                        mma_commit<kCG>(empty0 + 8 * stage);
+                        __syncwarp();
                         if (++stage == STAGES) stage = 0;
                     }
-                    mma_commit<kCG>(accf0 + 8 * buf);
                     buf ^= 1;
                     aphase ^= buf == 0;
                 }

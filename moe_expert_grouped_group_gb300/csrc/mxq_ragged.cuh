@@ -112,6 +112,17 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, ui
             "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "r"(z)
             : "memory");
 }
+// True in one lane of a converged warp, always the same. Behind this predicate (unlike behind a test of the
+// lane's number) the compiler keeps what is equal in all lanes, the MMAs' descriptors, in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ uint32_t cta_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
