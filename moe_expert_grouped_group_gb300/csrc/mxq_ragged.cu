@@ -245,9 +245,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const uint64_t ad = ad0 + (uint64_t)(stage * (S::kStage / 16));
                         const uint64_t bd = bd0 + (uint64_t)(stage * (S::kStage / 16));
                         if (ragged_end(T, r)) {
-                            if (!mbar_wait(fix0 + 8 * stage, fix_uses >> stage & 1, abort_flag)) goto done_mma;
+                            if (!mbar_wait_pair<kCG>(fix0 + 8 * stage, fix_uses >> stage & 1, abort_flag)) goto done_mma;
                             fix_uses ^= 1u << stage;
-                            if (kCG == 2) fence_cluster();
                         } else {
                             if (!mbar_wait(full0 + 8 * stage, full_uses >> stage & 1, abort_flag)) goto done_mma;
                             full_uses ^= 1u << stage;
@@ -446,50 +445,11 @@ int sm_count() {
     return v;
 }
 
-// Co-resident CTA pairs of the pair kernel on the current device.
-template <int kMode, bool kRegs>
-static int max_pairs() {
-    static std::atomic<int> cache[64];
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    if (dev < 64 && (n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2 * (sm_count() / 2));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = Shape<2>::smem(MXQ_MAX_EXPERTS);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, (void*)ragged_gemm_kernel<kMode, 2, kRegs>, &cfg) != cudaSuccess || n <= 0) {
-        cudaGetLastError();
-        n = sm_count() / 2;
-    }
-    if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 template <int kMode, int kCG, bool kRegs>
 static cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const Params& p, int64_t tiles, cudaStream_t s) {
     using S = Shape<kCG>;
-    cudaError_t e = cudaFuncSetAttribute(ragged_gemm_kernel<kMode, kCG, kRegs>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem(MXQ_MAX_EXPERTS));
-    if (e != cudaSuccess) return e;
-    const int64_t most = kCG == 2 ? max_pairs<kMode, kRegs>() : sm_count();
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(kCG * std::max<int64_t>(1, std::min(tiles, most))));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = S::smem(p.E);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCG;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, ragged_gemm_kernel<kMode, kCG, kRegs>, a, b, p);
+    return launch_persistent<kCG, ragged_gemm_kernel<kMode, kCG, kRegs>>(THREADS, S::smem(MXQ_MAX_EXPERTS), S::smem(p.E),
+                                                                         tiles, s, a, b, p);
 }
 
 template <int kMode, int kCG>

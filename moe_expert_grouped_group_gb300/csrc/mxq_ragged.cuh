@@ -8,6 +8,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "mxq_common.cuh"
 #include "mxq_ragged.h"
 
@@ -145,8 +148,34 @@ __device__ __forceinline__ void arrive_remote_relaxed(uint32_t cluster_bar) {
 __device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-// Order what other CTAs of the cluster released to this thread's completed waits before its later accesses.
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// mbar_wait that also acquires what threads of the pair's other CTA released with their arrivals.
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+template <int kCG>
+__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if constexpr (kCG == 1) return mbar_wait(bar, parity, abort_flag);
+    if (mbar_try_cluster(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    for (uint32_t i = 0;; ++i) {
+        if (mbar_try_cluster(bar, parity)) return true;
+        if ((i & 63) == 63) {
+            if (*abort_flag) return false;
+            if (globaltimer() - t0 > kWaitNs) {
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
 
 // Barrier `id` of `threads` threads; true in all of them when `v` is true in any.
 __device__ __forceinline__ bool group_any(int id, int threads, bool v) {
@@ -394,6 +423,41 @@ __device__ __forceinline__ void drain_ring(uint32_t full0, int stages, int64_t f
     volatile int unused = 0;
     for (int64_t i = fills > stages ? fills - stages : 0; i < fills; ++i)
         mbar_wait(full0 + 8 * (int)(i % stages), (uint32_t)(i / stages) & 1, &unused);
+}
+
+// ------------------------------------------------------------------ host side
+// Launches a persistent kernel of clusters of kCG CTAs, as many as fit the
+// device and no more than `tiles`. The kernel's attribute and co-residency are
+// set and asked for once per device.
+template <int kCG, auto kKernel, class... Args>
+static cudaError_t launch_persistent(int threads, int smem_max, int smem, int64_t tiles, cudaStream_t s,
+                                     const Args&... args) {
+    static std::atomic<int> cache[64];
+    int dev = 0, most = 0;
+    cudaGetDevice(&dev);
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCG;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(threads);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (dev >= 64 || (most = cache[dev].load(std::memory_order_acquire)) == 0) {
+        const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
+        if (e != cudaSuccess) return e;
+        cfg.gridDim = dim3(kCG * (sm_count() / kCG));
+        cfg.dynamicSmemBytes = smem_max;
+        if (cudaOccupancyMaxActiveClusters(&most, (void*)kKernel, &cfg) != cudaSuccess || most <= 0) {
+            cudaGetLastError();
+            most = sm_count() / kCG;
+        }
+        if (dev < 64) cache[dev].store(most, std::memory_order_release);
+    }
+    cfg.gridDim = dim3((unsigned)(kCG * std::max<int64_t>(1, std::min<int64_t>(tiles, most))));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, kKernel, args...);
 }
 
 }  // namespace ragged

@@ -11,14 +11,18 @@
 // tcgen05.mma kind::f16 sums them in fp32.
 //
 // The tile walk, the operands' sides (features on the MMA's M, tokens on its
-// N) and the edges are those of the bf16 products (mxq_ragged.cuh). Warp 0
-// loads int8 boxes, warps 10..17 widen them into the 128-byte-swizzled
-// operand stages, warp 1 issues the MMAs, warps 2..9 scale and store.
+// N), the edges and the two shapes (pairs of SMs; one SM for few rows) are
+// those of the bf16 products (mxq_ragged.cuh, mxq_ragged.cu). Warp 0 loads int8
+// boxes into a ring of their own, warps 10..17 widen them into the
+// 128-byte-swizzled operand stages, warp 1 issues the MMAs, warps 2..9 scale
+// and store. Sums of whole numbers below 2^24 are exact, so fp32 outputs need
+// no sums in registers here.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "mxq_internal.h"
 #include "mxq_ragged.cuh"
@@ -28,20 +32,30 @@ namespace mxq {
 namespace ragged {
 namespace i8 {
 
-constexpr int BK = 64;      // reduction depth of a stage
-constexpr int BN = 256;     // widest MMA N
-constexpr int RAWS = 3;     // int8 stages
-constexpr int STAGES = 3;   // widened stages
-constexpr int RAW_A = kFM * BK, RAW_BYTES = RAW_A + BN * BK;
-constexpr int A_BYTES = kFM * BK * 2, STAGE_BYTES = A_BYTES + BN * BK * 2;
+constexpr int BK = 64;  // reduction depth of a stage
 constexpr int EPI_WARPS = 8, CVT_WARPS = 8;
+constexpr int CVT_GROUP = 2;  // warps that widen one stage
 constexpr int THREADS = 64 + 32 * (EPI_WARPS + CVT_WARPS);
-constexpr int TMEM_COLS = 512;
-constexpr int RAW_REGION = STAGES * STAGE_BYTES;
-constexpr int BAR_REGION = RAW_REGION + RAWS * RAW_BYTES;
-constexpr int TABLE_REGION = BAR_REGION + 256;
-__host__ __device__ constexpr int smem_bytes(int E) { return 1024 + TABLE_REGION + 8 * (E + 1); }
-static_assert(smem_bytes(MXQ_MAX_EXPERTS) <= 232448, "shared memory over the per-block limit");
+
+template <int kCG>
+struct Shape {
+    static constexpr int kFeat = kFM * kCG;
+    static constexpr int kWide = kCG == 2 ? 256 : 32;
+    static constexpr int kStep = 16 * kCG;
+    static constexpr int kBox = kCG == 2 ? 64 : 32;  // token rows of a box
+    static constexpr int kRaws = kCG == 2 ? 4 : 9;   // int8 stages
+    static constexpr int kStages = CVT_WARPS / CVT_GROUP;  // widened stages
+    static constexpr int kRows = kFM + kWide / kCG;  // rows of a stage in one CTA: features, then tokens
+    static constexpr int kRaw = kRows * BK, kStage = kRows * BK * 2;
+    static constexpr int kTmem = 2 * kWide;
+    static constexpr int kRawAt = kStages * kStage;
+    static constexpr int kEpi = kRawAt + kRaws * kRaw;
+    static constexpr int kBars = kEpi + 2 * kEpiBytes;
+    static constexpr int kTables = kBars + 512;
+    __host__ __device__ static constexpr int smem(int E) { return 1024 + kTables + 8 * (E + 1); }
+    static_assert(1024 + kTables + 8 * (MXQ_MAX_EXPERTS + 1) <= 232448, "shared memory over the per-block limit");
+    static_assert(kBars % 8 == 0 && 8 * (2 * (kRaws + kStages) + 4) <= 512, "barrier region");
+};
 
 struct Params {
     const float *xs, *ws;
@@ -55,31 +69,36 @@ struct Params {
 };
 
 // Four int8 -> four f16, exact. With its sign bit flipped a code is q + 128 in
-// 0..255; under the high byte 0x64 that is the f16 1024 + 128 + q.
+// 0..255; under the high byte 0x64 that is the f16 1024 + 128 + q. Bytes 0 and
+// 2 come first, then 1 and 3: both operands' sums run over k in the same order.
 __device__ __forceinline__ uint2 widen4(uint32_t w) {
-    const uint32_t u = w ^ 0x80808080u, bias = 0x64806480u;  // 1152, 1152
-    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+    const uint32_t bias = 0x64806480u;  // 1152, 1152
+    uint32_t lo = (w & 0x00FF00FFu) ^ 0x64806480u, hi = (w >> 8 & 0x00FF00FFu) ^ 0x64806480u;
     __half2 a = __hsub2(*reinterpret_cast<__half2*>(&lo), *reinterpret_cast<const __half2*>(&bias));
     __half2 b = __hsub2(*reinterpret_cast<__half2*>(&hi), *reinterpret_cast<const __half2*>(&bias));
     return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
 
+template <int kCG, bool kF32>
 __global__ void __launch_bounds__(THREADS, 1)
     ragged_int8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Params p) {
+    using S = Shape<kCG>;
+    constexpr int RAWS = S::kRaws, STAGES = S::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align<1024>(smem_raw);
-    int32_t* s_off = reinterpret_cast<int32_t*>(smem + TABLE_REGION);
+    int32_t* s_off = reinterpret_cast<int32_t*>(smem + S::kTables);
     int32_t* s_slices = s_off + p.E + 1;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = kCG == 2 ? cta_rank() : 0;
 
-    const int bad = load_ragged(p.m_splits, p.E, p.M, BN, s_off, s_slices);
+    const int bad = load_ragged(p.m_splits, p.E, p.M, S::kWide, s_off, s_slices);
     if (bad) {
         report_status(p.status, bad);
         return;
     }
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_REGION);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
     const uint32_t rawf0 = smem_u32(bars), rawe0 = rawf0 + 8 * RAWS;
     const uint32_t full0 = rawe0 + 8 * RAWS, empty0 = full0 + 8 * STAGES;
     const uint32_t accf0 = empty0 + 8 * STAGES, acce0 = accf0 + 16;
@@ -88,139 +107,181 @@ __global__ void __launch_bounds__(THREADS, 1)
         s_abort = 0;
         for (int st = 0; st < RAWS; ++st) {
             mbar_init(rawf0 + 8 * st, 1);
-            mbar_init(rawe0 + 8 * st, CVT_WARPS);
+            mbar_init(rawe0 + 8 * st, CVT_GROUP);
         }
         for (int st = 0; st < STAGES; ++st) {
-            mbar_init(full0 + 8 * st, CVT_WARPS);
+            mbar_init(full0 + 8 * st, kCG * CVT_GROUP);
             mbar_init(empty0 + 8 * st, 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf0 + 8 * b, 1);
-            mbar_init(acce0 + 8 * b, EPI_WARPS);
+            mbar_init(acce0 + 8 * b, kCG * EPI_WARPS);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmA) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmB) : "memory");
     }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
-                     "r"(TMEM_COLS)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    if (warp == 1) tmem_alloc<kCG>(smem_u32(&s_tmem), S::kTmem);
     fence_before();
     __syncthreads();
+    if (kCG == 2) cluster_sync();
     fence_after();
     const uint32_t tmem = s_tmem;
-    const Walk<kFprop, kFM, BN, 16> W(p.N, p.K, p.E, s_off, s_slices, nullptr);
+    const Walk<kFprop, S::kFeat, S::kWide, S::kStep> W(p.N, p.K, p.E, s_off, s_slices, nullptr);
+    const int64_t first = blockIdx.x / kCG, stride = gridDim.x / kCG;
 
     if (warp == 0) {
-        // ------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int64_t fills = 0;
-            for (int64_t t = blockIdx.x; t < W.total; t += gridDim.x) {
-                const Tile T = W.get(t);
-                const int boxes = (T.n + 63) / 64;
-                for (int r = 0; r < T.red; r += BK) {
-                    if (!mbar_wait(rawe0 + 8 * stage, phase ^ 1, abort_flag)) {
-                        drain_ring(rawf0, RAWS, fills);
-                        goto done_producer;
-                    }
-                    const uint32_t fb = rawf0 + 8 * stage, a = smem_u32(smem + RAW_REGION + stage * RAW_BYTES);
-                    mbar_expect_tx(fb, RAW_A + boxes * 64 * BK);
-                    load_3d<1>(a, &tmA, fb, r, T.f0, T.e);
-                    for (int i = 0; i < boxes; ++i)
-                        tma_load_2d(a + RAW_A + i * 64 * BK, &tmB, fb, r, T.c0 + 64 * i);
-                    ++fills;
-                    if (++stage == RAWS) { stage = 0; phase ^= 1; }
+        // ------------------------------------------------------ TMA producer: this CTA's int8 boxes
+        int stage = 0;
+        uint32_t phase = 0;
+        int64_t fills = 0;
+        for (int64_t t = first; t < W.total; t += stride) {
+            const Tile T = W.get(t);
+            const int half = T.n / kCG, boxes = (half + S::kBox - 1) / S::kBox;
+            const int f = T.f0 + rank * kFM, c = T.c0 + rank * half;
+            for (int r = 0; r < T.red; r += BK) {
+                if (!mbar_wait(rawe0 + 8 * stage, phase ^ 1, abort_flag)) {
+                    drain_ring(rawf0, RAWS, fills);
+                    goto done_producer;
                 }
+                __syncwarp();
+                const uint32_t fb = rawf0 + 8 * stage, a = smem_u32(smem) + S::kRawAt + stage * S::kRaw;
+                if (elect_one()) {
+                    mbar_expect_tx(fb, (kFM + boxes * S::kBox) * BK);
+                    load_3d<1>(a, &tmA, fb, r, f, T.e);
+#pragma unroll
+                    for (int i = 0; i < S::kWide / kCG / S::kBox; ++i)
+                        if (i < boxes) load_2d<1>(a + (kFM + i * S::kBox) * BK, &tmB, fb, r, c + S::kBox * i);
+                }
+                __syncwarp();
+                ++fills;
+                if (++stage == RAWS) { stage = 0; phase ^= 1; }
             }
-        done_producer:;
         }
+    done_producer:;
     } else if (warp == 1) {
-        // ------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        // ------------------------------------------------------ MMA issuer (rank 0)
+        if (rank == 0) {
             int stage = 0, buf = 0;
             uint32_t phase = 0, aphase = 0;
             const uint32_t base = smem_u32(smem);
-            const uint64_t ad0 = smem_desc(base, 16, 1024), bd0 = smem_desc(base + A_BYTES, 16, 1024);
-            bool ok = true;
-            for (int64_t t = blockIdx.x; t < W.total && ok; t += gridDim.x) {
+            const uint64_t ad0 = smem_desc(base, 16, 1024), bd0 = smem_desc(base + kFM * BK * 2, 16, 1024);
+            for (int64_t t = first; t < W.total; t += stride) {
                 const Tile T = W.get(t);
-                const uint32_t id = idesc_f16(0, 0, 0, kFM, T.n);
-                ok = mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag);
-                for (int r = 0; r < T.red && ok; r += BK) {
-                    ok = mbar_wait(full0 + 8 * stage, phase, abort_flag);
-                    if (!ok) break;
+                const uint32_t id = idesc_f16(0, 0, 0, S::kFeat, T.n);
+                const uint32_t d = tmem + buf * S::kWide;
+                if (!mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag)) goto done_mma;
+                __syncwarp();
+                for (int r = 0; r < T.red; r += BK) {
+                    const uint64_t ad = ad0 + (uint64_t)(stage * (S::kStage / 16));
+                    const uint64_t bd = bd0 + (uint64_t)(stage * (S::kStage / 16));
+                    if (!mbar_wait_pair<kCG>(full0 + 8 * stage, phase, abort_flag)) goto done_mma;
+                    __syncwarp();
                     fence_after();
-                    const int steps = (min(BK, T.red - r) + 15) / 16;
-                    const uint64_t so = (uint64_t)(stage * (STAGE_BYTES / 16));
-                    for (int k = 0; k < steps; ++k)
-                        mma_f16<1>(tmem + buf * BN, ad0 + so + 2 * k, bd0 + so + 2 * k, id, (r | k) != 0);
-                    mma_commit<1>(empty0 + 8 * stage);
+                    const int steps = T.red - r >= BK ? BK / 16 : (T.red - r + 15) / 16;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < BK / 16; ++k)
+                            if (k < steps) mma_f16<kCG>(d, ad + 2 * k, bd + 2 * k, id, r > 0 || k > 0);
+                        mma_commit<kCG>(empty0 + 8 * stage);
+                        if (r + BK >= T.red) mma_commit<kCG>(accf0 + 8 * buf);
+                    }
+                    __syncwarp();
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
-                if (ok) mma_commit<1>(accf0 + 8 * buf);
                 buf ^= 1;
                 aphase ^= buf == 0;
             }
+        done_mma:;
         }
     } else if (warp < 2 + EPI_WARPS) {
         // ------------------------------------------------------ epilogue
-        const int q = warp & 3, half = (warp - 2) >> 2;
+        const int q = warp & 3, group = (warp - 2) >> 2;
+        uint8_t* stage = smem + S::kEpi + group * kEpiBytes;
         int buf = 0;
         uint32_t aphase = 0;
-        for (int64_t t = blockIdx.x; t < W.total; t += gridDim.x) {
+        for (int64_t t = first; t < W.total; t += stride) {
             const Tile T = W.get(t);
-            const int f = T.f0 + q * 32 + lane;
-            const bool live = f < p.N;
+            const int f0 = T.f0 + rank * kFM;
+            const int live = (int)min((int64_t)kFM, p.N - f0);
             const bool ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
-            __syncwarp();
-            if (!ok || *abort_flag) break;
+            if (group_any(1 + group, kEpiGroup, !ok || *abort_flag)) break;
             fence_after();
-            const float sw = live ? p.ws[(int64_t)T.e * p.N + f] : 0.0f;
-            const float b = p.bias && live ? __bfloat162float(p.bias[(int64_t)T.e * p.N + f]) : 0.0f;
-            for (int c = 32 * half; c < T.cols; c += 64) {
-                uint32_t v[32];
-                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * BN + c, v);
-                tmem_wait_ld();
-                if (live) {
+            const float* xs = p.xs + T.row0;
+            if constexpr (kF32) {
+                const int l = q * 32 + lane;
+                const int64_t at = (int64_t)T.e * p.N + f0 + l;
+                const float sw = l < live ? p.ws[at] : 0.0f;
+                const float b = p.bias && l < live ? __bfloat162float(p.bias[at]) : 0.0f;
+                for (int c = 32 * group; c < T.cols; c += 64) {
+                    uint32_t v[32];
+                    tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * S::kWide + c, v);
+                    tmem_wait_ld();
+                    if (l < live) {
+                        float* o = static_cast<float*>(p.out) + (T.row0 + c) * p.N + f0 + l;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (c + j >= T.cols) break;
-                        const int64_t m = T.c0 + c + j;
-                        const float y = __uint_as_float(v[j]) * __ldg(p.xs + m) * sw + b;
-                        if (p.out_f32) static_cast<float*>(p.out)[m * p.N + f] = y;
-                        else static_cast<__nv_bfloat16*>(p.out)[m * p.N + f] = __float2bfloat16_rn(y);
+                        for (int j = 0; j < 32; ++j)
+                            if (c + j < T.cols) o[j * p.N] = __uint_as_float(v[j]) * __ldg(xs + c + j) * sw + b;
                     }
+                }
+            } else {
+                float sw[4], b[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int l = q * 32 + (lane >> 2) + 8 * g;
+                    const int64_t at = (int64_t)T.e * p.N + f0 + l;
+                    sw[g] = l < live ? p.ws[at] : 0.0f;
+                    b[g] = p.bias && l < live ? __bfloat162float(p.bias[at]) : 0.0f;
+                }
+                for (int c = 32 * group; c < T.cols; c += 64) {
+                    // this thread's token scales: columns 8b + 2 (lane mod 4) and the next
+                    float sx[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int col = c + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+                        sx[i] = col < T.cols ? __ldg(xs + col) : 0.0f;
+                    }
+                    store_columns_bf16(tmem + buf * S::kWide + c, q, lane, 1 + group, stage,
+                                       static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * p.N + f0, p.N, live,
+                                       T.cols - c, [&](float v, int l, int col) {
+                                           const int g = (l >> 3) & 3;
+                                           return v * sx[(col >> 3) * 2 + (col & 1)] * sw[g] + b[g];
+                                       });
                 }
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acce0 + 8 * buf);
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive(acce0 + 8 * buf);
+                else arrive_remote_relaxed(mapa(acce0 + 8 * buf, 0));
+            }
             buf ^= 1;
             aphase ^= buf == 0;
         }
     } else {
-        // ------------------------------------------------------ int8 -> f16
-        const int ct = (int)threadIdx.x - 32 * (2 + EPI_WARPS);
-        int raw = 0, stage = 0;
-        uint32_t rphase = 0, phase = 0;
-        bool ok = true;
-        for (int64_t t = blockIdx.x; t < W.total && ok; t += gridDim.x) {
+        // ------------------------------------------------------ int8 -> f16, this CTA's rows
+        // A group of CVT_GROUP warps owns each widened stage, so that the latencies of its loads, of the
+        // proxy fence and of the arrival on rank 0 overlap the other groups' work.
+        const int slot = (warp - 2 - EPI_WARPS) / CVT_GROUP;
+        const int ct = (int)threadIdx.x - 32 * (2 + EPI_WARPS + slot * CVT_GROUP);
+        const uint32_t lead_full = kCG == 2 ? mapa(full0, 0) : full0;
+        uint8_t* dst = smem + slot * S::kStage;
+        int raw = slot % RAWS, block = 0;  // block: of this CTA's sequence, modulo STAGES
+        uint32_t rphase = slot / RAWS & 1, phase = 0;
+        for (int64_t t = first; t < W.total; t += stride) {
             const Tile T = W.get(t);
-            const int units = (kFM + T.n) * (BK / 16);  // 16-byte chunks of A's rows, then of B's
+            const int units = (kFM + T.n / kCG) * (BK / 16);  // 16-byte chunks
             for (int r = 0; r < T.red; r += BK) {
-                ok = mbar_wait(rawf0 + 8 * raw, rphase, abort_flag) && mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                const uint8_t* src = smem + RAW_REGION + raw * RAW_BYTES;
-                uint8_t* dst = smem + stage * STAGE_BYTES;
-                for (int i = ct; i < units; i += 32 * CVT_WARPS) {
+                const bool mine = block == slot;
+                if (++block == STAGES) block = 0;
+                if (!mine) continue;
+                const bool ok = mbar_wait(rawf0 + 8 * raw, rphase, abort_flag) &&
+                                mbar_wait(empty0 + 8 * slot, phase ^ 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) goto done_convert;
+                const uint8_t* src = smem + S::kRawAt + raw * S::kRaw;
+#pragma unroll
+                for (int i = ct; i < S::kRows * (BK / 16); i += 32 * CVT_GROUP) {
+                    if (i >= units) break;
                     const uint4 w = *reinterpret_cast<const uint4*>(src + i * 16);
                     const uint2 a = widen4(w.x), b = widen4(w.y), c = widen4(w.z), d = widen4(w.w);
                     const int row = i >> 2, ch = (i & 3) * 2;  // 128-byte rows, chunk ^= row mod 8
@@ -231,20 +292,24 @@ __global__ void __launch_bounds__(THREADS, 1)
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(full0 + 8 * stage);
                     mbar_arrive(rawe0 + 8 * raw);
+                    if (rank == 0) mbar_arrive(full0 + 8 * slot);
+                    else arrive_remote_release(lead_full + 8 * slot);
                 }
-                if (++raw == RAWS) { raw = 0; rphase ^= 1; }
-                if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                raw += STAGES;
+                if (raw >= RAWS) { raw -= RAWS; rphase ^= 1; }
+                phase ^= 1;
             }
         }
+    done_convert:;
     }
     fence_before();
     __syncthreads();
     if (s_abort && threadIdx.x == 0 && p.status) atomicOr(p.status, MXQ_STATUS_WAIT_TIMEOUT);
+    if (kCG == 2) cluster_sync();
     if (warp == 1) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+        tmem_dealloc<kCG>(tmem, S::kTmem);
     }
 }
 
@@ -290,22 +355,30 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* x, i
 
 }  // namespace i8
 
-cudaError_t run_int8(const Int8Call& c, cudaStream_t s) {
-    using namespace i8;
-    Params p{c.xs, c.ws, static_cast<const __nv_bfloat16*>(c.bias), c.M, c.N, c.K, c.E, c.m_splits, c.out, c.out_f32,
-             c.status};
+template <int kCG, bool kF32>
+static cudaError_t launch_int8(const CUtensorMap& a, const CUtensorMap& b, const i8::Params& p, int64_t tiles,
+                               cudaStream_t s) {
+    using S = i8::Shape<kCG>;
+    return launch_persistent<kCG, i8::ragged_int8_kernel<kCG, kF32>>(i8::THREADS, S::smem(MXQ_MAX_EXPERTS),
+                                                                     S::smem(p.E), tiles, s, a, b, p);
+}
+
+template <int kCG>
+static cudaError_t run_int8_shape(const Int8Call& c, cudaStream_t s) {
+    using S = i8::Shape<kCG>;
+    const i8::Params p{c.xs, c.ws, static_cast<const __nv_bfloat16*>(c.bias), c.M, c.N, c.K, c.E, c.m_splits, c.out,
+                       c.out_f32, c.status};
     const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {c.K, c.K * c.N}, db[2] = {c.K, c.M}, sb[1] = {c.K};
-    const int boxa[3] = {BK, kFM, 1}, boxb[2] = {BK, 64};
+    const int boxa[3] = {i8::BK, kFM, 1}, boxb[2] = {i8::BK, S::kBox};
     CUtensorMap a, b;
     if (!encode_tmap(&a, c.wq, 1, 3, da, sa, boxa, 0) || !encode_tmap(&b, c.xq, 1, 2, db, sb, boxb, 0))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(ragged_int8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes(MXQ_MAX_EXPERTS));
-    if (e != cudaSuccess) return e;
-    const int64_t tiles = (c.M / BN + std::min<int64_t>(c.E, c.M)) * ((c.N + kFM - 1) / kFM);
-    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, sm_count()));
-    ragged_int8_kernel<<<grid, THREADS, smem_bytes(c.E), s>>>(a, b, p);
-    return cudaGetLastError();
+    const int64_t tiles = (c.M / S::kWide + std::min<int64_t>(c.E, c.M)) * ((c.N + S::kFeat - 1) / S::kFeat);
+    return c.out_f32 ? launch_int8<kCG, true>(a, b, p, tiles, s) : launch_int8<kCG, false>(a, b, p, tiles, s);
+}
+
+cudaError_t run_int8(const Int8Call& c, cudaStream_t s) {
+    return c.M <= (int64_t)i8::Shape<1>::kWide * c.E ? run_int8_shape<1>(c, s) : run_int8_shape<2>(c, s);
 }
 
 cudaError_t run_int8_quantize(const void* x, int64_t M, int64_t K, int64_t ld, void* q, float* scale, cudaStream_t s) {
