@@ -6,17 +6,23 @@
 //
 // GB300's int8 tensor rate is a small fraction of its 16-bit floating rate, so
 // the codes travel as int8 (the bytes that a weight-bound call is made of) and
-// are widened to f16 in shared memory, exactly: |q| <= 128 fits f16's 11
-// significand bits. The products are then whole numbers below 2^14 and
-// tcgen05.mma kind::f16 sums them in fp32.
+// are widened to f16 on chip, exactly: |q| <= 128 fits f16's 11 significand
+// bits. The products are then whole numbers below 2^14 and tcgen05.mma
+// kind::f16 sums them in fp32; sums below 2^24 are exact, so fp32 outputs need
+// no sums in registers here.
 //
 // The tile walk, the operands' sides (features on the MMA's M, tokens on its
 // N), the edges and the two shapes (pairs of SMs; one SM for few rows) are
-// those of the bf16 products (mxq_ragged.cuh, mxq_ragged.cu). Warp 0 loads int8
-// boxes into a ring of their own, warps 10..17 widen them into the
-// 128-byte-swizzled operand stages, warp 1 issues the MMAs, warps 2..9 scale
-// and store. Sums of whole numbers below 2^24 are exact, so fp32 outputs need
-// no sums in registers here.
+// those of the bf16 products (mxq_ragged.cuh, mxq_ragged.cu).
+//
+// The widened weights go to TMEM, the widened tokens to shared memory. With
+// both in shared memory a 64-deep stage of 256 x 256 moves 96 KB or more through
+// it (load, read, write back twice as wide, read by the MMA), 750 cycles against
+// the MMA's 512; from TMEM the weights' second trip costs nothing there. TMEM
+// then holds two accumulators of 192 columns and four 64-deep slots of weights.
+// Warp 0 loads 128-deep int8 stages, warps 6..13 widen weights and 14..21
+// tokens, in two sets that take alternate stages so that one's latencies hide
+// behind the other's work; warp 1 issues the MMAs, warps 2..5 scale and store.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -32,29 +38,33 @@ namespace mxq {
 namespace ragged {
 namespace i8 {
 
-constexpr int BK = 64;  // reduction depth of a stage
-constexpr int EPI_WARPS = 8, CVT_WARPS = 8;
-constexpr int CVT_GROUP = 2;  // warps that widen one stage
-constexpr int THREADS = 64 + 32 * (EPI_WARPS + CVT_WARPS);
+constexpr int BK = 128;   // depth of an int8 stage
+constexpr int HK = 64;    // depth of a widened slot: half a stage
+constexpr int SLOTS = 4;  // set s widens into slots 2 s and 2 s + 1
+constexpr int EPI_WARPS = 4, CVT_WARPS = 4, SETS = 2;  // CVT_WARPS: for the weights and for the tokens of a set
+constexpr int THREADS = 32 * (2 + EPI_WARPS + 2 * SETS * CVT_WARPS);
 
 template <int kCG>
 struct Shape {
     static constexpr int kFeat = kFM * kCG;
-    static constexpr int kWide = kCG == 2 ? 256 : 32;
+    static constexpr int kWide = kCG == 2 ? 192 : 32;
     static constexpr int kStep = 16 * kCG;
-    static constexpr int kBox = kCG == 2 ? 64 : 32;  // token rows of a box
-    static constexpr int kRaws = kCG == 2 ? 4 : 9;   // int8 stages
-    static constexpr int kStages = CVT_WARPS / CVT_GROUP;  // widened stages
-    static constexpr int kRows = kFM + kWide / kCG;  // rows of a stage in one CTA: features, then tokens
-    static constexpr int kRaw = kRows * BK, kStage = kRows * BK * 2;
-    static constexpr int kTmem = 2 * kWide;
-    static constexpr int kRawAt = kStages * kStage;
+    static constexpr int kBox = 32;                  // token rows of a box
+    static constexpr int kTok = kWide / kCG;         // token rows of a stage in one CTA
+    static constexpr int kRaws = kCG == 2 ? 5 : 8;   // int8 stages
+    static constexpr int kRaw = (kFM + kTok) * BK;   // weights, then tokens
+    static constexpr int kSlot = kTok * HK * 2;      // widened tokens
+    static constexpr int kTmemA = 2 * kWide;         // the weights' slots follow the accumulators
+    static constexpr int kTmem = kCG == 2 ? 512 : 256;
+    static constexpr int kRawAt = SLOTS * kSlot;
     static constexpr int kEpi = kRawAt + kRaws * kRaw;
-    static constexpr int kBars = kEpi + 2 * kEpiBytes;
-    static constexpr int kTables = kBars + 512;
+    static constexpr int kBars = kEpi + kEpiBytes;
+    static constexpr int kTables = kBars + 256;
     __host__ __device__ static constexpr int smem(int E) { return 1024 + kTables + 8 * (E + 1); }
     static_assert(1024 + kTables + 8 * (MXQ_MAX_EXPERTS + 1) <= 232448, "shared memory over the per-block limit");
-    static_assert(kBars % 8 == 0 && 8 * (2 * (kRaws + kStages) + 4) <= 512, "barrier region");
+    static_assert(kBars % 8 == 0 && 8 * (2 * (kRaws + SLOTS) + 4) <= 256, "barrier region");
+    static_assert(kSlot % 1024 == 0 && kRaw % 1024 == 0, "the 128-byte swizzle repeats every 1024 bytes");
+    static_assert(kTmemA + SLOTS * HK / 2 <= kTmem, "TMEM columns");
 };
 
 struct Params {
@@ -83,7 +93,7 @@ template <int kCG, bool kF32>
 __global__ void __launch_bounds__(THREADS, 1)
     ragged_int8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Params p) {
     using S = Shape<kCG>;
-    constexpr int RAWS = S::kRaws, STAGES = S::kStages;
+    constexpr int RAWS = S::kRaws;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align<1024>(smem_raw);
     int32_t* s_off = reinterpret_cast<int32_t*>(smem + S::kTables);
@@ -100,17 +110,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
     const uint32_t rawf0 = smem_u32(bars), rawe0 = rawf0 + 8 * RAWS;
-    const uint32_t full0 = rawe0 + 8 * RAWS, empty0 = full0 + 8 * STAGES;
-    const uint32_t accf0 = empty0 + 8 * STAGES, acce0 = accf0 + 16;
+    const uint32_t full0 = rawe0 + 8 * RAWS, empty0 = full0 + 8 * SLOTS;
+    const uint32_t accf0 = empty0 + 8 * SLOTS, acce0 = accf0 + 16;
     volatile int* abort_flag = &s_abort;
     if (threadIdx.x == 0) {
         s_abort = 0;
         for (int st = 0; st < RAWS; ++st) {
             mbar_init(rawf0 + 8 * st, 1);
-            mbar_init(rawe0 + 8 * st, CVT_GROUP);
+            mbar_init(rawe0 + 8 * st, 2 * CVT_WARPS);
         }
-        for (int st = 0; st < STAGES; ++st) {
-            mbar_init(full0 + 8 * st, kCG * CVT_GROUP);
+        for (int st = 0; st < SLOTS; ++st) {
+            mbar_init(full0 + 8 * st, kCG * 2 * CVT_WARPS);
             mbar_init(empty0 + 8 * st, 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -150,7 +160,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     mbar_expect_tx(fb, (kFM + boxes * S::kBox) * BK);
                     load_3d<1>(a, &tmA, fb, r, f, T.e);
 #pragma unroll
-                    for (int i = 0; i < S::kWide / kCG / S::kBox; ++i)
+                    for (int i = 0; i < S::kTok / S::kBox; ++i)
                         if (i < boxes) load_2d<1>(a + (kFM + i * S::kBox) * BK, &tmB, fb, r, c + S::kBox * i);
                 }
                 __syncwarp();
@@ -162,32 +172,38 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer (rank 0)
         if (rank == 0) {
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, aphase = 0;
-            const uint32_t base = smem_u32(smem);
-            const uint64_t ad0 = smem_desc(base, 16, 1024), bd0 = smem_desc(base + kFM * BK * 2, 16, 1024);
+            int set = 0, buf = 0;
+            uint32_t phases = 0, aphase = 0;  // phases: bit of a slot = its parity
+            const uint64_t bd0 = smem_desc(smem_u32(smem), 16, 1024);
             for (int64_t t = first; t < W.total; t += stride) {
                 const Tile T = W.get(t);
                 const uint32_t id = idesc_f16(0, 0, 0, S::kFeat, T.n);
                 const uint32_t d = tmem + buf * S::kWide;
                 if (!mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag)) goto done_mma;
                 __syncwarp();
-                for (int r = 0; r < T.red; r += BK) {
-                    const uint64_t ad = ad0 + (uint64_t)(stage * (S::kStage / 16));
-                    const uint64_t bd = bd0 + (uint64_t)(stage * (S::kStage / 16));
-                    if (!mbar_wait_pair<kCG>(full0 + 8 * stage, phase, abort_flag)) goto done_mma;
-                    __syncwarp();
-                    fence_after();
-                    const int steps = T.red - r >= BK ? BK / 16 : (T.red - r + 15) / 16;
-                    if (elect_one()) {
+                for (int r = 0; r < T.red; r += BK, set ^= 1) {
 #pragma unroll
-                        for (int k = 0; k < BK / 16; ++k)
-                            if (k < steps) mma_f16<kCG>(d, ad + 2 * k, bd + 2 * k, id, r > 0 || k > 0);
-                        mma_commit<kCG>(empty0 + 8 * stage);
-                        if (r + BK >= T.red) mma_commit<kCG>(accf0 + 8 * buf);
+                    for (int h = 0; h < 2; ++h) {
+                        const int left = T.red - r - h * HK;
+                        if (left <= 0) break;
+                        const int slot = 2 * set + h;
+                        const uint32_t at = tmem + S::kTmemA + slot * (HK / 2);
+                        const uint64_t bd = bd0 + (uint64_t)(slot * (S::kSlot / 16));
+                        if (!mbar_wait_pair<kCG>(full0 + 8 * slot, phases >> slot & 1, abort_flag)) goto done_mma;
+                        phases ^= 1u << slot;
+                        __syncwarp();
+                        fence_after();
+                        const int steps = left >= HK ? HK / 16 : (left + 15) / 16;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < HK / 16; ++k)
+                                if (k < steps)
+                                    mma_f16_tmem<kCG>(d, at + 8 * k, bd + 2 * k, id, r > 0 || h > 0 || k > 0);
+                            mma_commit<kCG>(empty0 + 8 * slot);
+                            if (left <= HK) mma_commit<kCG>(accf0 + 8 * buf);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
                 buf ^= 1;
                 aphase ^= buf == 0;
@@ -196,8 +212,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (warp < 2 + EPI_WARPS) {
         // ------------------------------------------------------ epilogue
-        const int q = warp & 3, group = (warp - 2) >> 2;
-        uint8_t* stage = smem + S::kEpi + group * kEpiBytes;
+        const int q = warp & 3;
+        uint8_t* stage = smem + S::kEpi;
         int buf = 0;
         uint32_t aphase = 0;
         for (int64_t t = first; t < W.total; t += stride) {
@@ -205,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int f0 = T.f0 + rank * kFM;
             const int live = (int)min((int64_t)kFM, p.N - f0);
             const bool ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
-            if (group_any(1 + group, kEpiGroup, !ok || *abort_flag)) break;
+            if (group_any(1, kEpiGroup, !ok || *abort_flag)) break;
             fence_after();
             const float* xs = p.xs + T.row0;
             if constexpr (kF32) {
@@ -213,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int64_t at = (int64_t)T.e * p.N + f0 + l;
                 const float sw = l < live ? p.ws[at] : 0.0f;
                 const float b = p.bias && l < live ? __bfloat162float(p.bias[at]) : 0.0f;
-                for (int c = 32 * group; c < T.cols; c += 64) {
+                for (int c = 0; c < T.cols; c += 32) {
                     uint32_t v[32];
                     tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * S::kWide + c, v);
                     tmem_wait_ld();
@@ -233,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     sw[g] = l < live ? p.ws[at] : 0.0f;
                     b[g] = p.bias && l < live ? __bfloat162float(p.bias[at]) : 0.0f;
                 }
-                for (int c = 32 * group; c < T.cols; c += 64) {
+                for (int c = 0; c < T.cols; c += 32) {
                     // this thread's token scales: columns 8b + 2 (lane mod 4) and the next
                     float sx[8];
 #pragma unroll
@@ -241,7 +257,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const int col = c + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
                         sx[i] = col < T.cols ? __ldg(xs + col) : 0.0f;
                     }
-                    store_columns_bf16(tmem + buf * S::kWide + c, q, lane, 1 + group, stage,
+                    store_columns_bf16(tmem + buf * S::kWide + c, q, lane, 1, stage,
                                        static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * p.N + f0, p.N, live,
                                        T.cols - c, [&](float v, int l, int col) {
                                            const int g = (l >> 3) & 3;
@@ -260,45 +276,73 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else {
         // ------------------------------------------------------ int8 -> f16, this CTA's rows
-        // A group of CVT_GROUP warps owns each widened stage, so that the latencies of its loads, of the
-        // proxy fence and of the arrival on rank 0 overlap the other groups' work.
-        const int slot = (warp - 2 - EPI_WARPS) / CVT_GROUP;
-        const int ct = (int)threadIdx.x - 32 * (2 + EPI_WARPS + slot * CVT_GROUP);
+        const int cw = warp - 2 - EPI_WARPS;
+        const bool weights = cw < SETS * CVT_WARPS;
+        const int set = cw / CVT_WARPS % SETS, q = warp & 3;
+        const int ct = (int)threadIdx.x - 32 * (2 + EPI_WARPS + cw / CVT_WARPS * CVT_WARPS);
         const uint32_t lead_full = kCG == 2 ? mapa(full0, 0) : full0;
-        uint8_t* dst = smem + slot * S::kStage;
-        int raw = slot % RAWS, block = 0;  // block: of this CTA's sequence, modulo STAGES
-        uint32_t rphase = slot / RAWS & 1, phase = 0;
+        int raw = 0, turn = 0;
+        uint32_t rphase = 0, phases = 0;
         for (int64_t t = first; t < W.total; t += stride) {
             const Tile T = W.get(t);
-            const int units = (kFM + T.n / kCG) * (BK / 16);  // 16-byte chunks
+            const int units = T.n / kCG * (HK / 16);  // 16-byte chunks of tokens in half a stage
             for (int r = 0; r < T.red; r += BK) {
-                const bool mine = block == slot;
-                if (++block == STAGES) block = 0;
-                if (!mine) continue;
-                const bool ok = mbar_wait(rawf0 + 8 * raw, rphase, abort_flag) &&
-                                mbar_wait(empty0 + 8 * slot, phase ^ 1, abort_flag);
-                if (!__all_sync(0xffffffffu, ok)) goto done_convert;
-                const uint8_t* src = smem + S::kRawAt + raw * S::kRaw;
+                if (turn == set) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(rawf0 + 8 * raw, rphase, abort_flag))) goto done_convert;
+                    const uint8_t* src = smem + S::kRawAt + raw * S::kRaw;
 #pragma unroll
-                for (int i = ct; i < S::kRows * (BK / 16); i += 32 * CVT_GROUP) {
-                    if (i >= units) break;
-                    const uint4 w = *reinterpret_cast<const uint4*>(src + i * 16);
-                    const uint2 a = widen4(w.x), b = widen4(w.y), c = widen4(w.z), d = widen4(w.w);
-                    const int row = i >> 2, ch = (i & 3) * 2;  // 128-byte rows, chunk ^= row mod 8
-                    uint8_t* o = dst + row * 128;
-                    *reinterpret_cast<uint4*>(o + ((ch ^ (row & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-                    *reinterpret_cast<uint4*>(o + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(c.x, c.y, d.x, d.y);
+                    for (int h = 0; h < 2; ++h) {
+                        if (h * HK >= T.red - r) break;
+                        const int slot = 2 * set + h;
+                        if (!__all_sync(0xffffffffu, mbar_wait(empty0 + 8 * slot, phases >> slot & 1 ^ 1, abort_flag)))
+                            goto done_convert;
+                        phases ^= 1u << slot;
+                        if (weights) {
+                            // lane = feature: 64 codes of its 128-byte swizzled row (16-byte chunk ^= row mod 8)
+                            const uint8_t* row = src + (32 * q + lane) * BK;
+                            uint32_t v[32];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint4 w =
+                                    *reinterpret_cast<const uint4*>(row + (((4 * h + i) ^ (lane & 7)) << 4));
+                                const uint2 a = widen4(w.x), b = widen4(w.y), c = widen4(w.z), d = widen4(w.w);
+                                v[8 * i] = a.x, v[8 * i + 1] = a.y, v[8 * i + 2] = b.x, v[8 * i + 3] = b.y;
+                                v[8 * i + 4] = c.x, v[8 * i + 5] = c.y, v[8 * i + 6] = d.x, v[8 * i + 7] = d.y;
+                            }
+                            fence_after();  // the slot's last MMAs, seen through empty[slot], come before the writes
+                            tmem_st32(tmem + ((uint32_t)(32 * q) << 16) + S::kTmemA + slot * (HK / 2), v);
+                            tmem_wait_st();
+                            fence_before();
+                        } else {
+                            const uint8_t* tok = src + kFM * BK;
+                            uint8_t* dst = smem + slot * S::kSlot;
+#pragma unroll
+                            for (int i = ct; i < S::kTok * (HK / 16); i += 32 * CVT_WARPS) {
+                                if (i < units) {
+                                    const int row = i >> 2, ch = i & 3;
+                                    const uint4 w = *reinterpret_cast<const uint4*>(
+                                        tok + row * BK + (((4 * h + ch) ^ (row & 7)) << 4));
+                                    const uint2 a = widen4(w.x), b = widen4(w.y), c = widen4(w.z), d = widen4(w.w);
+                                    uint8_t* o = dst + row * 128;
+                                    *reinterpret_cast<uint4*>(o + (((2 * ch) ^ (row & 7)) << 4)) =
+                                        make_uint4(a.x, a.y, b.x, b.y);
+                                    *reinterpret_cast<uint4*>(o + (((2 * ch + 1) ^ (row & 7)) << 4)) =
+                                        make_uint4(c.x, c.y, d.x, d.y);
+                                }
+                            }
+                            fence_async_smem();
+                        }
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (rank == 0) mbar_arrive(full0 + 8 * slot);
+                            else arrive_remote_release(lead_full + 8 * slot);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(rawe0 + 8 * raw);
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(rawe0 + 8 * raw);
-                    if (rank == 0) mbar_arrive(full0 + 8 * slot);
-                    else arrive_remote_release(lead_full + 8 * slot);
-                }
-                raw += STAGES;
-                if (raw >= RAWS) { raw -= RAWS; rphase ^= 1; }
-                phase ^= 1;
+                turn ^= 1;
+                if (++raw == RAWS) { raw = 0; rphase ^= 1; }
             }
         }
     done_convert:;
@@ -371,7 +415,7 @@ static cudaError_t run_int8_shape(const Int8Call& c, cudaStream_t s) {
     const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {c.K, c.K * c.N}, db[2] = {c.K, c.M}, sb[1] = {c.K};
     const int boxa[3] = {i8::BK, kFM, 1}, boxb[2] = {i8::BK, S::kBox};
     CUtensorMap a, b;
-    if (!encode_tmap(&a, c.wq, 1, 3, da, sa, boxa, 0) || !encode_tmap(&b, c.xq, 1, 2, db, sb, boxb, 0))
+    if (!encode_tmap(&a, c.wq, 1, 3, da, sa, boxa, 128) || !encode_tmap(&b, c.xq, 1, 2, db, sb, boxb, 128))
         return cudaErrorInvalidValue;
     const int64_t tiles = (c.M / S::kWide + std::min<int64_t>(c.E, c.M)) * ((c.N + S::kFeat - 1) / S::kFeat);
     return c.out_f32 ? launch_int8<kCG, true>(a, b, p, tiles, s) : launch_int8<kCG, false>(a, b, p, tiles, s);
