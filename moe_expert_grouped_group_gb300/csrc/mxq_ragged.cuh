@@ -166,6 +166,13 @@ __device__ __forceinline__ void arrive_remote_relaxed(uint32_t cluster_bar) {
 __device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
+// Remote arrive after this thread's (warp's) writes to its own CTA's shared memory or TMEM, made visible to
+// the tensor core by fence.proxy.async or tcgen05.wait::st: a pair's MMA reads them through this SM, no
+// thread of the other CTA does, so the arrive has to follow them here and needs no cluster-wide release,
+// which would cost the warp about 800 cycles.
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
 // mbar_wait that also acquires what threads of the pair's other CTA released with their arrivals.
 __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
     uint32_t ok;

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const int slot = 2 * set + h;
                         const uint32_t at = tmem + S::kTmemA + slot * (HK / 2);
                         const uint64_t bd = bd0 + (uint64_t)(slot * (S::kSlot / 16));
-                        if (!mbar_wait_pair<kCG>(full0 + 8 * slot, phases >> slot & 1, abort_flag)) goto done_mma;
+                        if (!mbar_wait(full0 + 8 * slot, phases >> slot & 1, abort_flag)) goto done_mma;
                         phases ^= 1u << slot;
                         __syncwarp();
                         fence_after();
@@ -285,7 +285,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t rphase = 0, phases = 0;
         for (int64_t t = first; t < W.total; t += stride) {
             const Tile T = W.get(t);
-            const int units = T.n / kCG * (HK / 16);  // 16-byte chunks of tokens in half a stage
             for (int r = 0; r < T.red; r += BK) {
                 if (turn == set) {
                     if (!__all_sync(0xffffffffu, mbar_wait(rawf0 + 8 * raw, rphase, abort_flag))) goto done_convert;
@@ -314,28 +313,33 @@ __global__ void __launch_bounds__(THREADS, 1)
                             tmem_wait_st();
                             fence_before();
                         } else {
+                            // rows beyond the slice are widened too: what they hold is never stored
                             const uint8_t* tok = src + kFM * BK;
                             uint8_t* dst = smem + slot * S::kSlot;
+                            constexpr int kUnits = S::kTok * (HK / 16) / (32 * CVT_WARPS);  // 16-byte chunks a thread
+                            uint4 w[kUnits];
 #pragma unroll
-                            for (int i = ct; i < S::kTok * (HK / 16); i += 32 * CVT_WARPS) {
-                                if (i < units) {
-                                    const int row = i >> 2, ch = i & 3;
-                                    const uint4 w = *reinterpret_cast<const uint4*>(
-                                        tok + row * BK + (((4 * h + ch) ^ (row & 7)) << 4));
-                                    const uint2 a = widen4(w.x), b = widen4(w.y), c = widen4(w.z), d = widen4(w.w);
-                                    uint8_t* o = dst + row * 128;
-                                    *reinterpret_cast<uint4*>(o + (((2 * ch) ^ (row & 7)) << 4)) =
-                                        make_uint4(a.x, a.y, b.x, b.y);
-                                    *reinterpret_cast<uint4*>(o + (((2 * ch + 1) ^ (row & 7)) << 4)) =
-                                        make_uint4(c.x, c.y, d.x, d.y);
-                                }
+                            for (int u = 0; u < kUnits; ++u) {
+                                const int row = (ct >> 2) + u * 8 * CVT_WARPS;
+                                w[u] = *reinterpret_cast<const uint4*>(tok + row * BK +
+                                                                       (((4 * h + (ct & 3)) ^ (row & 7)) << 4));
+                            }
+#pragma unroll
+                            for (int u = 0; u < kUnits; ++u) {
+                                const int row = (ct >> 2) + u * 8 * CVT_WARPS, ch = 2 * (ct & 3);
+                                const uint2 a = widen4(w[u].x), b = widen4(w[u].y), c = widen4(w[u].z),
+                                            d = widen4(w[u].w);
+                                uint8_t* o = dst + row * 128;
+                                *reinterpret_cast<uint4*>(o + ((ch ^ (row & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+                                *reinterpret_cast<uint4*>(o + (((ch + 1) ^ (row & 7)) << 4)) =
+                                    make_uint4(c.x, c.y, d.x, d.y);
                             }
                             fence_async_smem();
                         }
                         __syncwarp();
                         if (lane == 0) {
                             if (rank == 0) mbar_arrive(full0 + 8 * slot);
-                            else arrive_remote_release(lead_full + 8 * slot);
+                            else arrive_remote(lead_full + 8 * slot);
                         }
                     }
                     __syncwarp();
