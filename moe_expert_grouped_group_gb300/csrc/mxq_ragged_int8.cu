@@ -19,7 +19,7 @@
 // both in shared memory a 64-deep stage of 256 x 256 moves 96 KB or more through
 // it (load, read, write back twice as wide, read by the MMA), 750 cycles against
 // the MMA's 512; from TMEM the weights' second trip costs nothing there. TMEM
-// then holds two accumulators of 192 columns and four 64-deep slots of weights.
+// then holds two accumulators of 192 columns and two 128-deep slots of weights.
 // Warp 0 loads 128-deep int8 stages, warps 6..13 widen weights and 14..21
 // tokens, in two sets that take alternate stages so that one's latencies hide
 // behind the other's work; warp 1 issues the MMAs, warps 2..5 scale and store.
@@ -39,9 +39,9 @@ namespace ragged {
 namespace i8 {
 
 constexpr int BK = 128;   // depth of an int8 stage
-constexpr int HK = 64;    // depth of a widened slot: half a stage
-constexpr int SLOTS = 4;  // set s widens into slots 2 s and 2 s + 1
-constexpr int EPI_WARPS = 4, CVT_WARPS = 4, SETS = 2;  // CVT_WARPS: for the weights and for the tokens of a set
+constexpr int HK = 64;    // half of it: 128 bytes of f16
+constexpr int EPI_WARPS = 4, CVT_WARPS = 4;  // CVT_WARPS: for the weights and for the tokens of a set
+constexpr int SETS = 2;                      // each with a widened slot of its own
 constexpr int THREADS = 32 * (2 + EPI_WARPS + 2 * SETS * CVT_WARPS);
 
 template <int kCG>
@@ -53,18 +53,18 @@ struct Shape {
     static constexpr int kTok = kWide / kCG;         // token rows of a stage in one CTA
     static constexpr int kRaws = kCG == 2 ? 5 : 8;   // int8 stages
     static constexpr int kRaw = (kFM + kTok) * BK;   // weights, then tokens
-    static constexpr int kSlot = kTok * HK * 2;      // widened tokens
+    static constexpr int kHalf = kTok * HK * 2;      // widened tokens of half a slot
     static constexpr int kTmemA = 2 * kWide;         // the weights' slots follow the accumulators
     static constexpr int kTmem = kCG == 2 ? 512 : 256;
-    static constexpr int kRawAt = SLOTS * kSlot;
+    static constexpr int kRawAt = SETS * 2 * kHalf;
     static constexpr int kEpi = kRawAt + kRaws * kRaw;
     static constexpr int kBars = kEpi + kEpiBytes;
     static constexpr int kTables = kBars + 256;
     __host__ __device__ static constexpr int smem(int E) { return 1024 + kTables + 8 * (E + 1); }
     static_assert(1024 + kTables + 8 * (MXQ_MAX_EXPERTS + 1) <= 232448, "shared memory over the per-block limit");
-    static_assert(kBars % 8 == 0 && 8 * (2 * (kRaws + SLOTS) + 4) <= 256, "barrier region");
-    static_assert(kSlot % 1024 == 0 && kRaw % 1024 == 0, "the 128-byte swizzle repeats every 1024 bytes");
-    static_assert(kTmemA + SLOTS * HK / 2 <= kTmem, "TMEM columns");
+    static_assert(kBars % 8 == 0 && 8 * (2 * (kRaws + SETS) + 4) <= 256, "barrier region");
+    static_assert(kHalf % 1024 == 0 && kRaw % 1024 == 0, "the 128-byte swizzle repeats every 1024 bytes");
+    static_assert(kTmemA + SETS * BK / 2 <= kTmem, "TMEM columns");
 };
 
 struct Params {
@@ -110,8 +110,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
     const uint32_t rawf0 = smem_u32(bars), rawe0 = rawf0 + 8 * RAWS;
-    const uint32_t full0 = rawe0 + 8 * RAWS, empty0 = full0 + 8 * SLOTS;
-    const uint32_t accf0 = empty0 + 8 * SLOTS, acce0 = accf0 + 16;
+    const uint32_t full0 = rawe0 + 8 * RAWS, empty0 = full0 + 8 * SETS;
+    const uint32_t accf0 = empty0 + 8 * SETS, acce0 = accf0 + 16;
     volatile int* abort_flag = &s_abort;
     if (threadIdx.x == 0) {
         s_abort = 0;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(rawf0 + 8 * st, 1);
             mbar_init(rawe0 + 8 * st, 2 * CVT_WARPS);
         }
-        for (int st = 0; st < SLOTS; ++st) {
+        for (int st = 0; st < SETS; ++st) {
             mbar_init(full0 + 8 * st, kCG * 2 * CVT_WARPS);
             mbar_init(empty0 + 8 * st, 1);
         }
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------ MMA issuer (rank 0)
         if (rank == 0) {
             int set = 0, buf = 0;
-            uint32_t phases = 0, aphase = 0;  // phases: bit of a slot = its parity
+            uint32_t phase = 0, aphase = 0;
             const uint64_t bd0 = smem_desc(smem_u32(smem), 16, 1024);
             for (int64_t t = first; t < W.total; t += stride) {
                 const Tile T = W.get(t);
@@ -181,29 +181,25 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint32_t d = tmem + buf * S::kWide;
                 if (!mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag)) goto done_mma;
                 __syncwarp();
-                for (int r = 0; r < T.red; r += BK, set ^= 1) {
+                for (int r = 0; r < T.red; r += BK) {
+                    const uint32_t at = tmem + S::kTmemA + set * (BK / 2);
+                    const uint64_t bd = bd0 + (uint64_t)(set * (2 * S::kHalf / 16));
+                    if (!mbar_wait(full0 + 8 * set, phase, abort_flag)) goto done_mma;
+                    __syncwarp();
+                    fence_after();
+                    const int steps = T.red - r >= BK ? BK / 16 : (T.red - r + 15) / 16;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int left = T.red - r - h * HK;
-                        if (left <= 0) break;
-                        const int slot = 2 * set + h;
-                        const uint32_t at = tmem + S::kTmemA + slot * (HK / 2);
-                        const uint64_t bd = bd0 + (uint64_t)(slot * (S::kSlot / 16));
-                        if (!mbar_wait(full0 + 8 * slot, phases >> slot & 1, abort_flag)) goto done_mma;
-                        phases ^= 1u << slot;
-                        __syncwarp();
-                        fence_after();
-                        const int steps = left >= HK ? HK / 16 : (left + 15) / 16;
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < HK / 16; ++k)
-                                if (k < steps)
-                                    mma_f16_tmem<kCG>(d, at + 8 * k, bd + 2 * k, id, r > 0 || h > 0 || k > 0);
-                            mma_commit<kCG>(empty0 + 8 * slot);
-                            if (left <= HK) mma_commit<kCG>(accf0 + 8 * buf);
-                        }
-                        __syncwarp();
+                        for (int k = 0; k < BK / 16; ++k)
+                            if (k < steps)
+                                mma_f16_tmem<kCG>(d, at + 8 * k, bd + (k >> 2) * (S::kHalf / 16) + 2 * (k & 3), id,
+                                                  r > 0 || k > 0);
+                        mma_commit<kCG>(empty0 + 8 * set);
+                        if (r + BK >= T.red) mma_commit<kCG>(accf0 + 8 * buf);
                     }
+                    __syncwarp();
+                    set ^= 1;
+                    phase ^= set == 0;
                 }
                 buf ^= 1;
                 aphase ^= buf == 0;
@@ -280,22 +276,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool weights = cw < SETS * CVT_WARPS;
         const int set = cw / CVT_WARPS % SETS, q = warp & 3;
         const int ct = (int)threadIdx.x - 32 * (2 + EPI_WARPS + cw / CVT_WARPS * CVT_WARPS);
-        const uint32_t lead_full = kCG == 2 ? mapa(full0, 0) : full0;
+        const uint32_t lead_full = kCG == 2 ? mapa(full0 + 8 * set, 0) : 0;
+        const uint32_t slot_tmem = tmem + ((uint32_t)(32 * q) << 16) + S::kTmemA + set * (BK / 2);
+        uint8_t* slot = smem + set * 2 * S::kHalf;
         int raw = 0, turn = 0;
-        uint32_t rphase = 0, phases = 0;
+        uint32_t rphase = 0, phase = 0;
         for (int64_t t = first; t < W.total; t += stride) {
             const Tile T = W.get(t);
             for (int r = 0; r < T.red; r += BK) {
                 if (turn == set) {
                     if (!__all_sync(0xffffffffu, mbar_wait(rawf0 + 8 * raw, rphase, abort_flag))) goto done_convert;
                     const uint8_t* src = smem + S::kRawAt + raw * S::kRaw;
+                    // the first half is widened into registers before the slot is free
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (h * HK >= T.red - r) break;
-                        const int slot = 2 * set + h;
-                        if (!__all_sync(0xffffffffu, mbar_wait(empty0 + 8 * slot, phases >> slot & 1 ^ 1, abort_flag)))
-                            goto done_convert;
-                        phases ^= 1u << slot;
                         if (weights) {
                             // lane = feature: 64 codes of its 128-byte swizzled row (16-byte chunk ^= row mod 8)
                             const uint8_t* row = src + (32 * q + lane) * BK;
@@ -308,14 +302,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 v[8 * i] = a.x, v[8 * i + 1] = a.y, v[8 * i + 2] = b.x, v[8 * i + 3] = b.y;
                                 v[8 * i + 4] = c.x, v[8 * i + 5] = c.y, v[8 * i + 6] = d.x, v[8 * i + 7] = d.y;
                             }
-                            fence_after();  // the slot's last MMAs, seen through empty[slot], come before the writes
-                            tmem_st32(tmem + ((uint32_t)(32 * q) << 16) + S::kTmemA + slot * (HK / 2), v);
-                            tmem_wait_st();
-                            fence_before();
+                            if (h == 0) {
+                                const bool ok = mbar_wait(empty0 + 8 * set, phase ^ 1, abort_flag);
+                                if (!__all_sync(0xffffffffu, ok)) goto done_convert;
+                                fence_after();  // the slot's last MMAs come before the writes
+                            }
+                            tmem_st32(slot_tmem + h * (HK / 2), v);
                         } else {
                             // rows beyond the slice are widened too: what they hold is never stored
                             const uint8_t* tok = src + kFM * BK;
-                            uint8_t* dst = smem + slot * S::kSlot;
                             constexpr int kUnits = S::kTok * (HK / 16) / (32 * CVT_WARPS);  // 16-byte chunks a thread
                             uint4 w[kUnits];
 #pragma unroll
@@ -324,26 +319,35 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 w[u] = *reinterpret_cast<const uint4*>(tok + row * BK +
                                                                        (((4 * h + (ct & 3)) ^ (row & 7)) << 4));
                             }
+                            if (h == 0) {
+                                const bool ok = mbar_wait(empty0 + 8 * set, phase ^ 1, abort_flag);
+                                if (!__all_sync(0xffffffffu, ok)) goto done_convert;
+                            }
 #pragma unroll
                             for (int u = 0; u < kUnits; ++u) {
                                 const int row = (ct >> 2) + u * 8 * CVT_WARPS, ch = 2 * (ct & 3);
                                 const uint2 a = widen4(w[u].x), b = widen4(w[u].y), c = widen4(w[u].z),
                                             d = widen4(w[u].w);
-                                uint8_t* o = dst + row * 128;
+                                uint8_t* o = slot + h * S::kHalf + row * 128;
                                 *reinterpret_cast<uint4*>(o + ((ch ^ (row & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
                                 *reinterpret_cast<uint4*>(o + (((ch + 1) ^ (row & 7)) << 4)) =
                                     make_uint4(c.x, c.y, d.x, d.y);
                             }
-                            fence_async_smem();
-                        }
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (rank == 0) mbar_arrive(full0 + 8 * slot);
-                            else arrive_remote(lead_full + 8 * slot);
                         }
                     }
+                    if (weights) {
+                        tmem_wait_st();
+                        fence_before();
+                    } else {
+                        fence_async_smem();
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(rawe0 + 8 * raw);
+                    if (lane == 0) {
+                        mbar_arrive(rawe0 + 8 * raw);
+                        if (rank == 0) mbar_arrive(full0 + 8 * set);
+                        else arrive_remote(lead_full);
+                    }
+                    phase ^= 1;
                 }
                 turn ^= 1;
                 if (++raw == RAWS) { raw = 0; rphase ^= 1; }
