@@ -39,10 +39,41 @@ __device__ __forceinline__ uint4 philox(uint64_t block, uint64_t offset, uint64_
     }
     return make_uint4(c0, c1, c2, c3);
 }
-__device__ __forceinline__ bool kept(const uint4& w, int j, uint32_t t) {
-    const uint32_t x = j < 2 ? w.x : j < 4 ? w.y : j < 6 ? w.z : w.w;
-    return ((j & 1) ? x >> 16 : x & 0xFFFFu) >= t;
+// Which elements are kept, as a threshold on a word shifted to the top of 32
+// bits: half >= t is (half << 16) > ((t - 1) << 16 | 0xFFFF) whatever the low
+// bits hold, for t = 1 .. 65536; `all` stands for t = 0. One shift (low halves
+// only) and one comparison an element.
+struct Keep {
+    uint32_t above;
+    bool all;
+};
+__host__ __device__ __forceinline__ Keep keep_of(uint32_t t) {
+    return Keep{t ? ((t - 1) << 16 | 0xFFFFu) : 0u, t == 0};
 }
+__device__ __forceinline__ bool kept(const uint4& w, int j, const Keep& k) {
+    const uint32_t x = j < 2 ? w.x : j < 4 ? w.y : j < 6 ? w.z : w.w;
+    return ((j & 1) ? x : x << 16) > k.above || k.all;
+}
+
+// Position of a thread's 8-element vector in rows of `per` vectors, and its
+// advance by `step` vectors, without a division in the loop.
+struct Cursor {
+    int64_t i, m;
+    uint32_t f;
+    int64_t dm;
+    uint32_t df;
+    __device__ Cursor(int64_t start, int64_t step, uint32_t per)
+        : i(start), m(start / per), f((uint32_t)(start % per)), dm(step / per), df((uint32_t)(step % per)) {}
+    __device__ void advance(int64_t step, uint32_t per) {
+        i += step;
+        m += dm;
+        f += df;
+        if (f >= per) {
+            f -= per;
+            ++m;
+        }
+    }
+};
 
 struct Rng {
     uint64_t seed, offset;
@@ -69,42 +100,62 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// Bound by HBM: 6 bytes an element, against about 25 issued instructions with
+// the generator's ten rounds shared by eight elements (two lanes to an
+// instruction in the activation).
 __global__ void __launch_bounds__(256) swiglu_dropout_fwd_kernel(const uint16_t* y, int64_t M, int64_t F,
-                                                                 const int64_t* rng, uint32_t t, float scale,
+                                                                 const int64_t* rng, Keep k, float scale,
                                                                  uint16_t* h) {
+    const uint32_t per = (uint32_t)(F / 8);
+    const int64_t vecs = M * per, step = (int64_t)gridDim.x * blockDim.x;
+    Cursor c((int64_t)blockIdx.x * blockDim.x + threadIdx.x, step, per);
+    if (c.i >= vecs) return;
     const Rng r = load_rng(rng);
-    const int64_t per = F / 8, vecs = M * per;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < vecs; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t m = i / per, f = (i - m * per) * 8;
-        float g[8], u[8], o[8];
-        unpack8(*reinterpret_cast<const uint4*>(y + m * 2 * F + f), g);
-        unpack8(*reinterpret_cast<const uint4*>(y + m * 2 * F + F + f), u);
-        const uint4 w = philox((uint64_t)i, r.offset, r.seed);
+    for (; c.i < vecs; c.advance(step, per)) {
+        const uint4* row = reinterpret_cast<const uint4*>(y + c.m * 2 * F);
+        const uint4 gw = row[c.f], uw = row[c.f + per];
+        const uint4 w = philox((uint64_t)c.i, r.offset, r.seed);
+        const uint32_t gs[4] = {gw.x, gw.y, gw.z, gw.w}, us[4] = {uw.x, uw.y, uw.z, uw.w};
+        float o[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = kept(w, j, t) ? __fmul_rn(swiglu_h(g[j], u[j]), scale) : 0.0f;
-        *reinterpret_cast<uint4*>(h + i * 8) = pack8(o);
+        for (int j = 0; j < 4; ++j) {
+            const float2 v = swiglu_h_x2(make_float2(bf16lo(gs[j]), bf16hi(gs[j])), make_float2(bf16lo(us[j]), bf16hi(us[j])));
+            const float2 s = f2unpack(f2mul(f2pack(v.x, v.y), f2splat(scale)));
+            o[2 * j] = kept(w, 2 * j, k) ? s.x : 0.0f;
+            o[2 * j + 1] = kept(w, 2 * j + 1, k) ? s.y : 0.0f;
+        }
+        *reinterpret_cast<uint4*>(h + c.i * 8) = pack8(o);
     }
 }
 
 __global__ void __launch_bounds__(256) swiglu_dropout_bwd_kernel(const uint16_t* dh, const uint16_t* y, int64_t M,
-                                                                 int64_t F, const int64_t* rng, uint32_t t,
-                                                                 float scale, uint16_t* dy) {
+                                                                 int64_t F, const int64_t* rng, Keep k, float scale,
+                                                                 uint16_t* dy) {
+    const uint32_t per = (uint32_t)(F / 8);
+    const int64_t vecs = M * per, step = (int64_t)gridDim.x * blockDim.x;
+    Cursor c((int64_t)blockIdx.x * blockDim.x + threadIdx.x, step, per);
+    if (c.i >= vecs) return;
     const Rng r = load_rng(rng);
-    const int64_t per = F / 8, vecs = M * per;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < vecs; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t m = i / per, f = (i - m * per) * 8;
-        float d[8], g[8], u[8], dg[8], du[8];
-        unpack8(*reinterpret_cast<const uint4*>(dh + i * 8), d);
-        unpack8(*reinterpret_cast<const uint4*>(y + m * 2 * F + f), g);
-        unpack8(*reinterpret_cast<const uint4*>(y + m * 2 * F + F + f), u);
-        const uint4 w = philox((uint64_t)i, r.offset, r.seed);
+    for (; c.i < vecs; c.advance(step, per)) {
+        const uint4* row = reinterpret_cast<const uint4*>(y + c.m * 2 * F);
+        const uint4 gw = row[c.f], uw = row[c.f + per], dw = reinterpret_cast<const uint4*>(dh)[c.i];
+        const uint4 w = philox((uint64_t)c.i, r.offset, r.seed);
+        const uint32_t gs[4] = {gw.x, gw.y, gw.z, gw.w}, us[4] = {uw.x, uw.y, uw.z, uw.w}, ds[4] = {dw.x, dw.y, dw.z, dw.w};
+        float dg[8], du[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            swiglu_grads(__fmul_rn(d[j], scale), g[j], u[j], dg[j], du[j]);
-            if (!kept(w, j, t)) dg[j] = du[j] = 0.0f;
+        for (int j = 0; j < 4; ++j) {
+            float2 a, b;
+            swiglu_grads_x2(f2unpack(f2mul(f2pack(bf16lo(ds[j]), bf16hi(ds[j])), f2splat(scale))),
+                            make_float2(bf16lo(gs[j]), bf16hi(gs[j])), make_float2(bf16lo(us[j]), bf16hi(us[j])), a, b);
+            const bool k0 = kept(w, 2 * j, k), k1 = kept(w, 2 * j + 1, k);
+            dg[2 * j] = k0 ? a.x : 0.0f;
+            dg[2 * j + 1] = k1 ? a.y : 0.0f;
+            du[2 * j] = k0 ? b.x : 0.0f;
+            du[2 * j + 1] = k1 ? b.y : 0.0f;
         }
-        *reinterpret_cast<uint4*>(dy + m * 2 * F + f) = pack8(dg);
-        *reinterpret_cast<uint4*>(dy + m * 2 * F + F + f) = pack8(du);
+        uint4* out = reinterpret_cast<uint4*>(dy + c.m * 2 * F);
+        out[c.f] = pack8(dg);
+        out[c.f + per] = pack8(du);
     }
 }
 
@@ -131,7 +182,7 @@ __device__ __forceinline__ void from_f32(__nv_bfloat16* p, float v) { *p = __flo
 // out may be x or residual: a thread reads its elements before it writes them.
 template <typename T>
 __global__ void __launch_bounds__(256) dropout_kernel(const T* x, const T* residual, int64_t n, const int64_t* rng,
-                                                      uint32_t t, float scale, T* out) {
+                                                      Keep k, float scale, T* out) {
     const Rng r = load_rng(rng);
     const int64_t vecs = (n + 7) / 8;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < vecs; i += (int64_t)gridDim.x * blockDim.x) {
@@ -142,7 +193,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T* x, const T* resid
             if (residual) load8(residual + 8 * i, a);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[j] = kept(w, j, t) ? __fmul_rn(v[j], scale) : 0.0f;
+                v[j] = kept(w, j, k) ? __fmul_rn(v[j], scale) : 0.0f;
                 if (residual) v[j] = __fadd_rn(v[j], a[j]);
             }
             store8(out + 8 * i, v);
@@ -150,7 +201,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T* x, const T* resid
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (8 * i + j < n) {
-                    float v = kept(w, j, t) ? __fmul_rn(to_f32(x[8 * i + j]), scale) : 0.0f;
+                    float v = kept(w, j, k) ? __fmul_rn(to_f32(x[8 * i + j]), scale) : 0.0f;
                     if (residual) v = __fadd_rn(v, to_f32(residual[8 * i + j]));
                     from_f32(out + 8 * i + j, v);
                 }
@@ -166,15 +217,15 @@ static float scale_of(uint32_t t) { return t >= 65536u ? 0.0f : (float)(65536.0 
 cudaError_t run_swiglu_dropout_fwd(const void* y, int64_t M, int64_t F, const int64_t* rng, uint32_t t, void* h,
                                    cudaStream_t s) {
     if (M == 0) return cudaSuccess;
-    swiglu_dropout_fwd_kernel<<<grid_for(M * (F / 8)), 256, 0, s>>>((const uint16_t*)y, M, F, rng, t, scale_of(t),
-                                                                    (uint16_t*)h);
+    swiglu_dropout_fwd_kernel<<<grid_for(M * (F / 8)), 256, 0, s>>>((const uint16_t*)y, M, F, rng, keep_of(t),
+                                                                    scale_of(t), (uint16_t*)h);
     return cudaGetLastError();
 }
 cudaError_t run_swiglu_dropout_bwd(const void* dh, const void* y, int64_t M, int64_t F, const int64_t* rng, uint32_t t,
                                    void* dy, cudaStream_t s) {
     if (M == 0) return cudaSuccess;
     swiglu_dropout_bwd_kernel<<<grid_for(M * (F / 8)), 256, 0, s>>>((const uint16_t*)dh, (const uint16_t*)y, M, F, rng,
-                                                                    t, scale_of(t), (uint16_t*)dy);
+                                                                    keep_of(t), scale_of(t), (uint16_t*)dy);
     return cudaGetLastError();
 }
 cudaError_t run_dropout(const void* x, const void* residual, int64_t n, int f32, const int64_t* rng, uint32_t t,
@@ -182,11 +233,11 @@ cudaError_t run_dropout(const void* x, const void* residual, int64_t n, int f32,
     if (n == 0) return cudaSuccess;
     const unsigned grid = grid_for((n + 7) / 8);
     if (f32)
-        dropout_kernel<float><<<grid, 256, 0, s>>>((const float*)x, (const float*)residual, n, rng, t, scale_of(t),
+        dropout_kernel<float><<<grid, 256, 0, s>>>((const float*)x, (const float*)residual, n, rng, keep_of(t), scale_of(t),
                                                    (float*)out);
     else
         dropout_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>((const __nv_bfloat16*)x, (const __nv_bfloat16*)residual, n,
-                                                           rng, t, scale_of(t), (__nv_bfloat16*)out);
+                                                           rng, keep_of(t), scale_of(t), (__nv_bfloat16*)out);
     return cudaGetLastError();
 }
 

@@ -120,7 +120,7 @@ int mxq_swiglu_dropout_fwd(const void* y_bf16, int64_t M, int64_t F, const int64
                            mxq_stream_t stream) {
     if (M != 0 && (!y_bf16 || !h_bf16)) return MXQ_ERR_NULL;
     if (int r = check_dropout(M, F, d_rng, p)) return r;
-    if (F <= 0 || F % 8) return MXQ_ERR_SHAPE;
+    if (F <= 0 || F % 8 || F > ((int64_t)1 << 31)) return MXQ_ERR_SHAPE;
     if (!aligned16(y_bf16) || !aligned16(h_bf16)) return MXQ_ERR_ALIGN;
     const cudaError_t e = mxq::ragged::run_swiglu_dropout_fwd(y_bf16, M, F, d_rng, (uint32_t)dropped(p), h_bf16,
                                                               (cudaStream_t)stream);
@@ -131,7 +131,7 @@ int mxq_swiglu_dropout_bwd(const void* dh_bf16, const void* y_bf16, int64_t M, i
                            double p, void* dy_bf16, mxq_stream_t stream) {
     if (M != 0 && (!dh_bf16 || !y_bf16 || !dy_bf16)) return MXQ_ERR_NULL;
     if (int r = check_dropout(M, F, d_rng, p)) return r;
-    if (F <= 0 || F % 8) return MXQ_ERR_SHAPE;
+    if (F <= 0 || F % 8 || F > ((int64_t)1 << 31)) return MXQ_ERR_SHAPE;
     if (!aligned16(dh_bf16) || !aligned16(y_bf16) || !aligned16(dy_bf16)) return MXQ_ERR_ALIGN;
     const cudaError_t e = mxq::ragged::run_swiglu_dropout_bwd(dh_bf16, y_bf16, M, F, d_rng, (uint32_t)dropped(p),
                                                               dy_bf16, (cudaStream_t)stream);

@@ -663,9 +663,22 @@ def swiglu_bwd_quantize(dh, y, m_splits, rowwise=True, colwise=True, swizzle=Tru
 # ------------------------------------------------ ragged bf16 and int8 products, dropout
 _I8 = (torch.int8,)
 _I64T = (torch.int64,)
+_BF16_F32 = _BF16 + _F32
 
 
-def _rows_ptr(t, name, dtypes):
+def _dev(t, name, nbytes, dtypes):
+    """_need and _ptr in one: the pointer of a tensor that may be passed, checked in one expression
+    (these calls can be as short as a small kernel), or the error that says what is wrong with it."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_cuda and t.is_contiguous()
+            and t.nbytes >= nbytes):
+        return t.data_ptr()
+    _need(t, name, nbytes, dtypes)
+    return _ptr(t)
+
+
+def _rows(t, name, dtypes):
     """Pointer and row stride of a 2-D CUDA tensor whose rows are contiguous (the tensor may be a
     slice of wider rows). The stride of a tensor with fewer than two rows is never used."""
     if not isinstance(t, torch.Tensor):
@@ -674,102 +687,99 @@ def _rows_ptr(t, name, dtypes):
         raise MXQError(f"{name}: tensor arguments must be CUDA tensors")
     if t.dtype not in dtypes:
         raise MXQError(f"{name}: dtype {t.dtype}, expected one of {[str(d) for d in dtypes]}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise MXQError(f"{name}: expected a 2-D tensor with contiguous rows")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.dim() != 2:
+        raise MXQError(f"{name}: expected a 2-D tensor")
+    rows, cols = t.shape
+    stride, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise MXQError(f"{name}: expected contiguous rows")
+    return t.data_ptr(), rows, cols, stride if rows > 1 else cols
 
 
 def _shape(t, name, want):
-    if tuple(t.shape) != tuple(want):
-        raise MXQError(f"{name}: shape {tuple(t.shape)}, expected {tuple(want)}")
+    if t.shape != want:
+        raise MXQError(f"{name}: shape {tuple(t.shape)}, expected {want}")
 
 
-def _out_flag(out, out_dtype, shape, dev, default, other, flag):
-    """The output tensor of a product and the flag for its element type."""
+def _out(out, out_dtype, shape, like, default, other, flag):
+    """The output tensor of a product, its pointer and the flag for its element type."""
     if out is None:
         dt = default if out_dtype is None else out_dtype
-        if dt not in (default, other):
+        if dt is not default and dt is not other:
             raise MXQError(f"out_dtype: {dt}, expected {default} or {other}")
-        out = torch.empty(shape, dtype=dt, device=dev)
-    else:
-        if out_dtype is not None and out.dtype != out_dtype:
-            raise MXQError(f"out: dtype {out.dtype}, out_dtype is {out_dtype}")
-        _shape(out, "out", shape)
-        _need(out, "out", 0, (default, other))
-    return out, (flag if out.dtype == other else 0)
+        out = like.new_empty(shape, dtype=dt)
+        return out, out.data_ptr(), flag if dt is other else 0
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise MXQError(f"out: dtype {out.dtype}, out_dtype is {out_dtype}")
+    _shape(out, "out", shape)
+    return out, _dev(out, "out", 0, (default, other)), flag if out.dtype is other else 0
 
 
 def _grouping(m_splits, E):
-    m_splits = _splits(m_splits)
-    if m_splits is None:
+    """Pointer of the E device-resident counts."""
+    p = _dev(_splits(m_splits), "m_splits", 0, _I64T)
+    if p is None:
         raise MXQError("m_splits is required")
     if m_splits.numel() != E:
         raise MXQError(f"m_splits: {m_splits.numel()} counts for {E} experts")
-    return _ptr(m_splits)
+    return p
 
 
 def ragged_gemm_fprop(x, w, m_splits, bias=None, out_dtype=None, status=None, out=None):
     """Y = X W_e^T (+ b_e) on bf16, any expert counts. x (M, K), its rows possibly a slice of wider
     ones; w (E, N, K); bias (E, N); Y (M, N) in bf16 (default) or fp32."""
-    xp, ldx = _rows_ptr(x, "x", _BF16)
-    M, K = x.shape
+    xp, M, K, ldx = _rows(x, "x", _BF16)
     E, N, Kw = w.shape
     _shape(w, "w", (E, N, K))
-    _need(w, "w", E * N * K * 2, _BF16)
-    _need(bias, "bias", E * N * 2, _BF16)
-    _need_flags(None, status)
-    out, flag = _out_flag(out, out_dtype, (M, N), x.device, torch.bfloat16, torch.float32, OUT_F32)
-    rc = lib().mxq_ragged_gemm_fprop(xp, ldx, _ptr(w), _ptr(bias), M, N, K, E, _grouping(m_splits, E), flag,
-                                     _ptr(out), _ptr(status), _stream())
-    _check(rc, "mxq_ragged_gemm_fprop")
+    out, op, flag = _out(out, out_dtype, (M, N), x, torch.bfloat16, torch.float32, OUT_F32)
+    rc = lib().mxq_ragged_gemm_fprop(xp, ldx, _dev(w, "w", 0, _BF16), _dev(bias, "bias", E * N * 2, _BF16), M, N, K, E,
+                                     _grouping(m_splits, E), flag, op, _dev(status, "status", 4, _I32), _stream())
+    if rc:
+        _check(rc, "mxq_ragged_gemm_fprop")
     return out
 
 
 def ragged_gemm_dgrad(dy, w, m_splits, out_dtype=None, status=None, out=None):
     """dX = dY W_e on bf16, any expert counts. dy (M, N), w (E, N, K); dX (M, K) in bf16 (default) or fp32."""
-    dyp, lddy = _rows_ptr(dy, "dy", _BF16)
-    M, N = dy.shape
+    dyp, M, N, lddy = _rows(dy, "dy", _BF16)
     E, Nw, K = w.shape
     _shape(w, "w", (E, N, K))
-    _need(w, "w", E * N * K * 2, _BF16)
-    _need_flags(None, status)
-    out, flag = _out_flag(out, out_dtype, (M, K), dy.device, torch.bfloat16, torch.float32, OUT_F32)
-    rc = lib().mxq_ragged_gemm_dgrad(dyp, lddy, _ptr(w), M, N, K, E, _grouping(m_splits, E), flag, _ptr(out),
-                                     _ptr(status), _stream())
-    _check(rc, "mxq_ragged_gemm_dgrad")
+    out, op, flag = _out(out, out_dtype, (M, K), dy, torch.bfloat16, torch.float32, OUT_F32)
+    rc = lib().mxq_ragged_gemm_dgrad(dyp, lddy, _dev(w, "w", 0, _BF16), M, N, K, E, _grouping(m_splits, E), flag, op,
+                                     _dev(status, "status", 4, _I32), _stream())
+    if rc:
+        _check(rc, "mxq_ragged_gemm_dgrad")
     return out
 
 
 def ragged_gemm_wgrad(dy, x, m_splits, accumulate=False, out_dtype=None, status=None, out=None):
     """dW_e = dY_e^T X_e on bf16, any expert counts. dy (M, N), x (M, K); dW (E, N, K) in fp32 (default)
     or bf16, added to `out` with accumulate."""
-    dyp, lddy = _rows_ptr(dy, "dy", _BF16)
-    xp, ldx = _rows_ptr(x, "x", _BF16)
-    M, N = dy.shape
-    K = x.shape[1]
+    dyp, M, N, lddy = _rows(dy, "dy", _BF16)
+    xp, Mx, K, ldx = _rows(x, "x", _BF16)
     _shape(x, "x", (M, K))
     if accumulate and out is None:
         raise MXQError("accumulate needs out")
     if _splits(m_splits) is None:
         raise MXQError("m_splits is required")
     E = m_splits.numel()
-    _need_flags(None, status)
-    out, flag = _out_flag(out, out_dtype, (E, N, K), dy.device, torch.float32, torch.bfloat16, OUT_BF16)
+    out, op, flag = _out(out, out_dtype, (E, N, K), dy, torch.float32, torch.bfloat16, OUT_BF16)
     rc = lib().mxq_ragged_gemm_wgrad(dyp, lddy, xp, ldx, M, N, K, E, _grouping(m_splits, E),
-                                     flag | (ACCUMULATE if accumulate else 0), _ptr(out), _ptr(status), _stream())
-    _check(rc, "mxq_ragged_gemm_wgrad")
+                                     flag | ACCUMULATE if accumulate else flag, op, _dev(status, "status", 4, _I32),
+                                     _stream())
+    if rc:
+        _check(rc, "mxq_ragged_gemm_wgrad")
     return out
 
 
 def int8_quantize_rows(x, out=None):
     """bf16 rows (M, K) -> (int8 codes (M, K), fp32 scales (M,)), x ~ q * scale."""
-    xp, ldx = _rows_ptr(x, "x", _BF16)
-    M, K = x.shape
-    q, scale = out if out is not None else (torch.empty((M, K), dtype=torch.int8, device=x.device),
-                                            torch.empty((M,), dtype=torch.float32, device=x.device))
-    _need(q, "q", M * K, _I8)
-    _need(scale, "scale", M * 4, _F32)
-    _check(lib().mxq_int8_quantize_rows(xp, ldx, M, K, _ptr(q), _ptr(scale), _stream()), "mxq_int8_quantize_rows")
+    xp, M, K, ldx = _rows(x, "x", _BF16)
+    q, scale = out if out is not None else (x.new_empty((M, K), dtype=torch.int8), x.new_empty(M, dtype=torch.float32))
+    rc = lib().mxq_int8_quantize_rows(xp, ldx, M, K, _dev(q, "q", M * K, _I8), _dev(scale, "scale", M * 4, _F32),
+                                      _stream())
+    if rc:
+        _check(rc, "mxq_int8_quantize_rows")
     return q, scale
 
 
@@ -779,52 +789,50 @@ def int8_gemm_fprop(xq, x_scale, wq, w_scale, m_splits, bias=None, out_dtype=Non
     M, K = xq.shape
     E, N, Kw = wq.shape
     _shape(wq, "wq", (E, N, K))
-    _need(xq, "xq", M * K, _I8)
-    _need(x_scale, "x_scale", M * 4, _F32)
-    _need(wq, "wq", E * N * K, _I8)
-    _need(w_scale, "w_scale", E * N * 4, _F32)
-    _need(bias, "bias", E * N * 2, _BF16)
-    _need_flags(None, status)
-    out, flag = _out_flag(out, out_dtype, (M, N), xq.device, torch.bfloat16, torch.float32, OUT_F32)
-    rc = lib().mxq_int8_gemm_fprop(_ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(bias), M, N, K, E,
-                                   _grouping(m_splits, E), flag, _ptr(out), _ptr(status), _stream())
-    _check(rc, "mxq_int8_gemm_fprop")
+    out, op, flag = _out(out, out_dtype, (M, N), xq, torch.bfloat16, torch.float32, OUT_F32)
+    rc = lib().mxq_int8_gemm_fprop(_dev(xq, "xq", 0, _I8), _dev(x_scale, "x_scale", M * 4, _F32),
+                                   _dev(wq, "wq", 0, _I8), _dev(w_scale, "w_scale", E * N * 4, _F32),
+                                   _dev(bias, "bias", E * N * 2, _BF16), M, N, K, E, _grouping(m_splits, E), flag, op,
+                                   _dev(status, "status", 4, _I32), _stream())
+    if rc:
+        _check(rc, "mxq_int8_gemm_fprop")
     return out
 
 
 def swiglu_dropout_fwd(y, rng, p, out=None):
     """h = D(silu(g) * u) of FC1's output y = [g | u] (M, 2F). rng: CUDA int64 {seed, offset}."""
     M, F2 = y.shape
-    out = out if out is not None else torch.empty((M, F2 // 2), dtype=torch.bfloat16, device=y.device)
-    _need(y, "y", M * F2 * 2, _BF16)
-    _need(rng, "rng", 16, _I64T)
-    _need(out, "out", M * (F2 // 2) * 2, _BF16)
-    _check(lib().mxq_swiglu_dropout_fwd(_ptr(y), M, F2 // 2, _ptr(rng), p, _ptr(out), _stream()),
-           "mxq_swiglu_dropout_fwd")
+    F = F2 // 2
+    if out is None:
+        out = y.new_empty((M, F), dtype=torch.bfloat16)
+    rc = lib().mxq_swiglu_dropout_fwd(_dev(y, "y", 0, _BF16), M, F, _dev(rng, "rng", 16, _I64T), p,
+                                      _dev(out, "out", M * F * 2, _BF16), _stream())
+    if rc:
+        _check(rc, "mxq_swiglu_dropout_fwd")
     return out
 
 
 def swiglu_dropout_bwd(dh, y, rng, p, out=None):
     """The gradient [dg | du] (M, 2F) of y from dh (M, F); rng and p those of the forward call."""
     M, F2 = y.shape
-    out = out if out is not None else torch.empty((M, F2), dtype=torch.bfloat16, device=y.device)
-    _need(dh, "dh", M * (F2 // 2) * 2, _BF16)
-    _need(y, "y", M * F2 * 2, _BF16)
-    _need(rng, "rng", 16, _I64T)
-    _need(out, "out", M * F2 * 2, _BF16)
-    _check(lib().mxq_swiglu_dropout_bwd(_ptr(dh), _ptr(y), M, F2 // 2, _ptr(rng), p, _ptr(out), _stream()),
-           "mxq_swiglu_dropout_bwd")
+    F = F2 // 2
+    if out is None:
+        out = y.new_empty((M, F2), dtype=torch.bfloat16)
+    rc = lib().mxq_swiglu_dropout_bwd(_dev(dh, "dh", M * F * 2, _BF16), _dev(y, "y", 0, _BF16), M, F,
+                                      _dev(rng, "rng", 16, _I64T), p, _dev(out, "out", M * F2 * 2, _BF16), _stream())
+    if rc:
+        _check(rc, "mxq_swiglu_dropout_bwd")
     return out
 
 
 def dropout(x, rng, p, residual=None, out=None):
     """D(x) (+ residual), bf16 or fp32; its own gradient when residual is None. out may be x or residual."""
-    _need(x, "x", 0, _BF16 + _F32)
-    out = out if out is not None else torch.empty_like(x)
-    n, size = x.numel(), x.element_size()
-    _need(residual, "residual", n * size, (x.dtype,))
-    _need(rng, "rng", 16, _I64T)
-    _need(out, "out", n * size, (x.dtype,))
-    _check(lib().mxq_dropout(_ptr(x), _ptr(residual), n, _ptr(rng), p, OUT_F32 if x.dtype == torch.float32 else 0,
-                             _ptr(out), _stream()), "mxq_dropout")
+    xp = _dev(x, "x", 0, _BF16_F32)
+    if out is None:
+        out = torch.empty_like(x)
+    size, same = x.nbytes, (x.dtype,)
+    rc = lib().mxq_dropout(xp, _dev(residual, "residual", size, same), x.numel(), _dev(rng, "rng", 16, _I64T), p,
+                           OUT_F32 if x.dtype is torch.float32 else 0, _dev(out, "out", size, same), _stream())
+    if rc:
+        _check(rc, "mxq_dropout")
     return out
