@@ -153,10 +153,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     // of a stage therefore follow their own uses, not the ring's laps.
     auto ragged_end = [](const Tile& T, int r) { return kMode == kWgrad && T.red - r < BK && ((T.red - r) & 15) != 0; };
     auto zero_rows = [&](const Tile& T, int r, int stage) {
-        const int left = T.red - r, per = (16 - (left & 15)) * 8, boxes = 2 + (T.n / kCG + 63) / 64;
-        uint8_t* s = smem + stage * S::kStage + left * 128;
-        for (int i = lane; i < per * boxes; i += 32)
-            *reinterpret_cast<uint4*>(s + i / per * 8192 + i % per * 16) = make_uint4(0u, 0u, 0u, 0u);
+        // a 16-byte chunk a lane, four rows at a time, box by box
+        const int left = (T.red - r) & 15, boxes = 2 + (T.n / kCG + 63) / 64;
+        uint8_t* s = smem + stage * S::kStage + (T.red - r + (lane >> 3)) * 128 + (lane & 7) * 16;
+        for (int i = 0; i < boxes; ++i)
+            for (int row = left + (lane >> 3), at = i * 8192; row < 16; row += 4, at += 512)
+                *reinterpret_cast<uint4*>(s + at) = make_uint4(0u, 0u, 0u, 0u);
         fence_async_smem();
         __syncwarp();
     };
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const uint64_t ad = ad0 + (uint64_t)(stage * (S::kStage / 16));
                         const uint64_t bd = bd0 + (uint64_t)(stage * (S::kStage / 16));
                         if (ragged_end(T, r)) {
-                            if (!mbar_wait_pair<kCG>(fix0 + 8 * stage, fix_uses >> stage & 1, abort_flag)) goto done_mma;
+                            if (!mbar_wait(fix0 + 8 * stage, fix_uses >> stage & 1, abort_flag)) goto done_mma;
                             fix_uses ^= 1u << stage;
                         } else {
                             if (!mbar_wait(full0 + 8 * stage, full_uses >> stage & 1, abort_flag)) goto done_mma;
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     zero_rows(T, last * BK, at);
                     if (lane == 0) {
                         if (rank == 0) mbar_arrive(fix0 + 8 * at);
-                        else arrive_remote_release(mapa(fix0 + 8 * at, 0));
+                        else arrive_remote(mapa(fix0 + 8 * at, 0));
                     }
                 }
                 stage = (at + 1) % STAGES;

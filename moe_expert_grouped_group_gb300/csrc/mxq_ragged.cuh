@@ -162,10 +162,6 @@ __device__ __forceinline__ uint32_t mapa(uint32_t a, uint32_t rank) {
 __device__ __forceinline__ void arrive_remote_relaxed(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-// Remote arrive that hands this thread's earlier writes to the waiter.
-__device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
 // Remote arrive after this thread's (warp's) writes to its own CTA's shared memory or TMEM, made visible to
 // the tensor core by fence.proxy.async or tcgen05.wait::st: a pair's MMA reads them through this SM, no
 // thread of the other CTA does, so the arrive has to follow them here and needs no cluster-wide release,
@@ -173,35 +169,6 @@ __device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar) {
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-// mbar_wait that also acquires what threads of the pair's other CTA released with their arrivals.
-__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-template <int kCG>
-__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-    if constexpr (kCG == 1) return mbar_wait(bar, parity, abort_flag);
-    if (mbar_try_cluster(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    for (uint32_t i = 0;; ++i) {
-        if (mbar_try_cluster(bar, parity)) return true;
-        if ((i & 63) == 63) {
-            if (*abort_flag) return false;
-            if (globaltimer() - t0 > kWaitNs) {
-                *abort_flag = 1;
-                return false;
-            }
-        }
-    }
-}
-
 // Barrier `id` of `threads` threads; true in all of them when `v` is true in any.
 __device__ __forceinline__ bool group_any(int id, int threads, bool v) {
     uint32_t r;
