@@ -9,7 +9,7 @@
 // MMA's M (TMEM lanes), its rows on the MMA's N (accumulator columns): W and
 // the tokens in fprop and dgrad, X and dY in wgrad. N is a field of the
 // instruction descriptor that may differ from tile to tile, so a slice of an
-// expert's rows costs MMA work in steps of 32 rows (16 on one SM), not 128.
+// expert's rows costs MMA work in steps of 32 rows, not 128.
 //
 // Majorness. X and dY of fprop / dgrad and W of fprop are K-major; W of dgrad
 // and both operands of wgrad are MN-major. All are staged as 128-byte-wide
@@ -28,12 +28,10 @@
 // matrix product 3.9e-7). Outputs that are not rounded to bf16 are therefore
 // summed in registers, one accumulator of FLUSH stages at a time (kRegs).
 //
-// Two shapes of the one kernel. Pairs of SMs (kCG = 2) share a tile of 256
-// features by up to 256 rows, each staging half of both operands: 32 KB a
-// stage and SM for the MMA work that costs one SM alone 48 KB. One SM
-// (kCG = 1) takes 128 features by up to 32 rows: what is left of the product
-// when experts have few rows is reading W, and its stages are small enough to
-// keep nine in flight.
+// A pair of SMs (a cluster of two CTAs, cta_group::2) shares a tile of 256
+// features by up to 256 rows, each staging half of both operands: 32 KB a stage
+// and SM for the MMA work that costs one SM alone 48 KB. Experts with few rows
+// go to mxq_ragged_few.cu.
 //
 // Persistent and warp-specialised: warp 0 issues TMA loads into a ring of
 // 64-deep stages, warp 1 owns TMEM and issues the MMAs (rank 0 of a pair),
@@ -59,22 +57,19 @@ constexpr int FLUSH = 8;  // stages an accumulator holds before it is added to t
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 96 + 32 * EPI_WARPS;
 
-template <int kCG>
-struct Shape {
-    static constexpr int kFeat = kFM * kCG;                   // features of a tile
-    static constexpr int kWide = kCG == 2 ? 256 : 32;         // widest MMA N
-    static constexpr int kStep = 16 * kCG;                    // its granularity
-    static constexpr int kBox = kCG == 2 ? 64 : 32;           // token rows of a K-major box
-    static constexpr int kStages = kCG == 2 ? 6 : 9;
-    static constexpr int kA = kFM * BK * 2, kStage = kA + kWide / kCG * BK * 2;
-    static constexpr int kTmem = 2 * kWide;
-    static constexpr int kEpi = kStages * kStage;             // staging of the bf16 epilogue, two groups
-    static constexpr int kBars = kEpi + 2 * kEpiBytes;
-    static constexpr int kTables = kBars + 512;
-    __host__ __device__ static constexpr int smem(int E) { return 1024 + kTables + 12 * (E + 1); }
-    static_assert(1024 + kTables + 12 * (MXQ_MAX_EXPERTS + 1) <= 232448, "shared memory over the per-block limit");
-    static_assert(kBars % 8 == 0 && 8 * (4 * kStages + 4) <= 512, "barrier region");
-};
+constexpr int CG = 2;                         // CTAs, and SMs, of a tile
+constexpr int FEAT = kFM * CG;                // features of a tile
+constexpr int WIDE = 256, STEP = 16 * CG;     // widest MMA N and its granularity
+constexpr int BOX = 64;                       // token rows of a K-major box
+constexpr int STAGES = 6;
+constexpr int A_BYTES = kFM * BK * 2, STAGE_BYTES = A_BYTES + WIDE / CG * BK * 2;
+constexpr int TMEM_COLS = 2 * WIDE;
+constexpr int EPI_REGION = STAGES * STAGE_BYTES;  // staging of the bf16 epilogue, two groups
+constexpr int BAR_REGION = EPI_REGION + 2 * kEpiBytes;
+constexpr int TABLE_REGION = BAR_REGION + 256;
+__host__ __device__ constexpr int smem_bytes(int E) { return 1024 + TABLE_REGION + 12 * (E + 1); }
+static_assert(smem_bytes(MXQ_MAX_EXPERTS) <= 232448, "shared memory over the per-block limit");
+static_assert(BAR_REGION % 8 == 0 && 8 * (4 * STAGES + 4) <= 256, "barrier region");
 
 struct Params {
     int64_t M, N, K;
@@ -86,23 +81,21 @@ struct Params {
     int32_t* status;
 };
 
-template <int kMode, int kCG, bool kRegs>
+template <int kMode, bool kRegs>
 __global__ void __launch_bounds__(THREADS, 1)
     ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Params p) {
-    using S = Shape<kCG>;
-    constexpr int STAGES = S::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align<1024>(smem_raw);
-    int32_t* s_off = reinterpret_cast<int32_t*>(smem + S::kTables);
+    int32_t* s_off = reinterpret_cast<int32_t*>(smem + TABLE_REGION);
     int32_t* s_slices = s_off + p.E + 1;
     int32_t* s_order = s_slices + p.E + 1;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = kCG == 2 ? cta_rank() : 0;
+    const uint32_t rank = cta_rank();
 
     // both CTAs of a pair find the same fault and stop before any cluster-wide step
-    const int bad = load_ragged(p.m_splits, p.E, p.M, S::kWide, s_off, s_slices);
+    const int bad = load_ragged(p.m_splits, p.E, p.M, WIDE, s_off, s_slices);
     if (bad) {
         report_status(p.status, bad);
         return;
@@ -118,7 +111,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             s_order[before] = e;
         }
     }
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_REGION);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, tail0 = empty0 + 8 * STAGES;
     const uint32_t fix0 = tail0 + 8 * STAGES, accf0 = fix0 + 8 * STAGES, acce0 = accf0 + 16;
     volatile int* abort_flag = &s_abort;
@@ -128,24 +121,24 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(full0 + 8 * st, 1);
             mbar_init(empty0 + 8 * st, 1);
             mbar_init(tail0 + 8 * st, 1);
-            mbar_init(fix0 + 8 * st, kCG);
+            mbar_init(fix0 + 8 * st, CG);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf0 + 8 * b, 1);
-            mbar_init(acce0 + 8 * b, kCG * EPI_WARPS);
+            mbar_init(acce0 + 8 * b, CG * EPI_WARPS);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmA) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmB) : "memory");
     }
-    if (warp == 1) tmem_alloc<kCG>(smem_u32(&s_tmem), S::kTmem);
+    if (warp == 1) tmem_alloc<CG>(smem_u32(&s_tmem), TMEM_COLS);
     fence_before();
     __syncthreads();
-    if (kCG == 2) cluster_sync();  // both CTAs' barriers exist before any load completes on rank 0's
+    cluster_sync();  // both CTAs' barriers exist before any load completes on rank 0's
     fence_after();
     const uint32_t tmem = s_tmem;
-    const Walk<kMode, S::kFeat, S::kWide, S::kStep> W(p.N, p.K, p.E, s_off, s_slices, s_order);
-    const int64_t first = blockIdx.x / kCG, stride = gridDim.x / kCG;
+    const Walk<kMode, FEAT, WIDE, STEP> W(p.N, p.K, p.E, s_off, s_slices, s_order);
+    const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
     constexpr bool a_mn = kMode != kFprop, b_mn = kMode == kWgrad;
     // An expert's last block of rows in wgrad, when it ends inside a step of 16: its loads complete on each
     // CTA's own tail[st], warp 10 of both CTAs zeroes the rows up to the next multiple of 16 and arrives on
@@ -154,8 +147,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto ragged_end = [](const Tile& T, int r) { return kMode == kWgrad && T.red - r < BK && ((T.red - r) & 15) != 0; };
     auto zero_rows = [&](const Tile& T, int r, int stage) {
         // a 16-byte chunk a lane, four rows at a time, box by box
-        const int left = (T.red - r) & 15, boxes = 2 + (T.n / kCG + 63) / 64;
-        uint8_t* s = smem + stage * S::kStage + (T.red - r + (lane >> 3)) * 128 + (lane & 7) * 16;
+        const int left = (T.red - r) & 15, boxes = 2 + (T.n / CG + 63) / 64;
+        uint8_t* s = smem + stage * STAGE_BYTES + (T.red - r + (lane >> 3)) * 128 + (lane & 7) * 16;
         for (int i = 0; i < boxes; ++i)
             for (int row = left + (lane >> 3), at = i * 8192; row < 16; row += 4, at += 512)
                 *reinterpret_cast<uint4*>(s + at) = make_uint4(0u, 0u, 0u, 0u);
@@ -170,10 +163,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t used = 0, full_uses = 0, tail_uses = 0, tail_last = 0;  // bits of stages
         for (int64_t t = first; t < W.total; t += stride) {
             const Tile T = W.get(t);
-            const int half = T.n / kCG;  // this CTA's columns of the tile: [rank * half, + half)
-            const int boxes = (half + S::kBox - 1) / S::kBox;
+            const int half = T.n / CG;  // this CTA's columns of the tile: [rank * half, + half)
+            const int boxes = (half + BOX - 1) / BOX;
             const int f = T.f0 + rank * kFM, c = T.c0 + rank * half;
-            const uint32_t bytes = S::kA + boxes * S::kBox * BK * 2;
+            const uint32_t bytes = A_BYTES + boxes * BOX * BK * 2;
             for (int r = 0; r < T.red; r += BK) {
                 if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag)) {
                     // a bounded wait expired: no copy may be in flight when the block ends
@@ -189,26 +182,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 const bool tail = ragged_end(T, r);
                 const uint32_t own = (tail ? tail0 : full0) + 8 * stage, bit = 1u << stage;
-                const uint32_t fb = kCG == 2 ? mapa(own, tail ? rank : 0) : own;
-                const uint32_t a = smem_u32(smem) + stage * S::kStage, b = a + S::kA;
+                const uint32_t fb = mapa(own, tail ? rank : 0);
+                const uint32_t a = smem_u32(smem) + stage * STAGE_BYTES, b = a + A_BYTES;
                 if (elect_one()) {
                     if (tail) mbar_expect_tx(own, bytes);
-                    else if (rank == 0) mbar_expect_tx(own, kCG * bytes);
+                    else if (rank == 0) mbar_expect_tx(own, CG * bytes);
                     if (kMode == kFprop) {
-                        load_3d<kCG>(a, &tmA, fb, r, f, T.e);
+                        load_3d<CG>(a, &tmA, fb, r, f, T.e);
                     } else if (kMode == kDgrad) {
-                        load_3d<kCG>(a, &tmA, fb, f, r, T.e);
-                        load_3d<kCG>(a + 8192, &tmA, fb, f + 64, r, T.e);
+                        load_3d<CG>(a, &tmA, fb, f, r, T.e);
+                        load_3d<CG>(a + 8192, &tmA, fb, f + 64, r, T.e);
                     } else {
-                        load_2d<kCG>(a, &tmA, fb, f, T.red0 + r);
-                        load_2d<kCG>(a + 8192, &tmA, fb, f + 64, T.red0 + r);
+                        load_2d<CG>(a, &tmA, fb, f, T.red0 + r);
+                        load_2d<CG>(a + 8192, &tmA, fb, f + 64, T.red0 + r);
                     }
 #pragma unroll
-                    for (int i = 0; i < S::kWide / kCG / S::kBox; ++i) {
-                        const uint32_t dst = b + S::kBox * BK * 2 * i;
+                    for (int i = 0; i < WIDE / CG / BOX; ++i) {
+                        const uint32_t dst = b + BOX * BK * 2 * i;
                         if (i < boxes) {
-                            if (kMode == kWgrad) load_2d<kCG>(dst, &tmB, fb, c + S::kBox * i, T.red0 + r);
-                            else load_2d<kCG>(dst, &tmB, fb, r, c + S::kBox * i);
+                            if (kMode == kWgrad) load_2d<CG>(dst, &tmB, fb, c + BOX * i, T.red0 + r);
+                            else load_2d<CG>(dst, &tmB, fb, r, c + BOX * i);
                         }
                     }
                 }
@@ -233,19 +226,19 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint32_t base = smem_u32(smem);
             // MN-major: 64-element chunks 8192 bytes apart, 8-row groups of the reduction 1024 apart
             const uint64_t ad0 = smem_desc(base, a_mn ? 8192 : 16, 1024);
-            const uint64_t bd0 = smem_desc(base + S::kA, b_mn ? 8192 : 16, 1024);
+            const uint64_t bd0 = smem_desc(base + A_BYTES, b_mn ? 8192 : 16, 1024);
             constexpr uint32_t a_step = (a_mn ? 2048 : 32) / 16, b_step = (b_mn ? 2048 : 32) / 16;  // 16 of the sum
             for (int64_t t = first; t < W.total; t += stride) {
                 const Tile T = W.get(t);
-                const uint32_t id = idesc_f16(1, a_mn, b_mn, S::kFeat, T.n);
+                const uint32_t id = idesc_f16(1, a_mn, b_mn, FEAT, T.n);
                 for (int r0 = 0; r0 < T.red; r0 += kRegs ? FLUSH * BK : T.red) {
                     const int r1 = kRegs ? min(T.red, r0 + FLUSH * BK) : T.red;
-                    const uint32_t d = tmem + buf * S::kWide;
+                    const uint32_t d = tmem + buf * WIDE;
                     if (!mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag)) goto done_mma;
                     __syncwarp();
                     for (int r = r0; r < r1; r += BK) {
-                        const uint64_t ad = ad0 + (uint64_t)(stage * (S::kStage / 16));
-                        const uint64_t bd = bd0 + (uint64_t)(stage * (S::kStage / 16));
+                        const uint64_t ad = ad0 + (uint64_t)(stage * (STAGE_BYTES / 16));
+                        const uint64_t bd = bd0 + (uint64_t)(stage * (STAGE_BYTES / 16));
                         if (ragged_end(T, r)) {
                             if (!mbar_wait(fix0 + 8 * stage, fix_uses >> stage & 1, abort_flag)) goto done_mma;
                             fix_uses ^= 1u << stage;
@@ -259,9 +252,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < BK / 16; ++k)
-                                if (k < steps) mma_f16<kCG>(d, ad + k * a_step, bd + k * b_step, id, r > r0 || k > 0);
-                            mma_commit<kCG>(empty0 + 8 * stage);
-                            if (r + BK >= r1) mma_commit<kCG>(accf0 + 8 * buf);
+                                if (k < steps) mma_f16<CG>(d, ad + k * a_step, bd + k * b_step, id, r > r0 || k > 0);
+                            mma_commit<CG>(empty0 + 8 * stage);
+                            if (r + BK >= r1) mma_commit<CG>(accf0 + 8 * buf);
                         }
                         __syncwarp();
                         if (++stage == STAGES) stage = 0;
@@ -296,7 +289,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
         // ------------------------------------------------------ epilogue
         const int q = warp & 3, group = (warp - 2) >> 2;  // two groups of four warps share the columns
-        uint8_t* stage = smem + S::kEpi + group * kEpiBytes;
+        uint8_t* stage = smem + EPI_REGION + group * kEpiBytes;
         const int64_t ld = kMode == kFprop ? p.N : p.K;  // features
         int buf = 0;
         uint32_t aphase = 0;
@@ -326,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 continue;
             }
             if constexpr (kRegs) {
-                constexpr int kChunks = (S::kWide + 63) / 64;  // 32-column chunks of a group
+                constexpr int kChunks = WIDE / 64;  // 32-column chunks of a group
                 float acc[kChunks][32];
                 bool ok = true;
                 for (int r0 = 0; r0 < T.red && ok; r0 += FLUSH * BK) {
@@ -342,7 +335,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                             for (int h = 0; h < 32; h += 16) {
                                 uint32_t v[16];
-                                tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + buf * S::kWide + c + h, v);
+                                tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + buf * WIDE + c + h, v);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int j = 0; j < 16; ++j)
@@ -389,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 for (int c = 32 * group; c < T.cols; c += 64)
-                    store_columns_bf16(tmem + buf * S::kWide + c, q, lane, 1 + group, stage,
+                    store_columns_bf16(tmem + buf * WIDE + c, q, lane, 1 + group, stage,
                                        static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * ld + f0, ld, live, T.cols - c,
                                        [&](float v, int l, int) { return v + b[(l >> 3) & 3]; });
                 drained();
@@ -399,10 +392,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_before();
     __syncthreads();
     if (s_abort && threadIdx.x == 0 && p.status) atomicOr(p.status, MXQ_STATUS_WAIT_TIMEOUT);
-    if (kCG == 2) cluster_sync();  // rank 0's MMAs have read this CTA's shared memory for the last time
+    cluster_sync();  // rank 0's MMAs have read this CTA's shared memory for the last time
     if (warp == 1) {
         fence_after();
-        tmem_dealloc<kCG>(tmem, S::kTmem);
+        tmem_dealloc<CG>(tmem, TMEM_COLS);
     }
 }
 
@@ -447,46 +440,43 @@ int sm_count() {
     return v;
 }
 
-template <int kMode, int kCG, bool kRegs>
+template <int kMode, bool kRegs>
 static cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const Params& p, int64_t tiles, cudaStream_t s) {
-    using S = Shape<kCG>;
-    return launch_persistent<kCG, ragged_gemm_kernel<kMode, kCG, kRegs>>(THREADS, S::smem(MXQ_MAX_EXPERTS), S::smem(p.E),
-                                                                         tiles, s, a, b, p);
+    return launch_persistent<CG, ragged_gemm_kernel<kMode, kRegs>>(THREADS, smem_bytes(MXQ_MAX_EXPERTS), smem_bytes(p.E),
+                                                                   tiles, s, a, b, p);
 }
 
-template <int kMode, int kCG>
+template <int kMode>
 static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
-    using S = Shape<kCG>;
     const Params p{c.M, c.N, c.K, c.E, c.m_splits, static_cast<const __nv_bfloat16*>(c.bias), c.out, c.out_f32,
                    c.accumulate, c.status};
     CUtensorMap a, b;
     bool ok;
-    const int64_t feats = ((kMode == kFprop ? c.N : c.K) + S::kFeat - 1) / S::kFeat;
-    int64_t tiles = (c.M / S::kWide + std::min<int64_t>(c.E, c.M)) * feats;  // no fewer than the device counts
+    const int64_t feats = ((kMode == kFprop ? c.N : c.K) + FEAT - 1) / FEAT;
+    int64_t tiles = (c.M / WIDE + std::min<int64_t>(c.E, c.M)) * feats;  // no fewer than the device counts
     if (kMode == kWgrad) {
-        tiles = feats * ((c.N + S::kWide - 1) / S::kWide) * c.E;
+        tiles = feats * ((c.N + WIDE - 1) / WIDE) * c.E;
         // with M == 0 nothing is loaded: any valid address does
         const int64_t rows = std::max<int64_t>(c.M, 1);
         const int64_t da[2] = {c.K, rows}, sa[1] = {2 * c.ld_tok}, db[2] = {c.N, rows}, sb[1] = {2 * c.ld_mat};
-        const int boxa[2] = {64, BK}, boxb[2] = {S::kBox, BK};
+        const int boxa[2] = {64, BK}, boxb[2] = {BOX, BK};
         ok = encode_tmap(&a, c.M ? c.tok : c.out, 2, 2, da, sa, boxa, 128) &&
              encode_tmap(&b, c.M ? c.mat : c.out, 2, 2, db, sb, boxb, 128);
     } else {
         const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {2 * c.K, 2 * c.K * c.N};
         const int64_t db[2] = {kMode == kDgrad ? c.N : c.K, c.M}, sb[1] = {2 * c.ld_tok};
-        const int boxa[3] = {64, kMode == kDgrad ? BK : kFM, 1}, boxb[2] = {BK, S::kBox};
+        const int boxa[3] = {64, kMode == kDgrad ? BK : kFM, 1}, boxb[2] = {BK, BOX};
         ok = encode_tmap(&a, c.mat, 2, 3, da, sa, boxa, 128) && encode_tmap(&b, c.tok, 2, 2, db, sb, boxb, 128);
     }
     if (!ok) return cudaErrorInvalidValue;
-    return c.out_f32 || c.accumulate ? launch<kMode, kCG, true>(a, b, p, tiles, s)
-                                     : launch<kMode, kCG, false>(a, b, p, tiles, s);
+    return c.out_f32 || c.accumulate ? launch<kMode, true>(a, b, p, tiles, s)
+                                     : launch<kMode, false>(a, b, p, tiles, s);
 }
 
 cudaError_t run_gemm(const GemmCall& c, cudaStream_t s) {
-    if (c.mode == kWgrad) return run_mode<kWgrad, 2>(c, s);
-    const bool few = c.M <= (int64_t)Shape<1>::kWide * c.E;
-    if (c.mode == kFprop) return few ? run_mode<kFprop, 1>(c, s) : run_mode<kFprop, 2>(c, s);
-    return few ? run_mode<kDgrad, 1>(c, s) : run_mode<kDgrad, 2>(c, s);
+    if (c.mode == kWgrad) return run_mode<kWgrad>(c, s);
+    if (c.M <= (int64_t)kFewRows * c.E) return run_gemm_few(c, s);
+    return c.mode == kFprop ? run_mode<kFprop>(c, s) : run_mode<kDgrad>(c, s);
 }
 
 }  // namespace ragged

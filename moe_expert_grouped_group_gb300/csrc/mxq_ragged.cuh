@@ -162,10 +162,37 @@ __device__ __forceinline__ uint32_t mapa(uint32_t a, uint32_t rank) {
 __device__ __forceinline__ void arrive_remote_relaxed(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-// Remote arrive after this thread's (warp's) writes to its own CTA's shared memory or TMEM, made visible to
-// the tensor core by fence.proxy.async or tcgen05.wait::st: a pair's MMA reads them through this SM, no
-// thread of the other CTA does, so the arrive has to follow them here and needs no cluster-wide release,
-// which would cost the warp about 800 cycles.
+// mbar_wait on what other CTAs of the cluster have sent or released.
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if (mbar_try_cluster(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    for (uint32_t i = 0;; ++i) {
+        if (mbar_try_cluster(bar, parity)) return true;
+        if ((i & 63) == 63) {
+            if (*abort_flag) return false;
+            if (globaltimer() - t0 > kWaitNs) {
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+// Remote arrive that follows this warp's earlier accesses to its own CTA's shared memory or TMEM: reads of a
+// buffer that another CTA fills again, or writes that fence.proxy.async or tcgen05.wait::st has made visible
+// to the tensor core (a pair's MMA reads them through this SM). What was accessed is on this SM, so the
+// arrive needs no cluster-wide release, which would wait for this warp's global stores as well: 800 to
+// 1500 cycles an arrive.
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
@@ -418,6 +445,85 @@ struct Walk {
             T.row0 = s.row;
         }
         return T;
+    }
+};
+
+// ------------------------------------------------------------ split sums
+// A tile of 128 features by kFewRows columns whose sum is split over a cluster
+// of kSplit CTAs: rank r gets columns [r * kOwn, + kOwn) of all partial sums
+// and adds them in rank order. Buffers of alternate tiles: [2][kSplit] of 128
+// lanes by kOwn columns, 32 KB for every kSplit. partf[2]: bytes received;
+// parte[2]: arrivals of the owners' warps that have read what this CTA sent.
+constexpr int kPartBytes = 2 * kFM * kFewRows * 4;
+
+__device__ __forceinline__ void st_async(uint32_t cluster_dst, uint32_t cluster_bar, float a, float b, float c, float d) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(cluster_dst),
+        "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(__float_as_uint(d)),
+        "r"(cluster_bar)
+        : "memory");
+}
+
+template <int kSplit>
+struct SplitSum {
+    static constexpr int kOwn = kFewRows / kSplit, kPart = kFM * kOwn * 4;
+    uint32_t buf, partf, parte;
+    int rank;
+    uint32_t tile = 0;
+
+    __device__ SplitSum(uint32_t buf_, uint32_t partf_, uint32_t parte_, int rank_)
+        : buf(buf_), partf(partf_), parte(parte_), rank(rank_) {}
+
+    // v: this CTA's partial sums of lane l on entry, the whole sums of its kOwn columns in v[0 .. kOwn - 1]
+    // on return. Called by the four warps that hold the 128 lanes; `first` is true in one of them. False
+    // when a bounded wait has expired.
+    __device__ bool exchange(float (&v)[kFewRows], int l, int lane, bool first, volatile int* abort_flag) {
+        if constexpr (kSplit > 1) {
+            const uint32_t side = tile & 1, phase = tile >> 1 & 1;
+            ++tile;
+            bool ok = mbar_wait_cluster(parte + 8 * side, phase ^ 1, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            if (first && lane == 0) mbar_expect_tx(partf + 8 * side, (kSplit - 1) * kPart);
+            const uint32_t mine = buf + (side * kSplit + rank) * kPart + l * kOwn * 4;
+#pragma unroll
+            for (int j = 0; j < kSplit; ++j)
+                if (j != rank) {
+                    const uint32_t dst = mapa(mine, j), bar = mapa(partf + 8 * side, j);
+#pragma unroll
+                    for (int i = 0; i < kOwn; i += 4)
+                        st_async(dst + 4 * i, bar, v[j * kOwn + i], v[j * kOwn + i + 1], v[j * kOwn + i + 2],
+                                 v[j * kOwn + i + 3]);
+                }
+            float own[kOwn];
+#pragma unroll
+            for (int j = 0; j < kSplit; ++j)
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i) own[i] = j == 0 || j == rank ? v[j * kOwn + i] : own[i];
+            ok = mbar_wait_cluster(partf + 8 * side, phase, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+#pragma unroll
+            for (int j = 0; j < kSplit; ++j) {
+                const uint32_t src = buf + (side * kSplit + j) * kPart + l * kOwn * 4;
+#pragma unroll
+                for (int i = 0; i < kOwn; i += 4) {
+                    float4 a = make_float4(own[i], own[i + 1], own[i + 2], own[i + 3]);
+                    if (j != rank)
+                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w)
+                                     : "r"(src + 4 * i)
+                                     : "memory");
+                    v[i] = j ? __fadd_rn(v[i], a.x) : a.x;
+                    v[i + 1] = j ? __fadd_rn(v[i + 1], a.y) : a.y;
+                    v[i + 2] = j ? __fadd_rn(v[i + 2], a.z) : a.z;
+                    v[i + 3] = j ? __fadd_rn(v[i + 3], a.w) : a.w;
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                for (int j = 0; j < kSplit; ++j)
+                    if (j != rank) arrive_remote(mapa(parte + 8 * side, j));
+        }
+        return true;
     }
 };
 

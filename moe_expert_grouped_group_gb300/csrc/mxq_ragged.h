@@ -28,6 +28,11 @@ struct GemmCall {
     int32_t* status;
 };
 cudaError_t run_gemm(const GemmCall& c, cudaStream_t s);
+// fprop and dgrad of at most kFewRows rows an expert on average
+constexpr int kFewRows = 32;
+cudaError_t run_gemm_few(const GemmCall& c, cudaStream_t s);
+// CTAs (1, 2, 4 or 8) that share a tile's sum of `blocks` stages when a product has `tiles` one-SM tiles
+int split_of(int64_t tiles, int64_t blocks);
 
 struct Int8Call {
     const void* xq;      // (M, K) int8
