@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "mxq_common.cuh"
+#include "mxq_ragged.cuh"
 #include "mxq_ragged.h"
 
 namespace mxq {
@@ -106,6 +107,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 __global__ void __launch_bounds__(256) swiglu_dropout_fwd_kernel(const uint16_t* y, int64_t M, int64_t F,
                                                                  const int64_t* rng, Keep k, float scale,
                                                                  uint16_t* h) {
+    wait_for_stream();
     const uint32_t per = (uint32_t)(F / 8);
     const int64_t vecs = M * per, step = (int64_t)gridDim.x * blockDim.x;
     Cursor c((int64_t)blockIdx.x * blockDim.x + threadIdx.x, step, per);
@@ -131,6 +133,7 @@ __global__ void __launch_bounds__(256) swiglu_dropout_fwd_kernel(const uint16_t*
 __global__ void __launch_bounds__(256) swiglu_dropout_bwd_kernel(const uint16_t* dh, const uint16_t* y, int64_t M,
                                                                  int64_t F, const int64_t* rng, Keep k, float scale,
                                                                  uint16_t* dy) {
+    wait_for_stream();
     const uint32_t per = (uint32_t)(F / 8);
     const int64_t vecs = M * per, step = (int64_t)gridDim.x * blockDim.x;
     Cursor c((int64_t)blockIdx.x * blockDim.x + threadIdx.x, step, per);
@@ -183,6 +186,7 @@ __device__ __forceinline__ void from_f32(__nv_bfloat16* p, float v) { *p = __flo
 template <typename T>
 __global__ void __launch_bounds__(256) dropout_kernel(const T* x, const T* residual, int64_t n, const int64_t* rng,
                                                       Keep k, float scale, T* out) {
+    wait_for_stream();
     const Rng r = load_rng(rng);
     const int64_t vecs = (n + 7) / 8;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < vecs; i += (int64_t)gridDim.x * blockDim.x) {
@@ -217,28 +221,24 @@ static float scale_of(uint32_t t) { return t >= 65536u ? 0.0f : (float)(65536.0 
 cudaError_t run_swiglu_dropout_fwd(const void* y, int64_t M, int64_t F, const int64_t* rng, uint32_t t, void* h,
                                    cudaStream_t s) {
     if (M == 0) return cudaSuccess;
-    swiglu_dropout_fwd_kernel<<<grid_for(M * (F / 8)), 256, 0, s>>>((const uint16_t*)y, M, F, rng, keep_of(t),
-                                                                    scale_of(t), (uint16_t*)h);
-    return cudaGetLastError();
+    return launch(swiglu_dropout_fwd_kernel, grid_for(M * (F / 8)), 256, s, (const uint16_t*)y, M, F, rng, keep_of(t),
+                  scale_of(t), (uint16_t*)h);
 }
 cudaError_t run_swiglu_dropout_bwd(const void* dh, const void* y, int64_t M, int64_t F, const int64_t* rng, uint32_t t,
                                    void* dy, cudaStream_t s) {
     if (M == 0) return cudaSuccess;
-    swiglu_dropout_bwd_kernel<<<grid_for(M * (F / 8)), 256, 0, s>>>((const uint16_t*)dh, (const uint16_t*)y, M, F, rng,
-                                                                    keep_of(t), scale_of(t), (uint16_t*)dy);
-    return cudaGetLastError();
+    return launch(swiglu_dropout_bwd_kernel, grid_for(M * (F / 8)), 256, s, (const uint16_t*)dh, (const uint16_t*)y, M, F,
+                  rng, keep_of(t), scale_of(t), (uint16_t*)dy);
 }
 cudaError_t run_dropout(const void* x, const void* residual, int64_t n, int f32, const int64_t* rng, uint32_t t,
                         void* out, cudaStream_t s) {
     if (n == 0) return cudaSuccess;
     const unsigned grid = grid_for((n + 7) / 8);
     if (f32)
-        dropout_kernel<float><<<grid, 256, 0, s>>>((const float*)x, (const float*)residual, n, rng, keep_of(t), scale_of(t),
-                                                   (float*)out);
-    else
-        dropout_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>((const __nv_bfloat16*)x, (const __nv_bfloat16*)residual, n,
-                                                           rng, keep_of(t), scale_of(t), (__nv_bfloat16*)out);
-    return cudaGetLastError();
+        return launch(dropout_kernel<float>, grid, 256, s, (const float*)x, (const float*)residual, n, rng, keep_of(t),
+                      scale_of(t), (float*)out);
+    return launch(dropout_kernel<__nv_bfloat16>, grid, 256, s, (const __nv_bfloat16*)x, (const __nv_bfloat16*)residual, n,
+                  rng, keep_of(t), scale_of(t), (__nv_bfloat16*)out);
 }
 
 }  // namespace ragged

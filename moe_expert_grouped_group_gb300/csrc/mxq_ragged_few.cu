@@ -62,12 +62,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = kSplit > 1 ? (int)cta_rank() : 0;
 
-    // all CTAs of a cluster find the same fault and stop before any cluster-wide step
-    const int bad = load_ragged(p.m_splits, p.E, p.M, WIDE, s_off, s_slices);
-    if (bad) {
-        report_status(p.status, bad);
-        return;
-    }
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_REGION);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
     const uint32_t accf0 = empty0 + 8 * STAGES, acce0 = accf0 + 16, partf0 = acce0 + 16, parte0 = partf0 + 16;
@@ -87,6 +81,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmA) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmB) : "memory");
+    }
+    // all CTAs of a cluster find the same fault and stop before any cluster-wide step
+    const int bad = load_ragged(p.m_splits, p.E, p.M, WIDE, s_off, s_slices);
+    if (bad) {
+        report_status(p.status, bad);
+        return;
     }
     if (warp == 1) tmem_alloc<1>(smem_u32(&s_tmem), TMEM_COLS);
     fence_before();

@@ -103,11 +103,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = kCG == 2 ? cta_rank() : 0;
 
-    const int bad = load_ragged(p.m_splits, p.E, p.M, S::kWide, s_off, s_slices);
-    if (bad) {
-        report_status(p.status, bad);
-        return;
-    }
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
     const uint32_t rawf0 = smem_u32(bars), rawe0 = rawf0 + 8 * RAWS;
     const uint32_t full0 = rawe0 + 8 * RAWS, empty0 = full0 + 8 * SETS;
@@ -130,6 +125,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmA) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmB) : "memory");
+    }
+    const int bad = load_ragged(p.m_splits, p.E, p.M, S::kWide, s_off, s_slices);
+    if (bad) {
+        report_status(p.status, bad);
+        return;
     }
     if (warp == 1) tmem_alloc<kCG>(smem_u32(&s_tmem), S::kTmem);
     fence_before();
@@ -370,6 +370,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 // NaN and its codes are 0, so that its outputs are NaN and nothing else is.
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* x, int64_t M, int64_t K, int64_t ld,
                                                             uint8_t* q, float* scale) {
+    wait_for_stream();
     __shared__ uint32_t s_top[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
@@ -436,9 +437,8 @@ cudaError_t run_int8(const Int8Call& c, cudaStream_t s) {
 cudaError_t run_int8_quantize(const void* x, int64_t M, int64_t K, int64_t ld, void* q, float* scale, cudaStream_t s) {
     if (M == 0) return cudaSuccess;
     const unsigned grid = (unsigned)std::min<int64_t>(M, (int64_t)sm_count() * 8);
-    i8::quantize_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const uint16_t*>(x), M, K, ld, static_cast<uint8_t*>(q),
-                                                  scale);
-    return cudaGetLastError();
+    return launch(i8::quantize_rows_kernel, grid, 256, s, static_cast<const uint16_t*>(x), M, K, ld,
+                  static_cast<uint8_t*>(q), scale);
 }
 
 }  // namespace ragged
