@@ -55,7 +55,7 @@ namespace ragged {
 constexpr int BK = 64;    // reduction depth of a stage: 128 bytes of bf16
 constexpr int FLUSH = 8;  // stages an accumulator holds before it is added to the registers (kRegs)
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 96 + 32 * EPI_WARPS;
+constexpr int THREADS = 128 + 32 * EPI_WARPS;
 
 constexpr int CG = 2;                         // CTAs, and SMs, of a tile
 constexpr int FEAT = kFM * CG;                // features of a tile
@@ -69,7 +69,7 @@ constexpr int BAR_REGION = EPI_REGION + 2 * kEpiBytes;
 constexpr int TABLE_REGION = BAR_REGION + 256;
 __host__ __device__ constexpr int smem_bytes(int E) { return 1024 + TABLE_REGION + 12 * (E + 1); }
 static_assert(smem_bytes(MXQ_MAX_EXPERTS) <= 232448, "shared memory over the per-block limit");
-static_assert(BAR_REGION % 8 == 0 && 8 * (4 * STAGES + 4) <= 256, "barrier region");
+static_assert(BAR_REGION % 8 == 0 && 8 * (4 * STAGES + 6) + 16 <= 256, "barrier region");
 
 struct Params {
     int64_t M, N, K;
@@ -83,7 +83,8 @@ struct Params {
 
 template <int kMode, bool kRegs>
 __global__ void __launch_bounds__(THREADS, 1)
-    ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Params p) {
+    ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmHalf, Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align<1024>(smem_raw);
     int32_t* s_off = reinterpret_cast<int32_t*>(smem + TABLE_REGION);
@@ -97,6 +98,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_REGION);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, tail0 = empty0 + 8 * STAGES;
     const uint32_t fix0 = tail0 + 8 * STAGES, accf0 = fix0 + 8 * STAGES, acce0 = accf0 + 16;
+    const uint32_t ready = acce0 + 16, taken = ready + 8, answer = (taken + 8 + 15) & ~15u;
     volatile int* abort_flag = &s_abort;
     if (threadIdx.x == 0) {
         s_abort = 0;
@@ -110,6 +112,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(accf0 + 8 * b, 1);
             mbar_init(acce0 + 8 * b, CG * EPI_WARPS);
         }
+        mbar_init(ready, 1);
+        mbar_init(taken, 5 + 2 * EPI_WARPS + (kMode == kWgrad ? 2 : 0));  // the warps of both CTAs that call next()
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmA) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmB) : "memory");
@@ -138,7 +142,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_after();
     const uint32_t tmem = s_tmem;
     const Walk<kMode, FEAT, WIDE, STEP> W(p.N, p.K, p.E, s_off, s_slices, s_order);
-    const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
+    TileQueue queue(answer, ready, mapa(taken, 0));
+    int64_t t = blockIdx.x / CG;
     constexpr bool a_mn = kMode != kFprop, b_mn = kMode == kWgrad;
     // An expert's last block of rows in wgrad, when it ends inside a step of 16: its loads complete on each
     // CTA's own tail[st], warp 10 of both CTAs zeroes the rows up to the next multiple of 16 and arrives on
@@ -161,12 +166,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         int stage = 0;
         uint32_t phase = 0;
         uint32_t used = 0, full_uses = 0, tail_uses = 0, tail_last = 0;  // bits of stages
-        for (int64_t t = first; t < W.total; t += stride) {
+        do {
+            if (t >= W.total) continue;
             const Tile T = W.get(t);
             const int half = T.n / CG;  // this CTA's columns of the tile: [rank * half, + half)
-            const int boxes = (half + BOX - 1) / BOX;
+            // rows of the other operand: whole boxes, and half a box at the end where that is enough
+            const bool half_box = kMode != kWgrad && (half - 1) % BOX < BOX / 2;
+            const int boxes = half_box ? half / BOX : (half + BOX - 1) / BOX;
             const int f = T.f0 + rank * kFM, c = T.c0 + rank * half;
-            const uint32_t bytes = A_BYTES + boxes * BOX * BK * 2;
+            const uint32_t bytes = A_BYTES + (2 * boxes + half_box) * (BOX * BK);
             for (int r = 0; r < T.red; r += BK) {
                 if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag)) {
                     // a bounded wait expired: no copy may be in flight when the block ends
@@ -204,6 +212,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             else load_2d<CG>(dst, &tmB, fb, r, c + BOX * i);
                         }
                     }
+                    if (half_box) load_2d<CG>(b + BOX * BK * 2 * boxes, &tmHalf, fb, r, c + BOX * boxes);
                 }
                 __syncwarp();
                 used |= bit;
@@ -216,7 +225,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (++stage == STAGES) { stage = 0; phase ^= 1; }
             }
-        }
+        } while (queue.next(t, lane, abort_flag) == TileQueue::kTile);
     done_producer:;
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer (rank 0)
@@ -228,7 +237,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint64_t ad0 = smem_desc(base, a_mn ? 8192 : 16, 1024);
             const uint64_t bd0 = smem_desc(base + A_BYTES, b_mn ? 8192 : 16, 1024);
             constexpr uint32_t a_step = (a_mn ? 2048 : 32) / 16, b_step = (b_mn ? 2048 : 32) / 16;  // 16 of the sum
-            for (int64_t t = first; t < W.total; t += stride) {
+            do {
+                if (t >= W.total) continue;
                 const Tile T = W.get(t);
                 const uint32_t id = idesc_f16(1, a_mn, b_mn, FEAT, T.n);
                 for (int r0 = 0; r0 < T.red; r0 += kRegs ? FLUSH * BK : T.red) {
@@ -262,7 +272,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     buf ^= 1;
                     aphase ^= buf == 0;
                 }
-            }
+            } while (queue.next(t, lane, abort_flag) == TileQueue::kTile);
         done_mma:;
         }
     } else if (warp == 2 + EPI_WARPS) {
@@ -270,7 +280,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (kMode == kWgrad) {
             int stage = 0;
             uint32_t uses = 0;  // bits of stages: parity of tail[st]
-            for (int64_t t = first; t < W.total; t += stride) {
+            do {
+                if (t >= W.total) continue;
                 const Tile T = W.get(t);
                 if (T.red == 0) continue;
                 const int last = (T.red - 1) / BK, at = (stage + last) % STAGES;
@@ -284,7 +295,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 stage = (at + 1) % STAGES;
+            } while (queue.next(t, lane, abort_flag) == TileQueue::kTile);
+        }
+    } else if (warp == 3 + EPI_WARPS) {
+        // ------------------------------------------------------ next tiles
+        for (uint32_t asked = 0;; asked ^= 1) {
+            if (rank == 0 && !mbar_wait(taken, asked ^ 1, abort_flag)) break;
+            __syncwarp();
+            if (elect_one()) {
+                mbar_expect_tx(ready, 16);
+                if (rank == 0) queue.ask();
             }
+            __syncwarp();
+            if (queue.next(t, lane, abort_flag) != TileQueue::kTile) break;
         }
     } else {
         // ------------------------------------------------------ epilogue
@@ -303,7 +326,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             buf ^= 1;
             aphase ^= buf == 0;
         };
-        for (int64_t t = first; t < W.total; t += stride) {
+        // the groups' warps meet at barriers: all of a group stop at a wait that expired, or none
+        auto next_tile = [&] {
+            const TileQueue::Result r = queue.next(t, lane, abort_flag);
+            return (kRegs || !group_any(1 + group, kEpiGroup, r == TileQueue::kAbort)) && r == TileQueue::kTile;
+        };
+        do {
+            if (t >= W.total) continue;
             const Tile T = W.get(t);
             const int f0 = T.f0 + rank * kFM;
             const int live = (int)min((int64_t)kFM, ld - f0);  // may be negative: nothing to store
@@ -370,7 +399,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             } else {
                 const bool ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
-                // the groups' warps meet at barriers below: all of a group stop, or none
                 if (group_any(1 + group, kEpiGroup, !ok || *abort_flag)) break;
                 fence_after();
                 float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -387,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                        [&](float v, int l, int) { return v + b[(l >> 3) & 3]; });
                 drained();
             }
-        }
+        } while (next_tile());
     }
     fence_before();
     __syncthreads();
@@ -441,16 +469,17 @@ int sm_count() {
 }
 
 template <int kMode, bool kRegs>
-static cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const Params& p, int64_t tiles, cudaStream_t s) {
-    return launch_persistent<CG, ragged_gemm_kernel<kMode, kRegs>>(THREADS, smem_bytes(MXQ_MAX_EXPERTS), smem_bytes(p.E),
-                                                                   tiles, s, a, b, p);
+static cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& half, const Params& p,
+                          int64_t tiles, cudaStream_t s) {
+    return launch_persistent<CG, true, ragged_gemm_kernel<kMode, kRegs>>(THREADS, smem_bytes(MXQ_MAX_EXPERTS), smem_bytes(p.E),
+                                                                   tiles, s, a, b, half, p);
 }
 
 template <int kMode>
 static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
     const Params p{c.M, c.N, c.K, c.E, c.m_splits, static_cast<const __nv_bfloat16*>(c.bias), c.out, c.out_f32,
                    c.accumulate, c.status};
-    CUtensorMap a, b;
+    CUtensorMap a, b, half;  // half: b in boxes of half the rows
     bool ok;
     const int64_t feats = ((kMode == kFprop ? c.N : c.K) + FEAT - 1) / FEAT;
     int64_t tiles = (c.M / WIDE + std::min<int64_t>(c.E, c.M)) * feats;  // no fewer than the device counts
@@ -462,15 +491,17 @@ static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
         const int boxa[2] = {64, BK}, boxb[2] = {BOX, BK};
         ok = encode_tmap(&a, c.M ? c.tok : c.out, 2, 2, da, sa, boxa, 128) &&
              encode_tmap(&b, c.M ? c.mat : c.out, 2, 2, db, sb, boxb, 128);
+        half = b;
     } else {
         const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {2 * c.K, 2 * c.K * c.N};
         const int64_t db[2] = {kMode == kDgrad ? c.N : c.K, c.M}, sb[1] = {2 * c.ld_tok};
-        const int boxa[3] = {64, kMode == kDgrad ? BK : kFM, 1}, boxb[2] = {BK, BOX};
-        ok = encode_tmap(&a, c.mat, 2, 3, da, sa, boxa, 128) && encode_tmap(&b, c.tok, 2, 2, db, sb, boxb, 128);
+        const int boxa[3] = {64, kMode == kDgrad ? BK : kFM, 1}, boxb[2] = {BK, BOX}, boxh[2] = {BK, BOX / 2};
+        ok = encode_tmap(&a, c.mat, 2, 3, da, sa, boxa, 128) && encode_tmap(&b, c.tok, 2, 2, db, sb, boxb, 128) &&
+             encode_tmap(&half, c.tok, 2, 2, db, sb, boxh, 128);
     }
     if (!ok) return cudaErrorInvalidValue;
-    return c.out_f32 || c.accumulate ? launch<kMode, true>(a, b, p, tiles, s)
-                                     : launch<kMode, false>(a, b, p, tiles, s);
+    return c.out_f32 || c.accumulate ? launch<kMode, true>(a, b, half, p, tiles, s)
+                                     : launch<kMode, false>(a, b, half, p, tiles, s);
 }
 
 cudaError_t run_gemm(const GemmCall& c, cudaStream_t s) {

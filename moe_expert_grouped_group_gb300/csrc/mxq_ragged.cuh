@@ -535,6 +535,54 @@ struct SplitSum {
     }
 };
 
+// ------------------------------------------------------------ tile queue
+// A grid of one cluster per tile, most of which never start: a cluster that
+// has a tile in hand takes the next one from the hardware's queue of clusters
+// not yet launched (clusterlaunchcontrol). So tiles of uneven cost go to
+// whichever SMs are free, with no counter in memory. One warp of a pair's rank
+// 0 asks; the answer arrives in both CTAs. It asks when every warp has taken
+// the last answer, that is while the tile before is being computed, so a
+// cluster holds one tile more than it works on.
+struct TileQueue {
+    uint32_t answer, ready, taken;  // 16 bytes; barrier of this CTA; barrier of rank 0 (cluster address)
+    uint32_t phase = 0;
+    enum Result { kDone = 0, kTile = 1, kAbort = 2 };
+
+    __device__ TileQueue(uint32_t answer_, uint32_t ready_, uint32_t taken_)
+        : answer(answer_), ready(ready_), taken(taken_) {}
+
+    // The next tile of this cluster, for a whole warp.
+    __device__ Result next(int64_t& tile, int lane, volatile int* abort_flag) {
+        const bool ok = mbar_wait(ready, phase, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) return kAbort;
+        phase ^= 1;
+        uint32_t valid, first;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t.reg .b32 y, z, w;\n\t"
+            "ld.shared.b128 a, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t"
+            "mov.u32 %1, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, a;\n\t}"
+            : "=&r"(valid), "=&r"(first)
+            : "r"(answer)
+            : "memory");
+        fence_async_smem();  // read before the next answer is written
+        __syncwarp();
+        if (lane == 0) arrive_remote(taken);
+        tile = first / 2;
+        return valid ? kTile : kDone;
+    }
+    // Asks for the next cluster; the answer goes to `answer` and `ready` of both CTAs.
+    __device__ void ask() const {
+        asm volatile(
+            "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 "
+            "[%0], [%1];" ::"r"(answer),
+            "r"(ready)
+            : "memory");
+    }
+};
+
 // On a bounded wait's expiry: wait, again at most about 2 s each, for the last
 // fills of the ring, so that no copy is in flight when the block ends.
 __device__ __forceinline__ void drain_ring(uint32_t full0, int stages, int64_t fills) {
@@ -544,10 +592,11 @@ __device__ __forceinline__ void drain_ring(uint32_t full0, int stages, int64_t f
 }
 
 // ------------------------------------------------------------------ host side
-// Launches a persistent kernel of clusters of kCG CTAs, as many as fit the
-// device and no more than `tiles`. The kernel's attribute and co-residency are
-// set and asked for once per device.
-template <int kCG, auto kKernel, class... Args>
+// Launches a kernel of clusters of kCG CTAs: one cluster per tile for a kernel
+// with a TileQueue, otherwise as many as fit the device and no more than
+// `tiles`. The kernel's attribute and co-residency are set and asked for once
+// per device.
+template <int kCG, bool kQueue, auto kKernel, class... Args>
 static cudaError_t launch_persistent(int threads, int smem_max, int smem, int64_t tiles, cudaStream_t s,
                                      const Args&... args) {
     static std::atomic<int> cache[64];
@@ -575,7 +624,9 @@ static cudaError_t launch_persistent(int threads, int smem_max, int smem, int64_
         if (dev < 64) cache[dev].store(most, std::memory_order_release);
     }
     cfg.numAttrs = 2;
-    cfg.gridDim = dim3((unsigned)(kCG * std::max<int64_t>(1, std::min<int64_t>(tiles, most))));
+    if (!kQueue) tiles = std::min<int64_t>(tiles, most);
+    if (tiles > ((int64_t)1 << 30) / kCG) return cudaErrorInvalidConfiguration;
+    cfg.gridDim = dim3((unsigned)(kCG * std::max<int64_t>(1, tiles)));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     return cudaLaunchKernelEx(&cfg, kKernel, args...);

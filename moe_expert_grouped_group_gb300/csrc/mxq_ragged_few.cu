@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 template <int kMode, int kSplit>
 static cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const Params& p, int64_t tiles, cudaStream_t s) {
-    return launch_persistent<kSplit, ragged_few_kernel<kMode, kSplit>>(THREADS, smem_bytes(MXQ_MAX_EXPERTS),
+    return launch_persistent<kSplit, false, ragged_few_kernel<kMode, kSplit>>(THREADS, smem_bytes(MXQ_MAX_EXPERTS),
                                                                       smem_bytes(p.E), tiles, s, a, b, p);
 }
 

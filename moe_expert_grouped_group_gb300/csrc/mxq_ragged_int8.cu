@@ -412,7 +412,7 @@ template <int kCG, bool kF32>
 static cudaError_t launch_int8(const CUtensorMap& a, const CUtensorMap& b, const i8::Params& p, int64_t tiles,
                                cudaStream_t s) {
     using S = i8::Shape<kCG>;
-    return launch_persistent<kCG, i8::ragged_int8_kernel<kCG, kF32>>(i8::THREADS, S::smem(MXQ_MAX_EXPERTS),
+    return launch_persistent<kCG, false, i8::ragged_int8_kernel<kCG, kF32>>(i8::THREADS, S::smem(MXQ_MAX_EXPERTS),
                                                                      S::smem(p.E), tiles, s, a, b, p);
 }
 
