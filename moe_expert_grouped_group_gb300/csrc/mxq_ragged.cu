@@ -64,8 +64,8 @@ constexpr int BOX = 64;                       // token rows of a K-major box
 constexpr int STAGES = 6;
 constexpr int A_BYTES = kFM * BK * 2, STAGE_BYTES = A_BYTES + WIDE / CG * BK * 2;
 constexpr int TMEM_COLS = 2 * WIDE;
-constexpr int EPI_REGION = STAGES * STAGE_BYTES;  // staging of the bf16 epilogue, two groups
-constexpr int BAR_REGION = EPI_REGION + 2 * kEpiBytes;
+constexpr int EPI_REGION = STAGES * STAGE_BYTES;  // staging of the bf16 epilogue, a buffer a warp
+constexpr int BAR_REGION = EPI_REGION + EPI_WARPS * kEpiBytes;
 constexpr int TABLE_REGION = BAR_REGION + 256;
 __host__ __device__ constexpr int smem_bytes(int E) { return 1024 + TABLE_REGION + 12 * (E + 1); }
 static_assert(smem_bytes(MXQ_MAX_EXPERTS) <= 232448, "shared memory over the per-block limit");
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
         // ------------------------------------------------------ epilogue
         const int q = warp & 3, group = (warp - 2) >> 2;  // two groups of four warps share the columns
-        uint8_t* stage = smem + EPI_REGION + group * kEpiBytes;
+        uint8_t* stage = smem + EPI_REGION + (warp - 2) * kEpiBytes;
         const int64_t ld = kMode == kFprop ? p.N : p.K;  // features
         int buf = 0;
         uint32_t aphase = 0;
@@ -325,11 +325,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             buf ^= 1;
             aphase ^= buf == 0;
-        };
-        // the groups' warps meet at barriers: all of a group stop at a wait that expired, or none
-        auto next_tile = [&] {
-            const TileQueue::Result r = queue.next(t, lane, abort_flag);
-            return (kRegs || !group_any(1 + group, kEpiGroup, r == TileQueue::kAbort)) && r == TileQueue::kTile;
         };
         do {
             if (t >= W.total) continue;
@@ -399,7 +394,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             } else {
                 const bool ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
-                if (group_any(1 + group, kEpiGroup, !ok || *abort_flag)) break;
+                if (!__all_sync(0xffffffffu, ok && !*abort_flag)) break;
                 fence_after();
                 float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 if (kMode == kFprop && p.bias) {
@@ -410,12 +405,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 for (int c = 32 * group; c < T.cols; c += 64)
-                    store_columns_bf16(tmem + buf * WIDE + c, q, lane, 1 + group, stage,
-                                       static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * ld + f0, ld, live, T.cols - c,
-                                       [&](float v, int l, int) { return v + b[(l >> 3) & 3]; });
+                    store_columns_bf16(tmem + ((uint32_t)(q * 32) << 16) + buf * WIDE + c, lane, stage,
+                                       static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * ld + f0 + 32 * q, ld,
+                                       live - 32 * q, T.cols - c, [&](float v, int l, int) { return v + b[l >> 3]; });
                 drained();
             }
-        } while (next_tile());
+        } while (queue.next(t, lane, abort_flag) == TileQueue::kTile);
     }
     fence_before();
     __syncthreads();

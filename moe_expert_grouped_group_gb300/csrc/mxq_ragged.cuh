@@ -203,27 +203,6 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-// Barrier `id` of `threads` threads; true in all of them when `v` is true in any.
-__device__ __forceinline__ bool group_any(int id, int threads, bool v) {
-    uint32_t r;
-    __syncwarp();
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)v), "r"(id), "r"(threads)
-        : "memory");
-    __syncwarp();
-    return r != 0;
-}
-__device__ __forceinline__ void group_sync(int id, int threads) {
-    __syncwarp();
-    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-    __syncwarp();
-}
-
 // 32 consecutive accumulator columns of this warp's 32 TMEM lanes
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
@@ -273,25 +252,26 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
 
 // ------------------------------------------------------------ bf16 epilogue
 // The accumulator is the transpose of the output tile (lane = feature, column =
-// output row), so 32 columns x 128 lanes go through a staging buffer: matrix
-// fragments out of TMEM, two columns rounded and packed at a time, transposed
-// on the way into shared memory (stmatrix .trans), then whole 256-byte row
-// pieces in 16-byte stores. Rows are 272 bytes apart: eight consecutive rows
-// start in different banks.
-constexpr int kEpiRow = 272, kEpiBytes = 32 * kEpiRow, kEpiGroup = 128;
+// output row), so each warp takes its 32 lanes by 32 columns through a staging
+// buffer of its own: matrix fragments out of TMEM, two columns rounded and
+// packed at a time, transposed on the way into shared memory (stmatrix
+// .trans), then 64-byte row pieces, eight rows to a store instruction. Rows
+// are 80 bytes apart: eight consecutive rows start in different banks. Four
+// warps writing 256-byte pieces together, at barriers, measured the same.
+constexpr int kEpiRow = 80, kEpiBytes = 32 * kEpiRow;
 
-// Columns c0 .. c0 + 31 of TMEM lanes 32 q + ... of the group's four warps, each value passed through
-// f(value, lane in 0..127, column in 0..31), to out + column * ld + lane for lanes < live and
-// columns < cols. Called by the four warps (q = 0..3) of barrier `id`.
+// Columns 0 .. 31 of the accumulator at tmem, lanes 32 q .. of it, each value passed through
+// f(value, lane in 0..31, column in 0..31), to out + column * ld + lane for lanes < live and
+// columns < cols. Called by a warp; `stage` is its own.
 template <class F>
-__device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int q, int lane, int id, uint8_t* stage,
-                                                   __nv_bfloat16* out, int64_t ld, int live, int cols, F f) {
+__device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int lane, uint8_t* stage, __nv_bfloat16* out,
+                                                   int64_t ld, int live, int cols, F f) {
     uint32_t v[2][16];
-    tmem_ld16x32(tmem + ((uint32_t)(q * 32) << 16), v[0]);
-    tmem_ld16x32(tmem + ((uint32_t)(q * 32 + 16) << 16), v[1]);
+    tmem_ld16x32(tmem, v[0]);
+    tmem_ld16x32(tmem + (16u << 16), v[1]);
     tmem_wait_ld();
     uint32_t w[4][4];  // [8-column block][8-lane block]
-    const int fl = q * 32 + (lane >> 2), fc = 2 * (lane & 3);
+    const int fl = lane >> 2, fc = 2 * (lane & 3);
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -299,19 +279,19 @@ __device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int q, int lan
             const int r = 4 * b + 2 * (g & 1), l = fl + 8 * g, col = 8 * b + fc;
             w[b][g] = bf16x2_bits(f(__uint_as_float(v[g >> 1][r]), l, col), f(__uint_as_float(v[g >> 1][r + 1]), l, col + 1));
         }
-    group_sync(id, kEpiGroup);  // the stage's last readers are done
-    const uint32_t at = smem_u32(stage) + (lane & 7) * kEpiRow + (q * 32 + (lane >> 3) * 8) * 2;
+    __syncwarp();  // the stage's last reads are done
+    const uint32_t at = smem_u32(stage) + (lane & 7) * kEpiRow + (lane >> 3) * 16;
 #pragma unroll
     for (int b = 0; b < 4; ++b)
         asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at + 8 * b * kEpiRow),
                      "r"(w[b][0]), "r"(w[b][1]), "r"(w[b][2]), "r"(w[b][3])
                      : "memory");
-    group_sync(id, kEpiGroup);
-    const int piece = lane & 15;
+    __syncwarp();
+    const int piece = lane & 3;
     if (piece * 8 < live)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int j = q * 8 + i * 2 + (lane >> 4);
+            const int j = i * 8 + (lane >> 2);
             if (j < cols)
                 *reinterpret_cast<uint4*>(out + j * ld + piece * 8) =
                     *reinterpret_cast<const uint4*>(stage + j * kEpiRow + piece * 16);

@@ -58,7 +58,7 @@ struct Shape {
     static constexpr int kTmem = kCG == 2 ? 512 : 256;
     static constexpr int kRawAt = SETS * 2 * kHalf;
     static constexpr int kEpi = kRawAt + kRaws * kRaw;
-    static constexpr int kBars = kEpi + kEpiBytes;
+    static constexpr int kBars = kEpi + EPI_WARPS * kEpiBytes;
     static constexpr int kTables = kBars + 256;
     __host__ __device__ static constexpr int smem(int E) { return 1024 + kTables + 8 * (E + 1); }
     static_assert(1024 + kTables + 8 * (MXQ_MAX_EXPERTS + 1) <= 232448, "shared memory over the per-block limit");
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp < 2 + EPI_WARPS) {
         // ------------------------------------------------------ epilogue
         const int q = warp & 3;
-        uint8_t* stage = smem + S::kEpi;
+        uint8_t* stage = smem + S::kEpi + (warp - 2) * kEpiBytes;
         int buf = 0;
         uint32_t aphase = 0;
         for (int64_t t = first; t < W.total; t += stride) {
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int f0 = T.f0 + rank * kFM;
             const int live = (int)min((int64_t)kFM, p.N - f0);
             const bool ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
-            if (group_any(1, kEpiGroup, !ok || *abort_flag)) break;
+            if (!__all_sync(0xffffffffu, ok && !*abort_flag)) break;
             fence_after();
             const float* xs = p.xs + T.row0;
             if constexpr (kF32) {
@@ -253,11 +253,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const int col = c + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
                         sx[i] = col < T.cols ? __ldg(xs + col) : 0.0f;
                     }
-                    store_columns_bf16(tmem + buf * S::kWide + c, q, lane, 1, stage,
-                                       static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * p.N + f0, p.N, live,
-                                       T.cols - c, [&](float v, int l, int col) {
-                                           const int g = (l >> 3) & 3;
-                                           return v * sx[(col >> 3) * 2 + (col & 1)] * sw[g] + b[g];
+                    store_columns_bf16(tmem + ((uint32_t)(q * 32) << 16) + buf * S::kWide + c, lane, stage,
+                                       static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * p.N + f0 + 32 * q, p.N,
+                                       live - 32 * q, T.cols - c, [&](float v, int l, int col) {
+                                           return v * sx[(col >> 3) * 2 + (col & 1)] * sw[l >> 3] + b[l >> 3];
                                        });
                 }
             }
