@@ -15,14 +15,19 @@
 // N), the edges and the two shapes (pairs of SMs; one SM for few rows) are
 // those of the bf16 products (mxq_ragged.cuh, mxq_ragged.cu).
 //
-// The widened weights go to TMEM, the widened tokens to shared memory. With
-// both in shared memory a 64-deep stage of 256 x 256 moves 96 KB or more through
-// it (load, read, write back twice as wide, read by the MMA), 750 cycles against
-// the MMA's 512; from TMEM the weights' second trip costs nothing there. TMEM
-// then holds two accumulators of 192 columns and two 128-deep slots of weights.
-// Warp 0 loads 128-deep int8 stages, warps 6..13 widen weights and 14..21
-// tokens, in two sets that take alternate stages so that one's latencies hide
-// behind the other's work; warp 1 issues the MMAs, warps 2..5 scale and store.
+// The widened weights go to TMEM, the widened tokens to shared memory: with
+// both in shared memory a 256 x 256 tile of a pair moves 96 KB and more through
+// it per 64 of K (load, read, write back twice as wide, read by the MMA), 750
+// cycles against the MMA's 512. An MMA that reads A from TMEM takes about 130
+// cycles per 16 of K however few its columns are, so the pair shape gives it
+// 256; its accumulator and three slots of weights then fill TMEM, and a tile's
+// epilogue is not hidden behind the next tile's MMAs: eight warps keep it
+// short, and its scales are fetched before the sums are done. The few-rows
+// shape (one SM, up to 32 tokens) has room for two accumulators.
+//
+// Warp 0 loads 128-deep int8 stages; sets of four warps for the weights and
+// four for the tokens take turns, so that one set's latencies hide behind the
+// others' work; warp 1 issues the MMAs; the epilogue's warps scale and store.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,33 +43,41 @@ namespace mxq {
 namespace ragged {
 namespace i8 {
 
-constexpr int BK = 128;   // depth of an int8 stage
-constexpr int HK = 64;    // half of it: 128 bytes of f16
-constexpr int EPI_WARPS = 4, CVT_WARPS = 4;  // CVT_WARPS: for the weights and for the tokens of a set
-constexpr int SETS = 2;                      // each with a widened slot of its own
-constexpr int THREADS = 32 * (2 + EPI_WARPS + 2 * SETS * CVT_WARPS);
+constexpr int BK = 128;  // depth of an int8 stage
+constexpr int HK = 64;   // half of it: 128 bytes of f16
+constexpr int CVT_WARPS = 4;  // of a set: for the weights, and as many for the tokens
 
 template <int kCG>
 struct Shape {
     static constexpr int kFeat = kFM * kCG;
-    static constexpr int kWide = kCG == 2 ? 192 : 32;
+    static constexpr int kWide = kCG == 2 ? 256 : kFewRows;
     static constexpr int kStep = 16 * kCG;
     static constexpr int kBox = 32;                  // token rows of a box
     static constexpr int kTok = kWide / kCG;         // token rows of a stage in one CTA
-    static constexpr int kRaws = kCG == 2 ? 5 : 8;   // int8 stages
+    static constexpr int kRaws = kCG == 2 ? 3 : 8;   // int8 stages
     static constexpr int kRaw = (kFM + kTok) * BK;   // weights, then tokens
+    static constexpr int kSets = kCG == 2 ? 2 : 3;   // of converting warps
+    static constexpr int kSlots = 3;                 // of widened operands
     static constexpr int kHalf = kTok * HK * 2;      // widened tokens of half a slot
-    static constexpr int kTmemA = 2 * kWide;         // the weights' slots follow the accumulators
+    static constexpr int kSlot = 2 * kHalf;
+    static constexpr int kBufs = kCG == 2 ? 1 : 2;   // accumulators
+    static constexpr int kTmemA = kBufs * kWide;     // the weights' slots follow them
+    static constexpr int kSlotCols = BK / 2;         // of its weights in TMEM
     static constexpr int kTmem = kCG == 2 ? 512 : 256;
-    static constexpr int kRawAt = SETS * 2 * kHalf;
+    static constexpr int kRawAt = kSlots * kSlot;
     static constexpr int kEpi = kRawAt + kRaws * kRaw;
-    static constexpr int kBars = kEpi + EPI_WARPS * kEpiBytes;
+    // warps: 0 loads, 1 MMAs, two idle; the epilogue; the weights' sets; the tokens' sets
+    static constexpr int kEpiWarps = kCG == 2 ? 8 : 4;
+    static constexpr int kEpiFirst = 4, kCvtFirst = kEpiFirst + kEpiWarps, kTokFirst = kCvtFirst + kSets * CVT_WARPS;
+    static constexpr int kThreads = 32 * (kTokFirst + kSets * CVT_WARPS);
+    static constexpr int kBars = kEpi + kEpiWarps * kEpiBytes;
     static constexpr int kTables = kBars + 256;
     __host__ __device__ static constexpr int smem(int E) { return 1024 + kTables + 8 * (E + 1); }
     static_assert(1024 + kTables + 8 * (MXQ_MAX_EXPERTS + 1) <= 232448, "shared memory over the per-block limit");
-    static_assert(kBars % 8 == 0 && 8 * (2 * (kRaws + SETS) + 4) <= 256, "barrier region");
+    static_assert(kBars % 8 == 0 && 8 * (2 * (kRaws + kSlots) + 4) <= 256, "barrier region");
+    static_assert(kRaws >= kSlots && kSlots >= kSets, "see the order of the conversion's waits");
     static_assert(kHalf % 1024 == 0 && kRaw % 1024 == 0, "the 128-byte swizzle repeats every 1024 bytes");
-    static_assert(kTmemA + SETS * BK / 2 <= kTmem, "TMEM columns");
+    static_assert(kTmemA + kSlots * kSlotCols <= kTmem, "TMEM columns");
 };
 
 struct Params {
@@ -90,10 +103,10 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
 }
 
 template <int kCG, bool kF32>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Shape<kCG>::kThreads, 1)
     ragged_int8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Params p) {
     using S = Shape<kCG>;
-    constexpr int RAWS = S::kRaws;
+    constexpr int RAWS = S::kRaws, SETS = S::kSets, SLOTS = S::kSlots;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align<1024>(smem_raw);
     int32_t* s_off = reinterpret_cast<int32_t*>(smem + S::kTables);
@@ -105,8 +118,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
     const uint32_t rawf0 = smem_u32(bars), rawe0 = rawf0 + 8 * RAWS;
-    const uint32_t full0 = rawe0 + 8 * RAWS, empty0 = full0 + 8 * SETS;
-    const uint32_t accf0 = empty0 + 8 * SETS, acce0 = accf0 + 16;
+    const uint32_t full0 = rawe0 + 8 * RAWS, empty0 = full0 + 8 * SLOTS;
+    const uint32_t accf0 = empty0 + 8 * SLOTS, acce0 = accf0 + 16;
     volatile int* abort_flag = &s_abort;
     if (threadIdx.x == 0) {
         s_abort = 0;
@@ -114,13 +127,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(rawf0 + 8 * st, 1);
             mbar_init(rawe0 + 8 * st, 2 * CVT_WARPS);
         }
-        for (int st = 0; st < SETS; ++st) {
+        for (int st = 0; st < SLOTS; ++st) {
             mbar_init(full0 + 8 * st, kCG * 2 * CVT_WARPS);
             mbar_init(empty0 + 8 * st, 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < S::kBufs; ++b) {
             mbar_init(accf0 + 8 * b, 1);
-            mbar_init(acce0 + 8 * b, kCG * EPI_WARPS);
+            mbar_init(acce0 + 8 * b, kCG * S::kEpiWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmA) : "memory");
@@ -140,39 +153,41 @@ __global__ void __launch_bounds__(THREADS, 1)
     const Walk<kFprop, S::kFeat, S::kWide, S::kStep> W(p.N, p.K, p.E, s_off, s_slices, nullptr);
     const int64_t first = blockIdx.x / kCG, stride = gridDim.x / kCG;
 
-    if (warp == 0) {
-        // ------------------------------------------------------ TMA producer: this CTA's int8 boxes
-        int stage = 0;
-        uint32_t phase = 0;
-        int64_t fills = 0;
-        for (int64_t t = first; t < W.total; t += stride) {
-            const Tile T = W.get(t);
-            const int half = T.n / kCG, boxes = (half + S::kBox - 1) / S::kBox;
-            const int f = T.f0 + rank * kFM, c = T.c0 + rank * half;
-            for (int r = 0; r < T.red; r += BK) {
-                if (!mbar_wait(rawe0 + 8 * stage, phase ^ 1, abort_flag)) {
-                    drain_ring(rawf0, RAWS, fills);
-                    goto done_producer;
+    // Registers. Pair shape: 7 groups of four warps start with 72 each, and 56 + 2 * 88 + 2 * 72 + 2 * 64 = 504;
+    // few rows: 8 groups start with 64, and 56 + 96 + 3 * 64 + 3 * 56 = 512.
+    if (warp < S::kEpiFirst) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0) {
+            // -------------------------------------------------- TMA producer: this CTA's int8 boxes
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t fills = 0;
+            for (int64_t t = first; t < W.total; t += stride) {
+                const Tile T = W.get(t);
+                const int half = T.n / kCG, boxes = (half + S::kBox - 1) / S::kBox;  // this CTA's rows
+                const int f = T.f0 + rank * kFM, c = T.c0 + rank * half;
+                for (int r = 0; r < T.red; r += BK) {
+                    if (!mbar_wait(rawe0 + 8 * stage, phase ^ 1, abort_flag)) {
+                        drain_ring(rawf0, RAWS, fills);
+                        goto done_producer;
+                    }
+                    __syncwarp();
+                    const uint32_t fb = rawf0 + 8 * stage, a = smem_u32(smem) + S::kRawAt + stage * S::kRaw;
+                    if (elect_one()) {
+                        mbar_expect_tx(fb, (kFM + boxes * S::kBox) * BK);
+                        load_3d<1>(a, &tmA, fb, r, f, T.e);
+                        for (int i = 0; i < boxes; ++i)
+                            load_2d<1>(a + (kFM + i * S::kBox) * BK, &tmB, fb, r, c + S::kBox * i);
+                    }
+                    __syncwarp();
+                    ++fills;
+                    if (++stage == RAWS) { stage = 0; phase ^= 1; }
                 }
-                __syncwarp();
-                const uint32_t fb = rawf0 + 8 * stage, a = smem_u32(smem) + S::kRawAt + stage * S::kRaw;
-                if (elect_one()) {
-                    mbar_expect_tx(fb, (kFM + boxes * S::kBox) * BK);
-                    load_3d<1>(a, &tmA, fb, r, f, T.e);
-#pragma unroll
-                    for (int i = 0; i < S::kTok / S::kBox; ++i)
-                        if (i < boxes) load_2d<1>(a + (kFM + i * S::kBox) * BK, &tmB, fb, r, c + S::kBox * i);
-                }
-                __syncwarp();
-                ++fills;
-                if (++stage == RAWS) { stage = 0; phase ^= 1; }
             }
-        }
-    done_producer:;
-    } else if (warp == 1) {
-        // ------------------------------------------------------ MMA issuer (rank 0)
-        if (rank == 0) {
-            int set = 0, buf = 0;
+        done_producer:;
+        } else if (warp == 1 && rank == 0) {
+            // -------------------------------------------------- MMA issuer (rank 0)
+            int slot = 0, buf = 0;
             uint32_t phase = 0, aphase = 0;
             const uint64_t bd0 = smem_desc(smem_u32(smem), 16, 1024);
             for (int64_t t = first; t < W.total; t += stride) {
@@ -182,9 +197,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag)) goto done_mma;
                 __syncwarp();
                 for (int r = 0; r < T.red; r += BK) {
-                    const uint32_t at = tmem + S::kTmemA + set * (BK / 2);
-                    const uint64_t bd = bd0 + (uint64_t)(set * (2 * S::kHalf / 16));
-                    if (!mbar_wait(full0 + 8 * set, phase, abort_flag)) goto done_mma;
+                    const uint32_t at = tmem + S::kTmemA + slot * S::kSlotCols;
+                    const uint64_t off = (uint64_t)(slot * (S::kSlot / 16));
+                    if (!mbar_wait(full0 + 8 * slot, phase, abort_flag)) goto done_mma;
                     __syncwarp();
                     fence_after();
                     const int steps = T.red - r >= BK ? BK / 16 : (T.red - r + 15) / 16;
@@ -192,45 +207,49 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                         for (int k = 0; k < BK / 16; ++k)
                             if (k < steps)
-                                mma_f16_tmem<kCG>(d, at + 8 * k, bd + (k >> 2) * (S::kHalf / 16) + 2 * (k & 3), id,
+                                mma_f16_tmem<kCG>(d, at + 8 * k, bd0 + off + (k >> 2) * (S::kHalf / 16) + 2 * (k & 3), id,
                                                   r > 0 || k > 0);
-                        mma_commit<kCG>(empty0 + 8 * set);
+                        mma_commit<kCG>(empty0 + 8 * slot);
                         if (r + BK >= T.red) mma_commit<kCG>(accf0 + 8 * buf);
                     }
                     __syncwarp();
-                    set ^= 1;
-                    phase ^= set == 0;
+                    if (++slot == SLOTS) { slot = 0; phase ^= 1; }
                 }
-                buf ^= 1;
-                aphase ^= buf == 0;
+                if (++buf == S::kBufs) { buf = 0; aphase ^= 1; }
             }
         done_mma:;
         }
-    } else if (warp < 2 + EPI_WARPS) {
+    } else if (warp < S::kCvtFirst) {
         // ------------------------------------------------------ epilogue
-        const int q = warp & 3;
-        uint8_t* stage = smem + S::kEpi + (warp - 2) * kEpiBytes;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCG == 2 ? 88 : 96));
+        const int q = warp & 3, group = (warp - S::kEpiFirst) >> 2;
+        constexpr int kGroups = S::kEpiWarps / 4;
+        uint8_t* stage = smem + S::kEpi + (warp - S::kEpiFirst) * kEpiBytes;
         int buf = 0;
         uint32_t aphase = 0;
         for (int64_t t = first; t < W.total; t += stride) {
             const Tile T = W.get(t);
-            const int f0 = T.f0 + rank * kFM;
-            const int live = (int)min((int64_t)kFM, p.N - f0);
-            const bool ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
-            if (!__all_sync(0xffffffffu, ok && !*abort_flag)) break;
-            fence_after();
+            const int f0 = T.f0 + rank * kFM + 32 * q;  // of this warp's 32 lanes
+            const int live = (int)min((int64_t)32, p.N - f0);
+            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * S::kWide;
+            // scales and bias are fetched while the sums are made
             const float* xs = p.xs + T.row0;
+            auto ready = [&] {
+                const bool ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
+                fence_after();
+                return __all_sync(0xffffffffu, ok && !*abort_flag) != 0;
+            };
             if constexpr (kF32) {
-                const int l = q * 32 + lane;
-                const int64_t at = (int64_t)T.e * p.N + f0 + l;
-                const float sw = l < live ? p.ws[at] : 0.0f;
-                const float b = p.bias && l < live ? __bfloat162float(p.bias[at]) : 0.0f;
-                for (int c = 0; c < T.cols; c += 32) {
+                const int64_t at = (int64_t)T.e * p.N + f0 + lane;
+                const float sw = lane < live ? p.ws[at] : 0.0f;
+                const float b = p.bias && lane < live ? __bfloat162float(p.bias[at]) : 0.0f;
+                if (!ready()) break;
+                for (int c = 32 * group; c < T.cols; c += 32 * kGroups) {
                     uint32_t v[32];
-                    tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * S::kWide + c, v);
+                    tmem_ld32(acc + c, v);
                     tmem_wait_ld();
-                    if (l < live) {
-                        float* o = static_cast<float*>(p.out) + (T.row0 + c) * p.N + f0 + l;
+                    if (lane < live) {
+                        float* o = static_cast<float*>(p.out) + (T.row0 + c) * p.N + f0 + lane;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (c + j < T.cols) o[j * p.N] = __uint_as_float(v[j]) * __ldg(xs + c + j) * sw + b;
@@ -240,23 +259,31 @@ __global__ void __launch_bounds__(THREADS, 1)
                 float sw[4], b[4];
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const int l = q * 32 + (lane >> 2) + 8 * g;
+                    const int l = (lane >> 2) + 8 * g;
                     const int64_t at = (int64_t)T.e * p.N + f0 + l;
                     sw[g] = l < live ? p.ws[at] : 0.0f;
                     b[g] = p.bias && l < live ? __bfloat162float(p.bias[at]) : 0.0f;
                 }
-                for (int c = 0; c < T.cols; c += 32) {
-                    // this thread's token scales: columns 8b + 2 (lane mod 4) and the next
-                    float sx[8];
+                // this thread's token scales in 32 columns: columns 8b + 2 (lane mod 4) and the next
+                float sx[8];
+                auto scales = [&](int c) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int col = c + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
                         sx[i] = col < T.cols ? __ldg(xs + col) : 0.0f;
                     }
-                    store_columns_bf16(tmem + ((uint32_t)(q * 32) << 16) + buf * S::kWide + c, lane, stage,
-                                       static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * p.N + f0 + 32 * q, p.N,
-                                       live - 32 * q, T.cols - c, [&](float v, int l, int col) {
-                                           return v * sx[(col >> 3) * 2 + (col & 1)] * sw[l >> 3] + b[l >> 3];
+                };
+                scales(32 * group);
+                if (!ready()) break;
+                for (int c = 32 * group; c < T.cols; c += 32 * kGroups) {
+                    float s[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[i] = sx[i];
+                    scales(c + 32 * kGroups);
+                    store_columns_bf16(acc + c, lane, stage,
+                                       static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * p.N + f0, p.N, live,
+                                       T.cols - c, [&](float v, int l, int col) {
+                                           return v * s[(col >> 3) * 2 + (col & 1)] * sw[l >> 3] + b[l >> 3];
                                        });
                 }
             }
@@ -266,93 +293,93 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (rank == 0) mbar_arrive(acce0 + 8 * buf);
                 else arrive_remote_relaxed(mapa(acce0 + 8 * buf, 0));
             }
-            buf ^= 1;
-            aphase ^= buf == 0;
+            if (++buf == S::kBufs) { buf = 0; aphase ^= 1; }
         }
     } else {
         // ------------------------------------------------------ int8 -> f16, this CTA's rows
-        const int cw = warp - 2 - EPI_WARPS;
-        const bool weights = cw < SETS * CVT_WARPS;
-        const int set = cw / CVT_WARPS % SETS, q = warp & 3;
-        const int ct = (int)threadIdx.x - 32 * (2 + EPI_WARPS + cw / CVT_WARPS * CVT_WARPS);
-        const uint32_t lead_full = kCG == 2 ? mapa(full0 + 8 * set, 0) : 0;
-        const uint32_t slot_tmem = tmem + ((uint32_t)(32 * q) << 16) + S::kTmemA + set * (BK / 2);
-        uint8_t* slot = smem + set * 2 * S::kHalf;
-        int raw = 0, turn = 0;
+        // A set's turn is every kSets-th stage: wait for the next slot and for the stage, load the codes into
+        // registers and free the stage, widen them into the slot. The slot comes first: its last MMAs are
+        // those of SLOTS stages ago, so all earlier stages have been loaded, and with no fewer than SLOTS of
+        // them a stage's barrier cannot be more than one phase behind what a set waits for, although the other
+        // sets' phases are not its own.
+        const bool weights = warp < S::kTokFirst;
+        const int set = (warp - (weights ? S::kCvtFirst : S::kTokFirst)) / CVT_WARPS;
+        const uint32_t lead_full = kCG == 2 ? mapa(full0, 0) : 0;
+        int raw = 0, turn = 0, slot = 0;
         uint32_t rphase = 0, phase = 0;
-        for (int64_t t = first; t < W.total; t += stride) {
-            const Tile T = W.get(t);
-            for (int r = 0; r < T.red; r += BK) {
-                if (turn == set) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(rawf0 + 8 * raw, rphase, abort_flag))) goto done_convert;
-                    const uint8_t* src = smem + S::kRawAt + raw * S::kRaw;
-                    // the first half is widened into registers before the slot is free
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (weights) {
-                            // lane = feature: 64 codes of its 128-byte swizzled row (16-byte chunk ^= row mod 8)
-                            const uint8_t* row = src + (32 * q + lane) * BK;
-                            uint32_t v[32];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint4 w =
-                                    *reinterpret_cast<const uint4*>(row + (((4 * h + i) ^ (lane & 7)) << 4));
-                                const uint2 a = widen4(w.x), b = widen4(w.y), c = widen4(w.z), d = widen4(w.w);
-                                v[8 * i] = a.x, v[8 * i + 1] = a.y, v[8 * i + 2] = b.x, v[8 * i + 3] = b.y;
-                                v[8 * i + 4] = c.x, v[8 * i + 5] = c.y, v[8 * i + 6] = d.x, v[8 * i + 7] = d.y;
-                            }
-                            if (h == 0) {
-                                const bool ok = mbar_wait(empty0 + 8 * set, phase ^ 1, abort_flag);
-                                if (!__all_sync(0xffffffffu, ok)) goto done_convert;
-                                fence_after();  // the slot's last MMAs come before the writes
-                            }
-                            tmem_st32(slot_tmem + h * (HK / 2), v);
-                        } else {
-                            // rows beyond the slice are widened too: what they hold is never stored
-                            const uint8_t* tok = src + kFM * BK;
-                            constexpr int kUnits = S::kTok * (HK / 16) / (32 * CVT_WARPS);  // 16-byte chunks a thread
-                            uint4 w[kUnits];
-#pragma unroll
-                            for (int u = 0; u < kUnits; ++u) {
-                                const int row = (ct >> 2) + u * 8 * CVT_WARPS;
-                                w[u] = *reinterpret_cast<const uint4*>(tok + row * BK +
-                                                                       (((4 * h + (ct & 3)) ^ (row & 7)) << 4));
-                            }
-                            if (h == 0) {
-                                const bool ok = mbar_wait(empty0 + 8 * set, phase ^ 1, abort_flag);
-                                if (!__all_sync(0xffffffffu, ok)) goto done_convert;
-                            }
-#pragma unroll
-                            for (int u = 0; u < kUnits; ++u) {
-                                const int row = (ct >> 2) + u * 8 * CVT_WARPS, ch = 2 * (ct & 3);
-                                const uint2 a = widen4(w[u].x), b = widen4(w[u].y), c = widen4(w[u].z),
-                                            d = widen4(w[u].w);
-                                uint8_t* o = slot + h * S::kHalf + row * 128;
-                                *reinterpret_cast<uint4*>(o + ((ch ^ (row & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-                                *reinterpret_cast<uint4*>(o + (((ch + 1) ^ (row & 7)) << 4)) =
-                                    make_uint4(c.x, c.y, d.x, d.y);
-                            }
+        auto convert = [&](auto&& load, auto&& widen) {
+            for (int64_t t = first; t < W.total; t += stride) {
+                const Tile T = W.get(t);
+                for (int r = 0; r < T.red; r += BK) {
+                    if (turn == set) {
+                        const bool ok = mbar_wait(empty0 + 8 * slot, phase ^ 1, abort_flag) &&
+                                        mbar_wait(rawf0 + 8 * raw, rphase, abort_flag);
+                        if (!__all_sync(0xffffffffu, ok)) return;
+                        load(smem + S::kRawAt + raw * S::kRaw);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(rawe0 + 8 * raw);
+                        widen();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (rank == 0) mbar_arrive(full0 + 8 * slot);
+                            else arrive_remote(lead_full + 8 * slot);
                         }
                     }
-                    if (weights) {
-                        tmem_wait_st();
-                        fence_before();
-                    } else {
-                        fence_async_smem();
-                    }
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(rawe0 + 8 * raw);
-                        if (rank == 0) mbar_arrive(full0 + 8 * set);
-                        else arrive_remote(lead_full);
-                    }
-                    phase ^= 1;
+                    if (++turn == SETS) turn = 0;
+                    if (++slot == SLOTS) { slot = 0; phase ^= 1; }
+                    if (++raw == RAWS) { raw = 0; rphase ^= 1; }
                 }
-                turn ^= 1;
-                if (++raw == RAWS) { raw = 0; rphase ^= 1; }
             }
+        };
+        if (weights) {
+            // lane = feature: 128 codes of its swizzled row (16-byte chunk ^= row mod 8)
+            const int q = warp & 3;
+            const uint32_t quarter = tmem + ((uint32_t)(32 * q) << 16) + S::kTmemA;
+            uint4 w[BK / 16];
+            convert(
+                [&](const uint8_t* src) {
+#pragma unroll
+                    for (int i = 0; i < BK / 16; ++i)
+                        w[i] = *reinterpret_cast<const uint4*>(src + (32 * q + lane) * BK + ((i ^ (lane & 7)) << 4));
+                },
+                [&] {
+                    fence_after();  // the slot's last MMAs come before the writes
+#pragma unroll
+                    for (int i = 0; i < BK / 16; ++i)
+                        tmem_st8(quarter + slot * S::kSlotCols + 8 * i, widen4(w[i].x), widen4(w[i].y), widen4(w[i].z),
+                                 widen4(w[i].w));
+                    tmem_wait_st();
+                    fence_before();
+                });
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCG == 2 ? 64 : 56));
+            // rows beyond the slice are widened too: what they hold is never stored
+            constexpr int kUnits = S::kTok * (BK / 16) / (32 * CVT_WARPS);  // 16-byte chunks a thread
+            const int ct = (int)threadIdx.x & (32 * CVT_WARPS - 1);
+            uint4 w[kUnits];
+            convert(
+                [&](const uint8_t* src) {
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u)  // as they lie: no two lanes in a bank
+                        w[u] = *reinterpret_cast<const uint4*>(src + kFM * BK + (ct + u * 32 * CVT_WARPS) * 16);
+                },
+                [&] {
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) {
+                        const int row = (ct >> 3) + u * 4 * CVT_WARPS, ch = (ct & 7) ^ (row & 7);  // chunk of 8
+                        const uint2 a = widen4(w[u].x), b = widen4(w[u].y), c = widen4(w[u].z), d = widen4(w[u].w);
+                        uint8_t* o = smem + slot * S::kSlot + (ch >> 2) * S::kHalf + row * 128;
+                        // a row's eight lanes: four write even chunks of one half while four write odd ones of the
+                        // other, so that no two meet in a bank
+                        const bool odd = ch & 4;
+                        const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
+                        const int at = (2 * (ch & 3) + odd) ^ (row & 7);
+                        *reinterpret_cast<uint4*>(o + (at << 4)) = odd ? hi : lo;
+                        *reinterpret_cast<uint4*>(o + ((at ^ 1) << 4)) = odd ? lo : hi;
+                    }
+                    fence_async_smem();
+                });
         }
-    done_convert:;
     }
     fence_before();
     __syncthreads();
@@ -411,7 +438,7 @@ template <int kCG, bool kF32>
 static cudaError_t launch_int8(const CUtensorMap& a, const CUtensorMap& b, const i8::Params& p, int64_t tiles,
                                cudaStream_t s) {
     using S = i8::Shape<kCG>;
-    return launch_persistent<kCG, false, i8::ragged_int8_kernel<kCG, kF32>>(i8::THREADS, S::smem(MXQ_MAX_EXPERTS),
+    return launch_persistent<kCG, false, i8::ragged_int8_kernel<kCG, kF32>>(S::kThreads, S::smem(MXQ_MAX_EXPERTS),
                                                                      S::smem(p.E), tiles, s, a, b, p);
 }
 
@@ -430,7 +457,7 @@ static cudaError_t run_int8_shape(const Int8Call& c, cudaStream_t s) {
 }
 
 cudaError_t run_int8(const Int8Call& c, cudaStream_t s) {
-    return c.M <= (int64_t)i8::Shape<1>::kWide * c.E ? run_int8_shape<1>(c, s) : run_int8_shape<2>(c, s);
+    return c.M <= (int64_t)kFewRows * c.E ? run_int8_shape<1>(c, s) : run_int8_shape<2>(c, s);
 }
 
 cudaError_t run_int8_quantize(const void* x, int64_t M, int64_t K, int64_t ld, void* q, float* scale, cudaStream_t s) {
