@@ -392,8 +392,67 @@ __global__ void __launch_bounds__(Shape<kCG>::kThreads, 1)
 }
 
 // ------------------------------------------------------------ row quantizer
-// One block per row. A row with an infinity or NaN has no scale: its scale is
-// NaN and its codes are 0, so that its outputs are NaN and nothing else is.
+// A row with an infinity or NaN has no scale: its scale is NaN and its codes
+// are 0, so that its outputs are NaN and nothing else is. bf16 magnitudes are
+// compared as bits, two at a time: they order as the values do.
+__device__ __forceinline__ uint32_t top2(uint32_t top, const uint4& w) {
+    return __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                  __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+}
+struct RowScale {
+    float inv, scale;
+    bool finite;
+    __device__ explicit RowScale(uint32_t top) {  // bits of the row's largest magnitude
+        finite = top < 0x7F80u;
+        const float amax = fmaxf(__uint_as_float(top << 16), 7.8886090522101181e-31f);  // 2^-100
+        inv = finite ? __fdiv_rn(127.0f, amax) : 0.0f;
+        scale = finite ? __fdiv_rn(amax, 127.0f) : __uint_as_float(0x7FC00000u);
+    }
+    __device__ uint2 codes(const uint4& w) const {
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int a = finite ? __float2int_rn(__fmul_rn(bf16lo(ws[j]), inv)) : 0;
+            const int b = finite ? __float2int_rn(__fmul_rn(bf16hi(ws[j]), inv)) : 0;
+            o[j >> 1] |= ((uint32_t)(a & 255) | (uint32_t)(b & 255) << 8) << (16 * (j & 1));
+        }
+        return make_uint2(o[0], o[1]);
+    }
+};
+
+// Rows of at most kLanes * kVec * 8 elements: kLanes lanes hold a row in
+// registers, so it is read once and no block waits. 16384 x 2048: 27.8 us with
+// the block kernel below, 14.1 us with this one; 1000000 x 128: 884 and 74 us.
+template <int kLanes, int kVec>
+__global__ void __launch_bounds__(256) quantize_rows_lanes_kernel(const uint16_t* x, int64_t M, int64_t K, int64_t ld,
+                                                                  uint8_t* q, float* scale) {
+    wait_for_stream();
+    const int l = threadIdx.x % kLanes, vecs = (int)(K / 8);
+    const int64_t step = (int64_t)gridDim.x * (256 / kLanes);
+    for (int64_t m0 = (int64_t)blockIdx.x * (256 / kLanes); m0 < M; m0 += step) {
+        const int64_t m = m0 + threadIdx.x / kLanes;
+        const bool live = m < M;
+        const uint4* row = reinterpret_cast<const uint4*>(x + m * ld);
+        uint4 w[kVec];
+        uint32_t top = 0;
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+            w[v] = live && l + v * kLanes < vecs ? row[l + v * kLanes] : make_uint4(0u, 0u, 0u, 0u);
+            top = top2(top, w[v]);
+        }
+        top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const RowScale s(top);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v)
+            if (live && l + v * kLanes < vecs) *reinterpret_cast<uint2*>(q + m * K + 8 * (l + v * kLanes)) = s.codes(w[v]);
+        if (live && l == 0) scale[m] = s.scale;
+    }
+}
+
+// Longer rows: a block each, read twice (the second time from cache).
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* x, int64_t M, int64_t K, int64_t ld,
                                                             uint8_t* q, float* scale) {
     wait_for_stream();
@@ -401,34 +460,17 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* x, i
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
         const uint4* row = reinterpret_cast<const uint4*>(x + m * ld);
-        uint32_t top = 0;  // two bf16 magnitudes: their bits order as the values do
-        for (int64_t i = threadIdx.x; i < K / 8; i += 256) {
-            const uint4 w = row[i];
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                                         __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
-        }
+        uint32_t top = 0;
+        for (int64_t i = threadIdx.x; i < K / 8; i += 256) top = top2(top, row[i]);
         top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
         __syncthreads();
         if (lane == 0) s_top[warp] = top;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = max(top, s_top[i]);
-        const bool finite = top < 0x7F80u;
-        const float amax = fmaxf(__uint_as_float(top << 16), 7.8886090522101181e-31f);  // 2^-100
-        const float inv = finite ? __fdiv_rn(127.0f, amax) : 0.0f;
-        for (int64_t i = threadIdx.x; i < K / 8; i += 256) {
-            const uint4 w = row[i];
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-            uint32_t o[2] = {0, 0};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int a = finite ? __float2int_rn(__fmul_rn(bf16lo(ws[j]), inv)) : 0;
-                const int b = finite ? __float2int_rn(__fmul_rn(bf16hi(ws[j]), inv)) : 0;
-                o[j >> 1] |= ((uint32_t)(a & 255) | (uint32_t)(b & 255) << 8) << (16 * (j & 1));
-            }
-            *reinterpret_cast<uint2*>(q + m * K + 8 * i) = make_uint2(o[0], o[1]);
-        }
-        if (threadIdx.x == 0) scale[m] = finite ? __fdiv_rn(amax, 127.0f) : __uint_as_float(0x7FC00000u);
+        const RowScale s(top);
+        for (int64_t i = threadIdx.x; i < K / 8; i += 256) *reinterpret_cast<uint2*>(q + m * K + 8 * i) = s.codes(row[i]);
+        if (threadIdx.x == 0) scale[m] = s.scale;
     }
 }
 
@@ -462,9 +504,14 @@ cudaError_t run_int8(const Int8Call& c, cudaStream_t s) {
 
 cudaError_t run_int8_quantize(const void* x, int64_t M, int64_t K, int64_t ld, void* q, float* scale, cudaStream_t s) {
     if (M == 0) return cudaSuccess;
-    const unsigned grid = (unsigned)std::min<int64_t>(M, (int64_t)sm_count() * 8);
-    return launch(i8::quantize_rows_kernel, grid, 256, s, static_cast<const uint16_t*>(x), M, K, ld,
-                  static_cast<uint8_t*>(q), scale);
+    const auto run = [&](auto kernel, int64_t rows) {
+        const unsigned grid = (unsigned)std::min<int64_t>((M + rows - 1) / rows, (int64_t)sm_count() * 8);
+        return launch(kernel, grid, 256, s, static_cast<const uint16_t*>(x), M, K, ld, static_cast<uint8_t*>(q), scale);
+    };
+    if (K <= 128) return run(i8::quantize_rows_lanes_kernel<8, 2>, 32);
+    if (K <= 512) return run(i8::quantize_rows_lanes_kernel<32, 2>, 8);
+    if (K <= 2048) return run(i8::quantize_rows_lanes_kernel<32, 8>, 8);
+    return run(i8::quantize_rows_kernel, 1);
 }
 
 }  // namespace ragged
