@@ -388,13 +388,17 @@ MXQ_API int mxq_swiglu_bwd_quantize(const void* dh_bf16, const void* y_bf16, int
  * The three products of an expert layer on bf16 operands, for expert counts
  * that are multiples of nothing: any m_e >= 0 with sum(m_e) == M (device
  * memory; a negative count or a wrong sum sets the status word and writes
- * nothing). N and K are multiples of 8, at most 2^20. x and dy may be slices
- * of wider rows: ldx, lddy are row strides in elements, multiples of 8 and at
- * least the row's width. W is one contiguous (E, N, K) tensor. Sums are fp32
- * and rounded once. An expert without rows reads nothing and, in wgrad, gets a
+ * nothing). M is at most 2^28; N and K are multiples of 8, at most 2^20. x and
+ * dy may be slices of wider rows: ldx, lddy are row strides in elements,
+ * multiples of 8 and at least the row's width. W is one contiguous (E, N, K)
+ * tensor. Outputs are contiguous and overlap no input. Sums are fp32 and
+ * rounded once. An expert without rows reads nothing and, in wgrad, gets a
  * zero dW (untouched with MXQ_ACCUMULATE). Infinities and NaN stay in the
  * rows (fprop, dgrad) or the expert (wgrad) that they belong to. Outputs are
- * the same bits from run to run. No workspace. */
+ * the same bits from run to run. No workspace.
+ *
+ * These calls, the int8 calls and dropout may begin while the stream's
+ * previous kernel ends; they wait for it before they read or write memory. */
 
 /* y[m,:] = x[m,:] . w[e(m)]^T (+ bias[e(m)]); y (M, N) bf16, or fp32 with
  * MXQ_OUT_F32; bias (E, N) bf16 or NULL. */

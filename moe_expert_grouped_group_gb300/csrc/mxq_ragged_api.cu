@@ -16,7 +16,8 @@ using mxq::fail_cuda;
 
 namespace {
 
-constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 512, kMaxWidth = (int64_t)1 << 20;
+// At most 2^28 rows: a wgrad tile that sums over all of them takes 1.5 s, less than the kernels' bounded waits.
+constexpr int64_t kMaxRows = (int64_t)1 << 28, kMaxWidth = (int64_t)1 << 20;
 
 // Shapes shared by the ragged products: every width a multiple of `step`.
 int check_ragged(int64_t M, int64_t N, int64_t K, int step_n, int step_k, int E, const int64_t* m_splits) {

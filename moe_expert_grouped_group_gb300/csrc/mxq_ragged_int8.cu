@@ -355,27 +355,27 @@ __global__ void __launch_bounds__(Shape<kCG>::kThreads, 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCG == 2 ? 64 : 56));
             // rows beyond the slice are widened too: what they hold is never stored
             constexpr int kUnits = S::kTok * (BK / 16) / (32 * CVT_WARPS);  // 16-byte chunks a thread
-            const int ct = (int)threadIdx.x & (32 * CVT_WARPS - 1);
+            // Eight lanes (a quarter warp) take four chunks of one row's first half of K and four of the next
+            // row's second half: no two of them meet in a bank, neither here nor where they write.
+            const int ct = (int)threadIdx.x & (32 * CVT_WARPS - 1), second = ct >> 2 & 1, cc = ct & 3;
+            auto row_of = [&](int u) { return (((ct >> 3) + u * 4 * CVT_WARPS) & ~1) + second; };
+            const int half = second ^ (ct >> 3 & 1);
             uint4 w[kUnits];
             convert(
                 [&](const uint8_t* src) {
 #pragma unroll
-                    for (int u = 0; u < kUnits; ++u)  // as they lie: no two lanes in a bank
-                        w[u] = *reinterpret_cast<const uint4*>(src + kFM * BK + (ct + u * 32 * CVT_WARPS) * 16);
+                    for (int u = 0; u < kUnits; ++u)
+                        w[u] = *reinterpret_cast<const uint4*>(src + (kFM + row_of(u)) * BK +
+                                                               (((4 * half + cc) ^ (row_of(u) & 7)) << 4));
                 },
                 [&] {
 #pragma unroll
                     for (int u = 0; u < kUnits; ++u) {
-                        const int row = (ct >> 3) + u * 4 * CVT_WARPS, ch = (ct & 7) ^ (row & 7);  // chunk of 8
                         const uint2 a = widen4(w[u].x), b = widen4(w[u].y), c = widen4(w[u].z), d = widen4(w[u].w);
-                        uint8_t* o = smem + slot * S::kSlot + (ch >> 2) * S::kHalf + row * 128;
-                        // a row's eight lanes: four write even chunks of one half while four write odd ones of the
-                        // other, so that no two meet in a bank
-                        const bool odd = ch & 4;
-                        const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
-                        const int at = (2 * (ch & 3) + odd) ^ (row & 7);
-                        *reinterpret_cast<uint4*>(o + (at << 4)) = odd ? hi : lo;
-                        *reinterpret_cast<uint4*>(o + ((at ^ 1) << 4)) = odd ? lo : hi;
+                        uint8_t* o = smem + slot * S::kSlot + half * S::kHalf + row_of(u) * 128;
+                        const int at = (2 * cc) ^ (row_of(u) & 7);
+                        *reinterpret_cast<uint4*>(o + (at << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+                        *reinterpret_cast<uint4*>(o + ((at ^ 1) << 4)) = make_uint4(c.x, c.y, d.x, d.y);
                     }
                     fence_async_smem();
                 });
