@@ -223,13 +223,13 @@ static float scale_of(uint32_t t) { return t >= 65536u ? 0.0f : (float)(65536.0 
 cudaError_t run_swiglu_dropout_fwd(const void* y, int64_t M, int64_t F, const int64_t* rng, uint32_t t, void* h,
                                    cudaStream_t s) {
     if (M == 0) return cudaSuccess;
-    return launch(swiglu_dropout_fwd_kernel, grid_for(M * (F / 8)), 256, s, (const uint16_t*)y, M, F, rng, keep_of(t),
+    return launch(swiglu_dropout_fwd_kernel, grid_for(M * (F / 8)), 256, s, 0, (const uint16_t*)y, M, F, rng, keep_of(t),
                   scale_of(t), (uint16_t*)h);
 }
 cudaError_t run_swiglu_dropout_bwd(const void* dh, const void* y, int64_t M, int64_t F, const int64_t* rng, uint32_t t,
                                    void* dy, cudaStream_t s) {
     if (M == 0) return cudaSuccess;
-    return launch(swiglu_dropout_bwd_kernel, grid_for(M * (F / 8)), 256, s, (const uint16_t*)dh, (const uint16_t*)y, M, F,
+    return launch(swiglu_dropout_bwd_kernel, grid_for(M * (F / 8)), 256, s, 0, (const uint16_t*)dh, (const uint16_t*)y, M, F,
                   rng, keep_of(t), scale_of(t), (uint16_t*)dy);
 }
 cudaError_t run_dropout(const void* x, const void* residual, int64_t n, int f32, const int64_t* rng, uint32_t t,
@@ -237,9 +237,9 @@ cudaError_t run_dropout(const void* x, const void* residual, int64_t n, int f32,
     if (n == 0) return cudaSuccess;
     const unsigned grid = grid_for((n + 7) / 8);
     if (f32)
-        return launch(dropout_kernel<float>, grid, 256, s, (const float*)x, (const float*)residual, n, rng, keep_of(t),
+        return launch(dropout_kernel<float>, grid, 256, s, 0, (const float*)x, (const float*)residual, n, rng, keep_of(t),
                       scale_of(t), (float*)out);
-    return launch(dropout_kernel<__nv_bfloat16>, grid, 256, s, (const __nv_bfloat16*)x, (const __nv_bfloat16*)residual, n,
+    return launch(dropout_kernel<__nv_bfloat16>, grid, 256, s, 0, (const __nv_bfloat16*)x, (const __nv_bfloat16*)residual, n,
                   rng, keep_of(t), scale_of(t), (__nv_bfloat16*)out);
 }
 

@@ -48,6 +48,12 @@ struct Int8Call {
     int32_t* status;
 };
 cudaError_t run_int8(const Int8Call& c, cudaStream_t s);
+// the int8 product, and fprop where its tiles leave SMs idle, of at most kVecRows rows an expert on average;
+// int8: K up to kVecDepth
+constexpr int kVecRows = 4;
+constexpr int64_t kVecDepth = (1 << 17) - 16;  // |codes| <= 128: sums below 2^31
+cudaError_t run_fprop_vec(const GemmCall& c, cudaStream_t s);
+cudaError_t run_int8_vec(const Int8Call& c, cudaStream_t s);
 cudaError_t run_int8_quantize(const void* x, int64_t M, int64_t K, int64_t ld, void* q, float* scale, cudaStream_t s);
 
 // Encodes a tensor map of 1-byte (E4M3 / int8 bytes) or 2-byte elements in up

@@ -13,7 +13,8 @@
 //
 // The tile walk, the operands' sides (features on the MMA's M, tokens on its
 // N), the edges and the two shapes (pairs of SMs; one SM for few rows) are
-// those of the bf16 products (mxq_ragged.cuh, mxq_ragged.cu).
+// those of the bf16 products (mxq_ragged.cuh, mxq_ragged.cu). A handful of rows
+// an expert goes to mxq_ragged_vec.cu.
 //
 // The widened weights go to TMEM, the widened tokens to shared memory: with
 // both in shared memory a 256 x 256 tile of a pair moves 96 KB and more through
@@ -499,6 +500,7 @@ static cudaError_t run_int8_shape(const Int8Call& c, cudaStream_t s) {
 }
 
 cudaError_t run_int8(const Int8Call& c, cudaStream_t s) {
+    if (c.M <= (int64_t)kVecRows * c.E && c.K <= kVecDepth) return run_int8_vec(c, s);
     return c.M <= (int64_t)kFewRows * c.E ? run_int8_shape<1>(c, s) : run_int8_shape<2>(c, s);
 }
 
@@ -506,7 +508,7 @@ cudaError_t run_int8_quantize(const void* x, int64_t M, int64_t K, int64_t ld, v
     if (M == 0) return cudaSuccess;
     const auto run = [&](auto kernel, int64_t rows) {
         const unsigned grid = (unsigned)std::min<int64_t>((M + rows - 1) / rows, (int64_t)sm_count() * 8);
-        return launch(kernel, grid, 256, s, static_cast<const uint16_t*>(x), M, K, ld, static_cast<uint8_t*>(q), scale);
+        return launch(kernel, grid, 256, s, 0, static_cast<const uint16_t*>(x), M, K, ld, static_cast<uint8_t*>(q), scale);
     };
     if (K <= 128) return run(i8::quantize_rows_lanes_kernel<8, 2>, 32);
     if (K <= 512) return run(i8::quantize_rows_lanes_kernel<32, 2>, 8);

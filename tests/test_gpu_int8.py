@@ -154,3 +154,38 @@ def test_wrong_counts_and_refusals(mxq):
     ):
         with pytest.raises(mxq.MXQError):
             call()
+
+
+# single tokens and a handful of rows an expert: dot products on the integer units; 9 rows in one of four
+# experts are two slices of it; 17 and 40 rows an expert go to the tensor cores
+@pytest.mark.parametrize("counts", [[1], [2], [3], [4], [0, 8], [9, 0, 0, 0], [1, 2, 3, 4, 5, 6], [0, 0, 0, 16, 0],
+                                    [17], [40, 3]])
+@pytest.mark.parametrize("N,K", [(8, 16), (24, 528), (136, 1008), (1000, 2048), (40, 7168)])
+def test_few_rows(mxq, counts, N, K):
+    M, E, ms = sum(counts), len(counts), dev_i64(counts)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    code = lambda *s: torch.randint(-128, 128, s, generator=g, device="cuda", dtype=torch.int8)  # noqa: E731
+    xq, wq, bias = code(M, K), code(E, N, K), rand(4, E, N, std=100.0)
+    xs, ws = torch.rand(M, generator=g, device="cuda") + 0.01, torch.rand(E, N, generator=g, device="cuda") + 0.01
+    ref, mag = fprop64(xq, wq, counts)
+    for e, r in spans(counts):
+        f = xs[r, None].double() * ws[e].double()
+        ref[r], mag[r] = ref[r] * f + bias[e].double(), mag[r] * f + bias[e].double().abs()
+    for dt, tag in ((BF16, "bf16"), (F32, "f32")):
+        y = mxq.int8_gemm_fprop(xq, xs, wq, ws, ms, bias=bias, out_dtype=dt)
+        assert_products(y, ref, mag, K, tag)
+        assert torch.equal(y, mxq.int8_gemm_fprop(xq, xs, wq, ws, ms, bias=bias, out_dtype=dt))
+
+
+def test_the_largest_sums_of_the_integer_path(mxq):
+    """K just below 2^17 with every code -128: the sum 2^31 - 2^18 still fits."""
+    K = (1 << 17) - 16
+    xq = torch.full((1, K), -128, dtype=torch.int8, device="cuda")
+    wq = torch.full((1, 8, K), -128, dtype=torch.int8, device="cuda")
+    one, ones = torch.ones(1, device="cuda"), torch.ones((1, 8), device="cuda")
+    y = mxq.int8_gemm_fprop(xq, one, wq, ones, dev_i64([1]), out_dtype=F32)
+    assert torch.all(y == float(K * 16384))
+    K = 1 << 17  # the tensor cores' fp32 sums
+    xq, wq = xq.new_full((1, K), -128), wq.new_full((1, 8, K), -128)
+    y = mxq.int8_gemm_fprop(xq, one, wq, ones, dev_i64([1]), out_dtype=F32)
+    assert torch.all((y - K * 16384.0).abs() <= K / 16 * 2.0 ** -22 * K * 16384.0)
