@@ -686,11 +686,14 @@ _empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", N
 
 def _new(shape, dtype, like):
     if _empty_strided is not None and like.get_device() == torch.cuda.current_device():
-        strides, n = [], 1
-        for d in reversed(shape):
-            strides.append(n)
-            n *= d
-        return _empty_strided(shape, tuple(strides[::-1]), dtype)
+        d = len(shape)
+        if d == 2:
+            strides = (shape[1], 1)
+        elif d == 3:
+            strides = (shape[1] * shape[2], shape[2], 1)
+        else:
+            strides = (1,) if d == 1 else torch.empty(shape, device="meta").stride()
+        return _empty_strided(shape, strides, dtype)
     return torch.empty(shape, dtype=dtype, device=like.device)
 
 
@@ -733,12 +736,14 @@ def _out(out, out_dtype, shape, like, default, other, flag):
 
 def _grouping(m_splits, E):
     """Pointer of the E device-resident counts."""
-    p = _dev(_splits(m_splits), "m_splits", 0, _I64T)
-    if p is None:
+    if (isinstance(m_splits, torch.Tensor) and m_splits.dtype is torch.int64 and m_splits.is_cuda
+            and m_splits.is_contiguous() and m_splits.numel() == E):
+        return m_splits.data_ptr()
+    if _splits(m_splits) is None:
         raise MXQError("m_splits is required")
     if m_splits.numel() != E:
         raise MXQError(f"m_splits: {m_splits.numel()} counts for {E} experts")
-    return p
+    return _ptr(m_splits)
 
 
 def ragged_gemm_fprop(x, w, m_splits, bias=None, out_dtype=None, status=None, out=None):
