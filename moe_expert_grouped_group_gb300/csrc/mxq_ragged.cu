@@ -391,22 +391,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (l < live) {
                     const float b =
                         kMode == kFprop && p.bias ? __bfloat162float(p.bias[(int64_t)T.e * p.N + f0 + l]) : 0.0f;
+                    // whole tiles without accumulation: nothing but stores, 128 bytes a warp
+                    auto each = [&](auto&& put) {
 #pragma unroll
-                    for (int i = 0; i < kChunks; ++i)
+                        for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int c = 64 * i + 32 * group + j;
-                            if (c >= T.cols) break;
-                            const int64_t at = (T.row0 + c) * ld + f0 + l;
-                            const float v = __fadd_rn(acc[i][j], b);
-                            if (p.out_f32) {
-                                float* o = static_cast<float*>(p.out) + at;
-                                *o = p.accumulate ? *o + v : v;
-                            } else {  // bf16 with accumulation
-                                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
-                                *o = __float2bfloat16_rn(__bfloat162float(*o) + v);
-                            }
-                        }
+                            for (int j = 0; j < 32; ++j) put(64 * i + 32 * group + j, __fadd_rn(acc[i][j], b));
+                    };
+                    const int64_t at = T.row0 * ld + f0 + l;
+                    if (p.out_f32 && !p.accumulate && T.cols == WIDE) {
+                        float* o = static_cast<float*>(p.out) + at;
+                        each([&](int c, float v) { o[c * ld] = v; });
+                    } else if (p.out_f32) {
+                        float* o = static_cast<float*>(p.out) + at;
+                        each([&](int c, float v) {
+                            if (c < T.cols) o[c * ld] = p.accumulate ? o[c * ld] + v : v;
+                        });
+                    } else {  // bf16 with accumulation
+                        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
+                        each([&](int c, float v) {
+                            if (c < T.cols) o[c * ld] = __float2bfloat16_rn(__bfloat162float(o[c * ld]) + v);
+                        });
+                    }
                 }
             } else {
                 const bool ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
