@@ -450,7 +450,7 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 bool encode_tmap(CUtensorMap* m, const void* base, int elem_bytes, int rank, const int64_t* dims,
-                 const int64_t* strides, const int* box, int swizzle_bytes) {
+                 const int64_t* strides, const int* box) {
     static EncodeTiledFn fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -471,7 +471,7 @@ bool encode_tmap(CUtensorMap* m, const void* base, int elem_bytes, int rank, con
     }
     return fn(m, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
               const_cast<void*>(base), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle_bytes == 0 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -506,15 +506,15 @@ static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
         const int64_t rows = std::max<int64_t>(c.M, 1);
         const int64_t da[2] = {c.K, rows}, sa[1] = {2 * c.ld_tok}, db[2] = {c.N, rows}, sb[1] = {2 * c.ld_mat};
         const int boxa[2] = {64, BK}, boxb[2] = {BOX, BK};
-        ok = encode_tmap(&a, c.M ? c.tok : c.out, 2, 2, da, sa, boxa, 128) &&
-             encode_tmap(&b, c.M ? c.mat : c.out, 2, 2, db, sb, boxb, 128);
+        ok = encode_tmap(&a, c.M ? c.tok : c.out, 2, 2, da, sa, boxa) &&
+             encode_tmap(&b, c.M ? c.mat : c.out, 2, 2, db, sb, boxb);
         half = b;
     } else {
         const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {2 * c.K, 2 * c.K * c.N};
         const int64_t db[2] = {kMode == kDgrad ? c.N : c.K, c.M}, sb[1] = {2 * c.ld_tok};
         const int boxa[3] = {64, kMode == kDgrad ? BK : kFM, 1}, boxb[2] = {BK, BOX}, boxh[2] = {BK, BOX / 2};
-        ok = encode_tmap(&a, c.mat, 2, 3, da, sa, boxa, 128) && encode_tmap(&b, c.tok, 2, 2, db, sb, boxb, 128) &&
-             encode_tmap(&half, c.tok, 2, 2, db, sb, boxh, 128);
+        ok = encode_tmap(&a, c.mat, 2, 3, da, sa, boxa) && encode_tmap(&b, c.tok, 2, 2, db, sb, boxb) &&
+             encode_tmap(&half, c.tok, 2, 2, db, sb, boxh);
     }
     if (!ok) return cudaErrorInvalidValue;
     return c.out_f32 || c.accumulate ? launch<kMode, true>(a, b, half, p, tiles, s)

@@ -1,6 +1,7 @@
-// mxq_ragged.cuh -- what the ragged grouped products (mxq_ragged.cu, bf16;
-// mxq_ragged_int8.cu, int8) share: the tables of a ragged grouping, the tile
-// walk and the tcgen05 wrappers for 16-bit floating operands.
+// mxq_ragged.cuh -- what the ragged grouped products (mxq_ragged.cu and
+// mxq_ragged_few.cu, bf16; mxq_ragged_int8.cu; mxq_ragged_vec.cu) share: the
+// tables of a ragged grouping, the tile walk and queue, split sums, the bf16
+// epilogue, the tcgen05 wrappers for 16-bit floating operands, the launchers.
 #pragma once
 
 #include <cuda.h>
@@ -17,8 +18,7 @@
 namespace mxq {
 namespace ragged {
 
-constexpr int kFM = 128;        // MMA M: rows of A (weight features) per CTA
-constexpr int kBoxBytes = 128;  // inner extent of every operand box: the 128-byte swizzle span
+constexpr int kFM = 128;  // MMA M: rows of A (features) per CTA
 
 // ------------------------------------------------------------ PTX wrappers
 // These kernels are launched so that they may begin while the stream's previous

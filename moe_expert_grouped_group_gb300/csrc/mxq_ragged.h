@@ -56,11 +56,11 @@ cudaError_t run_fprop_vec(const GemmCall& c, cudaStream_t s);
 cudaError_t run_int8_vec(const Int8Call& c, cudaStream_t s);
 cudaError_t run_int8_quantize(const void* x, int64_t M, int64_t K, int64_t ld, void* q, float* scale, cudaStream_t s);
 
-// Encodes a tensor map of 1-byte (E4M3 / int8 bytes) or 2-byte elements in up
+// Encodes a tensor map of int8 or bf16 elements (by their bytes) in up
 // to three dimensions: dims and box innermost first, strides in bytes of
-// dimensions 1 and 2, swizzle of 0 (none) or 128 bytes. False on failure.
+// dimensions 1 and 2, the 128-byte swizzle. False on failure.
 bool encode_tmap(CUtensorMap* m, const void* base, int elem_bytes, int rank, const int64_t* dims,
-                 const int64_t* strides, const int* box, int swizzle_bytes);
+                 const int64_t* strides, const int* box);
 int sm_count();
 
 // t of 65536 elements dropped; scale = 65536 / (65536 - t), 0 when t = 65536.

@@ -233,7 +233,7 @@ static cudaError_t run(const GemmCall& c, cudaStream_t s) {
     const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {2 * c.K, 2 * c.K * c.N}, db[2] = {red, c.M}, sb[1] = {2 * c.ld_tok};
     const int boxa[3] = {64, kMode == kDgrad ? BK : kFM, 1}, boxb[2] = {BK, WIDE};
     CUtensorMap a, b;
-    if (!encode_tmap(&a, c.mat, 2, 3, da, sa, boxa, 128) || !encode_tmap(&b, c.tok, 2, 2, db, sb, boxb, 128))
+    if (!encode_tmap(&a, c.mat, 2, 3, da, sa, boxa) || !encode_tmap(&b, c.tok, 2, 2, db, sb, boxb))
         return cudaErrorInvalidValue;
     const int64_t tiles = (c.M / WIDE + std::min<int64_t>(c.E, c.M)) * feats;  // no fewer than the device counts
     switch (split_of(tiles, (red + BK - 1) / BK)) {

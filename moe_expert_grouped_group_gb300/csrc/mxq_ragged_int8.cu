@@ -493,7 +493,7 @@ static cudaError_t run_int8_shape(const Int8Call& c, cudaStream_t s) {
     const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {c.K, c.K * c.N}, db[2] = {c.K, c.M}, sb[1] = {c.K};
     const int boxa[3] = {i8::BK, kFM, 1}, boxb[2] = {i8::BK, S::kBox};
     CUtensorMap a, b;
-    if (!encode_tmap(&a, c.wq, 1, 3, da, sa, boxa, 128) || !encode_tmap(&b, c.xq, 1, 2, db, sb, boxb, 128))
+    if (!encode_tmap(&a, c.wq, 1, 3, da, sa, boxa) || !encode_tmap(&b, c.xq, 1, 2, db, sb, boxb))
         return cudaErrorInvalidValue;
     const int64_t tiles = (c.M / S::kWide + std::min<int64_t>(c.E, c.M)) * ((c.N + S::kFeat - 1) / S::kFeat);
     return c.out_f32 ? launch_int8<kCG, true>(a, b, p, tiles, s) : launch_int8<kCG, false>(a, b, p, tiles, s);
