@@ -100,7 +100,8 @@ struct Params {
 template <int kMode, bool kRegs>
 __global__ void __launch_bounds__(THREADS, 1)
     ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ CUtensorMap tmHalf, Params p) {
+                       const __grid_constant__ CUtensorMap tmHalf, const __grid_constant__ CUtensorMap tmOut,
+                       Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align<1024>(smem_raw);
     int32_t* s_off = reinterpret_cast<int32_t*>(smem + TABLE_REGION);
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
         // ------------------------------------------------------ epilogue
         const int q = warp & 3, group = (warp - 2) >> 2;  // two groups of four warps share the columns
-        uint8_t* stage = smem + EPI_REGION + (warp - 2) * kEpiBytes;
+        uint8_t* stage = smem + EPI_REGION + (warp - 2) * (kMode == kWgrad ? kBoxBytes : kEpiBytes);
         const int64_t ld = kMode == kFprop ? p.N : p.K;  // features
         int buf = 0;
         uint32_t aphase = 0;
@@ -426,13 +427,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (l < live) b[g] = __bfloat162float(p.bias[(int64_t)T.e * p.N + f0 + l]);
                     }
                 }
-                for (int c = 32 * group; c < T.cols; c += 64)
-                    store_columns_bf16(tmem + ((uint32_t)(q * 32) << 16) + buf * WIDE + c, lane, stage,
-                                       static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * ld + f0 + 32 * q, ld,
-                                       live - 32 * q, T.cols - c, [&](float v, int l, int) { return v + b[l >> 3]; });
+                const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * WIDE;
+                for (int c = 32 * group; c < T.cols; c += 64) {
+                    if constexpr (kMode == kWgrad)
+                        store_box_bf16(acc + c, lane, stage, &tmOut, f0 + 32 * q, T.c0 + c, T.e, live > 32 * q);
+                    else
+                        store_columns_bf16(acc + c, lane, stage,
+                                           static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * ld + f0 + 32 * q, ld,
+                                           live - 32 * q, T.cols - c, [&](float v, int l, int) { return v + b[l >> 3]; });
+                }
                 drained();
             }
         } while (queue.next(t, lane, abort_flag) == TileQueue::kTile);
+        if (kMode == kWgrad && !kRegs) {  // the last boxes are written before the block leaves its shared memory
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            __syncwarp();
+        }
     }
     fence_before();
     __syncthreads();
@@ -450,7 +460,7 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 bool encode_tmap(CUtensorMap* m, const void* base, int elem_bytes, int rank, const int64_t* dims,
-                 const int64_t* strides, const int* box) {
+                 const int64_t* strides, const int* box, int swizzle_bytes) {
     static EncodeTiledFn fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -471,7 +481,7 @@ bool encode_tmap(CUtensorMap* m, const void* base, int elem_bytes, int rank, con
     }
     return fn(m, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
               const_cast<void*>(base), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B,
+              swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -486,17 +496,17 @@ int sm_count() {
 }
 
 template <int kMode, bool kRegs>
-static cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& half, const Params& p,
-                          int64_t tiles, cudaStream_t s) {
+static cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& half, const CUtensorMap& out,
+                          const Params& p, int64_t tiles, cudaStream_t s) {
     return launch_persistent<CG, true, ragged_gemm_kernel<kMode, kRegs>>(THREADS, smem_bytes(MXQ_MAX_EXPERTS), smem_bytes(p.E),
-                                                                   tiles, s, a, b, half, p);
+                                                                   tiles, s, a, b, half, out, p);
 }
 
 template <int kMode>
 static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
     const Params p{c.M, c.N, c.K, c.E, c.m_splits, static_cast<const __nv_bfloat16*>(c.bias), c.out, c.out_f32,
                    c.accumulate, c.status};
-    CUtensorMap a, b, half;  // half: b in boxes of half the rows
+    CUtensorMap a, b, half, out;  // half: b in boxes of half the rows; out: dW as bf16 (wgrad)
     bool ok;
     const int64_t feats = ((kMode == kFprop ? c.N : c.K) + FEAT - 1) / FEAT;
     int64_t tiles = (c.M / WIDE + std::min<int64_t>(c.E, c.M)) * feats;  // no fewer than the device counts
@@ -509,6 +519,9 @@ static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
         ok = encode_tmap(&a, c.M ? c.tok : c.out, 2, 2, da, sa, boxa) &&
              encode_tmap(&b, c.M ? c.mat : c.out, 2, 2, db, sb, boxb);
         half = b;
+        const int64_t dd[3] = {c.K, c.N, c.E}, sd[2] = {2 * c.K, 2 * c.K * c.N};
+        const int boxd[3] = {32, 32, 1};
+        if (ok && !c.out_f32) ok = encode_tmap(&out, c.out, 2, 3, dd, sd, boxd, 64);
     } else {
         const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {2 * c.K, 2 * c.K * c.N};
         const int64_t db[2] = {kMode == kDgrad ? c.N : c.K, c.M}, sb[1] = {2 * c.ld_tok};
@@ -516,9 +529,10 @@ static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
         ok = encode_tmap(&a, c.mat, 2, 3, da, sa, boxa) && encode_tmap(&b, c.tok, 2, 2, db, sb, boxb) &&
              encode_tmap(&half, c.tok, 2, 2, db, sb, boxh);
     }
+    if (kMode != kWgrad || c.out_f32) out = a;  // not read
     if (!ok) return cudaErrorInvalidValue;
-    return c.out_f32 || c.accumulate ? launch<kMode, true>(a, b, half, p, tiles, s)
-                                     : launch<kMode, false>(a, b, half, p, tiles, s);
+    return c.out_f32 || c.accumulate ? launch<kMode, true>(a, b, half, out, p, tiles, s)
+                                     : launch<kMode, false>(a, b, half, out, p, tiles, s);
 }
 
 cudaError_t run_gemm(const GemmCall& c, cudaStream_t s) {

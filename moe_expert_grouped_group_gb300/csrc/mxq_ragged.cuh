@@ -255,17 +255,14 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
 // warps writing 256-byte pieces together, at barriers, measured the same.
 constexpr int kEpiRow = 80, kEpiBytes = 32 * kEpiRow;
 
-// Columns 0 .. 31 of the accumulator at tmem, lanes 32 q .. of it, each value passed through
-// f(value, lane in 0..31, column in 0..31), to out + column * ld + lane for lanes < live and
-// columns < cols. Called by a warp; `stage` is its own.
+// Columns 0 .. 31 of 32 accumulator lanes at tmem, each value passed through f(value, lane in 0..31, column
+// in 0..31), rounded and packed two columns at a time: [8-column block][8-lane block] for stmatrix .trans.
 template <class F>
-__device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int lane, uint8_t* stage, __nv_bfloat16* out,
-                                                   int64_t ld, int live, int cols, F f) {
+__device__ __forceinline__ void columns_bf16(uint32_t tmem, int lane, uint32_t (&w)[4][4], F f) {
     uint32_t v[2][16];
     tmem_ld16x32(tmem, v[0]);
     tmem_ld16x32(tmem + (16u << 16), v[1]);
     tmem_wait_ld();
-    uint32_t w[4][4];  // [8-column block][8-lane block]
     const int fl = lane >> 2, fc = 2 * (lane & 3);
 #pragma unroll
     for (int b = 0; b < 4; ++b)
@@ -274,13 +271,25 @@ __device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int lane, uint
             const int r = 4 * b + 2 * (g & 1), l = fl + 8 * g, col = 8 * b + fc;
             w[b][g] = bf16x2_bits(f(__uint_as_float(v[g >> 1][r]), l, col), f(__uint_as_float(v[g >> 1][r + 1]), l, col + 1));
         }
+}
+
+__device__ __forceinline__ void stmatrix_trans(uint32_t row, const uint32_t (&w)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(row), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
+}
+
+// The same columns to out + column * ld + lane for lanes < live and columns < cols. Called by a warp; `stage`
+// is its own.
+template <class F>
+__device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int lane, uint8_t* stage, __nv_bfloat16* out,
+                                                   int64_t ld, int live, int cols, F f) {
+    uint32_t w[4][4];
+    columns_bf16(tmem, lane, w, f);
     __syncwarp();  // the stage's last reads are done
     const uint32_t at = smem_u32(stage) + (lane & 7) * kEpiRow + (lane >> 3) * 16;
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at + 8 * b * kEpiRow),
-                     "r"(w[b][0]), "r"(w[b][1]), "r"(w[b][2]), "r"(w[b][3])
-                     : "memory");
+    for (int b = 0; b < 4; ++b) stmatrix_trans(at + 8 * b * kEpiRow, w[b]);
     __syncwarp();
     const int piece = lane & 3;
     if (piece * 8 < live)
@@ -291,6 +300,35 @@ __device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int lane, uint
                 *reinterpret_cast<uint4*>(out + j * ld + piece * 8) =
                     *reinterpret_cast<const uint4*>(stage + j * kEpiRow + piece * 16);
         }
+}
+
+// The same columns without f as one box of a tensor map (32 lanes x 32 columns, 64-byte swizzle), at column x of
+// row y of matrix z; what lies outside the tensor is not written. For outputs whose rows all belong to the
+// call's matrix, so dW: its rows leave as 64 contiguous bytes without the warp's own reads and address
+// arithmetic (8 experts' dW of 4096 x 2048 from 16 rows each: 30.4 us against 37.6 with store_columns_bf16;
+// boxes of 64 x 32 by two warps at a barrier 31.7). `stage` is the warp's own, 512
+// bytes aligned; it is reused once the last box has been read. The caller waits for the last writes.
+constexpr int kBoxBytes = 2048;
+__device__ __forceinline__ void store_box_bf16(uint32_t tmem, int lane, uint8_t* stage, const CUtensorMap* map, int x,
+                                               int y, int z, bool inside) {
+    uint32_t w[4][4];
+    columns_bf16(tmem, lane, w, [](float v, int, int) { return v; });
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+    // rows of 64 bytes, their 16-byte pieces exchanged by the row's bits 1 and 2
+    const int row = lane & 7;
+    const uint32_t at = smem_u32(stage) + row * 64 + (((lane >> 3) ^ (row >> 1)) << 4);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) stmatrix_trans(at + 512 * b, w[b]);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0 && inside) {
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                         (uint64_t)map),
+                     "r"(x), "r"(y), "r"(z), "r"(smem_u32(stage))
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
 }
 
 // ------------------------------------------------------------ ragged grouping

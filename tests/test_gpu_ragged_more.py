@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from tests._gpu import dev_i64, lib, require_gpu
-from tests._ragged import assert_products, dgrad64, fprop64, philox_words
+from tests._ragged import assert_products, dgrad64, fprop64, philox_words, wgrad64
 from tests.test_gpu_ragged import rand
 
 pytestmark = pytest.mark.gpu
@@ -44,6 +44,22 @@ def test_fp32_sums_are_as_exact_as_fp32(mxq):
     dw = mxq.ragged_gemm_wgrad(dy, x, ms)
     ref = dy.double().t() @ x.double()
     assert ((dw[0].double() - ref).norm() / ref.norm()).item() < 2.0 ** -20
+
+
+# dW matrices that end inside a tile, a pair's second half and a 32 x 32 piece, every matrix beside another's
+@pytest.mark.parametrize("N,K", [(8, 8), (24, 40), (40, 136), (264, 264), (520, 1000), (1000, 520)])
+@pytest.mark.parametrize("dt,tag", [(BF16, "bf16"), (F32, "f32")])
+def test_wgrad_writes_its_matrices_only(mxq, N, K, dt, tag):
+    counts, pad = [3, 0, 70, 1, 200], 4096
+    E, M = len(counts), sum(counts)
+    dy, x = rand(1, M, N), rand(2, M, K)
+    whole = torch.full((2 * pad + E * N * K,), 7.0, device="cuda", dtype=dt)
+    out = whole[pad:-pad].view(E, N, K)
+    out.fill_(float("nan"))
+    mxq.ragged_gemm_wgrad(dy, x, dev_i64(counts), out=out)
+    assert bool((whole[:pad] == 7.0).all()) and bool((whole[-pad:] == 7.0).all())
+    assert not bool(out[1].any())
+    assert_products(out, *wgrad64(dy, x, counts), max(counts), tag)
 
 
 def test_offsets_past_32_bits(mxq):
