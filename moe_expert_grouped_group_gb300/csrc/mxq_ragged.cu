@@ -389,10 +389,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (!ok) break;
                 const int l = q * 32 + lane;
-                if (l < live) {
+                // dW as boxes by TMA where it is added to, where stores would need a test for each column, and after
+                // short sums, whose epilogue nothing hides (8 experts, 4096 x 2048, us by boxes and by the warps: 512
+                // rows each 74.2 and 79.8, 16 rows 55.9 and 58.0; 128 experts 1000 x 1000 104 and 114; 2048 rows each
+                // 200 and 196)
+                if (kMode == kWgrad && (p.accumulate || T.red <= FLUSH * BK || T.cols != WIDE)) {
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+                        for (int h = 0; h < 32; h += 16) {
+                            const int c = 64 * i + 32 * group + h;
+                            if (c < T.cols)
+                                store_box_f32(&acc[i][h], lane, stage, &tmOut, f0 + 32 * q, T.c0 + c, T.e, live > 32 * q,
+                                              p.accumulate);
+                        }
+                } else if (l < live) {
                     const float b =
                         kMode == kFprop && p.bias ? __bfloat162float(p.bias[(int64_t)T.e * p.N + f0 + l]) : 0.0f;
-                    // whole tiles without accumulation: nothing but stores, 128 bytes a warp
                     auto each = [&](auto&& put) {
 #pragma unroll
                         for (int i = 0; i < kChunks; ++i)
@@ -400,22 +413,27 @@ __global__ void __launch_bounds__(THREADS, 1)
                             for (int j = 0; j < 32; ++j) put(64 * i + 32 * group + j, __fadd_rn(acc[i][j], b));
                     };
                     const int64_t at = T.row0 * ld + f0 + l;
-                    if (p.out_f32 && !p.accumulate && T.cols == WIDE) {
-                        float* o = static_cast<float*>(p.out) + at;
+                    float* o = static_cast<float*>(p.out) + at;
+                    if (T.cols == WIDE) {  // whole tiles: nothing but stores, 128 bytes a warp
                         each([&](int c, float v) { o[c * ld] = v; });
-                    } else if (p.out_f32) {
-                        float* o = static_cast<float*>(p.out) + at;
+                    } else {
                         each([&](int c, float v) {
-                            if (c < T.cols) o[c * ld] = p.accumulate ? o[c * ld] + v : v;
-                        });
-                    } else {  // bf16 with accumulation
-                        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
-                        each([&](int c, float v) {
-                            if (c < T.cols) o[c * ld] = __float2bfloat16_rn(__bfloat162float(o[c * ld]) + v);
+                            if (c < T.cols) o[c * ld] = v;
                         });
                     }
                 }
             } else {
+                // dW's old values are read while the sums are made
+                constexpr int kBoxes = kMode == kWgrad ? WIDE / 64 : 1;
+                uint4 old[kBoxes][4];
+                if (kMode == kWgrad && p.accumulate) {
+#pragma unroll
+                    for (int i = 0; i < kBoxes; ++i) {
+                        const int c = 64 * i + 32 * group;
+                        load_rows_bf16(static_cast<const __nv_bfloat16*>(p.out) + (T.row0 + c) * ld + f0 + 32 * q, ld,
+                                       live - 32 * q, T.cols - c, lane, old[i]);
+                    }
+                }
                 const bool ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
                 if (!__all_sync(0xffffffffu, ok && !*abort_flag)) break;
                 fence_after();
@@ -428,10 +446,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * WIDE;
-                for (int c = 32 * group; c < T.cols; c += 64) {
-                    if constexpr (kMode == kWgrad)
-                        store_box_bf16(acc + c, lane, stage, &tmOut, f0 + 32 * q, T.c0 + c, T.e, live > 32 * q);
-                    else
+                if constexpr (kMode == kWgrad) {
+#pragma unroll
+                    for (int i = 0; i < kBoxes; ++i) {
+                        const int c = 64 * i + 32 * group;
+                        if (c < T.cols)
+                            store_box_bf16(acc + c, lane, stage, &tmOut, f0 + 32 * q, T.c0 + c, T.e, live > 32 * q,
+                                           p.accumulate, old[i]);
+                    }
+                } else {
+                    for (int c = 32 * group; c < T.cols; c += 64)
                         store_columns_bf16(acc + c, lane, stage,
                                            static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * ld + f0 + 32 * q, ld,
                                            live - 32 * q, T.cols - c, [&](float v, int l, int) { return v + b[l >> 3]; });
@@ -439,7 +463,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 drained();
             }
         } while (queue.next(t, lane, abort_flag) == TileQueue::kTile);
-        if (kMode == kWgrad && !kRegs) {  // the last boxes are written before the block leaves its shared memory
+        if (kMode == kWgrad) {  // the last boxes are written before the block leaves its shared memory
             if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
             __syncwarp();
         }
@@ -479,9 +503,14 @@ bool encode_tmap(CUtensorMap* m, const void* base, int elem_bytes, int rank, con
         b[i] = (cuuint32_t)box[i];
         if (i) s[i - 1] = (cuuint64_t)strides[i - 1];
     }
-    return fn(m, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+    return fn(m, elem_bytes == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+              : elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+              rank,
               const_cast<void*>(base), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              swizzle_bytes == 0    ? CU_TENSOR_MAP_SWIZZLE_NONE
+              : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                    : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -506,7 +535,7 @@ template <int kMode>
 static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
     const Params p{c.M, c.N, c.K, c.E, c.m_splits, static_cast<const __nv_bfloat16*>(c.bias), c.out, c.out_f32,
                    c.accumulate, c.status};
-    CUtensorMap a, b, half, out;  // half: b in boxes of half the rows; out: dW as bf16 (wgrad)
+    CUtensorMap a, b, half, out;  // half: b in boxes of half the rows; out: dW
     bool ok;
     const int64_t feats = ((kMode == kFprop ? c.N : c.K) + FEAT - 1) / FEAT;
     int64_t tiles = (c.M / WIDE + std::min<int64_t>(c.E, c.M)) * feats;  // no fewer than the device counts
@@ -519,9 +548,10 @@ static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
         ok = encode_tmap(&a, c.M ? c.tok : c.out, 2, 2, da, sa, boxa) &&
              encode_tmap(&b, c.M ? c.mat : c.out, 2, 2, db, sb, boxb);
         half = b;
-        const int64_t dd[3] = {c.K, c.N, c.E}, sd[2] = {2 * c.K, 2 * c.K * c.N};
-        const int boxd[3] = {32, 32, 1};
-        if (ok && !c.out_f32) ok = encode_tmap(&out, c.out, 2, 3, dd, sd, boxd, 64);
+        const int size = c.out_f32 ? 4 : 2;
+        const int64_t dd[3] = {c.K, c.N, c.E}, sd[2] = {size * c.K, size * c.K * c.N};
+        const int boxd[3] = {32, c.out_f32 ? 16 : 32, 1};
+        ok = ok && encode_tmap(&out, c.out, size, 3, dd, sd, boxd, c.out_f32 ? 0 : 64);
     } else {
         const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {2 * c.K, 2 * c.K * c.N};
         const int64_t db[2] = {kMode == kDgrad ? c.N : c.K, c.M}, sb[1] = {2 * c.ld_tok};
@@ -529,10 +559,10 @@ static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
         ok = encode_tmap(&a, c.mat, 2, 3, da, sa, boxa) && encode_tmap(&b, c.tok, 2, 2, db, sb, boxb) &&
              encode_tmap(&half, c.tok, 2, 2, db, sb, boxh);
     }
-    if (kMode != kWgrad || c.out_f32) out = a;  // not read
+    if (kMode != kWgrad) out = a;  // not read
     if (!ok) return cudaErrorInvalidValue;
-    return c.out_f32 || c.accumulate ? launch<kMode, true>(a, b, half, out, p, tiles, s)
-                                     : launch<kMode, false>(a, b, half, out, p, tiles, s);
+    return c.out_f32 ? launch<kMode, true>(a, b, half, out, p, tiles, s)
+                     : launch<kMode, false>(a, b, half, out, p, tiles, s);
 }
 
 cudaError_t run_gemm(const GemmCall& c, cudaStream_t s) {

@@ -255,21 +255,20 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
 // warps writing 256-byte pieces together, at barriers, measured the same.
 constexpr int kEpiRow = 80, kEpiBytes = 32 * kEpiRow;
 
-// Columns 0 .. 31 of 32 accumulator lanes at tmem, each value passed through f(value, lane in 0..31, column
-// in 0..31), rounded and packed two columns at a time: [8-column block][8-lane block] for stmatrix .trans.
+// Columns 0 .. 31 of 32 accumulator lanes at tmem, rounded and packed two columns at a time: [8-column block b]
+// [8-lane block g] for stmatrix .trans. A value is passed through f(value, b, g, which of the two columns).
 template <class F>
 __device__ __forceinline__ void columns_bf16(uint32_t tmem, int lane, uint32_t (&w)[4][4], F f) {
     uint32_t v[2][16];
     tmem_ld16x32(tmem, v[0]);
     tmem_ld16x32(tmem + (16u << 16), v[1]);
     tmem_wait_ld();
-    const int fl = lane >> 2, fc = 2 * (lane & 3);
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const int r = 4 * b + 2 * (g & 1), l = fl + 8 * g, col = 8 * b + fc;
-            w[b][g] = bf16x2_bits(f(__uint_as_float(v[g >> 1][r]), l, col), f(__uint_as_float(v[g >> 1][r + 1]), l, col + 1));
+            const int r = 4 * b + 2 * (g & 1);
+            w[b][g] = bf16x2_bits(f(__uint_as_float(v[g >> 1][r]), b, g, 0), f(__uint_as_float(v[g >> 1][r + 1]), b, g, 1));
         }
 }
 
@@ -279,13 +278,22 @@ __device__ __forceinline__ void stmatrix_trans(uint32_t row, const uint32_t (&w)
                  : "memory");
 }
 
-// The same columns to out + column * ld + lane for lanes < live and columns < cols. Called by a warp; `stage`
-// is its own.
+__device__ __forceinline__ void ldmatrix_trans(uint32_t row, uint32_t (&w)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(row)
+                 : "memory");
+}
+
+// The same columns, each value passed through f(value, lane in 0..31, column in 0..31), to
+// out + column * ld + lane for lanes < live and columns < cols. Called by a warp; `stage` is its own.
 template <class F>
 __device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int lane, uint8_t* stage, __nv_bfloat16* out,
                                                    int64_t ld, int live, int cols, F f) {
     uint32_t w[4][4];
-    columns_bf16(tmem, lane, w, f);
+    columns_bf16(tmem, lane, w, [&](float v, int b, int g, int half) {
+        return f(v, (lane >> 2) + 8 * g, 8 * b + 2 * (lane & 3) + half);
+    });
     __syncwarp();  // the stage's last reads are done
     const uint32_t at = smem_u32(stage) + (lane & 7) * kEpiRow + (lane >> 3) * 16;
 #pragma unroll
@@ -302,22 +310,51 @@ __device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int lane, uint
         }
 }
 
+// 32 rows of 32 bf16 at out, 64 contiguous bytes to four lanes; 0 beyond live and cols.
+__device__ __forceinline__ void load_rows_bf16(const __nv_bfloat16* out, int64_t ld, int live, int cols, int lane,
+                                               uint4 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = i * 8 + (lane >> 2), x = (lane & 3) * 8;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (x < live && j < cols) v[i] = *reinterpret_cast<const uint4*>(out + j * ld + x);
+    }
+}
 // The same columns without f as one box of a tensor map (32 lanes x 32 columns, 64-byte swizzle), at column x of
 // row y of matrix z; what lies outside the tensor is not written. For outputs whose rows all belong to the
 // call's matrix, so dW: its rows leave as 64 contiguous bytes without the warp's own reads and address
 // arithmetic (8 experts' dW of 4096 x 2048 from 16 rows each: 30.4 us against 37.6 with store_columns_bf16;
-// boxes of 64 x 32 by two warps at a barrier 31.7). `stage` is the warp's own, 512
-// bytes aligned; it is reused once the last box has been read. The caller waits for the last writes.
+// boxes of 64 x 32 by two warps at a barrier 31.7). `stage` is the warp's own, 512 bytes aligned; it is reused
+// once the last box has been read. The caller waits for the last writes. With add, `old` (load_rows_bf16) passes
+// through the stage into the fragments' layout and is added in fp32, before the one rounding (the same dW: 67 us,
+// floor 40; 16 loads at a time after the sums 697).
 constexpr int kBoxBytes = 2048;
 __device__ __forceinline__ void store_box_bf16(uint32_t tmem, int lane, uint8_t* stage, const CUtensorMap* map, int x,
-                                               int y, int z, bool inside) {
-    uint32_t w[4][4];
-    columns_bf16(tmem, lane, w, [](float v, int, int) { return v; });
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    __syncwarp();
+                                               int y, int z, bool inside, bool add, const uint4 (&old)[4]) {
     // rows of 64 bytes, their 16-byte pieces exchanged by the row's bits 1 and 2
     const int row = lane & 7;
     const uint32_t at = smem_u32(stage) + row * 64 + (((lane >> 3) ^ (row >> 1)) << 4);
+    uint32_t w[4][4];
+    if (add) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = i * 8 + (lane >> 2);
+            *reinterpret_cast<uint4*>(stage + j * 64 + (((lane & 3) ^ (j >> 1 & 3)) << 4)) = old[i];
+        }
+        __syncwarp();
+        uint32_t o[4][4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) ldmatrix_trans(at + 512 * b, o[b]);
+        columns_bf16(tmem, lane, w, [&](float v, int b, int g, int half) {
+            return v + __uint_as_float(half ? o[b][g] & 0xffff0000u : o[b][g] << 16);
+        });
+    } else {
+        columns_bf16(tmem, lane, w, [](float v, int, int, int) { return v; });
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+    __syncwarp();
 #pragma unroll
     for (int b = 0; b < 4; ++b) stmatrix_trans(at + 512 * b, w[b]);
     fence_async_smem();
@@ -327,6 +364,36 @@ __device__ __forceinline__ void store_box_bf16(uint32_t tmem, int lane, uint8_t*
                          (uint64_t)map),
                      "r"(x), "r"(y), "r"(z), "r"(smem_u32(stage))
                      : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+}
+
+// 16 columns of 32 fp32 lanes, one to a thread, as one box (32 lanes x 16 columns, no swizzle) written over the
+// matrix or added to it. The add is one fp32 addition, rounded to nearest in L2 (subnormals kept), each
+// element's only one of the call, so its result is that of the warp's own read, add and store. Those took 802 us
+// on 8 experts' dW of 4096 x 2048 from 16 rows each, every read waiting for the store before it; this 104 (268 MB
+// read and written: 79 at the copy rate).
+__device__ __forceinline__ void store_box_f32(const float* v, int lane, uint8_t* stage, const CUtensorMap* map, int x,
+                                              int y, int z, bool inside, bool add) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+    const uint32_t at = smem_u32(stage);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 128 * j + 4 * lane), "f"(v[j]) : "memory");
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0 && inside) {
+        if (add)
+            asm volatile(
+                "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                    (uint64_t)map),
+                "r"(x), "r"(y), "r"(z), "r"(at)
+                : "memory");
+        else
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                             (uint64_t)map),
+                         "r"(x), "r"(y), "r"(z), "r"(at)
+                         : "memory");
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
 }

@@ -56,9 +56,9 @@ cudaError_t run_fprop_vec(const GemmCall& c, cudaStream_t s);
 cudaError_t run_int8_vec(const Int8Call& c, cudaStream_t s);
 cudaError_t run_int8_quantize(const void* x, int64_t M, int64_t K, int64_t ld, void* q, float* scale, cudaStream_t s);
 
-// Encodes a tensor map of int8 or bf16 elements (by their bytes) in up
+// Encodes a tensor map of int8, bf16 or fp32 elements (by their bytes) in up
 // to three dimensions: dims and box innermost first, strides in bytes of
-// dimensions 1 and 2, the swizzle of 128 or 64 bytes. False on failure.
+// dimensions 1 and 2, the swizzle of 128, 64 or 0 (none) bytes. False on failure.
 bool encode_tmap(CUtensorMap* m, const void* base, int elem_bytes, int rank, const int64_t* dims,
                  const int64_t* strides, const int* box, int swizzle_bytes = 128);
 int sm_count();

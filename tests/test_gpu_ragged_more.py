@@ -62,6 +62,40 @@ def test_wgrad_writes_its_matrices_only(mxq, N, K, dt, tag):
     assert_products(out, *wgrad64(dy, x, counts), max(counts), tag)
 
 
+# adding to dW: fp32 is exactly one fp32 addition of the call's sums, at subnormals, infinities and NaN too; bf16 is
+# rounded once, from the fp32 sum with the old value; an empty expert's matrix and everything beside stay as they were
+@pytest.mark.parametrize("N,K", [(8, 8), (40, 136), (264, 264), (1000, 520)])
+@pytest.mark.parametrize("counts", [[3, 0, 70, 1, 200], [0, 1500, 1]])
+def test_wgrad_adds_once(mxq, N, K, counts):
+    E, M, pad, ms = len(counts), sum(counts), 4096, dev_i64(counts)
+    dy, x = rand(1, M, N), rand(2, M, K)
+    dy[:, 1], dy[:, 2] = 2.0 ** -126, 0.0  # sums about the smallest normal number; sums of 0
+    prior = rand(5, E, N, K).float() * 3
+    prior[:, 1] = 2.0 ** -127
+    prior[:, 3], prior[:, 4], prior[:, 5] = float("nan"), float("inf"), -0.0
+    dw = mxq.ragged_gemm_wgrad(dy, x, ms)
+    whole = torch.full((2 * pad + E * N * K,), 7.0, device="cuda")
+    out = whole[pad:-pad].view(E, N, K)
+    out.copy_(prior)
+    mxq.ragged_gemm_wgrad(dy, x, ms, out=out, accumulate=True)
+    full = [e for e in range(E) if counts[e]]
+    want = prior.clone()
+    want[full] = (prior.cpu()[full] + dw.cpu()[full]).cuda()
+    assert torch.equal(out.nan_to_num(1e30), want.nan_to_num(1e30)) and torch.equal(out.isnan(), want.isnan())
+    assert bool((whole[:pad] == 7.0).all()) and bool((whole[-pad:] == 7.0).all())
+    whole = torch.full((2 * pad + E * N * K,), 7.0, device="cuda", dtype=BF16)
+    out = whole[pad:-pad].view(E, N, K)
+    out.copy_(prior)
+    ref, mag = wgrad64(dy, x, counts)
+    old = out.double()
+    mxq.ragged_gemm_wgrad(dy, x, ms, out=out, accumulate=True)
+    finite = old[0, :, 0].isfinite()  # rows 3 and 4 hold the NaN and the infinities
+    finite[1] = False  # subnormal in bf16: no relative bound
+    assert_products(out[:, finite], ref[:, finite] + old[:, finite], mag[:, finite] + old[:, finite].abs(), max(counts), "bf16")
+    assert bool(out[:, 3].isnan().all()) and bool((out[:, 4] == float("inf")).all())
+    assert bool((whole[:pad] == 7.0).all()) and bool((whole[-pad:] == 7.0).all())
+
+
 def test_offsets_past_32_bits(mxq):
     M, N, K = 70000, 32768, 8  # 2.3e9 outputs
     x, w, counts = rand(1, M, K), rand(3, 2, N, K), [40001, 29999]
