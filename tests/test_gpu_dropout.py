@@ -55,6 +55,23 @@ def test_dropout(mxq, n, p, dtype):
         assert torch.equal(mxq.dropout(x, rng(seed, offset), p), x)
 
 
+# several vectors a thread (beyond one for each of the device's threads), ends inside a block's vectors
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
+@pytest.mark.parametrize("n", [1 << 22, (1 << 22) + 8 * 700 + 3])
+def test_large_dropout(mxq, n, dtype):
+    x, r, p = rand(1, n, dtype=dtype), rand(2, n, dtype=dtype), 0.3
+    d = drop64(x, 11, 13, p).cuda()
+    got = mxq.dropout(x, rng(11, 13), p)
+    assert torch.equal(got != 0, d != 0)
+    assert torch.all((got.double() - d).abs() <= tolerance(dtype) * d.abs())
+    want = mxq.dropout(x, rng(11, 13), p, residual=r)
+    assert torch.all((want.double() - (d + r.double())).abs() <= tolerance(dtype) * (d.abs() + r.double().abs()))
+    mxq.dropout(x, rng(11, 13), p, residual=r, out=r)
+    assert torch.equal(r, want)
+    mxq.dropout(x, rng(11, 13), p, out=x)
+    assert torch.equal(x, got)
+
+
 def test_negative_seed_and_offset_are_their_64_bits(mxq):
     x = torch.ones(5000, device="cuda")
     got = mxq.dropout(x, rng(-3, -7), 0.5)
