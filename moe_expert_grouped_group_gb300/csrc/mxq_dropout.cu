@@ -80,7 +80,7 @@ struct Rng {
     uint64_t seed, offset;
 };
 __device__ __forceinline__ Rng load_rng(const int64_t* rng) {
-    return Rng{(uint64_t)__ldg(rng), (uint64_t)__ldg(rng + 1)};
+    return Rng{(uint64_t)rng[0], (uint64_t)rng[1]};
 }
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {

@@ -26,6 +26,10 @@ constexpr int kFM = 128;  // MMA M: rows of A (features) per CTA
 // parameters and shared memory, after it everything earlier in the stream has
 // completed and is visible. It takes the launch latency off a chain of short
 // kernels (16 rows, 8 experts, 2048 x 4096: 28.7 -> 26.0 us a call).
+// A kernel that begins early runs beside the one that writes its inputs, so
+// nothing global is read-only for its lifetime: no __ldg, ld.global.nc or const
+// __restrict__ here (the compiler may take such loads before the wait), only
+// plain loads behind it.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -405,7 +409,7 @@ __device__ __forceinline__ void store_box_f32(const float* v, int lane, uint8_t*
 // added, so the sum cannot wrap) and returns a status bit mask. Called by all
 // threads of the block; all of them wait for the stream and fetch counts, so
 // that many experts cost one memory latency, then one warp sums them.
-__device__ __forceinline__ int load_ragged(const int64_t* __restrict__ d_m_splits, int E, int64_t M, int width,
+__device__ __forceinline__ int load_ragged(const int64_t* d_m_splits, int E, int64_t M, int width,
                                            int32_t* off, int32_t* slices) {
     __shared__ int s_bad;
     if (threadIdx.x == 0) s_bad = 0;

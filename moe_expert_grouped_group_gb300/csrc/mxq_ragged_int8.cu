@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(Shape<kCG>::kThreads, 1)
                         float* o = static_cast<float*>(p.out) + (T.row0 + c) * p.N + f0 + lane;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (c + j < T.cols) o[j * p.N] = __uint_as_float(v[j]) * __ldg(xs + c + j) * sw + b;
+                            if (c + j < T.cols) o[j * p.N] = __uint_as_float(v[j]) * xs[c + j] * sw + b;
                     }
                 }
             } else {
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(Shape<kCG>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int col = c + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
-                        sx[i] = col < T.cols ? __ldg(xs + col) : 0.0f;
+                        sx[i] = col < T.cols ? xs[col] : 0.0f;
                     }
                 };
                 scales(32 * group);

@@ -49,7 +49,7 @@ struct Params {
 
 __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
@@ -138,7 +138,7 @@ __device__ __forceinline__ void product(const Params& p, int e, int64_t row, int
         for (int c = 0; c < CHANNELS; ++c) a[c] = Op::open(raw[c]);
 #pragma unroll
         for (int t = 0; t < kTokens; ++t) {
-            const auto b = Op::open(__ldg(reinterpret_cast<const uint4*>(x + min(t, rows - 1) * p.ldx)));
+            const auto b = Op::open(*reinterpret_cast<const uint4*>(x + min(t, rows - 1) * p.ldx));
 #pragma unroll
             for (int c = 0; c < CHANNELS; ++c) acc[c][t] = Op::add(a[c], b, acc[c][t]);
         }
