@@ -432,8 +432,12 @@ MXQ_API int mxq_int8_quantize_rows(const void* x_bf16, int64_t ldx, int64_t M, i
 
 /* y[m,n] = (sum_k xq[m,k] wq[e,n,k]) x_scale[m] w_scale[e,n] (+ bias[e,n]);
  * xq (M, K) and wq (E, N, K) int8, scales fp32 (M) and (E, N), bias (E, N) bf16
- * or NULL, y (M, N) bf16 or, with MXQ_OUT_F32, fp32. The sum is fp32 over whole
- * numbers. Grouping as in the bf16 products; K % 16 == 0, N % 8 == 0. */
+ * or NULL, y (M, N) bf16 or, with MXQ_OUT_F32, fp32. fp32 outputs: the sum is
+ * exact for K < 2^17 - 15 whatever the codes, is rounded to fp32 once and then
+ * once for each scale and the bias, so a row's result does not depend on the
+ * rows beside it; longer sums are added up in fp32 from exact parts of 1024.
+ * bf16 outputs: the same, rounded to bf16, except that sums past 2^24 may be
+ * truncated by up to 2^-23 per 16 of K while K <= 2^15. Grouping as in the bf16 products; K % 16 == 0, N % 8 == 0. */
 MXQ_API int mxq_int8_gemm_fprop(const void* xq, const float* x_scale, const void* wq, const float* w_scale,
                                 const void* bias_bf16, int64_t M, int64_t N, int64_t K, int E,
                                 const int64_t* d_m_splits, int flags, void* y, int32_t* d_status,

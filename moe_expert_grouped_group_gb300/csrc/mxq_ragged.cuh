@@ -259,14 +259,16 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
 // warps writing 256-byte pieces together, at barriers, measured the same.
 constexpr int kEpiRow = 80, kEpiBytes = 32 * kEpiRow;
 
-// Columns 0 .. 31 of 32 accumulator lanes at tmem, rounded and packed two columns at a time: [8-column block b]
-// [8-lane block g] for stmatrix .trans. A value is passed through f(value, b, g, which of the two columns).
-template <class F>
-__device__ __forceinline__ void columns_bf16(uint32_t tmem, int lane, uint32_t (&w)[4][4], F f) {
-    uint32_t v[2][16];
+// Columns 0 .. 31 of 32 accumulator lanes at tmem as matrix fragments.
+__device__ __forceinline__ void load_columns(uint32_t tmem, uint32_t (&v)[2][16]) {
     tmem_ld16x32(tmem, v[0]);
     tmem_ld16x32(tmem + (16u << 16), v[1]);
     tmem_wait_ld();
+}
+// They, rounded and packed two columns at a time: [8-column block b][8-lane block g] for stmatrix .trans. A value is
+// passed through f(value, b, g, which of the two columns).
+template <class F>
+__device__ __forceinline__ void columns_bf16(const uint32_t (&v)[2][16], uint32_t (&w)[4][4], F f) {
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -292,10 +294,10 @@ __device__ __forceinline__ void ldmatrix_trans(uint32_t row, uint32_t (&w)[4]) {
 // The same columns, each value passed through f(value, lane in 0..31, column in 0..31), to
 // out + column * ld + lane for lanes < live and columns < cols. Called by a warp; `stage` is its own.
 template <class F>
-__device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int lane, uint8_t* stage, __nv_bfloat16* out,
-                                                   int64_t ld, int live, int cols, F f) {
+__device__ __forceinline__ void store_columns_bf16(const uint32_t (&x)[2][16], int lane, uint8_t* stage,
+                                                   __nv_bfloat16* out, int64_t ld, int live, int cols, F f) {
     uint32_t w[4][4];
-    columns_bf16(tmem, lane, w, [&](float v, int b, int g, int half) {
+    columns_bf16(x, w, [&](float v, int b, int g, int half) {
         return f(v, (lane >> 2) + 8 * g, 8 * b + 2 * (lane & 3) + half);
     });
     __syncwarp();  // the stage's last reads are done
@@ -312,6 +314,13 @@ __device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int lane, uint
                 *reinterpret_cast<uint4*>(out + j * ld + piece * 8) =
                     *reinterpret_cast<const uint4*>(stage + j * kEpiRow + piece * 16);
         }
+}
+template <class F>
+__device__ __forceinline__ void store_columns_bf16(uint32_t tmem, int lane, uint8_t* stage, __nv_bfloat16* out,
+                                                   int64_t ld, int live, int cols, F f) {
+    uint32_t v[2][16];
+    load_columns(tmem, v);
+    store_columns_bf16(v, lane, stage, out, ld, live, cols, f);
 }
 
 // 32 rows of 32 bf16 at out, 64 contiguous bytes to four lanes; 0 beyond live and cols.
@@ -338,7 +347,7 @@ __device__ __forceinline__ void store_box_bf16(uint32_t tmem, int lane, uint8_t*
     // rows of 64 bytes, their 16-byte pieces exchanged by the row's bits 1 and 2
     const int row = lane & 7;
     const uint32_t at = smem_u32(stage) + row * 64 + (((lane >> 3) ^ (row >> 1)) << 4);
-    uint32_t w[4][4];
+    uint32_t v[2][16], w[4][4];
     if (add) {
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncwarp();
@@ -351,11 +360,13 @@ __device__ __forceinline__ void store_box_bf16(uint32_t tmem, int lane, uint8_t*
         uint32_t o[4][4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) ldmatrix_trans(at + 512 * b, o[b]);
-        columns_bf16(tmem, lane, w, [&](float v, int b, int g, int half) {
+        load_columns(tmem, v);
+        columns_bf16(v, w, [&](float v, int b, int g, int half) {
             return v + __uint_as_float(half ? o[b][g] & 0xffff0000u : o[b][g] << 16);
         });
     } else {
-        columns_bf16(tmem, lane, w, [](float v, int, int, int) { return v; });
+        load_columns(tmem, v);
+        columns_bf16(v, w, [](float v, int, int, int) { return v; });
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
     __syncwarp();

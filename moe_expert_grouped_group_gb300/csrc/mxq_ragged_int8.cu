@@ -7,9 +7,25 @@
 // GB300's int8 tensor rate is a small fraction of its 16-bit floating rate, so
 // the codes travel as int8 (the bytes that a weight-bound call is made of) and
 // are widened to f16 on chip, exactly: |q| <= 128 fits f16's 11 significand
-// bits. The products are then whole numbers below 2^14 and tcgen05.mma
-// kind::f16 sums them in fp32; sums below 2^24 are exact, so fp32 outputs need
-// no sums in registers here.
+// bits. The products are then whole numbers up to 2^14 and tcgen05.mma
+// kind::f16 sums them in fp32, exactly while sums stay within 2^24: 1024 of K
+// whatever the codes. Past that the tensor core truncates, up to 2^-23 of the
+// sum per 16 of K (codes of one sign: 3e-6 at K = 4096, 2e-3 at 2^17). So sums
+// that may pass 2^24 are drained every 1024 of K and added in registers
+// (kDeep): as 32-bit integers, exact, while no sum can leave them (K up to
+// kVecDepth), in fp32 beyond. fp32 outputs take that shape where K > 1024 and
+// so are the same bits as those of the dot products, whatever shares the call.
+// bf16 outputs take it where K > 2^15: below, the truncation is under 2^-12 of
+// the sum of the products' magnitudes, an eighth of bf16's rounding, and
+// zero-mean codes, whose sums stay within 2^24, have none.
+//
+// What kDeep costs: a pair's sums fill the registers at 128 columns, half of
+// what an MMA with A in TMEM takes in the same time, against which the epilogue
+// is hidden by a second accumulator. fp32, 8 experts, 16384 rows, us, in one
+// truncating accumulator and as it is: 2048 x 4096 253 and 304, 7168 x 2048 320
+// and 458 (bf16: 190 and 293). One set of converting warps leaves the epilogue
+// its registers; with two it spilled (339 and 460). Few rows: 8 experts x 16
+// 19.9 and 20.8, 64 x 16 113 and 118.
 //
 // The tile walk, the operands' sides (features on the MMA's M, tokens on its
 // N), the edges and the two shapes (pairs of SMs; one SM for few rows) are
@@ -47,21 +63,23 @@ namespace i8 {
 constexpr int BK = 128;  // depth of an int8 stage
 constexpr int HK = 64;   // half of it: 128 bytes of f16
 constexpr int CVT_WARPS = 4;  // of a set: for the weights, and as many for the tokens
+constexpr int CHUNK = 1024;  // of K whose sums are whole numbers in fp32: |codes| <= 128
+constexpr int64_t kTruncDepth = 1 << 15;
 
-template <int kCG>
+template <int kCG, bool kDeep>
 struct Shape {
     static constexpr int kFeat = kFM * kCG;
-    static constexpr int kWide = kCG == 2 ? 256 : kFewRows;
+    static constexpr int kWide = kCG == 1 ? kFewRows : kDeep ? 128 : 256;
     static constexpr int kStep = 16 * kCG;
     static constexpr int kBox = 32;                  // token rows of a box
     static constexpr int kTok = kWide / kCG;         // token rows of a stage in one CTA
     static constexpr int kRaws = kCG == 2 ? 3 : 8;   // int8 stages
     static constexpr int kRaw = (kFM + kTok) * BK;   // weights, then tokens
-    static constexpr int kSets = kCG == 2 ? 2 : 3;   // of converting warps
+    static constexpr int kSets = kCG == 1 ? 3 : kDeep ? 1 : 2;  // of converting warps
     static constexpr int kSlots = 3;                 // of widened operands
     static constexpr int kHalf = kTok * HK * 2;      // widened tokens of half a slot
     static constexpr int kSlot = 2 * kHalf;
-    static constexpr int kBufs = kCG == 2 ? 1 : 2;   // accumulators
+    static constexpr int kBufs = kWide == 256 ? 1 : 2;  // accumulators
     static constexpr int kTmemA = kBufs * kWide;     // the weights' slots follow them
     static constexpr int kSlotCols = BK / 2;         // of its weights in TMEM
     static constexpr int kTmem = kCG == 2 ? 512 : 256;
@@ -71,6 +89,13 @@ struct Shape {
     static constexpr int kEpiWarps = kCG == 2 ? 8 : 4;
     static constexpr int kEpiFirst = 4, kCvtFirst = kEpiFirst + kEpiWarps, kTokFirst = kCvtFirst + kSets * CVT_WARPS;
     static constexpr int kThreads = 32 * (kTokFirst + kSets * CVT_WARPS);
+    // registers a thread: at launch, and then of the first four warps, the epilogue's, the weights' and the tokens'
+    static constexpr int kStartRegs = 65536 / kThreads / 8 * 8, kCtlRegs = 56;
+    static constexpr int kEpiRegs = kCG == 1 ? 96 : kDeep ? 136 : 88;
+    static constexpr int kWeiRegs = kCG == 1 ? 64 : kDeep ? 80 : 72, kTokRegs = kCG == 1 ? 56 : 64;
+    static_assert(4 * kCtlRegs + kEpiWarps * kEpiRegs + kSets * CVT_WARPS * (kWeiRegs + kTokRegs) <=
+                      kThreads / 32 * kStartRegs,
+                  "the warps' registers are those that the block starts with");
     static constexpr int kBars = kEpi + kEpiWarps * kEpiBytes;
     static constexpr int kTables = kBars + 256;
     __host__ __device__ static constexpr int smem(int E) { return 1024 + kTables + 8 * (E + 1); }
@@ -103,10 +128,43 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
     return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
 
-template <int kCG, bool kF32>
-__global__ void __launch_bounds__(Shape<kCG>::kThreads, 1)
+// Sums of a column's pieces of CHUNK, as the bits of an integer (`whole`) or of an fp32 value.
+struct Pieces {
+    bool whole;
+    __device__ __forceinline__ static uint32_t add_whole(uint32_t sum, uint32_t v, bool first) {
+        const uint32_t i = (uint32_t)__float2int_rn(__uint_as_float(v));
+        return first ? i : sum + i;
+    }
+    __device__ __forceinline__ static uint32_t add_fp32(uint32_t sum, uint32_t v, bool first) {
+        return first ? v : __float_as_uint(__fadd_rn(__uint_as_float(sum), __uint_as_float(v)));
+    }
+    template <int n>
+    __device__ __forceinline__ void add(uint32_t* sum, const uint32_t (&v)[n], bool first) const {
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < n; ++j) sum[j] = add_whole(sum[j], v[j], first);
+        } else {
+#pragma unroll
+            for (int j = 0; j < n; ++j) sum[j] = add_fp32(sum[j], v[j], first);
+        }
+    }
+    template <int n>
+    __device__ __forceinline__ void finish(uint32_t* sum) const {
+        if (whole)
+#pragma unroll
+            for (int j = 0; j < n; ++j) sum[j] = __float_as_uint(__int2float_rn((int)sum[j]));
+    }
+};
+
+// The steps of every shape, and of the dot products: each one fp32 rounding.
+__device__ __forceinline__ float scaled(float sum, float xs, float ws, float bias) {
+    return __fadd_rn(__fmul_rn(__fmul_rn(sum, xs), ws), bias);
+}
+
+template <int kCG, bool kF32, bool kDeep>
+__global__ void __launch_bounds__(Shape<kCG, kDeep>::kThreads, 1)
     ragged_int8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Params p) {
-    using S = Shape<kCG>;
+    using S = Shape<kCG, kDeep>;
     constexpr int RAWS = S::kRaws, SETS = S::kSets, SLOTS = S::kSlots;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align<1024>(smem_raw);
@@ -154,10 +212,8 @@ __global__ void __launch_bounds__(Shape<kCG>::kThreads, 1)
     const Walk<kFprop, S::kFeat, S::kWide, S::kStep> W(p.N, p.K, p.E, s_off, s_slices, nullptr);
     const int64_t first = blockIdx.x / kCG, stride = gridDim.x / kCG;
 
-    // Registers. Pair shape: 7 groups of four warps start with 72 each, and 56 + 2 * 88 + 2 * 72 + 2 * 64 = 504;
-    // few rows: 8 groups start with 64, and 56 + 96 + 3 * 64 + 3 * 56 = 512.
     if (warp < S::kEpiFirst) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kCtlRegs));
         if (warp == 0) {
             // -------------------------------------------------- TMA producer: this CTA's int8 boxes
             int stage = 0;
@@ -194,35 +250,38 @@ __global__ void __launch_bounds__(Shape<kCG>::kThreads, 1)
             for (int64_t t = first; t < W.total; t += stride) {
                 const Tile T = W.get(t);
                 const uint32_t id = idesc_f16(0, 0, 0, S::kFeat, T.n);
-                const uint32_t d = tmem + buf * S::kWide;
-                if (!mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag)) goto done_mma;
-                __syncwarp();
-                for (int r = 0; r < T.red; r += BK) {
-                    const uint32_t at = tmem + S::kTmemA + slot * S::kSlotCols;
-                    const uint64_t off = (uint64_t)(slot * (S::kSlot / 16));
-                    if (!mbar_wait(full0 + 8 * slot, phase, abort_flag)) goto done_mma;
+                for (int r0 = 0; r0 < T.red; r0 += kDeep ? CHUNK : T.red) {
+                    const int r1 = kDeep ? min(T.red, r0 + CHUNK) : T.red;
+                    const uint32_t d = tmem + buf * S::kWide;
+                    if (!mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag)) goto done_mma;
                     __syncwarp();
-                    fence_after();
-                    const int steps = T.red - r >= BK ? BK / 16 : (T.red - r + 15) / 16;
-                    if (elect_one()) {
+                    for (int r = r0; r < r1; r += BK) {
+                        const uint32_t at = tmem + S::kTmemA + slot * S::kSlotCols;
+                        const uint64_t off = (uint64_t)(slot * (S::kSlot / 16));
+                        if (!mbar_wait(full0 + 8 * slot, phase, abort_flag)) goto done_mma;
+                        __syncwarp();
+                        fence_after();
+                        const int steps = T.red - r >= BK ? BK / 16 : (T.red - r + 15) / 16;
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < BK / 16; ++k)
-                            if (k < steps)
-                                mma_f16_tmem<kCG>(d, at + 8 * k, bd0 + off + (k >> 2) * (S::kHalf / 16) + 2 * (k & 3), id,
-                                                  r > 0 || k > 0);
-                        mma_commit<kCG>(empty0 + 8 * slot);
-                        if (r + BK >= T.red) mma_commit<kCG>(accf0 + 8 * buf);
+                            for (int k = 0; k < BK / 16; ++k)
+                                if (k < steps)
+                                    mma_f16_tmem<kCG>(d, at + 8 * k, bd0 + off + (k >> 2) * (S::kHalf / 16) + 2 * (k & 3),
+                                                      id, r > r0 || k > 0);
+                            mma_commit<kCG>(empty0 + 8 * slot);
+                            if (r + BK >= r1) mma_commit<kCG>(accf0 + 8 * buf);
+                        }
+                        __syncwarp();
+                        if (++slot == SLOTS) { slot = 0; phase ^= 1; }
                     }
-                    __syncwarp();
-                    if (++slot == SLOTS) { slot = 0; phase ^= 1; }
+                    if (++buf == S::kBufs) { buf = 0; aphase ^= 1; }
                 }
-                if (++buf == S::kBufs) { buf = 0; aphase ^= 1; }
             }
         done_mma:;
         }
     } else if (warp < S::kCvtFirst) {
         // ------------------------------------------------------ epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCG == 2 ? 88 : 96));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kEpiRegs));
         const int q = warp & 3, group = (warp - S::kEpiFirst) >> 2;
         constexpr int kGroups = S::kEpiWarps / 4;
         uint8_t* stage = smem + S::kEpi + (warp - S::kEpiFirst) * kEpiBytes;
@@ -232,7 +291,7 @@ __global__ void __launch_bounds__(Shape<kCG>::kThreads, 1)
             const Tile T = W.get(t);
             const int f0 = T.f0 + rank * kFM + 32 * q;  // of this warp's 32 lanes
             const int live = (int)min((int64_t)32, p.N - f0);
-            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * S::kWide;
+            const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
             // scales and bias are fetched while the sums are made
             const float* xs = p.xs + T.row0;
             auto ready = [&] {
@@ -240,21 +299,66 @@ __global__ void __launch_bounds__(Shape<kCG>::kThreads, 1)
                 fence_after();
                 return __all_sync(0xffffffffu, ok && !*abort_flag) != 0;
             };
+            auto drained = [&] {
+                fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(acce0 + 8 * buf);
+                    else arrive_remote_relaxed(mapa(acce0 + 8 * buf, 0));
+                }
+                if (++buf == S::kBufs) { buf = 0; aphase ^= 1; }
+            };
+            // kDeep: the sums of this warp's columns, 32 of every 32 * kGroups
+            constexpr int kMine = S::kWide / (32 * kGroups);
+            const Pieces pieces{p.K <= kVecDepth};
+            auto each_piece = [&](auto&& take) {  // take(column's place in kMine, column, first piece)
+                for (int r0 = 0; r0 < T.red; r0 += CHUNK) {
+                    if (!ready()) return false;
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i)
+                        if (32 * (group + kGroups * i) < T.cols)
+                            take(i, lanes + buf * S::kWide + 32 * (group + kGroups * i), r0 == 0);
+                    drained();
+                }
+                return true;
+            };
             if constexpr (kF32) {
                 const int64_t at = (int64_t)T.e * p.N + f0 + lane;
                 const float sw = lane < live ? p.ws[at] : 0.0f;
                 const float b = p.bias && lane < live ? __bfloat162float(p.bias[at]) : 0.0f;
-                if (!ready()) break;
-                for (int c = 32 * group; c < T.cols; c += 32 * kGroups) {
-                    uint32_t v[32];
-                    tmem_ld32(acc + c, v);
-                    tmem_wait_ld();
-                    if (lane < live) {
-                        float* o = static_cast<float*>(p.out) + (T.row0 + c) * p.N + f0 + lane;
+                auto store = [&](const uint32_t* v, int c) {
+                    if (lane >= live) return;
+                    float* o = static_cast<float*>(p.out) + (T.row0 + c) * p.N + f0 + lane;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (c + j < T.cols) o[j * p.N] = __uint_as_float(v[j]) * xs[c + j] * sw + b;
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j < T.cols) o[j * p.N] = scaled(__uint_as_float(v[j]), xs[c + j], sw, b);
+                };
+                if constexpr (kDeep) {
+                    uint32_t sum[kMine][32];
+                    const bool ok = each_piece([&](int i, uint32_t at, bool first) {
+#pragma unroll
+                        for (int h = 0; h < 32; h += 16) {
+                            uint32_t v[16];
+                            tmem_ld16(at + h, v);
+                            tmem_wait_ld();
+                            pieces.add(&sum[i][h], v, first);
+                        }
+                    });
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) {
+                        pieces.finish<32>(sum[i]);
+                        store(sum[i], 32 * (group + kGroups * i));
                     }
+                } else {
+                    if (!ready()) break;
+                    for (int c = 32 * group; c < T.cols; c += 32 * kGroups) {
+                        uint32_t v[32];
+                        tmem_ld32(lanes + buf * S::kWide + c, v);
+                        tmem_wait_ld();
+                        store(v, c);
+                    }
+                    drained();
                 }
             } else {
                 float sw[4], b[4];
@@ -274,27 +378,50 @@ __global__ void __launch_bounds__(Shape<kCG>::kThreads, 1)
                         sx[i] = col < T.cols ? xs[col] : 0.0f;
                     }
                 };
-                scales(32 * group);
-                if (!ready()) break;
-                for (int c = 32 * group; c < T.cols; c += 32 * kGroups) {
-                    float s[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) s[i] = sx[i];
-                    scales(c + 32 * kGroups);
-                    store_columns_bf16(acc + c, lane, stage,
-                                       static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * p.N + f0, p.N, live,
-                                       T.cols - c, [&](float v, int l, int col) {
-                                           return v * s[(col >> 3) * 2 + (col & 1)] * sw[l >> 3] + b[l >> 3];
+                auto store = [&](auto&& v, int c) {
+                    store_columns_bf16(v, lane, stage, static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * p.N + f0, p.N,
+                                       live, T.cols - c, [&](float v, int l, int col) {
+                                           return scaled(v, sx[(col >> 3) * 2 + (col & 1)], sw[l >> 3], b[l >> 3]);
                                        });
+                };
+                if constexpr (kDeep) {
+                    uint32_t sum[kMine][2][16];
+                    const bool ok = each_piece([&](int i, uint32_t at, bool first) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t v[16];
+                            tmem_ld16x32(at + ((uint32_t)(16 * h) << 16), v);
+                            tmem_wait_ld();
+                            pieces.add(sum[i][h], v, first);
+                        }
+                    });
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) {
+                        const int c = 32 * (group + kGroups * i);
+                        if (c >= T.cols) break;
+                        pieces.finish<16>(sum[i][0]);
+                        pieces.finish<16>(sum[i][1]);
+                        scales(c);
+                        store(sum[i], c);
+                    }
+                } else {
+                    scales(32 * group);
+                    if (!ready()) break;
+                    for (int c = 32 * group; c < T.cols; c += 32 * kGroups) {
+                        float s[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) s[i] = sx[i];
+                        scales(c + 32 * kGroups);
+                        store_columns_bf16(lanes + buf * S::kWide + c, lane, stage,
+                                           static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * p.N + f0, p.N, live,
+                                           T.cols - c, [&](float v, int l, int col) {
+                                               return scaled(v, s[(col >> 3) * 2 + (col & 1)], sw[l >> 3], b[l >> 3]);
+                                           });
+                    }
+                    drained();
                 }
             }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (rank == 0) mbar_arrive(acce0 + 8 * buf);
-                else arrive_remote_relaxed(mapa(acce0 + 8 * buf, 0));
-            }
-            if (++buf == S::kBufs) { buf = 0; aphase ^= 1; }
         }
     } else {
         // ------------------------------------------------------ int8 -> f16, this CTA's rows
@@ -333,6 +460,8 @@ __global__ void __launch_bounds__(Shape<kCG>::kThreads, 1)
             }
         };
         if (weights) {
+            if constexpr (S::kWeiRegs < S::kStartRegs)
+                asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kWeiRegs));
             // lane = feature: 128 codes of its swizzled row (16-byte chunk ^= row mod 8)
             const int q = warp & 3;
             const uint32_t quarter = tmem + ((uint32_t)(32 * q) << 16) + S::kTmemA;
@@ -353,7 +482,7 @@ __global__ void __launch_bounds__(Shape<kCG>::kThreads, 1)
                     fence_before();
                 });
         } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCG == 2 ? 64 : 56));
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kTokRegs));
             // rows beyond the slice are widened too: what they hold is never stored
             constexpr int kUnits = S::kTok * (BK / 16) / (32 * CVT_WARPS);  // 16-byte chunks a thread
             // Eight lanes (a quarter warp) take four chunks of one row's first half of K and four of the next
@@ -477,17 +606,17 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* x, i
 
 }  // namespace i8
 
-template <int kCG, bool kF32>
+template <int kCG, bool kF32, bool kDeep>
 static cudaError_t launch_int8(const CUtensorMap& a, const CUtensorMap& b, const i8::Params& p, int64_t tiles,
                                cudaStream_t s) {
-    using S = i8::Shape<kCG>;
-    return launch_persistent<kCG, false, i8::ragged_int8_kernel<kCG, kF32>>(S::kThreads, S::smem(MXQ_MAX_EXPERTS),
+    using S = i8::Shape<kCG, kDeep>;
+    return launch_persistent<kCG, false, i8::ragged_int8_kernel<kCG, kF32, kDeep>>(S::kThreads, S::smem(MXQ_MAX_EXPERTS),
                                                                      S::smem(p.E), tiles, s, a, b, p);
 }
 
-template <int kCG>
+template <int kCG, bool kDeep>
 static cudaError_t run_int8_shape(const Int8Call& c, cudaStream_t s) {
-    using S = i8::Shape<kCG>;
+    using S = i8::Shape<kCG, kDeep>;
     const i8::Params p{c.xs, c.ws, static_cast<const __nv_bfloat16*>(c.bias), c.M, c.N, c.K, c.E, c.m_splits, c.out,
                        c.out_f32, c.status};
     const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {c.K, c.K * c.N}, db[2] = {c.K, c.M}, sb[1] = {c.K};
@@ -496,12 +625,14 @@ static cudaError_t run_int8_shape(const Int8Call& c, cudaStream_t s) {
     if (!encode_tmap(&a, c.wq, 1, 3, da, sa, boxa) || !encode_tmap(&b, c.xq, 1, 2, db, sb, boxb))
         return cudaErrorInvalidValue;
     const int64_t tiles = (c.M / S::kWide + std::min<int64_t>(c.E, c.M)) * ((c.N + S::kFeat - 1) / S::kFeat);
-    return c.out_f32 ? launch_int8<kCG, true>(a, b, p, tiles, s) : launch_int8<kCG, false>(a, b, p, tiles, s);
+    return c.out_f32 ? launch_int8<kCG, true, kDeep>(a, b, p, tiles, s) : launch_int8<kCG, false, kDeep>(a, b, p, tiles, s);
 }
 
 cudaError_t run_int8(const Int8Call& c, cudaStream_t s) {
     if (c.M <= (int64_t)kVecRows * c.E && c.K <= kVecDepth) return run_int8_vec(c, s);
-    return c.M <= (int64_t)kFewRows * c.E ? run_int8_shape<1>(c, s) : run_int8_shape<2>(c, s);
+    const bool deep = c.K > (c.out_f32 ? i8::CHUNK : i8::kTruncDepth);
+    if (c.M <= (int64_t)kFewRows * c.E) return deep ? run_int8_shape<1, true>(c, s) : run_int8_shape<1, false>(c, s);
+    return deep ? run_int8_shape<2, true>(c, s) : run_int8_shape<2, false>(c, s);
 }
 
 cudaError_t run_int8_quantize(const void* x, int64_t M, int64_t K, int64_t ld, void* q, float* scale, cudaStream_t s) {
