@@ -28,6 +28,17 @@
 // matrix product 3.9e-7). Outputs that are not rounded to bf16 are therefore
 // summed in registers, one accumulator of FLUSH stages at a time (kRegs).
 //
+// Long sums to bf16. A step of 16 terms may lose up to 2^-23 of the sum, in the
+// same direction for terms of one sign: 2^-12, a sixteenth of bf16's rounding,
+// in one accumulator of kTruncDepth = 2^15 terms, and some 2^-8 in one of 2^20.
+// So a tile with more terms (an expert's rows in wgrad; K or N otherwise) is
+// summed in pieces of LONG_FLUSH stages in one accumulator, which the epilogue's
+// warps add up in the other one, where the tile's epilogue then finds the sum.
+// The MMAs wait while a piece is added, which at 128 stages a piece is not
+// noticed (2 experts, 131072 rows, 2048 x 2048: 649 us in one accumulator, 648
+// to 666 so). Sums in registers beside the shorter tiles' code did not fit: the
+// spills took adding to bf16 dW from 67 to 186 us.
+//
 // A pair of SMs (a cluster of two CTAs, cta_group::2) shares a tile of 256
 // features by up to 256 rows, each staging half of both operands: 32 KB a stage
 // and SM for the MMA work that costs one SM alone 48 KB. Experts with few rows
@@ -70,6 +81,7 @@ namespace ragged {
 
 constexpr int BK = 64;    // reduction depth of a stage: 128 bytes of bf16
 constexpr int FLUSH = 8;  // stages an accumulator holds before it is added to the registers (kRegs)
+constexpr int LONG_FLUSH = 128;  // and before it is added to the other accumulator (more than kTruncDepth terms)
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 
@@ -167,6 +179,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // rank 0's fix[st], and the MMAs wait for that instead of full[st]. The parities of full, tail and fix
     // of a stage therefore follow their own uses, not the ring's laps.
     auto ragged_end = [](const Tile& T, int r) { return kMode == kWgrad && T.red - r < BK && ((T.red - r) & 15) != 0; };
+    auto long_sum = [](const Tile& T) { return !kRegs && T.red > kTruncDepth; };
+    auto piece = [&](const Tile& T) { return kRegs ? FLUSH * BK : long_sum(T) ? LONG_FLUSH * BK : T.red; };
     auto zero_rows = [&](const Tile& T, int r, int stage) {
         // a 16-byte chunk a lane, four rows at a time, box by box
         const int left = (T.red - r) & 15, boxes = 2 + (T.n / CG + 63) / 64;
@@ -248,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------ MMA issuer (rank 0)
         if (rank == 0) {
             int stage = 0, buf = 0;
-            uint32_t aphase = 0, full_uses = 0, fix_uses = 0;  // bits of stages: parities
+            uint32_t acc_uses = 0, full_uses = 0, fix_uses = 0;  // bits of accumulators and stages: parities
             const uint32_t base = smem_u32(smem);
             // MN-major: 64-element chunks 8192 bytes apart, 8-row groups of the reduction 1024 apart
             const uint64_t ad0 = smem_desc(base, a_mn ? 8192 : 16, 1024);
@@ -258,11 +272,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (t >= W.total) continue;
                 const Tile T = W.get(t);
                 const uint32_t id = idesc_f16(1, a_mn, b_mn, FEAT, T.n);
-                for (int r0 = 0; r0 < T.red; r0 += kRegs ? FLUSH * BK : T.red) {
-                    const int r1 = kRegs ? min(T.red, r0 + FLUSH * BK) : T.red;
+                for (int r0 = 0, r1; r0 < T.red; r0 = r1) {
+                    r1 = min(T.red, r0 + piece(T));
                     const uint32_t d = tmem + buf * WIDE;
-                    if (!mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag)) goto done_mma;
+                    if (!mbar_wait(acce0 + 8 * buf, (acc_uses >> buf & 1) ^ 1, abort_flag)) goto done_mma;
                     __syncwarp();
+                    acc_uses ^= 1u << buf;
                     for (int r = r0; r < r1; r += BK) {
                         const uint64_t ad = ad0 + (uint64_t)(stage * (STAGE_BYTES / 16));
                         const uint64_t bd = bd0 + (uint64_t)(stage * (STAGE_BYTES / 16));
@@ -286,9 +301,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         __syncwarp();
                         if (++stage == STAGES) stage = 0;
                     }
-                    buf ^= 1;
-                    aphase ^= buf == 0;
+                    if (!long_sum(T)) buf ^= 1;
                 }
+                if (long_sum(T)) acc_uses ^= 2u >> buf;  // the epilogue's use of the other accumulator
             } while (queue.next(t, lane, abort_flag) == TileQueue::kTile);
         done_mma:;
         }
@@ -332,16 +347,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint8_t* stage = smem + EPI_REGION + (warp - 2) * (kMode == kWgrad ? kBoxBytes : kEpiBytes);
         const int64_t ld = kMode == kFprop ? p.N : p.K;  // features
         int buf = 0;
-        uint32_t aphase = 0;
-        auto drained = [&] {
+        uint32_t acc_uses = 0;  // bits of accumulators: parities
+        auto filled = [&] {
+            const bool ok = mbar_wait(accf0 + 8 * buf, acc_uses >> buf & 1, abort_flag);
+            acc_uses ^= 1u << buf;
+            return __all_sync(0xffffffffu, ok && !*abort_flag) != 0;
+        };
+        auto drained = [&](int b) {
             fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (rank == 0) mbar_arrive(acce0 + 8 * buf);
-                else arrive_remote_relaxed(mapa(acce0 + 8 * buf, 0));
+                if (rank == 0) mbar_arrive(acce0 + 8 * b);
+                else arrive_remote_relaxed(mapa(acce0 + 8 * b, 0));
             }
-            buf ^= 1;
-            aphase ^= buf == 0;
         };
         do {
             if (t >= W.total) continue;
@@ -364,9 +382,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 float acc[kChunks][32];
                 bool ok = true;
                 for (int r0 = 0; r0 < T.red && ok; r0 += FLUSH * BK) {
-                    ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
-                    __syncwarp();
-                    ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+                    ok = filled();
                     if (!ok) break;
                     fence_after();
 #pragma unroll
@@ -385,7 +401,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                             }
                         }
                     }
-                    drained();
+                    drained(buf);
+                    buf ^= 1;
                 }
                 if (!ok) break;
                 const int l = q * 32 + lane;
@@ -434,8 +451,36 @@ __global__ void __launch_bounds__(THREADS, 1)
                                        live - 32 * q, T.cols - c, lane, old[i]);
                     }
                 }
-                const bool ok = mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
-                if (!__all_sync(0xffffffffu, ok && !*abort_flag)) break;
+                const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+                int from = buf;  // the accumulator that holds the sums
+                bool ok = true;
+                if (long_sum(T)) {
+                    from ^= 1;
+                    for (int r0 = 0; r0 < T.red; r0 += piece(T)) {
+                        ok = filled();
+                        if (!ok) break;
+                        fence_after();
+                        for (int c = 32 * group; c < T.cols; c += 64)
+#pragma unroll
+                            for (int h = 0; h < 32; h += 16) {
+                                uint32_t v[16], s[16];
+                                tmem_ld16(lanes + buf * WIDE + c + h, v);
+                                tmem_ld16(lanes + from * WIDE + c + h, s);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    if (r0 > 0)
+                                        v[j] = __float_as_uint(__fadd_rn(__uint_as_float(s[j]), __uint_as_float(v[j])));
+                                tmem_st16(lanes + from * WIDE + c + h, v);
+                            }
+                        tmem_wait_st();
+                        drained(buf);
+                    }
+                } else {
+                    ok = filled();
+                    buf ^= 1;
+                }
+                if (!ok) break;
                 fence_after();
                 float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 if (kMode == kFprop && p.bias) {
@@ -445,7 +490,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (l < live) b[g] = __bfloat162float(p.bias[(int64_t)T.e * p.N + f0 + l]);
                     }
                 }
-                const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * WIDE;
+                const uint32_t acc = lanes + from * WIDE;
                 if constexpr (kMode == kWgrad) {
 #pragma unroll
                     for (int i = 0; i < kBoxes; ++i) {
@@ -460,7 +505,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                            static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c) * ld + f0 + 32 * q, ld,
                                            live - 32 * q, T.cols - c, [&](float v, int l, int) { return v + b[l >> 3]; });
                 }
-                drained();
+                drained(from);
             }
         } while (queue.next(t, lane, abort_flag) == TileQueue::kTile);
         if (kMode == kWgrad) {  // the last boxes are written before the block leaves its shared memory

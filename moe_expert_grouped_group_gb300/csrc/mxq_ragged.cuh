@@ -19,6 +19,9 @@ namespace mxq {
 namespace ragged {
 
 constexpr int kFM = 128;  // MMA M: rows of A (features) per CTA
+// Terms of a sum rounded to bf16 beyond which it is not left to one accumulator, which truncates: up to 2^-23 of the
+// sum per 16 terms, 2^-12 at this length.
+constexpr int64_t kTruncDepth = 1 << 15;
 
 // ------------------------------------------------------------ PTX wrappers
 // These kernels are launched so that they may begin while the stream's previous
@@ -240,6 +243,15 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, uint2 a, uint2 b, uint2
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(a.x), "r"(a.y),
                  "r"(b.x), "r"(b.y), "r"(c.x), "r"(c.y), "r"(d.x), "r"(d.y)
                  : "memory");
+}
+// Writes 16 consecutive columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }

@@ -15,8 +15,8 @@
 // (kDeep): as 32-bit integers, exact, while no sum can leave them (K up to
 // kVecDepth), in fp32 beyond. fp32 outputs take that shape where K > 1024 and
 // so are the same bits as those of the dot products, whatever shares the call.
-// bf16 outputs take it where K > 2^15: below, the truncation is under 2^-12 of
-// the sum of the products' magnitudes, an eighth of bf16's rounding, and
+// bf16 outputs take it where K > kTruncDepth = 2^15: below, the truncation is under 2^-12 of
+// the sum of the products' magnitudes, a sixteenth of bf16's rounding, and
 // zero-mean codes, whose sums stay within 2^24, have none.
 //
 // What kDeep costs: a pair's sums fill the registers at 128 columns, half of
@@ -64,7 +64,6 @@ constexpr int BK = 128;  // depth of an int8 stage
 constexpr int HK = 64;   // half of it: 128 bytes of f16
 constexpr int CVT_WARPS = 4;  // of a set: for the weights, and as many for the tokens
 constexpr int CHUNK = 1024;  // of K whose sums are whole numbers in fp32: |codes| <= 128
-constexpr int64_t kTruncDepth = 1 << 15;
 
 template <int kCG, bool kDeep>
 struct Shape {
@@ -630,7 +629,7 @@ static cudaError_t run_int8_shape(const Int8Call& c, cudaStream_t s) {
 
 cudaError_t run_int8(const Int8Call& c, cudaStream_t s) {
     if (c.M <= (int64_t)kVecRows * c.E && c.K <= kVecDepth) return run_int8_vec(c, s);
-    const bool deep = c.K > (c.out_f32 ? i8::CHUNK : i8::kTruncDepth);
+    const bool deep = c.K > (c.out_f32 ? i8::CHUNK : kTruncDepth);
     if (c.M <= (int64_t)kFewRows * c.E) return deep ? run_int8_shape<1, true>(c, s) : run_int8_shape<1, false>(c, s);
     return deep ? run_int8_shape<2, true>(c, s) : run_int8_shape<2, false>(c, s);
 }
