@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 
 import torch
@@ -720,6 +721,26 @@ def _shape(t, name, want):
         raise MXQError(f"{name}: shape {tuple(t.shape)}, expected {want}")
 
 
+def _packed(t, name, want, dtypes):
+    """Pointer of a tensor of shape `want` that may be passed: its own bytes would not tell a transposed
+    one. Dimensions of one do not count, and a flat tensor of as many elements is the same memory."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.shape == want and t.dtype in dtypes and t.is_cuda and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, name, 0, dtypes)
+    if t.numel() != math.prod(want) or (t.dim() != 1 and [d for d in t.shape if d != 1] != [d for d in want if d != 1]):
+        raise MXQError(f"{name}: shape {tuple(t.shape)}, expected {tuple(want)}")
+    return _ptr(t)
+
+
+def _gate_up(y):
+    """Rows and half the width of FC1's output [g | u]."""
+    if y.dim() != 2 or y.shape[1] % 2:
+        raise MXQError(f"y: shape {tuple(y.shape)}, expected (M, 2F)")
+    return y.shape[0], y.shape[1] // 2
+
+
 def _out(out, out_dtype, shape, like, default, other, flag):
     """The output tensor of a product, its pointer and the flag for its element type."""
     if out is None:
@@ -753,7 +774,7 @@ def ragged_gemm_fprop(x, w, m_splits, bias=None, out_dtype=None, status=None, ou
     E, N, Kw = w.shape
     _shape(w, "w", (E, N, K))
     out, op, flag = _out(out, out_dtype, (M, N), x, torch.bfloat16, torch.float32, OUT_F32)
-    rc = lib().mxq_ragged_gemm_fprop(xp, ldx, _dev(w, "w", 0, _BF16), _dev(bias, "bias", E * N * 2, _BF16), M, N, K, E,
+    rc = lib().mxq_ragged_gemm_fprop(xp, ldx, _dev(w, "w", 0, _BF16), _packed(bias, "bias", (E, N), _BF16), M, N, K, E,
                                      _grouping(m_splits, E), flag, op, _dev(status, "status", 4, _I32), _stream())
     if rc:
         _check(rc, "mxq_ragged_gemm_fprop")
@@ -797,8 +818,8 @@ def int8_quantize_rows(x, out=None):
     """bf16 rows (M, K) -> (int8 codes (M, K), fp32 scales (M,)), x ~ q * scale."""
     xp, M, K, ldx = _rows(x, "x", _BF16)
     q, scale = out if out is not None else (_new((M, K), torch.int8, x), _new((M,), torch.float32, x))
-    rc = lib().mxq_int8_quantize_rows(xp, ldx, M, K, _dev(q, "q", M * K, _I8), _dev(scale, "scale", M * 4, _F32),
-                                      _stream())
+    rc = lib().mxq_int8_quantize_rows(xp, ldx, M, K, _packed(q, "q", (M, K), _I8),
+                                      _packed(scale, "scale", (M,), _F32), _stream())
     if rc:
         _check(rc, "mxq_int8_quantize_rows")
     return q, scale
@@ -811,9 +832,9 @@ def int8_gemm_fprop(xq, x_scale, wq, w_scale, m_splits, bias=None, out_dtype=Non
     E, N, Kw = wq.shape
     _shape(wq, "wq", (E, N, K))
     out, op, flag = _out(out, out_dtype, (M, N), xq, torch.bfloat16, torch.float32, OUT_F32)
-    rc = lib().mxq_int8_gemm_fprop(_dev(xq, "xq", 0, _I8), _dev(x_scale, "x_scale", M * 4, _F32),
-                                   _dev(wq, "wq", 0, _I8), _dev(w_scale, "w_scale", E * N * 4, _F32),
-                                   _dev(bias, "bias", E * N * 2, _BF16), M, N, K, E, _grouping(m_splits, E), flag, op,
+    rc = lib().mxq_int8_gemm_fprop(_dev(xq, "xq", 0, _I8), _packed(x_scale, "x_scale", (M,), _F32),
+                                   _dev(wq, "wq", 0, _I8), _packed(w_scale, "w_scale", (E, N), _F32),
+                                   _packed(bias, "bias", (E, N), _BF16), M, N, K, E, _grouping(m_splits, E), flag, op,
                                    _dev(status, "status", 4, _I32), _stream())
     if rc:
         _check(rc, "mxq_int8_gemm_fprop")
@@ -822,12 +843,11 @@ def int8_gemm_fprop(xq, x_scale, wq, w_scale, m_splits, bias=None, out_dtype=Non
 
 def swiglu_dropout_fwd(y, rng, p, out=None):
     """h = D(silu(g) * u) of FC1's output y = [g | u] (M, 2F). rng: CUDA int64 {seed, offset}."""
-    M, F2 = y.shape
-    F = F2 // 2
+    M, F = _gate_up(y)
     if out is None:
         out = _new((M, F), torch.bfloat16, y)
     rc = lib().mxq_swiglu_dropout_fwd(_dev(y, "y", 0, _BF16), M, F, _dev(rng, "rng", 16, _I64T), p,
-                                      _dev(out, "out", M * F * 2, _BF16), _stream())
+                                      _packed(out, "out", (M, F), _BF16), _stream())
     if rc:
         _check(rc, "mxq_swiglu_dropout_fwd")
     return out
@@ -835,12 +855,11 @@ def swiglu_dropout_fwd(y, rng, p, out=None):
 
 def swiglu_dropout_bwd(dh, y, rng, p, out=None):
     """The gradient [dg | du] (M, 2F) of y from dh (M, F); rng and p those of the forward call."""
-    M, F2 = y.shape
-    F = F2 // 2
+    M, F = _gate_up(y)
     if out is None:
-        out = _new((M, F2), torch.bfloat16, y)
-    rc = lib().mxq_swiglu_dropout_bwd(_dev(dh, "dh", M * F * 2, _BF16), _dev(y, "y", 0, _BF16), M, F,
-                                      _dev(rng, "rng", 16, _I64T), p, _dev(out, "out", M * F2 * 2, _BF16), _stream())
+        out = _new((M, 2 * F), torch.bfloat16, y)
+    rc = lib().mxq_swiglu_dropout_bwd(_packed(dh, "dh", (M, F), _BF16), _dev(y, "y", 0, _BF16), M, F,
+                                      _dev(rng, "rng", 16, _I64T), p, _packed(out, "out", (M, 2 * F), _BF16), _stream())
     if rc:
         _check(rc, "mxq_swiglu_dropout_bwd")
     return out
@@ -851,9 +870,9 @@ def dropout(x, rng, p, residual=None, out=None):
     xp = _dev(x, "x", 0, _BF16_F32)
     if out is None:
         out = _new(tuple(x.shape), x.dtype, x)
-    size, same = x.nbytes, (x.dtype,)
-    rc = lib().mxq_dropout(xp, _dev(residual, "residual", size, same), x.numel(), _dev(rng, "rng", 16, _I64T), p,
-                           OUT_F32 if x.dtype is torch.float32 else 0, _dev(out, "out", size, same), _stream())
+    shape, same = x.shape, (x.dtype,)
+    rc = lib().mxq_dropout(xp, _packed(residual, "residual", shape, same), x.numel(), _dev(rng, "rng", 16, _I64T), p,
+                           OUT_F32 if x.dtype is torch.float32 else 0, _packed(out, "out", shape, same), _stream())
     if rc:
         _check(rc, "mxq_dropout")
     return out
