@@ -423,7 +423,8 @@ MXQ_API int mxq_ragged_gemm_wgrad(const void* dy_bf16, int64_t lddy, const void*
 /* ---- Ragged grouped products in int8 -------------------------------------
  *
  * Symmetric int8 with one fp32 scale per token and per output channel, for
- * serving quantized experts. */
+ * serving quantized experts. Scales need no alignment but a float's, so those
+ * of a slice of rows may be passed. */
 
 /* Quantizes the rows of x (M, K), row stride ldx: scale[m] = a / 127 and
  * q[m,k] = rint(x[m,k] * (127 / a)) with a = max(max_k |x[m,k]|, 2^-100), each

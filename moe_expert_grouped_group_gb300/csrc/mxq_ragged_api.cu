@@ -28,6 +28,8 @@ int check_ragged(int64_t M, int64_t N, int64_t K, int step_n, int step_k, int E,
     if (!m_splits) return MXQ_ERR_NULL;
     return device_pointer(m_splits) ? MXQ_OK : MXQ_ERR_HOST_POINTER;
 }
+// per-row and per-channel scales are read and written one float at a time
+bool aligned4(const float* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 bool bad_stride(int64_t ld, int64_t width) { return ld < width || ld % 8 || ld > ((int64_t)1 << 36); }
 
 int run(const mxq::ragged::GemmCall& c, mxq_stream_t stream) {
@@ -96,7 +98,7 @@ int mxq_int8_quantize_rows(const void* x_bf16, int64_t ldx, int64_t M, int64_t K
     if (M != 0 && (!x_bf16 || !q || !scale)) return MXQ_ERR_NULL;
     if (!arch_ok()) return MXQ_ERR_ARCH;
     if (M < 0 || M > kMaxRows || K <= 0 || K > kMaxWidth || K % 16 || bad_stride(ldx, K)) return MXQ_ERR_SHAPE;
-    if (!aligned16(x_bf16) || !aligned16(q) || !aligned16(scale)) return MXQ_ERR_ALIGN;
+    if (!aligned16(x_bf16) || !aligned16(q) || !aligned4(scale)) return MXQ_ERR_ALIGN;
     const cudaError_t e = mxq::ragged::run_int8_quantize(x_bf16, M, K, ldx, q, scale, (cudaStream_t)stream);
     return e == cudaSuccess ? MXQ_OK : fail_cuda(e);
 }
@@ -107,7 +109,7 @@ int mxq_int8_gemm_fprop(const void* xq, const float* x_scale, const void* wq, co
     if (flags & ~MXQ_OUT_F32) return MXQ_ERR_FLAGS;
     if (!wq || !w_scale || (M != 0 && (!xq || !x_scale || !y))) return MXQ_ERR_NULL;
     if (int r = check_ragged(M, N, K, 8, 16, E, d_m_splits)) return r;
-    if (!aligned16(xq) || !aligned16(x_scale) || !aligned16(wq) || !aligned16(w_scale) || !aligned16(bias_bf16) ||
+    if (!aligned16(xq) || !aligned4(x_scale) || !aligned16(wq) || !aligned4(w_scale) || !aligned16(bias_bf16) ||
         !aligned16(y))
         return MXQ_ERR_ALIGN;
     if (M == 0) return MXQ_OK;

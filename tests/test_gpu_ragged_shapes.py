@@ -70,3 +70,24 @@ def test_bias_scales_and_codes(mxq):
     want = mxq.int8_gemm_fprop(xq, xs, wq, ws.view(E, N), ms, bias=bias)
     # a column of scales, and the flat scales and bias of all experts
     assert torch.equal(mxq.int8_gemm_fprop(xq, xs.view(M, 1), wq, ws, ms, bias=bias.view(-1)), want)
+
+
+@pytest.mark.parametrize("counts", [[1, 2], [17, 14], [100, 29]], ids=str)
+def test_scales_at_any_float(mxq, counts):
+    """A slice of a batch: its scales begin at any float of the batch's."""
+    m = sum(counts)
+    x, w, ms = rand(1, m + 3, K), rand(3, E, N, K), dev_i64(counts)
+    wq, ws = mxq.int8_quantize_rows(w.view(E * N, K))
+    wq, ws = wq.view(E, N, K), ws.view(E, N)
+    xq, xs = mxq.int8_quantize_rows(x)
+    for at in (1, 2, 3):
+        rows = slice(at, at + m)
+        codes, scales = torch.empty_like(xq[rows]), torch.zeros(m + 6, device="cuda")
+        mxq.int8_quantize_rows(x[rows], out=(codes, scales[at:at + m]))
+        assert torch.equal(scales[at:at + m], xs[rows]) and not scales[:at].any() and not scales[at + m:].any()
+        late = torch.zeros(E * N + 3, device="cuda")
+        late[at:at + E * N] = ws.view(-1)
+        for dt in (BF16, torch.float32):
+            want = mxq.int8_gemm_fprop(xq[rows], xs[rows].clone(), wq, ws, ms, out_dtype=dt)
+            got = mxq.int8_gemm_fprop(xq[rows], xs[rows], wq, late[at:at + E * N].view(E, N), ms, out_dtype=dt)
+            assert torch.equal(got, want)
