@@ -680,13 +680,33 @@ def _dev(t, name, nbytes, dtypes):
 
 
 # Allocation of an output on the current device without the argument parsing and dispatch of
-# torch.empty (about 1 us against 3 to 5 between other calls, as much as a small kernel); torch's
-# public call where the fast one is missing or the tensor belongs on another device.
+# torch.empty (about 1 us against 3 to 5 between other calls, as much as a small kernel). It is not
+# a public call, so it is tried once: torch.empty is used where it is missing, takes other arguments
+# or gives another tensor, where the tensor belongs on another device, and under
+# torch.use_deterministic_algorithms, which fills what torch.empty returns.
 _empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 
 
+_fast_empty = None  # the call, or False, once it has been tried
+
+
+def _try_fast_empty():
+    global _fast_empty
+    _fast_empty = False
+    try:
+        t = _empty_strided((2, 3), (3, 1), torch.int8)
+        if (t.shape == (2, 3) and t.stride() == (3, 1) and t.dtype is torch.int8 and t.storage_offset() == 0
+                and t.get_device() == torch.cuda.current_device()):
+            _fast_empty = _empty_strided
+    except Exception:  # whatever a changed signature raises
+        pass
+
+
 def _new(shape, dtype, like):
-    if _empty_strided is not None and like.get_device() == torch.cuda.current_device():
+    if _fast_empty is None:
+        _try_fast_empty()
+    if (_fast_empty and like.get_device() == torch.cuda.current_device()
+            and not torch.are_deterministic_algorithms_enabled()):
         d = len(shape)
         if d == 2:
             strides = (shape[1], 1)
@@ -694,7 +714,7 @@ def _new(shape, dtype, like):
             strides = (shape[1] * shape[2], shape[2], 1)
         else:
             strides = (1,) if d == 1 else torch.empty(shape, device="meta").stride()
-        return _empty_strided(shape, strides, dtype)
+        return _fast_empty(shape, strides, dtype)
     return torch.empty(shape, dtype=dtype, device=like.device)
 
 
@@ -736,9 +756,10 @@ def _packed(t, name, want, dtypes):
 
 def _gate_up(y):
     """Rows and half the width of FC1's output [g | u]."""
-    if y.dim() != 2 or y.shape[1] % 2:
-        raise MXQError(f"y: shape {tuple(y.shape)}, expected (M, 2F)")
-    return y.shape[0], y.shape[1] // 2
+    shape = y.shape
+    if len(shape) != 2 or shape[1] & 1:
+        raise MXQError(f"y: shape {tuple(shape)}, expected (M, 2F)")
+    return shape[0], shape[1] >> 1
 
 
 def _out(out, out_dtype, shape, like, default, other, flag):
@@ -817,9 +838,13 @@ def ragged_gemm_wgrad(dy, x, m_splits, accumulate=False, out_dtype=None, status=
 def int8_quantize_rows(x, out=None):
     """bf16 rows (M, K) -> (int8 codes (M, K), fp32 scales (M,)), x ~ q * scale."""
     xp, M, K, ldx = _rows(x, "x", _BF16)
-    q, scale = out if out is not None else (_new((M, K), torch.int8, x), _new((M,), torch.float32, x))
-    rc = lib().mxq_int8_quantize_rows(xp, ldx, M, K, _packed(q, "q", (M, K), _I8),
-                                      _packed(scale, "scale", (M,), _F32), _stream())
+    if out is None:
+        q, scale = _new((M, K), torch.int8, x), _new((M,), torch.float32, x)
+        qp, sp = q.data_ptr(), scale.data_ptr()
+    else:
+        q, scale = out
+        qp, sp = _packed(q, "q", (M, K), _I8), _packed(scale, "scale", (M,), _F32)
+    rc = lib().mxq_int8_quantize_rows(xp, ldx, M, K, qp, sp, _stream())
     if rc:
         _check(rc, "mxq_int8_quantize_rows")
     return q, scale
@@ -846,8 +871,11 @@ def swiglu_dropout_fwd(y, rng, p, out=None):
     M, F = _gate_up(y)
     if out is None:
         out = _new((M, F), torch.bfloat16, y)
+        op = out.data_ptr()
+    else:
+        op = _packed(out, "out", (M, F), _BF16)
     rc = lib().mxq_swiglu_dropout_fwd(_dev(y, "y", 0, _BF16), M, F, _dev(rng, "rng", 16, _I64T), p,
-                                      _packed(out, "out", (M, F), _BF16), _stream())
+                                      op, _stream())
     if rc:
         _check(rc, "mxq_swiglu_dropout_fwd")
     return out
@@ -858,8 +886,11 @@ def swiglu_dropout_bwd(dh, y, rng, p, out=None):
     M, F = _gate_up(y)
     if out is None:
         out = _new((M, 2 * F), torch.bfloat16, y)
+        op = out.data_ptr()
+    else:
+        op = _packed(out, "out", (M, 2 * F), _BF16)
     rc = lib().mxq_swiglu_dropout_bwd(_packed(dh, "dh", (M, F), _BF16), _dev(y, "y", 0, _BF16), M, F,
-                                      _dev(rng, "rng", 16, _I64T), p, _packed(out, "out", (M, 2 * F), _BF16), _stream())
+                                      _dev(rng, "rng", 16, _I64T), p, op, _stream())
     if rc:
         _check(rc, "mxq_swiglu_dropout_bwd")
     return out
@@ -867,12 +898,14 @@ def swiglu_dropout_bwd(dh, y, rng, p, out=None):
 
 def dropout(x, rng, p, residual=None, out=None):
     """D(x) (+ residual), bf16 or fp32; its own gradient when residual is None. out may be x or residual."""
-    xp = _dev(x, "x", 0, _BF16_F32)
+    xp, shape, same = _dev(x, "x", 0, _BF16_F32), x.shape, (x.dtype,)
     if out is None:
-        out = _new(tuple(x.shape), x.dtype, x)
-    shape, same = x.shape, (x.dtype,)
+        out = _new(tuple(shape), x.dtype, x)
+        op = out.data_ptr()
+    else:
+        op = _packed(out, "out", shape, same)
     rc = lib().mxq_dropout(xp, _packed(residual, "residual", shape, same), x.numel(), _dev(rng, "rng", 16, _I64T), p,
-                           OUT_F32 if x.dtype is torch.float32 else 0, _packed(out, "out", shape, same), _stream())
+                           OUT_F32 if x.dtype is torch.float32 else 0, op, _stream())
     if rc:
         _check(rc, "mxq_dropout")
     return out
