@@ -425,10 +425,14 @@ __global__ void __launch_bounds__(Shape<kCG, kDeep>::kThreads, 1)
     } else {
         // ------------------------------------------------------ int8 -> f16, this CTA's rows
         // A set's turn is every kSets-th stage: wait for the next slot and for the stage, load the codes into
-        // registers and free the stage, widen them into the slot. The slot comes first: its last MMAs are
+        // registers, widen them into the slot, free the stage. The slot comes first: its last MMAs are
         // those of SLOTS stages ago, so all earlier stages have been loaded, and with no fewer than SLOTS of
         // them a stage's barrier cannot be more than one phase behind what a set waits for, although the other
         // sets' phases are not its own.
+        // The stage is freed when its codes have been used, behind a fence: TMA writes the next fill through
+        // another proxy, and an arrival that only followed the loads overtook those that waited behind the
+        // epilogue's stores (fp32, K = 7168: codes of the next fill in 1 call of 100). Freed between the loads and
+        // the widening, with the fence there, 16384 rows take 218 us in place of 213.
         const bool weights = warp < S::kTokFirst;
         const int set = (warp - (weights ? S::kCvtFirst : S::kTokFirst)) / CVT_WARPS;
         const uint32_t lead_full = kCG == 2 ? mapa(full0, 0) : 0;
@@ -443,11 +447,11 @@ __global__ void __launch_bounds__(Shape<kCG, kDeep>::kThreads, 1)
                                         mbar_wait(rawf0 + 8 * raw, rphase, abort_flag);
                         if (!__all_sync(0xffffffffu, ok)) return;
                         load(smem + S::kRawAt + raw * S::kRaw);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(rawe0 + 8 * raw);
                         widen();
+                        if (weights) fence_async_smem();  // the tokens' writes end with one
                         __syncwarp();
                         if (lane == 0) {
+                            mbar_arrive(rawe0 + 8 * raw);
                             if (rank == 0) mbar_arrive(full0 + 8 * slot);
                             else arrive_remote(lead_full + 8 * slot);
                         }

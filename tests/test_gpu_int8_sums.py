@@ -80,3 +80,20 @@ def test_a_token_alone_and_in_a_batch(mxq):
     for m in (1, 20):
         alone = mxq.int8_gemm_fprop(xq[:m], xs[:m], wq, ws, dev_i64([m]), bias=bias, out_dtype=F32)
         assert torch.equal(alone, batch[:m])
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=str)
+@pytest.mark.parametrize("K,calls", [(2048, 400), (7168, 300)])
+def test_stages_are_read_before_they_are_filled_again(mxq, dt, K, calls):
+    """Whole tiles whose stores go on while the next tile's stages are loaded, again and again."""
+    counts, N = [2049, 700], 1024
+    xq, xs, wq, ws, _ = inputs(counts, N, K, -128, 128)
+    ms, wrong = dev_i64(counts), torch.zeros((), dtype=torch.int64, device="cuda")
+    zero = torch.zeros((2, N), dtype=BF16, device="cuda")
+    want = steps32(xq, xs, wq, ws, zero, counts).to(dt)
+    y = torch.empty_like(want)
+    for _ in range(calls):
+        y.fill_(float("nan"))
+        mxq.int8_gemm_fprop(xq, xs, wq, ws, ms, out=y)
+        wrong += (y != want).sum()
+    assert wrong.item() == 0
