@@ -202,13 +202,16 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
         }
     }
 }
-// Remote arrive that follows this warp's earlier accesses to its own CTA's shared memory or TMEM: reads of a
-// buffer that another CTA fills again, or writes that fence.proxy.async or tcgen05.wait::st has made visible
-// to the tensor core (a pair's MMA reads them through this SM). What was accessed is on this SM, so the
-// arrive needs no cluster-wide release, which would wait for this warp's global stores as well: 800 to
-// 1500 cycles an arrive.
+// Remote arrive that follows this warp's earlier accesses to its own CTA's shared memory or TMEM, which
+// fence.proxy.async or tcgen05.wait::st has completed: an answer of the tile queue that has been read, or writes
+// that a pair's MMA reads through this SM. What was accessed is on this SM, so the arrive needs no cluster-wide
+// release, which would wait for this warp's global stores as well: 800 to 1500 cycles an arrive.
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// Remote arrive behind plain shared-memory loads: it may not overtake them (0.2 us each).
+__device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 // 32 consecutive accumulator columns of this warp's 32 TMEM lanes
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -590,9 +593,10 @@ struct SplitSum {
         : buf(buf_), partf(partf_), parte(parte_), rank(rank_) {}
 
     // v: this CTA's partial sums of lane l on entry, the whole sums of its kOwn columns in v[0 .. kOwn - 1]
-    // on return. Called by the four warps that hold the 128 lanes; `first` is true in one of them. False
-    // when a bounded wait has expired.
-    __device__ bool exchange(float (&v)[kFewRows], int l, int lane, bool first, volatile int* abort_flag) {
+    // on return. Called by the four warps that hold the 128 lanes; `first` is true in one of them; `again`: the
+    // cluster has a tile after the next one, which fills this tile's buffer again. False when a bounded wait has
+    // expired.
+    __device__ bool exchange(float (&v)[kFewRows], int l, int lane, bool first, bool again, volatile int* abort_flag) {
         if constexpr (kSplit > 1) {
             const uint32_t side = tile & 1, phase = tile >> 1 & 1;
             ++tile;
@@ -634,9 +638,9 @@ struct SplitSum {
                 }
             }
             __syncwarp();
-            if (lane == 0)
+            if (again && lane == 0)
                 for (int j = 0; j < kSplit; ++j)
-                    if (j != rank) arrive_remote(mapa(parte + 8 * side, j));
+                    if (j != rank) arrive_remote_release(mapa(parte + 8 * side, j));
         }
         return true;
     }

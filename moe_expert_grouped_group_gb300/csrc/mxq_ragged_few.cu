@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int j = 0; j < WIDE; ++j)
                     acc[j] = r0 == rb ? __uint_as_float(v[j]) : __fadd_rn(acc[j], __uint_as_float(v[j]));
             }
-            if (!ok || !split.exchange(acc, l, lane, q == 0, abort_flag)) break;
+            if (!ok || !split.exchange(acc, l, lane, q == 0, t + 2 * stride < W.total, abort_flag)) break;
             if (T.f0 + l >= ld) continue;
             const float b = kMode == kFprop && p.bias ? __bfloat162float(p.bias[(int64_t)T.e * p.N + T.f0 + l]) : 0.0f;
 #pragma unroll
