@@ -612,9 +612,15 @@ static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
 
 cudaError_t run_gemm(const GemmCall& c, cudaStream_t s) {
     if (c.mode == kWgrad) return run_mode<kWgrad>(c, s);
+    // One-SM tiles up to as many rows as one holds, on average. W of 2048 x 4096, us, fprop and dgrad, one SM against
+    // pairs: 8 experts of 16 rows each 26.2 and 23.7 against 27.4 and 25.5, of 32 26.6 and 24.0 against 27.4 and 25.7,
+    // of 40 39.9 and 38.1 against 27.8 and 25.9; 64 experts of 32 168 and 163 against 170 and 159. Uneven counts need
+    // more one-SM tiles: 32 rows on average in Dirichlet(0.3) shares 30.7 and 38.0 against 26.7 and 25.5 (8 experts),
+    // 194 and 182 against 135 and 134 (64); all on one expert 20.9 and 20.2 against 15.9 and 23.9 (8), 130 and 124
+    // against 27 and 25 (64).
     if (c.M <= (int64_t)kFewRows * c.E) {
-        // dot products where the one-SM tiles would leave SMs idle (2048 x 4096, us: 1 row of 1 expert 4.9
-        // against 8.3, 4 rows 6.7 against 8.4; 8 experts fill the SMs: 1 row each 26.2 and 26.3, 4 rows 32.8
+        // dot products where the one-SM tiles would leave SMs idle (2048 x 4096, us: 1 row of 1 expert 4.3
+        // against 7.7, 4 rows 5.9 against 7.7; 8 experts fill the SMs: 1 row each 26.2 and 26.3, 4 rows 32.8
         // and 27.0)
         const int64_t tiles = std::min<int64_t>(c.E, c.M) * ((c.N + kFM - 1) / kFM);
         if (c.mode == kFprop && c.M <= (int64_t)kVecRows * c.E && tiles <= sm_count()) return run_fprop_vec(c, s);

@@ -22,10 +22,10 @@
 // What kDeep costs: a pair's sums fill the registers at 128 columns, half of
 // what an MMA with A in TMEM takes in the same time, against which the epilogue
 // is hidden by a second accumulator. fp32, 8 experts, 16384 rows, us, in one
-// truncating accumulator and as it is: 2048 x 4096 253 and 304, 7168 x 2048 320
-// and 458 (bf16: 190 and 293). One set of converting warps leaves the epilogue
-// its registers; with two it spilled (339 and 460). Few rows: 8 experts x 16
-// 19.9 and 20.8, 64 x 16 113 and 118.
+// truncating accumulator and as it is: 2048 x 4096 253 and 310, 7168 x 2048 320
+// and 482 (bf16: 193 and 293). One set of converting warps leaves the epilogue
+// its registers; with two it spilled (2048 x 4096 a tenth slower). Few rows: 8
+// experts x 16 19.9 and 20.9, 64 x 16 113 and 118.
 //
 // The tile walk, the operands' sides (features on the MMA's M, tokens on its
 // N), the edges and the two shapes (pairs of SMs; one SM for few rows) are
@@ -556,7 +556,7 @@ struct RowScale {
 
 // Rows of at most kLanes * kVec * 8 elements: kLanes lanes hold a row in
 // registers, so it is read once and no block waits. 16384 x 2048: 27.8 us with
-// the block kernel below, 14.1 us with this one; 1000000 x 128: 884 and 74 us.
+// the block kernel below, 14.1 to 17.4 us with this one; 1000000 x 128: 884 and 74 us.
 template <int kLanes, int kVec>
 __global__ void __launch_bounds__(256) quantize_rows_lanes_kernel(const uint16_t* x, int64_t M, int64_t K, int64_t ld,
                                                                   uint8_t* q, float* scale) {
@@ -585,7 +585,8 @@ __global__ void __launch_bounds__(256) quantize_rows_lanes_kernel(const uint16_t
     }
 }
 
-// Longer rows: a block each, read twice (the second time from cache).
+// Longer rows: a block each, read twice (the second time from cache). 16384 x 4096: 51.7 us, x 7168: 67.7 us; 131072 x
+// 7168: 437 us (floors, at 3 bytes an element: 30, 52 and 415).
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* x, int64_t M, int64_t K, int64_t ld,
                                                             uint8_t* q, float* scale) {
     wait_for_stream();
@@ -633,6 +634,10 @@ static cudaError_t run_int8_shape(const Int8Call& c, cudaStream_t s) {
 
 cudaError_t run_int8(const Int8Call& c, cudaStream_t s) {
     if (c.M <= (int64_t)kVecRows * c.E && c.K <= kVecDepth) return run_int8_vec(c, s);
+    // One-SM tiles up to as many rows as one holds, on average. W of 2048 x 4096, bf16, us, one SM against pairs: 8
+    // experts of 32 rows each 19.0 against 24.6, of 48 34.3 against 24.8; 64 experts of 32 113 against 145, of 48 211
+    // against 146. Uneven counts need more one-SM tiles: 32 rows on average in Dirichlet(0.3) shares 26.4 against 26.0
+    // (8 experts), 157 against 120 (64); all on one expert 19.0 against 17.7 (8), 111 against 31 (64).
     const bool deep = c.K > (c.out_f32 ? i8::CHUNK : kTruncDepth);
     if (c.M <= (int64_t)kFewRows * c.E) return deep ? run_int8_shape<1, true>(c, s) : run_int8_shape<1, false>(c, s);
     return deep ? run_int8_shape<2, true>(c, s) : run_int8_shape<2, false>(c, s);

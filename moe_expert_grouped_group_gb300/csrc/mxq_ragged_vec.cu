@@ -15,9 +15,13 @@
 // its 128. The tensor-core shapes pay more at their ends, and an int8 MMA with A
 // in TMEM takes 130 cycles per 16 of K however few its columns are. W of 2048 x
 // 4096, graph replay, us (tensor-core shape -> this one):
-//   int8  1 expert x 1 row 11.5 -> 4.0   8 x 2 19.3 -> 10.9   64 x 2 112 -> 89 (6.0 TB/s)
-//         64 x 4 112 -> 114              8 x 8 19.3 -> 18.5   64 x 8 112 -> 151
-//   bf16  1 expert x 1 row  8.3 -> 4.9   8 x 1 26.3 -> 26.2    8 x 4 27.0 -> 32.8
+//   int8  1 expert x 1 row 11.5 -> 4.0   8 x 2 18.8 -> 10.3   64 x 2 112 -> 88 (6.0 TB/s)
+//         8 x 4 18.7 -> 13.0   64 x 4 112 -> 114   8 x 8 19.3 -> 18.5   64 x 8 112 -> 151
+//   bf16  1 expert x 1 row  7.7 -> 4.3   1 x 4 7.7 -> 5.9   4 x 4 11.6 -> 14.1   8 x 4 27.0 -> 32.8
+// The rule goes by the average, the only thing the host knows. Its price is a crowded expert among empty ones, whose
+// W is read (from L2) once for each eight of its rows: int8 with all rows on one expert
+//         8 x 4 11.4 -> 10.9   64 x 1 11.8 -> 17.8   64 x 2 11.9 -> 34.8   64 x 4 19.5 -> 66.4
+// and with Dirichlet(0.3) shares 8 x 4 18.8 -> 13.7, 64 x 2 59.0 -> 61.4, 64 x 4 66.5 -> 102.
 #include <cuda_bf16.h>
 
 #include <algorithm>
