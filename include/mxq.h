@@ -133,7 +133,8 @@ enum {
     MXQ_OP_GEMM_WGRAD = 6,
     MXQ_OP_SWIGLU_BWD_QUANTIZE = 7,
     MXQ_OP_SCALED_BIAS = 8,
-    MXQ_OP_GEMM_DGRAD_SWIGLU = 9
+    MXQ_OP_GEMM_DGRAD_SWIGLU = 9,
+    MXQ_OP_NORM_RESIDUAL_BWD = 10
 };
 
 /* Library version (major*10000 + minor*100 + patch). */
@@ -400,7 +401,7 @@ MXQ_API int mxq_swiglu_bwd_quantize(const void* dh_bf16, const void* y_bf16, int
  * rows (fprop, dgrad) or the expert (wgrad) that they belong to. Outputs are
  * the same bits from run to run. No workspace.
  *
- * These calls, the int8 calls and dropout may begin while the stream's
+ * These calls, the int8 and fp8 calls, dropout and the norms may begin while the stream's
  * previous kernel ends; they wait for it before they read or write memory. */
 
 /* y[m,:] = x[m,:] . w[e(m)]^T (+ bias[e(m)]); y (M, N) bf16, or fp32 with
@@ -446,6 +447,82 @@ MXQ_API int mxq_int8_gemm_fprop(const void* xq, const float* x_scale, const void
                                 const void* bias_bf16, int64_t M, int64_t N, int64_t K, int E,
                                 const int64_t* d_m_splits, int flags, void* y, int32_t* d_status,
                                 mxq_stream_t stream);
+
+/* ---- Ragged grouped products in fp8 with a scale per block ---------------
+ *
+ * E4M3 codes (bytes) with fp32 scales: one for 128 consecutive values of a
+ * token's row, one for 128 x 128 values of a weight. Scales of rows are
+ * (ceil(width / 128), M), a row's neighbours side by side; those of a weight
+ * (E, ceil(N / 128), ceil(K / 128)). A block at an edge covers what there is.
+ * Scales need no alignment but a float's. Any fp32 scales may be given, also
+ * those of a checkpoint. Grouping as in the bf16 products. */
+
+/* Quantizes the rows of x (M, K), row stride ldx: with a the largest magnitude
+ * of a block, at least 2^-100, scale = a / 448 and q = the E4M3 value nearest to
+ * x * (448 / a), each step one IEEE fp32 rounding, ties to even. A block that
+ * holds an infinity or NaN gets scale NaN and codes 0. K % 16 == 0, K <= 2^20. */
+MXQ_API int mxq_fp8_quantize_rows(const void* x_bf16, int64_t ldx, int64_t M, int64_t K, void* q, float* scale,
+                                  mxq_stream_t stream);
+
+/* The same for a weight (E, N, K) and its 128 x 128 blocks. N % 8 == 0, K % 16
+ * == 0; at most 2^31 - 1 blocks. */
+MXQ_API int mxq_fp8_quantize_weight(const void* w_bf16, int64_t N, int64_t K, int E, void* q, float* scale,
+                                    mxq_stream_t stream);
+
+/* y[m,n] = sum_j x_scale[j,m] w_scale[e,n/128,j] (sum over block j of
+ * xq[m,k] wq[e,n,k]) (+ bias[e,n]); y (M, N) bf16, or fp32 with MXQ_OUT_F32;
+ * bias (E, N) bf16 or NULL. A block's 128 products are summed by the tensor core
+ * (truncating, up to 2^-23 of their magnitudes for every 32), blocks in fp32 by
+ * fused multiply-adds with the product of the two scales rounded to fp32.
+ * K % 16 == 0, N % 8 == 0. */
+MXQ_API int mxq_fp8_gemm_fprop(const void* xq, const float* x_scale, const void* wq, const float* w_scale,
+                               const void* bias_bf16, int64_t M, int64_t N, int64_t K, int E,
+                               const int64_t* d_m_splits, int flags, void* y, int32_t* d_status, mxq_stream_t stream);
+
+/* dx[m,k] = sum_j dy_scale[j,m] w_scale[e,j,k/128] (sum over block j of dyq[m,n]
+ * wq[e,n,k]) from the same codes of w; dx (M, K) bf16, or fp32 with MXQ_OUT_F32.
+ * N % 16 == 0, K % 16 == 0. The gradient of w is mxq_ragged_gemm_wgrad's, on the
+ * bf16 operands: its sum runs over tokens, along which rows' scales differ. */
+MXQ_API int mxq_fp8_gemm_dgrad(const void* dyq, const float* dy_scale, const void* wq, const float* w_scale, int64_t M,
+                               int64_t N, int64_t K, int E, const int64_t* d_m_splits, int flags, void* dx,
+                               int32_t* d_status, mxq_stream_t stream);
+
+/* ---- Norms before and after a block --------------------------------------
+ *
+ *   r' = r + scale * gate[m] * N(x; post_weight),   n = N(r'; pre_weight),
+ *   N(v; w)[m,f] = v[m,f] * w[f] / sqrt(mean over f of v[m,f]^2 + eps)
+ *
+ * x is a block's output, r the residual stream, n the next block's input.
+ * Tensors (M, F) and weights (F) are all bf16, or all fp32 with MXQ_OUT_F32;
+ * gate (M), stats (2, M) and the gradients of the weights and of gate are fp32.
+ * Arithmetic is fp32, each result rounded once; n is made from r' before its
+ * rounding. F % 8 == 0, F <= 16384, M <= 2^28. scale is finite, eps > 0
+ * (MXQ_ERR_VALUE otherwise). An infinity or NaN stays in its row (the weights'
+ * gradients are sums over rows). */
+
+/* NULL for: residual (0), post_weight (x itself instead of its norm), gate (1);
+ * pre_weight and n_out together (no n); res_out (r' is not kept; n_out is then
+ * required); stats (none are kept). stats[0] is 1 / sqrt(mean(x^2) + eps) (1
+ * without post_weight), stats[1] that of r' (1 without pre_weight). res_out may
+ * be residual or x, n_out may be x. */
+MXQ_API int mxq_norm_residual_fwd(const void* x, const void* residual, const void* post_weight, const void* pre_weight,
+                                  const float* gate, int64_t M, int64_t F, double scale, double eps, int flags,
+                                  void* res_out, void* n_out, float* stats, mxq_stream_t stream);
+
+/* The gradients from dres (of r'; NULL: zero) and dn (of n; NULL exactly when
+ * pre_weight is), at least one of them. x, res (the forward call's r'), stats,
+ * the weights, gate and scale are the forward call's; x is read only with
+ * post_weight or gate, res only with pre_weight, stats only with a weight. dx
+ * and dresidual (M, F): NULL where not wanted, at least one of them; dresidual
+ * may be dres. dpost_weight, dpre_weight (F) and dgate (M) exactly where there
+ * is a post_weight, pre_weight, gate; with M == 0 the weights' are zero. ws:
+ * mxq_workspace_bytes(MXQ_OP_NORM_RESIDUAL_BWD, M, 0, F, 0, 0) bytes, needed
+ * with a weight; not shared by calls that may overlap. The same bits from run
+ * to run. */
+MXQ_API int mxq_norm_residual_bwd(const void* dres, const void* dn, const void* x, const void* res, const float* stats,
+                                  const void* post_weight, const void* pre_weight, const float* gate, int64_t M,
+                                  int64_t F, double scale, int flags, void* dx, void* dresidual, float* dpost_weight,
+                                  float* dpre_weight, float* dgate, void* ws, size_t ws_bytes, mxq_stream_t stream);
 
 /* ---- Dropout from a counter ----------------------------------------------
  *

@@ -8,6 +8,10 @@ from . import mxq  # noqa: F401
 from .mxq import (  # noqa: F401
     MXQError,
     dropout,
+    fp8_gemm_dgrad,
+    fp8_gemm_fprop,
+    fp8_quantize_rows,
+    fp8_quantize_weight,
     group_quantize,
     group_quantize_scaled_bias,
     grouped_dbias,
@@ -19,6 +23,8 @@ from .mxq import (  # noqa: F401
     int8_gemm_fprop,
     int8_quantize_rows,
     new_status,
+    norm_residual_bwd,
+    norm_residual_fwd,
     probe_mma_stream,
     ragged_gemm_dgrad,
     ragged_gemm_fprop,

@@ -105,6 +105,8 @@ size_t mxq_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E, int f
             return 2 * (size_t)(M / 128) * (size_t)K * sizeof(float);
         case MXQ_OP_GEMM_DGRAD_SWIGLU:  // dY1 column sums per 32 rows: (M/32, 2K)
             return (size_t)(M / 32) * (size_t)(2 * K) * sizeof(float);
+        case MXQ_OP_NORM_RESIDUAL_BWD:
+            return M >= 0 && K > 0 && K <= mxq::kNormMaxWidth ? mxq::norm_bwd_workspace(M, K) : 0;
         default: return 0;
     }
 }

@@ -135,4 +135,30 @@ cudaError_t run_dbias_finalize(const float* partials, int64_t M, int64_t K, int 
 cudaError_t run_swiglu_fwd(const void* y, int64_t M, int64_t F, void* h, cudaStream_t s);
 cudaError_t run_swiglu_bwd(const void* dh, const void* y, int64_t M, int64_t F, void* dy, cudaStream_t s);
 
+// Norms before and after a block (mxq_norm.cu): r' = r + scale gate N(x; post), n = N(r'; pre), and the gradients.
+// Null: residual (zero), post (no norm of x), pre (no n), gate (1), res, stats (not written); dres (zero), dx, dr.
+constexpr int64_t kNormMaxWidth = 16384;
+struct NormFwd {
+    const void *x, *residual, *post, *pre;
+    const float* gate;
+    int64_t M, F;
+    float scale, eps;
+    int f32;
+    void *res, *n;
+    float* stats;  // (2, M)
+};
+struct NormBwd {
+    const void *dres, *dn, *x, *res, *post, *pre;
+    const float *gate, *stats;
+    int64_t M, F;
+    float scale;
+    int f32;
+    void *dx, *dr;
+    float *dpost, *dpre, *dgate;
+    float* partials;  // workspace of norm_bwd_workspace(M, F) bytes
+};
+size_t norm_bwd_workspace(int64_t M, int64_t F);
+cudaError_t run_norm_fwd(const NormFwd& c, cudaStream_t s);
+cudaError_t run_norm_bwd(const NormBwd& c, cudaStream_t s);
+
 }  // namespace mxq

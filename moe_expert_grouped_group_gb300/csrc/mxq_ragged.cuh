@@ -745,13 +745,13 @@ static cudaError_t launch_persistent(int threads, int smem_max, int smem, int64_
 
 // Launches a kernel that begins with wait_for_stream().
 template <class... Params, class... Args>
-static cudaError_t launch(void (*kernel)(Params...), unsigned grid, unsigned threads, cudaStream_t s, int smem,
+static cudaError_t launch(void (*kernel)(Params...), dim3 grid, unsigned threads, cudaStream_t s, int smem,
                           Args... args) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;

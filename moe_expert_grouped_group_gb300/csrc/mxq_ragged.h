@@ -56,6 +56,26 @@ cudaError_t run_fprop_vec(const GemmCall& c, cudaStream_t s);
 cudaError_t run_int8_vec(const Int8Call& c, cudaStream_t s);
 cudaError_t run_int8_quantize(const void* x, int64_t M, int64_t K, int64_t ld, void* q, float* scale, cudaStream_t s);
 
+// fp8 products with a scale for each block of kFp8Block values of a row and kFp8Block x kFp8Block of a weight.
+constexpr int kFp8Block = 128;
+struct Fp8Call {
+    int mode;            // kFprop or kDgrad
+    const void* tq;      // fprop: codes of X (M, K); dgrad: of dY (M, N)
+    const float* ts;     // their scales (blocks of the sum, M)
+    const void* wq;      // (E, N, K) codes
+    const float* ws;     // (E, blocks of N, blocks of K)
+    const void* bias;    // fprop: (E, N) bf16 or null
+    int64_t M, N, K;
+    int E;
+    const int64_t* m_splits;
+    void* out;           // fprop (M, N), dgrad (M, K)
+    int out_f32;
+    int32_t* status;
+};
+cudaError_t run_fp8(const Fp8Call& c, cudaStream_t s);
+cudaError_t run_fp8_quantize_rows(const void* x, int64_t M, int64_t K, int64_t ld, void* q, float* scale, cudaStream_t s);
+cudaError_t run_fp8_quantize_weight(const void* w, int64_t N, int64_t K, int E, void* q, float* scale, cudaStream_t s);
+
 // Encodes a tensor map of int8, bf16 or fp32 elements (by their bytes) in up
 // to three dimensions: dims and box innermost first, strides in bytes of
 // dimensions 1 and 2, the swizzle of 128, 64 or 0 (none) bytes. False on failure.

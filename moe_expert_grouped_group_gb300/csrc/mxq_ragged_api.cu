@@ -1,6 +1,6 @@
 // mxq_ragged_api.cu -- extern "C" entry points of the ragged grouped products
-// (bf16, int8) and of dropout declared in include/mxq.h: host-side checks, then
-// one launch on the caller's stream. Nothing here synchronizes or allocates.
+// (bf16, int8, fp8), of dropout and of a block's norms declared in
+// include/mxq.h: host-side checks, then one or two launches on the caller's stream. Nothing here synchronizes or allocates.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -37,6 +37,11 @@ int run(const mxq::ragged::GemmCall& c, mxq_stream_t stream) {
     return e == cudaSuccess ? MXQ_OK : fail_cuda(e);
 }
 
+int run_fp8(const mxq::ragged::Fp8Call& c, mxq_stream_t stream) {
+    const cudaError_t e = mxq::ragged::run_fp8(c, (cudaStream_t)stream);
+    return e == cudaSuccess ? MXQ_OK : fail_cuda(e);
+}
+
 // p -> elements dropped of 65536, or -1 if p is outside [0, 1]
 int64_t dropped(double p) { return p >= 0.0 && p <= 1.0 ? (int64_t)std::nearbyint(p * 65536.0) : -1; }
 
@@ -46,6 +51,12 @@ int check_dropout(int64_t M, int64_t F, const int64_t* d_rng, double p) {
     if (!d_rng) return MXQ_ERR_NULL;
     if (!device_pointer(d_rng)) return MXQ_ERR_HOST_POINTER;
     return dropped(p) < 0 ? MXQ_ERR_VALUE : MXQ_OK;
+}
+
+int check_norm(int64_t M, int64_t F, double scale) {
+    if (!arch_ok()) return MXQ_ERR_ARCH;
+    if (M < 0 || M > kMaxRows || F <= 0 || F % 8 || F > mxq::kNormMaxWidth) return MXQ_ERR_SHAPE;
+    return std::isfinite((float)scale) ? MXQ_OK : MXQ_ERR_VALUE;
 }
 
 }  // namespace
@@ -119,6 +130,57 @@ int mxq_int8_gemm_fprop(const void* xq, const float* x_scale, const void* wq, co
     return e == cudaSuccess ? MXQ_OK : fail_cuda(e);
 }
 
+int mxq_fp8_quantize_rows(const void* x_bf16, int64_t ldx, int64_t M, int64_t K, void* q, float* scale,
+                          mxq_stream_t stream) {
+    if (M != 0 && (!x_bf16 || !q || !scale)) return MXQ_ERR_NULL;
+    if (!arch_ok()) return MXQ_ERR_ARCH;
+    if (M < 0 || M > kMaxRows || K <= 0 || K > kMaxWidth || K % 16 || bad_stride(ldx, K)) return MXQ_ERR_SHAPE;
+    if (!aligned16(x_bf16) || !aligned16(q) || !aligned4(scale)) return MXQ_ERR_ALIGN;
+    const cudaError_t e = mxq::ragged::run_fp8_quantize_rows(x_bf16, M, K, ldx, q, scale, (cudaStream_t)stream);
+    return e == cudaSuccess ? MXQ_OK : fail_cuda(e);
+}
+
+int mxq_fp8_quantize_weight(const void* w_bf16, int64_t N, int64_t K, int E, void* q, float* scale,
+                            mxq_stream_t stream) {
+    if (!w_bf16 || !q || !scale) return MXQ_ERR_NULL;
+    if (!arch_ok()) return MXQ_ERR_ARCH;
+    if (N <= 0 || K <= 0 || N > kMaxWidth || K > kMaxWidth || N % 8 || K % 16 || E < 1 || E > MXQ_MAX_EXPERTS)
+        return MXQ_ERR_SHAPE;
+    if (((N + 127) / 128) * ((K + 127) / 128) * E > 0x7FFFFFFF) return MXQ_ERR_SHAPE;
+    if (!aligned16(w_bf16) || !aligned16(q) || !aligned4(scale)) return MXQ_ERR_ALIGN;
+    const cudaError_t e = mxq::ragged::run_fp8_quantize_weight(w_bf16, N, K, E, q, scale, (cudaStream_t)stream);
+    return e == cudaSuccess ? MXQ_OK : fail_cuda(e);
+}
+
+int mxq_fp8_gemm_fprop(const void* xq, const float* x_scale, const void* wq, const float* w_scale,
+                       const void* bias_bf16, int64_t M, int64_t N, int64_t K, int E, const int64_t* d_m_splits,
+                       int flags, void* y, int32_t* d_status, mxq_stream_t stream) {
+    if (flags & ~MXQ_OUT_F32) return MXQ_ERR_FLAGS;
+    if (!wq || !w_scale || (M != 0 && (!xq || !x_scale || !y))) return MXQ_ERR_NULL;
+    if (int r = check_ragged(M, N, K, 8, 16, E, d_m_splits)) return r;
+    if (!aligned16(xq) || !aligned4(x_scale) || !aligned16(wq) || !aligned4(w_scale) || !aligned16(bias_bf16) ||
+        !aligned16(y))
+        return MXQ_ERR_ALIGN;
+    if (M == 0) return MXQ_OK;
+    return run_fp8({mxq::ragged::kFprop, xq, x_scale, wq, w_scale, bias_bf16, M, N, K, E, d_m_splits, y,
+                    (flags & MXQ_OUT_F32) != 0, d_status},
+                   stream);
+}
+
+int mxq_fp8_gemm_dgrad(const void* dyq, const float* dy_scale, const void* wq, const float* w_scale, int64_t M,
+                       int64_t N, int64_t K, int E, const int64_t* d_m_splits, int flags, void* dx, int32_t* d_status,
+                       mxq_stream_t stream) {
+    if (flags & ~MXQ_OUT_F32) return MXQ_ERR_FLAGS;
+    if (!wq || !w_scale || (M != 0 && (!dyq || !dy_scale || !dx))) return MXQ_ERR_NULL;
+    if (int r = check_ragged(M, N, K, 16, 16, E, d_m_splits)) return r;
+    if (!aligned16(dyq) || !aligned4(dy_scale) || !aligned16(wq) || !aligned4(w_scale) || !aligned16(dx))
+        return MXQ_ERR_ALIGN;
+    if (M == 0) return MXQ_OK;
+    return run_fp8({mxq::ragged::kDgrad, dyq, dy_scale, wq, w_scale, nullptr, M, N, K, E, d_m_splits, dx,
+                    (flags & MXQ_OUT_F32) != 0, d_status},
+                   stream);
+}
+
 int mxq_swiglu_dropout_fwd(const void* y_bf16, int64_t M, int64_t F, const int64_t* d_rng, double p, void* h_bf16,
                            mxq_stream_t stream) {
     if (M != 0 && (!y_bf16 || !h_bf16)) return MXQ_ERR_NULL;
@@ -149,6 +211,47 @@ int mxq_dropout(const void* x, const void* residual, int64_t n, const int64_t* d
     if (!aligned16(x) || !aligned16(residual) || !aligned16(out)) return MXQ_ERR_ALIGN;
     const cudaError_t e = mxq::ragged::run_dropout(x, residual, n, (flags & MXQ_OUT_F32) != 0, d_rng,
                                                    (uint32_t)dropped(p), out, (cudaStream_t)stream);
+    return e == cudaSuccess ? MXQ_OK : fail_cuda(e);
+}
+
+int mxq_norm_residual_fwd(const void* x, const void* residual, const void* post_weight, const void* pre_weight,
+                          const float* gate, int64_t M, int64_t F, double scale, double eps, int flags, void* res_out,
+                          void* n_out, float* stats, mxq_stream_t stream) {
+    if (flags & ~MXQ_OUT_F32) return MXQ_ERR_FLAGS;
+    if (M != 0 && (!x || (!res_out && !n_out) || !n_out != !pre_weight)) return MXQ_ERR_NULL;
+    if (int r = check_norm(M, F, scale)) return r;
+    if (!(eps > 0.0 && std::isfinite((float)eps) && (float)eps > 0.0f)) return MXQ_ERR_VALUE;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(post_weight) || !aligned16(pre_weight) || !aligned4(gate) ||
+        !aligned16(res_out) || !aligned16(n_out) || !aligned4(stats))
+        return MXQ_ERR_ALIGN;
+    const cudaError_t e = mxq::run_norm_fwd({x, residual, post_weight, pre_weight, gate, M, F, (float)scale, (float)eps,
+                                             (flags & MXQ_OUT_F32) != 0, res_out, n_out, stats},
+                                            (cudaStream_t)stream);
+    return e == cudaSuccess ? MXQ_OK : fail_cuda(e);
+}
+
+int mxq_norm_residual_bwd(const void* dres, const void* dn, const void* x, const void* res, const float* stats,
+                          const void* post_weight, const void* pre_weight, const float* gate, int64_t M, int64_t F,
+                          double scale, int flags, void* dx, void* dresidual, float* dpost_weight, float* dpre_weight,
+                          float* dgate, void* ws, size_t ws_bytes, mxq_stream_t stream) {
+    if (flags & ~MXQ_OUT_F32) return MXQ_ERR_FLAGS;
+    if (!post_weight != !dpost_weight || !pre_weight != !dpre_weight) return MXQ_ERR_NULL;
+    if (M != 0) {
+        if (!dx && !dresidual) return MXQ_ERR_NULL;
+        if ((!dres && !dn) || !dn != !pre_weight || !gate != !dgate) return MXQ_ERR_NULL;
+        if ((pre_weight && !res) || ((post_weight || gate) && !x) || ((post_weight || pre_weight) && !stats))
+            return MXQ_ERR_NULL;
+    }
+    if (int r = check_norm(M, F, scale)) return r;
+    if (!aligned16(dres) || !aligned16(dn) || !aligned16(x) || !aligned16(res) || !aligned4(stats) ||
+        !aligned16(post_weight) || !aligned16(pre_weight) || !aligned4(gate) || !aligned16(dx) || !aligned16(dresidual) ||
+        !aligned16(dpost_weight) || !aligned16(dpre_weight) || !aligned4(dgate) || !aligned16(ws))
+        return MXQ_ERR_ALIGN;
+    if ((post_weight || pre_weight) && (!ws || ws_bytes < mxq::norm_bwd_workspace(M, F))) return MXQ_ERR_WORKSPACE;
+    const cudaError_t e = mxq::run_norm_bwd({dres, dn, x, res, post_weight, pre_weight, gate, stats, M, F, (float)scale,
+                                             (flags & MXQ_OUT_F32) != 0, dx, dresidual, dpost_weight, dpre_weight, dgate,
+                                             static_cast<float*>(ws)},
+                                            (cudaStream_t)stream);
     return e == cudaSuccess ? MXQ_OK : fail_cuda(e);
 }
 

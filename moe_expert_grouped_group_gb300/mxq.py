@@ -22,7 +22,7 @@ from .build import LIB
 ROWWISE, COLWISE, SWIZZLE, DEQUANT_OUT, ACCUMULATE, OUT_BF16, PAD_EXPERTS, OUT_F32 = 1, 2, 4, 8, 16, 32, 64, 128
 OP_GROUP_QUANTIZE, OP_REQUANT_COLWISE, OP_GROUPED_DBIAS = 1, 2, 3
 OP_GEMM_FPROP, OP_GEMM_DGRAD, OP_GEMM_WGRAD, OP_SWIGLU_BWD_QUANTIZE, OP_SCALED_BIAS = 4, 5, 6, 7, 8
-OP_GEMM_DGRAD_SWIGLU = 9
+OP_GEMM_DGRAD_SWIGLU, OP_NORM_RESIDUAL_BWD = 9, 10
 PROBE_ZEROS, PROBE_RANDOM = 0, 1
 STATUS_SPLIT_UNALIGNED, STATUS_SPLIT_NEGATIVE, STATUS_SPLIT_SUM, STATUS_WAIT_TIMEOUT = 1, 2, 4, 8
 
@@ -35,7 +35,8 @@ SYMBOLS = [
     "mxq_scale_bytes_grouped", "mxq_grouped_gemm_fprop_ex", "mxq_grouped_gemm_dgrad_ex", "mxq_probe_mma_stream",
     "mxq_probe_mma_stream_ex", "mxq_selftest_wait_timeout", "mxq_ragged_gemm_fprop", "mxq_ragged_gemm_dgrad",
     "mxq_ragged_gemm_wgrad", "mxq_int8_quantize_rows", "mxq_int8_gemm_fprop", "mxq_swiglu_dropout_fwd",
-    "mxq_swiglu_dropout_bwd", "mxq_dropout",
+    "mxq_swiglu_dropout_bwd", "mxq_dropout", "mxq_fp8_quantize_rows", "mxq_fp8_quantize_weight", "mxq_fp8_gemm_fprop",
+    "mxq_fp8_gemm_dgrad", "mxq_norm_residual_fwd", "mxq_norm_residual_bwd",
 ]
 
 
@@ -91,6 +92,13 @@ def load(path: str = LIB) -> ctypes.CDLL:
     L.mxq_swiglu_dropout_fwd.argtypes = [_P, _I64, _I64, _P, _F64, _P, _P]
     L.mxq_swiglu_dropout_bwd.argtypes = [_P, _P, _I64, _I64, _P, _F64, _P, _P]
     L.mxq_dropout.argtypes = [_P, _P, _I64, _P, _F64, _INT, _P, _P]
+    L.mxq_fp8_quantize_rows.argtypes = [_P, _I64, _I64, _I64, _P, _P, _P]
+    L.mxq_fp8_quantize_weight.argtypes = [_P, _I64, _I64, _INT, _P, _P, _P]
+    L.mxq_fp8_gemm_fprop.argtypes = [_P, _P, _P, _P, _P, _I64, _I64, _I64, _INT, _P, _INT, _P, _P, _P]
+    L.mxq_fp8_gemm_dgrad.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _INT, _P, _INT, _P, _P, _P]
+    L.mxq_norm_residual_fwd.argtypes = [_P, _P, _P, _P, _P, _I64, _I64, _F64, _F64, _INT, _P, _P, _P, _P]
+    L.mxq_norm_residual_bwd.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _F64, _INT, _P, _P, _P, _P, _P, _P,
+                                        _SZ, _P]
     L.mxq_status_read.argtypes = [_P, _P, _P]
     L.mxq_probe_mma_stream.argtypes = [_I64, _P, _P]
     L.mxq_probe_mma_stream.restype = _INT
@@ -105,7 +113,8 @@ def load(path: str = LIB) -> ctypes.CDLL:
               "mxq_grouped_gemm_dgrad", "mxq_grouped_gemm_wgrad", "mxq_swiglu_fwd", "mxq_swiglu_bwd",
               "mxq_status_read", "mxq_ragged_gemm_fprop", "mxq_ragged_gemm_dgrad", "mxq_ragged_gemm_wgrad",
               "mxq_int8_quantize_rows", "mxq_int8_gemm_fprop", "mxq_swiglu_dropout_fwd", "mxq_swiglu_dropout_bwd",
-              "mxq_dropout"):
+              "mxq_dropout", "mxq_fp8_quantize_rows", "mxq_fp8_quantize_weight", "mxq_fp8_gemm_fprop",
+              "mxq_fp8_gemm_dgrad", "mxq_norm_residual_fwd", "mxq_norm_residual_bwd"):
         getattr(L, a).restype = _INT
     return L
 
@@ -909,3 +918,157 @@ def dropout(x, rng, p, residual=None, out=None):
     if rc:
         _check(rc, "mxq_dropout")
     return out
+
+
+# ------------------------------------------------ fp8 products with a scale per block, norms of a block
+_E4M3 = tuple(d for d in (torch.uint8, getattr(torch, "float8_e4m3fn", None)) if d is not None)
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def fp8_quantize_rows(x, out=None):
+    """bf16 rows (M, K) -> (E4M3 codes (M, K) uint8, fp32 scales (ceil(K/128), M)): one scale for 128
+    values of a row, x ~ q * scale."""
+    xp, M, K, ldx = _rows(x, "x", _BF16)
+    if out is None:
+        q, scale = _new((M, K), torch.uint8, x), _new((_blocks(K), M), torch.float32, x)
+        qp, sp = q.data_ptr(), scale.data_ptr()
+    else:
+        q, scale = out
+        qp, sp = _packed(q, "q", (M, K), _E4M3), _packed(scale, "scale", (_blocks(K), M), _F32)
+    rc = lib().mxq_fp8_quantize_rows(xp, ldx, M, K, qp, sp, _stream())
+    if rc:
+        _check(rc, "mxq_fp8_quantize_rows")
+    return q, scale
+
+
+def fp8_quantize_weight(w, out=None):
+    """bf16 weight (E, N, K) -> (E4M3 codes (E, N, K) uint8, fp32 scales (E, ceil(N/128), ceil(K/128)))."""
+    wp = _dev(w, "w", 0, _BF16)
+    if w is None or w.dim() != 3:
+        raise MXQError("w: expected a 3-D tensor (E, N, K)")
+    E, N, K = w.shape
+    want = (E, _blocks(N), _blocks(K))
+    if out is None:
+        q, scale = _new((E, N, K), torch.uint8, w), _new(want, torch.float32, w)
+        qp, sp = q.data_ptr(), scale.data_ptr()
+    else:
+        q, scale = out
+        qp, sp = _packed(q, "q", (E, N, K), _E4M3), _packed(scale, "scale", want, _F32)
+    rc = lib().mxq_fp8_quantize_weight(wp, N, K, E, qp, sp, _stream())
+    if rc:
+        _check(rc, "mxq_fp8_quantize_weight")
+    return q, scale
+
+
+def fp8_gemm_fprop(xq, x_scale, wq, w_scale, m_splits, bias=None, out_dtype=None, status=None, out=None):
+    """Y = X W_e^T (+ b_e) on E4M3 codes with a scale per block. xq (M, K), x_scale (ceil(K/128), M),
+    wq (E, N, K), w_scale (E, ceil(N/128), ceil(K/128)), bias (E, N); Y (M, N) in bf16 (default) or fp32."""
+    M, K = xq.shape
+    E, N, Kw = wq.shape
+    _shape(wq, "wq", (E, N, K))
+    out, op, flag = _out(out, out_dtype, (M, N), xq, torch.bfloat16, torch.float32, OUT_F32)
+    rc = lib().mxq_fp8_gemm_fprop(_dev(xq, "xq", 0, _E4M3), _packed(x_scale, "x_scale", (_blocks(K), M), _F32),
+                                  _dev(wq, "wq", 0, _E4M3),
+                                  _packed(w_scale, "w_scale", (E, _blocks(N), _blocks(K)), _F32),
+                                  _packed(bias, "bias", (E, N), _BF16), M, N, K, E, _grouping(m_splits, E), flag, op,
+                                  _dev(status, "status", 4, _I32), _stream())
+    if rc:
+        _check(rc, "mxq_fp8_gemm_fprop")
+    return out
+
+
+def fp8_gemm_dgrad(dyq, dy_scale, wq, w_scale, m_splits, out_dtype=None, status=None, out=None):
+    """dX = dY W_e on E4M3 codes with a scale per block. dyq (M, N), dy_scale (ceil(N/128), M), wq and
+    w_scale those of fp8_gemm_fprop; dX (M, K) in bf16 (default) or fp32."""
+    M, N = dyq.shape
+    E, Nw, K = wq.shape
+    _shape(wq, "wq", (E, N, K))
+    out, op, flag = _out(out, out_dtype, (M, K), dyq, torch.bfloat16, torch.float32, OUT_F32)
+    rc = lib().mxq_fp8_gemm_dgrad(_dev(dyq, "dyq", 0, _E4M3), _packed(dy_scale, "dy_scale", (_blocks(N), M), _F32),
+                                  _dev(wq, "wq", 0, _E4M3),
+                                  _packed(w_scale, "w_scale", (E, _blocks(N), _blocks(K)), _F32), M, N, K, E,
+                                  _grouping(m_splits, E), flag, op, _dev(status, "status", 4, _I32), _stream())
+    if rc:
+        _check(rc, "mxq_fp8_gemm_dgrad")
+    return out
+
+
+def _norm_row(t, name):
+    p = _dev(t, name, 0, _BF16_F32)
+    if p is None or t.dim() != 2:
+        raise MXQError(f"{name}: expected a 2-D tensor (M, F)")
+    return p
+
+
+def norm_residual_fwd(x, residual=None, post_weight=None, pre_weight=None, gate=None, scale=1.0, eps=1e-6,
+                      res_out=True, stats_out=True, out=None):
+    """r' = residual + scale * gate[m] * N(x; post_weight) and n = N(r'; pre_weight), RMS norms N.
+
+    x, residual (M, F) and weights (F,) all bf16 or all fp32, gate (M,) fp32. Returns (r', n, stats): n is
+    None without pre_weight, r' with res_out=False, stats (2, M) fp32 (what the backward call needs) with
+    stats_out=False. out: a (r', n, stats) to write to, None where it is to be made; r' may be residual or
+    x, n may be x."""
+    xp, (M, F), same = _norm_row(x, "x"), x.shape, (x.dtype,)
+    r, n, stats = out if out is not None else (None, None, None)
+    if not res_out:
+        r = None
+    elif r is None:
+        r = _new((M, F), x.dtype, x)
+    if pre_weight is None:
+        n = None
+    elif n is None:
+        n = _new((M, F), x.dtype, x)
+    if not stats_out:
+        stats = None
+    elif stats is None:
+        stats = _new((2, M), torch.float32, x)
+    rc = lib().mxq_norm_residual_fwd(
+        xp, _packed(residual, "residual", (M, F), same), _packed(post_weight, "post_weight", (F,), same),
+        _packed(pre_weight, "pre_weight", (F,), same), _packed(gate, "gate", (M,), _F32), M, F, scale, eps,
+        OUT_F32 if x.dtype is torch.float32 else 0, _packed(r, "r'", (M, F), same), _packed(n, "n", (M, F), same),
+        _packed(stats, "stats", (2, M), _F32), _stream())
+    if rc:
+        _check(rc, "mxq_norm_residual_fwd")
+    return r, n, stats
+
+
+def norm_residual_bwd(dres, dn, x, res, stats, post_weight=None, pre_weight=None, gate=None, scale=1.0, out=None,
+                      workspace=None):
+    """The gradients of norm_residual_fwd from dres (of r', may be None) and dn (of n, None exactly without
+    pre_weight). x, weights, gate and scale are the forward call's, res its r' and stats its statistics; x
+    may be None without post_weight and gate, res without pre_weight. Returns a dict: dx, dresidual (M, F),
+    dpost_weight, dpre_weight (F,) fp32, dgate (M,) fp32, those of arguments that were given. out: tensors
+    to write to, by the same names; dresidual may be dres."""
+    like = dn if dn is not None else dres
+    if like is None:
+        raise MXQError("dres or dn is required")
+    _norm_row(like, "dn" if dn is not None else "dres")
+    (M, F), same = like.shape, (like.dtype,)
+    o = dict(out or {})
+    _fill(o, "dx", lambda: _new((M, F), like.dtype, like))
+    _fill(o, "dresidual", lambda: _new((M, F), like.dtype, like))
+    ws = None
+    if post_weight is not None:
+        _fill(o, "dpost_weight", lambda: _new((F,), torch.float32, like))
+    if pre_weight is not None:
+        _fill(o, "dpre_weight", lambda: _new((F,), torch.float32, like))
+    if gate is not None:
+        _fill(o, "dgate", lambda: _new((M,), torch.float32, like))
+    if post_weight is not None or pre_weight is not None:
+        ws = workspace if workspace is not None else _new((max(16, workspace_bytes(OP_NORM_RESIDUAL_BWD, M, 0, F, 0)),),
+                                                          torch.uint8, like)
+    rc = lib().mxq_norm_residual_bwd(
+        _packed(dres, "dres", (M, F), same), _packed(dn, "dn", (M, F), same), _packed(x, "x", (M, F), same),
+        _packed(res, "res", (M, F), same), _packed(stats, "stats", (2, M), _F32),
+        _packed(post_weight, "post_weight", (F,), same), _packed(pre_weight, "pre_weight", (F,), same),
+        _packed(gate, "gate", (M,), _F32), M, F, scale, OUT_F32 if like.dtype is torch.float32 else 0,
+        _packed(o["dx"], "dx", (M, F), same), _packed(o["dresidual"], "dresidual", (M, F), same),
+        _packed(o.get("dpost_weight"), "dpost_weight", (F,), _F32), _packed(o.get("dpre_weight"), "dpre_weight", (F,), _F32),
+        _packed(o.get("dgate"), "dgate", (M,), _F32), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+        _stream())
+    if rc:
+        _check(rc, "mxq_norm_residual_bwd")
+    return o
