@@ -421,6 +421,25 @@ MXQ_API int mxq_ragged_gemm_wgrad(const void* dy_bf16, int64_t lddy, const void*
                                   int64_t N, int64_t K, int E, const int64_t* d_m_splits, int flags, void* dw,
                                   int32_t* d_status, mxq_stream_t stream);
 
+/* FC1 of a gated MLP with its activation: [g | u] = x[m,:] . w[e(m)]^T (+
+ * bias[e(m)]) for w (E, 2F, K), gate first, bias (E, 2F) bf16 or NULL, and
+ * h[m,:] = silu(g) * u, h (M, F) bf16, made from the fp32 sums in the steps of
+ * mxq_swiglu_fwd and rounded once (so not the bits of mxq_swiglu_fwd on the
+ * rounded [g | u]). y_out (M, 2F) bf16 gets [g | u], what the backward pass
+ * needs; NULL: it is not written. F % 8 == 0, 2F <= 2^20. */
+MXQ_API int mxq_ragged_gemm_fprop_swiglu(const void* x_bf16, int64_t ldx, const void* w_bf16, const void* bias_bf16,
+                                         int64_t M, int64_t F, int64_t K, int E, const int64_t* d_m_splits, void* h,
+                                         void* y_out, int32_t* d_status, mxq_stream_t stream);
+
+/* FC2's dgrad through the activation: dh[m,:] = dy[m,:] . w[e(m)] for FC2's
+ * weight w (E, N, F), and the gradient dy1 (M, 2F) = [dg | du] of the saved
+ * y1 = [g | u] (M, 2F) in the steps of mxq_swiglu_bwd; dh is neither rounded nor
+ * written. h_out (M, F) gets silu(g) * u again, for FC2's wgrad, so that h need
+ * not be kept; NULL: it is not written. F % 8 == 0, 2F <= 2^20. */
+MXQ_API int mxq_ragged_gemm_dgrad_swiglu(const void* dy_bf16, int64_t lddy, const void* w_bf16, const void* y1_bf16,
+                                         int64_t M, int64_t N, int64_t F, int E, const int64_t* d_m_splits, void* dy1,
+                                         void* h_out, int32_t* d_status, mxq_stream_t stream);
+
 /* ---- Ragged grouped products in int8 -------------------------------------
  *
  * Symmetric int8 with one fp32 scale per token and per output channel, for

@@ -27,7 +27,9 @@ from .mxq import (  # noqa: F401
     norm_residual_fwd,
     probe_mma_stream,
     ragged_gemm_dgrad,
+    ragged_gemm_dgrad_swiglu,
     ragged_gemm_fprop,
+    ragged_gemm_fprop_swiglu,
     ragged_gemm_wgrad,
     requant_colwise,
     requant_colwise_scaled_bias,

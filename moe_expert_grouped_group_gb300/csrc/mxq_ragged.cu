@@ -75,6 +75,7 @@
 #include "mxq_internal.h"
 #include "mxq_ragged.cuh"
 #include "mxq_ragged.h"
+#include "mxq_ragged_swiglu.cuh"
 
 namespace mxq {
 namespace ragged {
@@ -107,6 +108,8 @@ struct Params {
     void* out;
     int out_f32, accumulate;
     int32_t* status;
+    const __nv_bfloat16* y;  // the SwiGLU modes
+    __nv_bfloat16* side;
 };
 
 template <int kMode, bool kRegs>
@@ -170,10 +173,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     cluster_sync();  // both CTAs' barriers exist before any load completes on rank 0's
     fence_after();
     const uint32_t tmem = s_tmem;
-    const Walk<kMode, FEAT, WIDE, STEP> W(p.N, p.K, p.E, s_off, s_slices, s_order);
+    constexpr Mode kProduct = product_of(kMode);
+    constexpr int kFeatures = kMode == kFpropSwiglu ? kFM / 2 : kFM;  // of a CTA's lanes
+    const Walk<kProduct, CG * kFeatures, WIDE, STEP> W(p.N, p.K, p.E, s_off, s_slices, s_order);
     TileQueue queue(answer, ready, mapa(taken, 0));
     int64_t t = blockIdx.x / CG;
-    constexpr bool a_mn = kMode != kFprop, b_mn = kMode == kWgrad;
+    constexpr bool a_mn = kProduct != kFprop, b_mn = kMode == kWgrad;
     // An expert's last block of rows in wgrad, when it ends inside a step of 16: its loads complete on each
     // CTA's own tail[st], warp 10 of both CTAs zeroes the rows up to the next multiple of 16 and arrives on
     // rank 0's fix[st], and the MMAs wait for that instead of full[st]. The parities of full, tail and fix
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // rows of the other operand: whole boxes, and half a box at the end where that is enough
             const bool half_box = kMode != kWgrad && (half - 1) % BOX < BOX / 2;
             const int boxes = half_box ? half / BOX : (half + BOX - 1) / BOX;
-            const int f = T.f0 + rank * kFM, c = T.c0 + rank * half;
+            const int f = T.f0 + rank * kFeatures, c = T.c0 + rank * half;
             const uint32_t bytes = A_BYTES + (2 * boxes + half_box) * (BOX * BK);
             for (int r = 0; r < T.red; r += BK) {
                 if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag)) {
@@ -226,9 +231,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (elect_one()) {
                     if (tail) mbar_expect_tx(own, bytes);
                     else if (rank == 0) mbar_expect_tx(own, CG * bytes);
-                    if (kMode == kFprop) {
+                    if (kMode == kFpropSwiglu) {
+                        load_5d_pair(a, &tmA, fb, r, f / kGateRows, T.e);
+                    } else if (kMode == kFprop) {
                         load_3d<CG>(a, &tmA, fb, r, f, T.e);
-                    } else if (kMode == kDgrad) {
+                    } else if (kProduct == kDgrad) {
                         load_3d<CG>(a, &tmA, fb, f, r, T.e);
                         load_3d<CG>(a + 8192, &tmA, fb, f + 64, r, T.e);
                     } else {
@@ -345,7 +352,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------ epilogue
         const int q = warp & 3, group = (warp - 2) >> 2;  // two groups of four warps share the columns
         uint8_t* stage = smem + EPI_REGION + (warp - 2) * (kMode == kWgrad ? kBoxBytes : kEpiBytes);
-        const int64_t ld = kMode == kFprop ? p.N : p.K;  // features
+        const int64_t ld = kProduct == kFprop ? p.N : p.K;  // features
         int buf = 0;
         uint32_t acc_uses = 0;  // bits of accumulators: parities
         auto filled = [&] {
@@ -364,8 +371,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         do {
             if (t >= W.total) continue;
             const Tile T = W.get(t);
-            const int f0 = T.f0 + rank * kFM;
-            const int live = (int)min((int64_t)kFM, ld - f0);  // may be negative: nothing to store
+            const int f0 = T.f0 + rank * kFeatures;
+            const int live = (int)min((int64_t)kFeatures, ld - f0);  // may be negative: nothing to store
             if (kMode == kWgrad && T.red == 0) {
                 // an empty expert: 16-byte stores of zero, a row piece of 128 features at a time
                 if (!p.accumulate) {
@@ -451,6 +458,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                                        live - 32 * q, T.cols - c, lane, old[i]);
                     }
                 }
+                // the first columns' [g | u] likewise
+                uint4 gate[4], up[4];
+                const auto load_gate_up = [&](int c) {
+                    const __nv_bfloat16* y = p.y + (T.row0 + c) * 2 * ld + f0 + 32 * q;
+                    load_rows_bf16(y, 2 * ld, live - 32 * q, T.cols - c, lane, gate);
+                    load_rows_bf16(y + ld, 2 * ld, live - 32 * q, T.cols - c, lane, up);
+                };
+                if constexpr (kMode == kDgradSwiglu) load_gate_up(32 * group);
                 const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
                 int from = buf;  // the accumulator that holds the sums
                 bool ok = true;
@@ -482,6 +497,40 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (!ok) break;
                 fence_after();
+                if constexpr (kMode == kFpropSwiglu) {
+                    const int f = f0 + 16 * q, mine = live - 16 * q;
+                    float bg[2] = {0.0f, 0.0f}, bu[2] = {0.0f, 0.0f};
+                    if (p.bias) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int l = (lane >> 2) + 8 * k;
+                            if (l < mine) {
+                                bg[k] = __bfloat162float(p.bias[(int64_t)T.e * 2 * ld + f + l]);
+                                bu[k] = __bfloat162float(p.bias[(int64_t)T.e * 2 * ld + ld + f + l]);
+                            }
+                        }
+                    }
+                    for (int c = 32 * group; c < T.cols; c += 64) {
+                        const int64_t row = T.row0 + c;
+                        store_swiglu(lanes + from * WIDE + c, lane, smem_u32(stage),
+                                     static_cast<__nv_bfloat16*>(p.out) + row * ld + f,
+                                     p.side ? p.side + row * 2 * ld + f : nullptr, ld, mine, T.cols - c, bg, bu);
+                    }
+                    drained(from);
+                    continue;
+                }
+                if constexpr (kMode == kDgradSwiglu) {
+                    for (int c = 32 * group; c < T.cols; c += 64) {
+                        const int64_t row = T.row0 + c;
+                        const int f = f0 + 32 * q;
+                        store_swiglu_grads(lanes + from * WIDE + c, lane, smem_u32(stage), gate, up,
+                                           static_cast<__nv_bfloat16*>(p.out) + row * 2 * ld + f,
+                                           p.side ? p.side + row * ld + f : nullptr, ld, live - 32 * q, T.cols - c,
+                                           [&] { load_gate_up(c + 64); });
+                    }
+                    drained(from);
+                    continue;
+                }
                 float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 if (kMode == kFprop && p.bias) {
 #pragma unroll
@@ -540,9 +589,9 @@ bool encode_tmap(CUtensorMap* m, const void* base, int elem_bytes, int rank, con
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<EncodeTiledFn>(f);
     });
-    if (!fn || !base || rank < 1 || rank > 3) return false;
-    cuuint64_t d[3], s[2];
-    cuuint32_t b[3], es[3] = {1, 1, 1};
+    if (!fn || !base || rank < 1 || rank > 5) return false;
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5], es[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < rank; ++i) {
         d[i] = (cuuint64_t)dims[i];
         b[i] = (cuuint32_t)box[i];
@@ -579,10 +628,12 @@ static cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUte
 template <int kMode>
 static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
     const Params p{c.M, c.N, c.K, c.E, c.m_splits, static_cast<const __nv_bfloat16*>(c.bias), c.out, c.out_f32,
-                   c.accumulate, c.status};
+                   c.accumulate, c.status, static_cast<const __nv_bfloat16*>(c.y), static_cast<__nv_bfloat16*>(c.side)};
+    constexpr Mode kProduct = product_of(kMode);
+    constexpr int kFeat = kMode == kFpropSwiglu ? FEAT / 2 : FEAT;
     CUtensorMap a, b, half, out;  // half: b in boxes of half the rows; out: dW
     bool ok;
-    const int64_t feats = ((kMode == kFprop ? c.N : c.K) + FEAT - 1) / FEAT;
+    const int64_t feats = ((kProduct == kFprop ? c.N : c.K) + kFeat - 1) / kFeat;
     int64_t tiles = (c.M / WIDE + std::min<int64_t>(c.E, c.M)) * feats;  // no fewer than the device counts
     if (kMode == kWgrad) {
         tiles = feats * ((c.N + WIDE - 1) / WIDE) * c.E;
@@ -599,19 +650,25 @@ static cudaError_t run_mode(const GemmCall& c, cudaStream_t s) {
         ok = ok && encode_tmap(&out, c.out, size, 3, dd, sd, boxd, c.out_f32 ? 0 : 64);
     } else {
         const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {2 * c.K, 2 * c.K * c.N};
-        const int64_t db[2] = {kMode == kDgrad ? c.N : c.K, c.M}, sb[1] = {2 * c.ld_tok};
-        const int boxa[3] = {64, kMode == kDgrad ? BK : kFM, 1}, boxb[2] = {BK, BOX}, boxh[2] = {BK, BOX / 2};
-        ok = encode_tmap(&a, c.mat, 2, 3, da, sa, boxa) && encode_tmap(&b, c.tok, 2, 2, db, sb, boxb) &&
+        const int64_t db[2] = {kProduct == kDgrad ? c.N : c.K, c.M}, sb[1] = {2 * c.ld_tok};
+        const int boxa[3] = {64, kProduct == kDgrad ? BK : kFM, 1}, boxb[2] = {BK, BOX}, boxh[2] = {BK, BOX / 2};
+        ok = (kMode == kFpropSwiglu ? encode_gate_up(&a, c.mat, c.E, c.N, c.K, kFM / (2 * kGateRows))
+                                    : encode_tmap(&a, c.mat, 2, 3, da, sa, boxa)) &&
+             encode_tmap(&b, c.tok, 2, 2, db, sb, boxb) &&
              encode_tmap(&half, c.tok, 2, 2, db, sb, boxh);
     }
     if (kMode != kWgrad) out = a;  // not read
     if (!ok) return cudaErrorInvalidValue;
-    return c.out_f32 ? launch<kMode, true>(a, b, half, out, p, tiles, s)
-                     : launch<kMode, false>(a, b, half, out, p, tiles, s);
+    if constexpr (kMode != kProduct) return launch<kMode, false>(a, b, half, out, p, tiles, s);
+    else
+        return c.out_f32 ? launch<kMode, true>(a, b, half, out, p, tiles, s)
+                         : launch<kMode, false>(a, b, half, out, p, tiles, s);
 }
 
 cudaError_t run_gemm(const GemmCall& c, cudaStream_t s) {
     if (c.mode == kWgrad) return run_mode<kWgrad>(c, s);
+    if (c.mode == kDgradSwiglu) return run_mode<kDgradSwiglu>(c, s);
+    if (c.mode == kFpropSwiglu) return c.M <= (int64_t)kFewRows * c.E ? run_gemm_few(c, s) : run_mode<kFpropSwiglu>(c, s);
     // One-SM tiles up to as many rows as one holds, on average. W of 2048 x 4096, us, fprop and dgrad, one SM against
     // pairs: 8 experts of 16 rows each 26.2 and 23.7 against 27.4 and 25.5, of 32 26.6 and 24.0 against 27.4 and 25.7,
     // of 40 39.9 and 38.1 against 27.8 and 25.9; 64 experts of 32 168 and 163 against 170 and 159. Uneven counts need

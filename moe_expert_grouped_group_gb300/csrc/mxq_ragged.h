@@ -10,7 +10,13 @@
 namespace mxq {
 namespace ragged {
 
-enum Mode { kFprop = 0, kDgrad = 1, kWgrad = 2 };
+// kFpropSwiglu: fprop of W1 (E, 2N, K), out = h (M, N), side = [g | u] (M, 2N) or null. kDgradSwiglu: dgrad through the
+// activation, y = the saved [g | u] (M, 2K), out = its gradient (M, 2K), side = h (M, K) or null.
+enum Mode { kFprop = 0, kDgrad = 1, kWgrad = 2, kFpropSwiglu = 3, kDgradSwiglu = 4 };
+// the product that a mode is, its epilogue aside
+__host__ __device__ constexpr Mode product_of(int mode) {
+    return mode == kFpropSwiglu ? kFprop : mode == kDgradSwiglu ? kDgrad : (Mode)mode;
+}
 
 struct GemmCall {
     int mode;
@@ -26,6 +32,8 @@ struct GemmCall {
     int out_f32;
     int accumulate;      // wgrad
     int32_t* status;
+    const void* y = nullptr;  // the SwiGLU modes
+    void* side = nullptr;
 };
 cudaError_t run_gemm(const GemmCall& c, cudaStream_t s);
 // fprop and dgrad of at most kFewRows rows an expert on average
@@ -77,8 +85,8 @@ cudaError_t run_fp8_quantize_rows(const void* x, int64_t M, int64_t K, int64_t l
 cudaError_t run_fp8_quantize_weight(const void* w, int64_t N, int64_t K, int E, void* q, float* scale, cudaStream_t s);
 
 // Encodes a tensor map of int8, bf16 or fp32 elements (by their bytes) in up
-// to three dimensions: dims and box innermost first, strides in bytes of
-// dimensions 1 and 2, the swizzle of 128, 64 or 0 (none) bytes. False on failure.
+// to five dimensions: dims and box innermost first, strides in bytes of
+// dimensions 1 and up, the swizzle of 128, 64 or 0 (none) bytes. False on failure.
 bool encode_tmap(CUtensorMap* m, const void* base, int elem_bytes, int rank, const int64_t* dims,
                  const int64_t* strides, const int* box, int swizzle_bytes = 128);
 int sm_count();

@@ -104,6 +104,34 @@ int mxq_ragged_gemm_wgrad(const void* dy_bf16, int64_t lddy, const void* x_bf16,
                stream);
 }
 
+int mxq_ragged_gemm_fprop_swiglu(const void* x_bf16, int64_t ldx, const void* w_bf16, const void* bias_bf16, int64_t M,
+                                 int64_t F, int64_t K, int E, const int64_t* d_m_splits, void* h, void* y_out,
+                                 int32_t* d_status, mxq_stream_t stream) {
+    if (!w_bf16 || (M != 0 && (!x_bf16 || !h))) return MXQ_ERR_NULL;
+    if (int r = check_ragged(M, F, K, 8, 8, E, d_m_splits)) return r;
+    if (2 * F > kMaxWidth || bad_stride(ldx, K)) return MXQ_ERR_SHAPE;
+    if (!aligned16(x_bf16) || !aligned16(w_bf16) || !aligned16(bias_bf16) || !aligned16(h) || !aligned16(y_out))
+        return MXQ_ERR_ALIGN;
+    if (M == 0) return MXQ_OK;
+    return run({mxq::ragged::kFpropSwiglu, x_bf16, ldx, w_bf16, 0, bias_bf16, M, F, K, E, d_m_splits, h, 0, 0, d_status,
+                nullptr, y_out},
+               stream);
+}
+
+int mxq_ragged_gemm_dgrad_swiglu(const void* dy_bf16, int64_t lddy, const void* w_bf16, const void* y1_bf16, int64_t M,
+                                 int64_t N, int64_t F, int E, const int64_t* d_m_splits, void* dy1, void* h_out,
+                                 int32_t* d_status, mxq_stream_t stream) {
+    if (!w_bf16 || (M != 0 && (!dy_bf16 || !y1_bf16 || !dy1))) return MXQ_ERR_NULL;
+    if (int r = check_ragged(M, N, F, 8, 8, E, d_m_splits)) return r;
+    if (2 * F > kMaxWidth || bad_stride(lddy, N)) return MXQ_ERR_SHAPE;
+    if (!aligned16(dy_bf16) || !aligned16(w_bf16) || !aligned16(y1_bf16) || !aligned16(dy1) || !aligned16(h_out))
+        return MXQ_ERR_ALIGN;
+    if (M == 0) return MXQ_OK;
+    return run({mxq::ragged::kDgradSwiglu, dy_bf16, lddy, w_bf16, 0, nullptr, M, N, F, E, d_m_splits, dy1, 0, 0, d_status,
+                y1_bf16, h_out},
+               stream);
+}
+
 int mxq_int8_quantize_rows(const void* x_bf16, int64_t ldx, int64_t M, int64_t K, void* q, float* scale,
                            mxq_stream_t stream) {
     if (M != 0 && (!x_bf16 || !q || !scale)) return MXQ_ERR_NULL;

@@ -20,6 +20,7 @@
 #include "mxq_internal.h"
 #include "mxq_ragged.cuh"
 #include "mxq_ragged.h"
+#include "mxq_ragged_swiglu.cuh"
 
 namespace mxq {
 namespace ragged {
@@ -48,6 +49,7 @@ struct Params {
     void* out;
     int out_f32;
     int32_t* status;
+    __nv_bfloat16* side;  // kFpropSwiglu
 };
 
 template <int kMode, int kSplit>
@@ -94,7 +96,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (kSplit > 1) cluster_sync();  // the others' barriers exist before any partial sum is sent
     fence_after();
     const uint32_t tmem = s_tmem;
-    const Walk<kMode, kFM, WIDE, STEP> W(p.N, p.K, p.E, s_off, s_slices, nullptr);
+    constexpr int kFeatures = kMode == kFpropSwiglu ? kFM / 2 : kFM;  // of a tile's lanes
+    const Walk<product_of(kMode), kFeatures, WIDE, STEP> W(p.N, p.K, p.E, s_off, s_slices, nullptr);
     const int64_t first = blockIdx.x / kSplit, stride = gridDim.x / kSplit;
     // this CTA's part of the reduction, the same for every tile
     const int red = (int)(kMode == kDgrad ? p.N : p.K), blocks = (red + BK - 1) / BK;
@@ -117,7 +120,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint32_t fb = full0 + 8 * stage, a = smem_u32(smem) + stage * STAGE_BYTES;
                 if (elect_one()) {
                     mbar_expect_tx(fb, STAGE_BYTES);
-                    if (kMode == kFprop) {
+                    if (kMode == kFpropSwiglu) {
+                        load_5d(a, &tmA, fb, r, T.f0 / kGateRows, T.e);
+                    } else if (kMode == kFprop) {
                         load_3d<1>(a, &tmA, fb, r, T.f0, T.e);
                     } else {
                         load_3d<1>(a, &tmA, fb, T.f0, r, T.e);
@@ -171,7 +176,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
         // ------------------------------------------------------ epilogue: lane = feature
         const int q = warp & 3, l = q * 32 + lane;
-        const int64_t ld = kMode == kFprop ? p.N : p.K;
+        const int64_t ld = kMode == kDgrad ? p.K : p.N;
         int buf = 0;
         uint32_t aphase = 0;
         SplitSum<kSplit> split(smem_u32(smem) + PART_REGION, partf0, parte0, rank);
@@ -197,6 +202,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                     acc[j] = r0 == rb ? __uint_as_float(v[j]) : __fadd_rn(acc[j], __uint_as_float(v[j]));
             }
             if (!ok || !split.exchange(acc, l, lane, q == 0, t + 2 * stride < W.total, abort_flag)) break;
+            if constexpr (kMode == kFpropSwiglu) {
+                // lanes: eight gate features, the same eight of up, the next eight, ...
+                const int f = T.f0 + l / (2 * kGateRows) * kGateRows + l % kGateRows;
+                const bool up = l & kGateRows, live = f < ld;
+                const int64_t in_y = up ? ld + f : f;
+                const float b = live && p.bias ? __bfloat162float(p.bias[(int64_t)T.e * 2 * ld + in_y]) : 0.0f;
+#pragma unroll
+                for (int j = 0; j < WIDE / kSplit; ++j) {
+                    const int c = rank * (WIDE / kSplit) + j;
+                    if (c >= T.cols) break;
+                    const float v = __fadd_rn(acc[j], b), u = __shfl_down_sync(0xffffffffu, v, kGateRows);
+                    const int64_t row = T.row0 + c;
+                    if (live && p.side) p.side[row * 2 * ld + in_y] = __float2bfloat16_rn(v);
+                    if (live && !up) static_cast<__nv_bfloat16*>(p.out)[row * ld + f] = __float2bfloat16_rn(swiglu_h(v, u));
+                }
+                continue;
+            }
             if (T.f0 + l >= ld) continue;
             const float b = kMode == kFprop && p.bias ? __bfloat162float(p.bias[(int64_t)T.e * p.N + T.f0 + l]) : 0.0f;
 #pragma unroll
@@ -228,12 +250,16 @@ static cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const Para
 
 template <int kMode>
 static cudaError_t run(const GemmCall& c, cudaStream_t s) {
-    const Params p{c.M, c.N, c.K, c.E, c.m_splits, static_cast<const __nv_bfloat16*>(c.bias), c.out, c.out_f32, c.status};
-    const int64_t red = kMode == kDgrad ? c.N : c.K, feats = ((kMode == kFprop ? c.N : c.K) + kFM - 1) / kFM;
+    const Params p{c.M, c.N, c.K, c.E, c.m_splits, static_cast<const __nv_bfloat16*>(c.bias), c.out, c.out_f32, c.status,
+                   static_cast<__nv_bfloat16*>(c.side)};
+    constexpr int kFeat = kMode == kFpropSwiglu ? kFM / 2 : kFM;
+    const int64_t red = kMode == kDgrad ? c.N : c.K, feats = ((kMode == kDgrad ? c.K : c.N) + kFeat - 1) / kFeat;
     const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {2 * c.K, 2 * c.K * c.N}, db[2] = {red, c.M}, sb[1] = {2 * c.ld_tok};
     const int boxa[3] = {64, kMode == kDgrad ? BK : kFM, 1}, boxb[2] = {BK, WIDE};
     CUtensorMap a, b;
-    if (!encode_tmap(&a, c.mat, 2, 3, da, sa, boxa) || !encode_tmap(&b, c.tok, 2, 2, db, sb, boxb))
+    if (!(kMode == kFpropSwiglu ? encode_gate_up(&a, c.mat, c.E, c.N, c.K, kFM / (2 * kGateRows))
+                                : encode_tmap(&a, c.mat, 2, 3, da, sa, boxa)) ||
+        !encode_tmap(&b, c.tok, 2, 2, db, sb, boxb))
         return cudaErrorInvalidValue;
     const int64_t tiles = (c.M / WIDE + std::min<int64_t>(c.E, c.M)) * feats;  // no fewer than the device counts
     switch (split_of(tiles, (red + BK - 1) / BK)) {
@@ -247,7 +273,9 @@ static cudaError_t run(const GemmCall& c, cudaStream_t s) {
 }  // namespace few
 
 cudaError_t run_gemm_few(const GemmCall& c, cudaStream_t s) {
-    return c.mode == kFprop ? few::run<kFprop>(c, s) : few::run<kDgrad>(c, s);
+    return c.mode == kFpropSwiglu ? few::run<kFpropSwiglu>(c, s)
+           : c.mode == kFprop     ? few::run<kFprop>(c, s)
+                                  : few::run<kDgrad>(c, s);
 }
 
 // As many CTAs to a tile as still leave every tile in one wave and four stages

@@ -36,7 +36,8 @@ SYMBOLS = [
     "mxq_probe_mma_stream_ex", "mxq_selftest_wait_timeout", "mxq_ragged_gemm_fprop", "mxq_ragged_gemm_dgrad",
     "mxq_ragged_gemm_wgrad", "mxq_int8_quantize_rows", "mxq_int8_gemm_fprop", "mxq_swiglu_dropout_fwd",
     "mxq_swiglu_dropout_bwd", "mxq_dropout", "mxq_fp8_quantize_rows", "mxq_fp8_quantize_weight", "mxq_fp8_gemm_fprop",
-    "mxq_fp8_gemm_dgrad", "mxq_norm_residual_fwd", "mxq_norm_residual_bwd",
+    "mxq_fp8_gemm_dgrad", "mxq_norm_residual_fwd", "mxq_norm_residual_bwd", "mxq_ragged_gemm_fprop_swiglu",
+    "mxq_ragged_gemm_dgrad_swiglu",
 ]
 
 
@@ -87,6 +88,8 @@ def load(path: str = LIB) -> ctypes.CDLL:
     L.mxq_ragged_gemm_fprop.argtypes = [_P, _I64, _P, _P, _I64, _I64, _I64, _INT, _P, _INT, _P, _P, _P]
     L.mxq_ragged_gemm_dgrad.argtypes = [_P, _I64, _P, _I64, _I64, _I64, _INT, _P, _INT, _P, _P, _P]
     L.mxq_ragged_gemm_wgrad.argtypes = [_P, _I64, _P, _I64, _I64, _I64, _I64, _INT, _P, _INT, _P, _P, _P]
+    L.mxq_ragged_gemm_fprop_swiglu.argtypes = [_P, _I64, _P, _P, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P]
+    L.mxq_ragged_gemm_dgrad_swiglu.argtypes = [_P, _I64, _P, _P, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P]
     L.mxq_int8_quantize_rows.argtypes = [_P, _I64, _I64, _I64, _P, _P, _P]
     L.mxq_int8_gemm_fprop.argtypes = [_P, _P, _P, _P, _P, _I64, _I64, _I64, _INT, _P, _INT, _P, _P, _P]
     L.mxq_swiglu_dropout_fwd.argtypes = [_P, _I64, _I64, _P, _F64, _P, _P]
@@ -114,7 +117,8 @@ def load(path: str = LIB) -> ctypes.CDLL:
               "mxq_status_read", "mxq_ragged_gemm_fprop", "mxq_ragged_gemm_dgrad", "mxq_ragged_gemm_wgrad",
               "mxq_int8_quantize_rows", "mxq_int8_gemm_fprop", "mxq_swiglu_dropout_fwd", "mxq_swiglu_dropout_bwd",
               "mxq_dropout", "mxq_fp8_quantize_rows", "mxq_fp8_quantize_weight", "mxq_fp8_gemm_fprop",
-              "mxq_fp8_gemm_dgrad", "mxq_norm_residual_fwd", "mxq_norm_residual_bwd"):
+              "mxq_fp8_gemm_dgrad", "mxq_norm_residual_fwd", "mxq_norm_residual_bwd", "mxq_ragged_gemm_fprop_swiglu",
+              "mxq_ragged_gemm_dgrad_swiglu"):
         getattr(L, a).restype = _INT
     return L
 
@@ -842,6 +846,47 @@ def ragged_gemm_wgrad(dy, x, m_splits, accumulate=False, out_dtype=None, status=
     if rc:
         _check(rc, "mxq_ragged_gemm_wgrad")
     return out
+
+
+def ragged_gemm_fprop_swiglu(x, w, m_splits, bias=None, y_out=False, status=None, out=None):
+    """h = silu(g) * u of [g | u] = X W1_e^T (+ b_e) on bf16, any expert counts. x (M, K), its rows possibly a
+    slice of wider ones; w (E, 2F, K), gate first; bias (E, 2F). Returns h (M, F) or, with y_out, h and
+    [g | u] (M, 2F). out: what is returned, to write to."""
+    xp, M, K, ldx = _rows(x, "x", _BF16)
+    E, F2, Kw = w.shape
+    _shape(w, "w", (E, F2, K))
+    if F2 & 1:
+        raise MXQError(f"w: shape {tuple(w.shape)}, expected (E, 2F, K)")
+    F = F2 >> 1
+    if out is None:
+        h, y = _new((M, F), torch.bfloat16, x), _new((M, F2), torch.bfloat16, x) if y_out else None
+    else:
+        h, y = out if y_out else (out, None)
+    rc = lib().mxq_ragged_gemm_fprop_swiglu(xp, ldx, _dev(w, "w", 0, _BF16), _packed(bias, "bias", (E, F2), _BF16), M, F, K,
+                                            E, _grouping(m_splits, E), _packed(h, "h", (M, F), _BF16),
+                                            _packed(y, "y", (M, F2), _BF16), _dev(status, "status", 4, _I32), _stream())
+    if rc:
+        _check(rc, "mxq_ragged_gemm_fprop_swiglu")
+    return (h, y) if y_out else h
+
+
+def ragged_gemm_dgrad_swiglu(dy, w, y1, m_splits, h_out=False, status=None, out=None):
+    """The gradient [dg | du] of y1 = [g | u] (M, 2F) from FC2's output gradient: dh = dY W2_e, then the SwiGLU
+    backward, on bf16, any expert counts. dy (M, N), its rows possibly a slice of wider ones; w (E, N, F).
+    Returns [dg | du] (M, 2F) or, with h_out, it and h = silu(g) * u (M, F). out: what is returned, to write to."""
+    dyp, M, N, lddy = _rows(dy, "dy", _BF16)
+    E, Nw, F = w.shape
+    _shape(w, "w", (E, N, F))
+    if out is None:
+        d, h = _new((M, 2 * F), torch.bfloat16, dy), _new((M, F), torch.bfloat16, dy) if h_out else None
+    else:
+        d, h = out if h_out else (out, None)
+    rc = lib().mxq_ragged_gemm_dgrad_swiglu(dyp, lddy, _dev(w, "w", 0, _BF16), _packed(y1, "y1", (M, 2 * F), _BF16), M, N, F,
+                                            E, _grouping(m_splits, E), _packed(d, "dy1", (M, 2 * F), _BF16),
+                                            _packed(h, "h", (M, F), _BF16), _dev(status, "status", 4, _I32), _stream())
+    if rc:
+        _check(rc, "mxq_ragged_gemm_dgrad_swiglu")
+    return (d, h) if h_out else d
 
 
 def int8_quantize_rows(x, out=None):

@@ -1,4 +1,4 @@
-"""The entry points of the block-scaled fp8 products and of a block's norms refuse bad arguments on the host, before any
+"""The entry points of the gated products, the block-scaled fp8 products and a block's norms refuse bad arguments on the host, before any
 pointer is used, and the definitions that the GPU tests compare with agree with differences (CPU only)."""
 import pytest
 import torch
@@ -20,6 +20,8 @@ def L():
 
 
 CALLS = {
+    "mxq_ragged_gemm_fprop_swiglu": (P, K, P, P, M, F, K, E, P, P, P, None, None),
+    "mxq_ragged_gemm_dgrad_swiglu": (P, N, P, P, M, N, F, E, P, P, P, None, None),
     "mxq_fp8_quantize_rows": (P, K, M, K, P, P, None),
     "mxq_fp8_quantize_weight": (P, N, K, E, P, P, None),
     "mxq_fp8_gemm_fprop": (P, P, P, P, None, M, N, K, E, P, 0, P, None, None),
@@ -28,6 +30,8 @@ CALLS = {
     "mxq_norm_residual_bwd": (P, P, P, P, P, P, P, P, M, F, 1.0, 0, P, P, P, P, P, P, BIG, None),
 }
 REQUIRED = {
+    "mxq_ragged_gemm_fprop_swiglu": (0, 2, 8, 9),
+    "mxq_ragged_gemm_dgrad_swiglu": (0, 2, 3, 8, 9),
     "mxq_fp8_quantize_rows": (0, 4, 5),
     "mxq_fp8_quantize_weight": (0, 4, 5),
     "mxq_fp8_gemm_fprop": (0, 1, 2, 3, 9, 11),
