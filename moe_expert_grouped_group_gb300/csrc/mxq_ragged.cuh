@@ -499,8 +499,11 @@ struct Slice {
     int row, rows, n;  // first token row, rows of the expert in it, MMA N
 };
 __device__ __forceinline__ Slice slice_of(int off, int m, int count, int i, int step) {
-    const int64_t units = (m + step - 1) / step;
-    const int u0 = (int)(units * i / count), u1 = (int)(units * (i + 1) / count);
+    const int units = (m + step - 1) / step;
+    // 64-bit divisions take several hundred cycles: 32-bit ones wherever the products fit
+    const bool fits = (uint64_t)units * count < (1ull << 32);
+    const int u0 = fits ? (int)((uint32_t)units * (uint32_t)i / (uint32_t)count) : (int)((int64_t)units * i / count);
+    const int u1 = fits ? (int)((uint32_t)units * (uint32_t)(i + 1) / (uint32_t)count) : (int)((int64_t)units * (i + 1) / count);
     Slice s;
     s.n = (u1 - u0) * step;
     s.row = off + u0 * step;
@@ -549,12 +552,12 @@ struct Walk {
             T.red = off[T.e + 1] - T.red0;
             T.row0 = T.e * N + T.c0;
         } else {
-            // slices of an expert run fastest, so that the CTAs of one wave share its weight rows
-            T.e = owner_of(slices, E, (int32_t)(t / feats));
+            // slices of an expert run fastest, so that the CTAs of one wave share its weight rows (t < 2^31: the outputs of more tiles would not fit the device)
+            T.e = owner_of(slices, E, (int32_t)((uint32_t)t / (uint32_t)feats));
             const int count = slices[T.e + 1] - slices[T.e];
-            const int64_t r = t - (int64_t)slices[T.e] * feats;
-            const Slice s = slice_of(off[T.e], off[T.e + 1] - off[T.e], count, (int)(r % count), kStep);
-            T.f0 = (int)(r / count) * kFeat;
+            const uint32_t r = (uint32_t)(t - (int64_t)slices[T.e] * feats), f = r / (uint32_t)count;
+            const Slice s = slice_of(off[T.e], off[T.e + 1] - off[T.e], count, (int)(r - f * count), kStep);
+            T.f0 = (int)f * kFeat;
             T.c0 = s.row;
             T.cols = s.rows;
             T.n = s.n;

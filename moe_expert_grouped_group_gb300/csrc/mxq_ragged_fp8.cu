@@ -12,16 +12,20 @@
 // product of two scales differs from block to block and row to row. So an
 // accumulator holds one block (four MMAs of 32 k, kind::f8f6f4), and the
 // epilogue's warps add it to sums in registers, one fused multiply-add an
-// element, while the MMAs fill the other accumulator. The tile walk, the
-// operands' sides (features on the MMA's M, tokens on its N), the edges and the
-// pairs of SMs are those of the bf16 products (mxq_ragged.cuh, mxq_ragged.cu);
-// a stage is 128 deep and has their 32 KB an SM.
+// element, while the MMAs fill the other accumulator. That is the bottleneck:
+// everything an accumulator holds leaves TMEM once a block.
 //
-// Accumulators are read as matrix fragments (two columns of a lane side by
-// side), so a thread needs the scales of 8 columns of 32 rather than of all 32.
-// A warp fetches the rows' scales some blocks ahead, multiplies them by the
-// weight's, which is one number for a block and an SM's 128 features, and
-// leaves them in shared memory in the order in which the fragments want them.
+// Which operand is which. In the pair kernel the tokens are on the MMA's M: a
+// thread of the epilogue has one token, so one factor for a block and 128
+// features, and reads TMEM 32 lanes at a time. With the features on M, as in
+// the bf16 products, the factor differs from column to column: 256 factors a
+// block from shared memory cost more than the FMAs (a warp's 128 columns with
+// them 743 cycles, without 316), and fragment loads, which need few factors,
+// take TMEM twice as long (560). The price is that a tile has 256 rows whatever
+// the expert has; experts so small that it matters are bound by their weights'
+// bytes. Experts with few rows on average go to the kernel below, whose tokens
+// are on N.
+//
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -30,6 +34,7 @@
 #include "mxq_internal.h"
 #include "mxq_ragged.cuh"
 #include "mxq_ragged.h"
+#include "mxq_ragged_swiglu.cuh"
 
 namespace mxq {
 namespace ragged {
@@ -38,8 +43,8 @@ namespace f8 {
 constexpr int BK = kFp8Block;  // reduction depth of a stage: 128 bytes, one block of scales
 
 // Instruction descriptor for kind::f8f6f4, e4m3 x e4m3 (formats 0) with fp32 accumulation; fields as in idesc_f16.
-__device__ __forceinline__ uint32_t idesc_e4m3(uint32_t a_mn, uint32_t m, uint32_t n) {
-    return (1u << 4) | (a_mn << 15) | ((n >> 3) << 17) | ((m >> 4) << 24);
+__device__ __forceinline__ uint32_t idesc_e4m3(uint32_t a_mn, uint32_t b_mn, uint32_t m, uint32_t n) {
+    return (1u << 4) | (a_mn << 15) | (b_mn << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 template <int kCG>
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t accum) {
@@ -78,11 +83,9 @@ __device__ __forceinline__ int64_t weight_scale_at(const Params& p, int e, int f
     return kMode == kFprop ? (e * p.ws_rows + i) * p.ws_cols + j : (e * p.ws_rows + j) * p.ws_cols + i;
 }
 
-// Where a slot of scales keeps column j: of 16 columns, the four that a thread's fragments hold (8b + 2c and the next,
-// b = 0 and 1) lie side by side.
-__device__ __forceinline__ int slot_of(int j) { return (j & ~15) + ((j >> 1 & 3) << 2) + ((j >> 3 & 1) << 1) + (j & 1); }
-
-// The scales of the tiles' columns, block by block, through a ring of slots in shared memory.
+// The scales of the tiles' columns, block by block, through a ring of slots in shared memory. A slot keeps its columns in
+// the order in which matrix fragments want them: of 16 columns, the four that a thread holds (8b + 2c and the next, b = 0
+// and 1) side by side.
 template <int kWide, int kSlots>
 struct Scales {
     static constexpr int kBytes = kSlots * kWide * 4, kBatch = 4, kPer = kWide / 32;
@@ -102,7 +105,7 @@ struct Scales {
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
                 w[b] = 0.0f;
-                if (j + b < j1 && f < (kMode == kFprop ? p.N : p.K)) w[b] = p.ws[weight_scale_at<kMode>(p, T.e, f, j + b)];
+                if (j + b < j1) w[b] = p.ws[weight_scale_at<kMode>(p, T.e, f, j + b)];
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
                     const int c = 32 * i + lane;
@@ -115,10 +118,11 @@ struct Scales {
                 if (j + b >= j1) break;
                 if (!__all_sync(0xffffffffu, mbar_wait(empty + 8 * slot, phase ^ 1, abort_flag))) return false;
 #pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * (slot * kWide + slot_of(32 * i + lane))),
-                                 "f"(v[b][i] * w[b])
-                                 : "memory");
+                for (int i = 0; i < kPer; ++i) {
+                    const int c = 32 * i + lane;
+                    const int to = (c & ~15) + ((c >> 1 & 3) << 2) + ((c >> 3 & 1) << 1) + (c & 1);
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * (slot * kWide + to)), "f"(v[b][i] * w[b]) : "memory");
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full + 8 * slot);
                 step();
@@ -137,49 +141,114 @@ struct Scales {
     }
 };
 
-// Sums of 32 columns by this warp's 32 lanes as fragments: [16-lane half][2b + g]: lanes t/4 + 8g of the half, columns
-// 8b + 2(t mod 4) and the next.
-using Sums = uint64_t[2][8];
+// Sums of 32 columns by 16 lanes as a matrix fragment: [2b + g]: lane t/4 + 8g, columns 8b + 2(t mod 4) and the next.
+using Sums = uint64_t[8];
 
-// sums += the accumulator's columns (loaded as fragments) times their scales
-__device__ __forceinline__ void add_scaled(Sums& s, const uint32_t (&v)[2][16], float4 lo, float4 hi) {
+// sums += the accumulator's columns (loaded as a fragment) times their scales
+__device__ __forceinline__ void add_scaled(Sums& s, const uint32_t (&v)[16], float4 lo, float4 hi) {
     const uint64_t k[4] = {f2pack(lo.x, lo.y), f2pack(lo.z, lo.w), f2pack(hi.x, hi.y), f2pack(hi.z, hi.w)};
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            s[h][i] = f2fma(f2pack(__uint_as_float(v[h][2 * i]), __uint_as_float(v[h][2 * i + 1])), k[i >> 1], s[h][i]);
+    for (int i = 0; i < 8; ++i)
+        s[i] = f2fma(f2pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), k[i >> 1], s[i]);
 }
 
 // ------------------------------------------------------------ pairs of SMs
 namespace pair {
 
 constexpr int CG = 2;
-constexpr int FEAT = kFM * CG;
-constexpr int WIDE = 256, STEP = 16 * CG;
-constexpr int BOX = 64;
-constexpr int STAGES = 6;
-constexpr int SLOTS = 8;
+constexpr int ROWS = kFM * CG;   // token rows of a tile, on the MMA's M
+constexpr int WIDE = 256;        // features of a tile, on its N: two blocks of the weight
+constexpr int STAGES = 4;
+constexpr int AHEAD = 4;         // blocks whose scales are fetched together
 constexpr int EPI_FIRST = 4, EPI_WARPS = 8;
 constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
-constexpr int CTL_REGS = 80, EPI_REGS = 208;
+constexpr int CTL_REGS = 40, EPI_REGS = 232;
 static_assert(EPI_FIRST * CTL_REGS + EPI_WARPS * EPI_REGS <= THREADS / 32 * (65536 / THREADS / 8 * 8),
               "the warps' registers are those that the block starts with");
 constexpr int A_BYTES = kFM * BK, STAGE_BYTES = A_BYTES + WIDE / CG * BK;
 constexpr int TMEM_COLS = 2 * WIDE;
-constexpr int EPI_REGION = STAGES * STAGE_BYTES;  // staging of the bf16 epilogue, kBoxBytes a warp
-using Ring = Scales<WIDE, SLOTS>;
-constexpr int SCALE_REGION = EPI_REGION + EPI_WARPS * kBoxBytes;
-constexpr int BAR_REGION = SCALE_REGION + Ring::kBytes;
-constexpr int TABLE_REGION = BAR_REGION + 320;
+constexpr int BOX_BYTES = 32 * 128;               // 32 rows of 128 bytes
+constexpr int EPI_REGION = STAGES * STAGE_BYTES;  // staging of the epilogue, two boxes a warp
+constexpr int BAR_REGION = EPI_REGION + 2 * EPI_WARPS * BOX_BYTES;
+constexpr int BOARD_REGION = BAR_REGION + 256;  // a tile, see Board
+constexpr int TABLE_REGION = BOARD_REGION + 64;
 __host__ __device__ constexpr int smem_bytes(int E) { return 1024 + TABLE_REGION + 8 * (E + 1); }
 static_assert(smem_bytes(MXQ_MAX_EXPERTS) <= 232448, "shared memory over the per-block limit");
-static_assert(BAR_REGION % 16 == 0 && 8 * (2 * STAGES + 2 * SLOTS + 6) + 16 <= 320, "barrier region");
+static_assert(BAR_REGION % 1024 == 0 && 8 * (2 * STAGES + 8) + 16 <= 256, "barrier region");
+
+// out[row + i][f0 + c] for i < rows, c < n: rows are of expert e, whose slices have ROWS each
+struct Tile {
+    int e, f0, row, rows, n;
+};
+
+// Slices of an expert run fastest, so that the CTAs of one wave share its weight (a tile's number is below 2^31: the
+// outputs of more would not fit the device).
+struct Walk {
+    int feats, E;
+    int64_t width, total;
+    const int32_t *off, *slices;
+    __device__ Walk(int64_t width_, int E_, const int32_t* off_, const int32_t* slices_)
+        : E(E_), width(width_), off(off_), slices(slices_) {
+        feats = (int)((width + WIDE - 1) / WIDE);
+        total = (int64_t)slices[E] * feats;
+    }
+    __device__ Tile get(int64_t t) const {
+        Tile T;
+        T.e = owner_of(slices, E, (int32_t)((uint32_t)t / (uint32_t)feats));
+        const uint32_t count = slices[T.e + 1] - slices[T.e], r = (uint32_t)(t - (int64_t)slices[T.e] * feats);
+        const int f = (int)(r / count), i = (int)(r - f * count);
+        T.f0 = f * WIDE;
+        T.row = off[T.e] + i * ROWS;
+        T.rows = min(ROWS, off[T.e + 1] - T.row);
+        T.n = width - T.f0 > WIDE / 2 ? WIDE : WIDE / 2;
+        return T;
+    }
+};
+
+// The next tile of a CTA, as its last control warp finds it: where a tile lies takes several hundred cycles of divisions,
+// so it is computed once, ahead, and left here for the other warps. A tile with e < 0 ends the kernel.
+struct Board {
+    uint32_t at, full, empty;
+    uint32_t phase = 0;
+    __device__ Board(uint32_t at_, uint32_t full_, uint32_t empty_) : at(at_), full(full_), empty(empty_) {}
+    // Leaves T and waits until all have taken it, so that a CTA holds one tile more than it works on. A whole warp; false
+    // when a bounded wait has expired.
+    __device__ bool put(const Tile& T, int lane, volatile int* abort_flag) {
+        if (lane == 0) {
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(T.e), "r"(T.f0), "r"(T.row), "r"(T.rows)
+                         : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 16), "r"(T.n) : "memory");
+            mbar_arrive(full);
+        }
+        __syncwarp();
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(empty, phase, abort_flag)) != 0;
+        phase ^= 1;
+        return ok;
+    }
+    // The next tile, for a whole warp; e < 0 at the end or when a bounded wait has expired.
+    __device__ Tile take(int lane, volatile int* abort_flag) {
+        Tile T;
+        T.e = -1;
+        if (!__all_sync(0xffffffffu, mbar_wait(full, phase, abort_flag))) return T;
+        phase ^= 1;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(T.e), "=r"(T.f0), "=r"(T.row), "=r"(T.rows)
+                     : "r"(at)
+                     : "memory");
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(T.n) : "r"(at + 16) : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty);
+        return T;
+    }
+};
+
+// 16-byte piece i (of 8) of a row of 128 bytes under the 128-byte swizzle
+__device__ __forceinline__ uint32_t box_piece(uint32_t box, int row, int i) { return box + row * 128 + ((i ^ (row & 7)) << 4); }
 
 template <int kMode>
 __global__ void __launch_bounds__(THREADS, 1)
     ragged_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      const __grid_constant__ CUtensorMap tmHalf, Params p) {
+                      const __grid_constant__ CUtensorMap tmOut, Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align<1024>(smem_raw);
     int32_t* s_off = reinterpret_cast<int32_t*>(smem + TABLE_REGION);
@@ -190,9 +259,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t rank = cta_rank();
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_REGION);
-    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, sfull0 = empty0 + 8 * STAGES;
-    const uint32_t sempty0 = sfull0 + 8 * SLOTS, accf0 = sempty0 + 8 * SLOTS, acce0 = accf0 + 16;
-    const uint32_t ready = acce0 + 16, taken = ready + 8, answer = (taken + 8 + 15) & ~15u;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, accf0 = empty0 + 8 * STAGES, acce0 = accf0 + 16;
+    const uint32_t bfull = acce0 + 16, bempty = bfull + 8, ready = bempty + 8, taken = ready + 8;
+    const uint32_t answer = (taken + 8 + 15) & ~15u;
     volatile int* abort_flag = &s_abort;
     if (threadIdx.x == 0) {
         s_abort = 0;
@@ -200,22 +269,20 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(full0 + 8 * st, 1);
             mbar_init(empty0 + 8 * st, 1);
         }
-        for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(sfull0 + 8 * i, 1);
-            mbar_init(sempty0 + 8 * i, EPI_WARPS);
-        }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf0 + 8 * b, 1);
             mbar_init(acce0 + 8 * b, CG * EPI_WARPS);
         }
+        mbar_init(bfull, 1);
+        mbar_init(bempty, 1 + EPI_WARPS + (rank == 0));  // loads, the epilogue; the MMAs
         mbar_init(ready, 1);
-        mbar_init(taken, 7 + 2 * EPI_WARPS);  // the warps of both CTAs that call next()
+        mbar_init(taken, CG);  // one warp of each CTA asks for tiles
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmA) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmB) : "memory");
     }
     // both CTAs of a pair find the same fault and stop before any cluster-wide step
-    const int bad = load_ragged(p.m_splits, p.E, p.M, WIDE, s_off, s_slices);
+    const int bad = load_ragged(p.m_splits, p.E, p.M, ROWS, s_off, s_slices);
     if (bad) {
         report_status(p.status, bad);
         return;
@@ -226,10 +293,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     cluster_sync();  // both CTAs' barriers exist before any load completes on rank 0's
     fence_after();
     const uint32_t tmem = s_tmem;
-    const Walk<kMode, FEAT, WIDE, STEP> W(p.N, p.K, p.E, s_off, s_slices, nullptr);
-    TileQueue queue(answer, ready, mapa(taken, 0));
-    Ring ring(smem_u32(smem) + SCALE_REGION, sfull0, sempty0);
-    int64_t t = blockIdx.x / CG;
+    const int red = (int)(kMode == kFprop ? p.K : p.N);      // terms of a sum
+    const int64_t ld = kMode == kFprop ? p.N : p.K;          // features
+    Board board(smem_u32(smem) + BOARD_REGION, bfull, bempty);
 
     if (warp < EPI_FIRST) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTL_REGS));
@@ -238,56 +304,47 @@ __global__ void __launch_bounds__(THREADS, 1)
             int stage = 0;
             uint32_t phase = 0;
             int64_t fills = 0;
-            do {
-                if (t >= W.total) continue;
-                const Tile T = W.get(t);
-                const int half = T.n / CG;  // this CTA's columns of the tile: [rank * half, + half)
-                // token rows: whole boxes, and half a box at the end where that is enough
-                const bool half_box = (half - 1) % BOX < BOX / 2;
-                const int boxes = half_box ? half / BOX : (half + BOX - 1) / BOX;
-                const int f = T.f0 + rank * kFM, c = T.c0 + rank * half;
-                const uint32_t bytes = A_BYTES + (2 * boxes + half_box) * (BOX / 2 * BK);
-                for (int r = 0; r < T.red; r += BK) {
-                    if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag)) {
-                        if (rank == 0) drain_ring(full0, STAGES, fills);  // both CTAs' loads complete on rank 0's
-                        goto done_producer;
-                    }
+            for (;;) {
+                const Tile T = board.take(lane, abort_flag);
+                if (T.e < 0) break;
+                const int m = T.row + rank * kFM, f = T.f0 + rank * (T.n / CG);
+                for (int r = 0; r < red; r += BK) {
+                    if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag)) goto done_producer;
                     __syncwarp();
                     const uint32_t own = full0 + 8 * stage, fb = mapa(own, 0);
                     const uint32_t a = smem_u32(smem) + stage * STAGE_BYTES, b = a + A_BYTES;
                     if (elect_one()) {
-                        if (rank == 0) mbar_expect_tx(own, CG * bytes);
-                        if (kMode == kFprop) load_3d<CG>(a, &tmA, fb, r, f, T.e);
-                        else load_3d<CG>(a, &tmA, fb, f, r, T.e);
-#pragma unroll
-                        for (int i = 0; i < WIDE / CG / BOX; ++i)
-                            if (i < boxes) load_2d<CG>(b + BOX * BK * i, &tmB, fb, r, c + BOX * i);
-                        if (half_box) load_2d<CG>(b + BOX * BK * boxes, &tmHalf, fb, r, c + BOX * boxes);
+                        if (rank == 0) mbar_expect_tx(own, CG * STAGE_BYTES);
+                        load_2d<CG>(a, &tmA, fb, r, m);
+                        if (kMode == kFprop) load_3d<CG>(b, &tmB, fb, r, f, T.e);
+                        else load_3d<CG>(b, &tmB, fb, f, r, T.e);
                     }
                     __syncwarp();
                     ++fills;
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
-            } while (queue.next(t, lane, abort_flag) == TileQueue::kTile);
-        done_producer:;
+            }
+        done_producer:
+            // a bounded wait expired: no copy may be in flight when the block ends (both CTAs' loads complete on rank 0's)
+            if (*abort_flag && rank == 0) drain_ring(full0, STAGES, fills);
         } else if (warp == 1) {
             // -------------------------------------------------- MMA issuer (rank 0)
             if (rank == 0) {
                 int stage = 0, buf = 0;
                 uint32_t phase = 0, aphase = 0;
                 const uint32_t base = smem_u32(smem);
-                // MN-major A: one 128-byte chunk of features, 8-row groups of the reduction 1024 bytes apart
+                // MN-major B: one 128-byte chunk of features, 8-row groups of the reduction 1024 bytes apart
                 const uint64_t ad0 = smem_desc(base, 16, 1024), bd0 = smem_desc(base + A_BYTES, 16, 1024);
-                constexpr uint32_t a_step = (kMode == kDgrad ? 4096 : 32) / 16, b_step = 32 / 16;  // 32 of the sum
-                do {
-                    if (t >= W.total) continue;
-                    const Tile T = W.get(t);
-                    const uint32_t id = idesc_e4m3(kMode == kDgrad, FEAT, T.n);
-                    for (int r = 0; r < T.red; r += BK) {
+                constexpr uint32_t a_step = 32 / 16, b_step = (kMode == kDgrad ? 4096 : 32) / 16;  // 32 of the sum
+                for (;;) {
+                    const Tile T = board.take(lane, abort_flag);
+                    if (T.e < 0) break;
+                    const uint32_t id = idesc_e4m3(0, kMode == kDgrad, ROWS, T.n);
+                    for (int r = 0; r < red; r += BK) {
                         const uint64_t ad = ad0 + (uint64_t)(stage * (STAGE_BYTES / 16));
                         const uint64_t bd = bd0 + (uint64_t)(stage * (STAGE_BYTES / 16));
-                        if (!mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag)) goto done_mma;
                         if (!mbar_wait(full0 + 8 * stage, phase, abort_flag)) goto done_mma;
+                        if (!mbar_wait(acce0 + 8 * buf, aphase ^ 1, abort_flag)) goto done_mma;
                         __syncwarp();
                         fence_after();
                         if (elect_one()) {
@@ -302,19 +359,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                         buf ^= 1;
                         aphase ^= buf == 0;
                     }
-                } while (queue.next(t, lane, abort_flag) == TileQueue::kTile);
+                }
             done_mma:;
             }
-        } else if (warp == 2) {
-            // -------------------------------------------------- scales
-            do {
-                if (t >= W.total) continue;
-                const Tile T = W.get(t);
-                if (!ring.template produce<kMode>(p, T, T.f0 + rank * kFM, 0, (T.red + BK - 1) / BK, lane, abort_flag)) break;
-            } while (queue.next(t, lane, abort_flag) == TileQueue::kTile);
-        } else {
-            // -------------------------------------------------- next tiles
+        } else if (warp == 3) {
+            // -------------------------------------------------- tiles
+            const Walk W(ld, p.E, s_off, s_slices);
+            TileQueue queue(answer, ready, mapa(taken, 0));
+            int64_t t = blockIdx.x / CG;
             for (uint32_t asked = 0;; asked ^= 1) {
+                if (t < W.total && !board.put(W.get(t), lane, abort_flag)) break;
                 if (rank == 0 && !mbar_wait(taken, asked ^ 1, abort_flag)) break;
                 __syncwarp();
                 if (elect_one()) {
@@ -322,117 +376,162 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (rank == 0) queue.ask();
                 }
                 __syncwarp();
-                if (queue.next(t, lane, abort_flag) != TileQueue::kTile) break;
+                if (queue.next(t, lane, abort_flag) != TileQueue::kTile) {
+                    board.put(Tile{-1, 0, 0, 0, 0}, lane, abort_flag);
+                    break;
+                }
             }
         }
     } else {
-        // ------------------------------------------------------ epilogue
+        // ------------------------------------------------------ epilogue: lane = token row
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
-        const int q = warp & 3, group = (warp - EPI_FIRST) >> 2;  // two groups of four warps share the columns
-        uint8_t* stage = smem + EPI_REGION + (warp - EPI_FIRST) * kBoxBytes;
-        const int64_t ld = kMode == kFprop ? p.N : p.K;  // features
-        constexpr int kChunks = WIDE / 64;               // 32-column chunks of a group
-        int buf = 0;
-        uint32_t aphase = 0;
+        // two groups of four warps: a group has one of the tile's two blocks of features
+        const int q = warp & 3, group = (warp - EPI_FIRST) >> 2;
+        const uint32_t stage = smem_u32(smem) + EPI_REGION + (warp - EPI_FIRST) * 2 * BOX_BYTES;
+        constexpr int kParts = WIDE / 32;  // 16 columns each
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + group * (WIDE / 2);
         const uint32_t acce = mapa(acce0, 0);
-        do {
-            if (t >= W.total) continue;
-            const Tile T = W.get(t);
-            Sums acc[kChunks];
+        const int blocks = (red + BK - 1) / BK;
+        int buf = 0, boxes = 0;
+        uint32_t aphase = 0;
+        float x[AHEAD], w[AHEAD];  // scales of the next blocks: of this thread's row, of the group's features
+        const auto fetch = [&](const Tile& T, int j0) {
+            const int i = 128 * (int)rank + 32 * q + lane, f = T.f0 + group * BK;
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[i][h][j] = 0;
-            bool ok = true;
-            for (int r = 0; r < T.red; r += BK) {
-                ok = mbar_wait(ring.full + 8 * ring.slot, ring.phase, abort_flag) &&
-                     mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
-                ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-                if (!ok) break;
-                fence_after();
-#pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    const int c = 64 * i + 32 * group;
-                    if (c < T.cols) {
-                        uint32_t v[2][16];
-                        const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + buf * WIDE + c;
-                        tmem_ld16x32(at, v[0]);
-                        tmem_ld16x32(at + (16u << 16), v[1]);
-                        const float4 lo = ring.get(c, lane), hi = ring.get(c + 16, lane);
-                        tmem_wait_ld();
-                        add_scaled(acc[i], v, lo, hi);
-                    }
-                }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (rank == 0) mbar_arrive(acce0 + 8 * buf);
-                    else arrive_remote_relaxed(acce + 8 * buf);
-                    mbar_arrive(ring.empty + 8 * ring.slot);
-                }
-                ring.step();
-                buf ^= 1;
-                aphase ^= buf == 0;
-            }
-            if (!ok) break;
-            const int f0 = T.f0 + rank * kFM + 32 * q;
-            const int live = (int)min((int64_t)32, ld - f0);  // may be negative: nothing to store
-            float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (kMode == kFprop && p.bias) {
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int l = (lane >> 2) + 8 * g;
-                    if (l < live) b[g] = __bfloat162float(p.bias[(int64_t)T.e * p.N + f0 + l]);
+            for (int j = 0; j < AHEAD; ++j) {
+                x[j] = w[j] = 0.0f;
+                if (j0 + j < blocks && f < ld) {
+                    w[j] = p.ws[weight_scale_at<kMode>(p, T.e, f, j0 + j)];
+                    if (i < T.rows) x[j] = p.xs[(j0 + j) * p.M + T.row + i];
                 }
             }
+        };
+        Tile T = board.take(lane, abort_flag);
+        if (T.e >= 0) fetch(T, 0);
+        while (T.e >= 0) {
+            uint64_t acc[kParts][8];  // sums of two columns each
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const int c0 = 64 * i + 32 * group;
-                if (c0 >= T.cols) continue;
-                if (p.out_f32) {
-                    // eight lanes write 32 contiguous bytes
-                    float* o = static_cast<float*>(p.out) + (T.row0 + c0) * ld + f0;
+            for (int i = 0; i < kParts; ++i)
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
+                for (int j = 0; j < 8; ++j) acc[i][j] = 0;
+            for (int j0 = 0; j0 < blocks; j0 += AHEAD) {
+                float s[AHEAD];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int l = (lane >> 2) + 8 * g, c = 8 * j + 2 * (lane & 3);
-                            const float2 v = f2unpack(acc[i][g >> 1][2 * j + (g & 1)]);
-                            if (l < live && c0 + c < T.cols) o[c * ld + l] = v.x + b[g];
-                            if (l < live && c0 + c + 1 < T.cols) o[(c + 1) * ld + l] = v.y + b[g];
-                        }
-                } else {
-                    // transposed through the warp's stage: rows of 64 bytes, their 16-byte pieces exchanged by the
-                    // row's bits 1 and 2
-                    const int row = lane & 7;
-                    const uint32_t at = smem_u32(stage) + row * 64 + (((lane >> 3) ^ (row >> 1)) << 4);
-                    __syncwarp();  // the stage's last reads are done
+                for (int j = 0; j < AHEAD; ++j) s[j] = x[j] * w[j];
+                fetch(T, j0 + AHEAD);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const float2 v = f2unpack(acc[i][g >> 1][2 * j + (g & 1)]);
-                            w[g] = bf16x2_bits(v.x + b[g], v.y + b[g]);
-                        }
-                        stmatrix_trans(at + 512 * j, w);
-                    }
+                for (int j = 0; j < AHEAD; ++j) {
+                    if (j0 + j >= blocks) break;
+                    // after an expired wait the others return at once; the tile is then not stored
+                    mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
                     __syncwarp();
-                    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + (T.row0 + c0) * ld + f0;
-                    const int piece = lane & 3;
-                    if (piece * 8 < live)
+                    fence_after();
+                    const uint64_t k = f2splat(s[j]);
+                    uint32_t v[2][16];
+                    const uint32_t at = lanes + buf * WIDE;
+                    tmem_ld16(at, v[0]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int c = 8 * j + (lane >> 2);
-                            if (c0 + c < T.cols)
-                                *reinterpret_cast<uint4*>(o + c * ld + piece * 8) =
-                                    *reinterpret_cast<const uint4*>(stage + c * 64 + ((piece ^ (c >> 1 & 3)) << 4));
+                    for (int i = 0; i < kParts; ++i) {
+                        tmem_wait_ld();
+                        if (i + 1 < kParts) {
+                            tmem_ld16(at + 16 * (i + 1), v[(i + 1) & 1]);  // on its way while this part is added
+                        } else {
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (rank == 0) mbar_arrive(acce0 + 8 * buf);
+                                else arrive_remote_relaxed(acce + 8 * buf);
+                            }
                         }
+#pragma unroll
+                        for (int l = 0; l < 8; ++l)
+                            acc[i][l] = f2fma(f2pack(__uint_as_float(v[i & 1][2 * l]), __uint_as_float(v[i & 1][2 * l + 1])), k,
+                                              acc[i][l]);
+                    }
+                    buf ^= 1;
+                    aphase ^= buf == 0;
                 }
             }
-        } while (queue.next(t, lane, abort_flag) == TileQueue::kTile);
+            const Tile done = T;
+            T = board.take(lane, abort_flag);
+            if (T.e >= 0) fetch(T, 0);
+            if (__any_sync(0xffffffffu, *abort_flag)) break;
+
+            const int f0 = done.f0 + group * BK, row = done.row + 128 * (int)rank + 32 * q;
+            const int live = (int)min((int64_t)BK, ld - f0);  // features; may be negative: nothing to store
+            const int rows = min(32, done.rows - 128 * (int)rank - 32 * q);
+            if (live <= 0 || rows <= 0) continue;
+            if (kMode == kFprop && p.bias) {
+                const __nv_bfloat16* bias = p.bias + (int64_t)done.e * p.N + f0;
+#pragma unroll
+                for (int i = 0; i < kParts; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (16 * i + 8 * h >= live) continue;
+                        const uint4 b = *reinterpret_cast<const uint4*>(bias + 16 * i + 8 * h);
+                        const uint32_t u[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int l = 0; l < 4; ++l)
+                            acc[i][4 * h + l] = f2add(acc[i][4 * h + l], f2pack(bf16lo(u[l]), bf16hi(u[l])));
+                    }
+            }
+            // rows of 128 bytes through shared memory: 64 bf16 or 32 fp32, by TMA where all 32 rows are the slice's
+            const auto store_box = [&](int column, auto put) {
+                const uint32_t box = stage + (boxes & 1) * BOX_BYTES;
+                ++boxes;
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                __syncwarp();
+                put(box);
+                if (rows == 32) {
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && column < live)
+                        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                                         (uint64_t)&tmOut),
+                                     "r"(f0 + column), "r"(row), "r"(box)
+                                     : "memory");
+                } else {
+                    __syncwarp();
+                    const int size = p.out_f32 ? 4 : 2, piece = lane & 7;
+                    uint8_t* o = static_cast<uint8_t*>(p.out) + ((int64_t)row * ld + f0 + column) * size + piece * 16;
+                    if (column * size + piece * 16 < live * size)
+                        for (int m = lane >> 3; m < rows; m += 4)
+                            *reinterpret_cast<uint4*>(o + m * ld * size) = ld_shared(box_piece(box, m, piece));
+                    __syncwarp();
+                }
+                if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            };
+            if (p.out_f32) {
+#pragma unroll
+                for (int i = 0; i < kParts; i += 2)
+                    store_box(16 * i, [&](uint32_t box) {
+#pragma unroll
+                        for (int h = 0; h < 8; ++h) {
+                            const float2 a = f2unpack(acc[i + (h >> 2)][2 * (h & 3)]), b = f2unpack(acc[i + (h >> 2)][2 * (h & 3) + 1]);
+                            st_shared(box_piece(box, lane, h), make_uint4(__float_as_uint(a.x), __float_as_uint(a.y),
+                                                                          __float_as_uint(b.x), __float_as_uint(b.y)));
+                        }
+                    });
+            } else {
+#pragma unroll
+                for (int i = 0; i < kParts; i += 4)
+                    store_box(16 * i, [&](uint32_t box) {
+#pragma unroll
+                        for (int h = 0; h < 8; ++h) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int l = 0; l < 4; ++l) {
+                                const float2 a = f2unpack(acc[i + (h >> 1)][4 * (h & 1) + l]);
+                                u[l] = bf16x2_bits(a.x, a.y);
+                            }
+                            st_shared(box_piece(box, lane, h), make_uint4(u[0], u[1], u[2], u[3]));
+                        }
+                    });
+            }
+        }
+        // the last boxes are written before the block leaves its shared memory
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
     fence_before();
     __syncthreads();
@@ -560,7 +659,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         constexpr uint32_t a_step = (kMode == kDgrad ? 4096 : 32) / 16, b_step = 32 / 16;
         for (int64_t t = first; t < W.total; t += stride) {
             const Tile T = W.get(t);
-            const uint32_t id = idesc_e4m3(kMode == kDgrad, kFM, T.n);
+            const uint32_t id = idesc_e4m3(kMode == kDgrad, 0, kFM, T.n);
             for (int j = jb; j < je; ++j) {
                 const uint64_t ad = ad0 + (uint64_t)(stage * (STAGE_BYTES / 16));
                 const uint64_t bd = bd0 + (uint64_t)(stage * (STAGE_BYTES / 16));
@@ -596,7 +695,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         SplitSum<kSplit> split(smem_u32(smem) + PART_REGION, partf0, parte0, rank);
         for (int64_t t = first; t < W.total; t += stride) {
             const Tile T = W.get(t);
-            Sums acc;
+            Sums acc[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -622,7 +721,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 ring.step();
                 if (++buf == BUFS) { buf = 0; aphase ^= 1; }
-                add_scaled(acc, v, lo, hi);
+                add_scaled(acc[0], v[0], lo, hi);
+                add_scaled(acc[1], v[1], lo, hi);
             }
             // sums in the order [8-column block][column of the two][8-lane block], which a split divides
             float s[WIDE];
@@ -764,16 +864,18 @@ static Params params(const Fp8Call& c) {
 template <int kMode>
 static cudaError_t run_pair(const Fp8Call& c, cudaStream_t s) {
     using namespace pair;
-    const int64_t red = kMode == kDgrad ? c.N : c.K, feats = ((kMode == kFprop ? c.N : c.K) + FEAT - 1) / FEAT;
-    const int64_t da[3] = {c.K, c.N, c.E}, sa[2] = {c.K, c.K * c.N}, db[2] = {red, c.M}, sb[1] = {red};
-    const int boxa[3] = {BK, kFM, 1}, boxb[2] = {BK, BOX}, boxh[2] = {BK, BOX / 2};
-    CUtensorMap a, b, half;
-    if (!encode_tmap(&a, c.wq, 1, 3, da, sa, boxa) || !encode_tmap(&b, c.tq, 1, 2, db, sb, boxb) ||
-        !encode_tmap(&half, c.tq, 1, 2, db, sb, boxh))
+    const int64_t red = kMode == kDgrad ? c.N : c.K, width = kMode == kFprop ? c.N : c.K, size = c.out_f32 ? 4 : 2;
+    const int64_t da[2] = {red, c.M}, sa[1] = {red}, db[3] = {c.K, c.N, c.E}, sb[2] = {c.K, c.K * c.N};
+    const int64_t dd[2] = {width, c.M}, sd[1] = {size * width};
+    const int boxa[2] = {BK, kFM}, boxb[3] = {BK, kFM, 1}, boxd[2] = {128 / (int)size, 32};
+    CUtensorMap a, b, out;
+    if (!encode_tmap(&a, c.tq, 1, 2, da, sa, boxa) || !encode_tmap(&b, c.wq, 1, 3, db, sb, boxb) ||
+        !encode_tmap(&out, c.out, (int)size, 2, dd, sd, boxd))
         return cudaErrorInvalidValue;
-    const int64_t tiles = (c.M / WIDE + std::min<int64_t>(c.E, c.M)) * feats;  // no fewer than the device counts
+    // no fewer than the device counts
+    const int64_t tiles = (c.M / ROWS + std::min<int64_t>(c.E, c.M)) * ((width + WIDE - 1) / WIDE);
     return launch_persistent<CG, true, ragged_fp8_kernel<kMode>>(THREADS, smem_bytes(MXQ_MAX_EXPERTS), smem_bytes(c.E),
-                                                                 tiles, s, a, b, half, params(c));
+                                                                 tiles, s, a, b, out, params(c));
 }
 
 template <int kMode, int kSplit>
