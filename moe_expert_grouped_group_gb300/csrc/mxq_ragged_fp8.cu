@@ -159,22 +159,25 @@ constexpr int CG = 2;
 constexpr int ROWS = kFM * CG;   // token rows of a tile, on the MMA's M
 constexpr int WIDE = 256;        // features of a tile, on its N: two blocks of the weight
 constexpr int STAGES = 4;
-constexpr int AHEAD = 4;         // blocks whose scales are fetched together
+constexpr int SLOTS = 8;         // blocks whose scales are on chip
+constexpr int AHEAD = 2;         // and of how many the loads are in flight together
 constexpr int EPI_FIRST = 4, EPI_WARPS = 8;
 constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
-constexpr int CTL_REGS = 40, EPI_REGS = 232;
+constexpr int CTL_REGS = 56, EPI_REGS = 224;
 static_assert(EPI_FIRST * CTL_REGS + EPI_WARPS * EPI_REGS <= THREADS / 32 * (65536 / THREADS / 8 * 8),
               "the warps' registers are those that the block starts with");
 constexpr int A_BYTES = kFM * BK, STAGE_BYTES = A_BYTES + WIDE / CG * BK;
 constexpr int TMEM_COLS = 2 * WIDE;
 constexpr int BOX_BYTES = 32 * 128;               // 32 rows of 128 bytes
 constexpr int EPI_REGION = STAGES * STAGE_BYTES;  // staging of the epilogue, two boxes a warp
-constexpr int BAR_REGION = EPI_REGION + 2 * EPI_WARPS * BOX_BYTES;
-constexpr int BOARD_REGION = BAR_REGION + 256;  // a tile, see Board
+constexpr int SLOT_BYTES = 2 * kFM * 4;           // a factor for each of this CTA's rows and each block of features
+constexpr int SCALE_REGION = EPI_REGION + 2 * EPI_WARPS * BOX_BYTES;
+constexpr int BAR_REGION = SCALE_REGION + SLOTS * SLOT_BYTES;
+constexpr int BOARD_REGION = BAR_REGION + 320;  // a tile, see Board
 constexpr int TABLE_REGION = BOARD_REGION + 64;
 __host__ __device__ constexpr int smem_bytes(int E) { return 1024 + TABLE_REGION + 8 * (E + 1); }
 static_assert(smem_bytes(MXQ_MAX_EXPERTS) <= 232448, "shared memory over the per-block limit");
-static_assert(BAR_REGION % 1024 == 0 && 8 * (2 * STAGES + 8) + 16 <= 256, "barrier region");
+static_assert(BAR_REGION % 1024 == 0 && 8 * (2 * STAGES + 2 * SLOTS + 8) + 16 <= 320, "barrier region");
 
 // out[row + i][f0 + c] for i < rows, c < n: rows are of expert e, whose slices have ROWS each
 struct Tile {
@@ -260,7 +263,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_REGION);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, accf0 = empty0 + 8 * STAGES, acce0 = accf0 + 16;
-    const uint32_t bfull = acce0 + 16, bempty = bfull + 8, ready = bempty + 8, taken = ready + 8;
+    const uint32_t sfull0 = acce0 + 16, sempty0 = sfull0 + 8 * SLOTS;
+    const uint32_t bfull = sempty0 + 8 * SLOTS, bempty = bfull + 8, ready = bempty + 8, taken = ready + 8;
     const uint32_t answer = (taken + 8 + 15) & ~15u;
     volatile int* abort_flag = &s_abort;
     if (threadIdx.x == 0) {
@@ -273,8 +277,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(accf0 + 8 * b, 1);
             mbar_init(acce0 + 8 * b, CG * EPI_WARPS);
         }
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(sfull0 + 8 * i, 1);
+            mbar_init(sempty0 + 8 * i, EPI_WARPS);
+        }
         mbar_init(bfull, 1);
-        mbar_init(bempty, 1 + EPI_WARPS + (rank == 0));  // loads, the epilogue; the MMAs
+        mbar_init(bempty, 2 + EPI_WARPS + (rank == 0));  // loads, scales, the epilogue; the MMAs
         mbar_init(ready, 1);
         mbar_init(taken, CG);  // one warp of each CTA asks for tiles
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -295,6 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = s_tmem;
     const int red = (int)(kMode == kFprop ? p.K : p.N);      // terms of a sum
     const int64_t ld = kMode == kFprop ? p.N : p.K;          // features
+    const int blocks = (red + BK - 1) / BK;
     Board board(smem_u32(smem) + BOARD_REGION, bfull, bempty);
 
     if (warp < EPI_FIRST) {
@@ -362,7 +371,51 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             done_mma:;
             }
-        } else if (warp == 3) {
+        } else if (warp == 2) {
+            // -------------------------------------------------- scales
+            const uint32_t at = smem_u32(smem) + SCALE_REGION + 4 * lane;
+            int slot = 0;
+            uint32_t phase = 0;
+            for (;;) {
+                const Tile T = board.take(lane, abort_flag);
+                if (T.e < 0) break;
+                const int rows = T.rows - 128 * (int)rank;  // of this CTA
+                const float* xs = p.xs + T.row + 128 * (int)rank + lane;
+                for (int j0 = 0; j0 < blocks; j0 += AHEAD) {
+                    float x[AHEAD][4], w[AHEAD][2];
+#pragma unroll
+                    for (int j = 0; j < AHEAD; ++j) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            w[j][g] = 0.0f;
+                            const int f = T.f0 + g * BK;
+                            if (j0 + j < blocks && f < ld) w[j][g] = p.ws[weight_scale_at<kMode>(p, T.e, f, j0 + j)];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            x[j][i] = 0.0f;
+                            if (j0 + j < blocks && 32 * i + lane < rows) x[j][i] = xs[(j0 + j) * p.M + 32 * i];
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < AHEAD; ++j) {
+                        if (j0 + j >= blocks) break;
+                        if (!__all_sync(0xffffffffu, mbar_wait(sempty0 + 8 * slot, phase ^ 1, abort_flag))) goto done_scales;
+#pragma unroll
+                        for (int g = 0; g < 2; ++g)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + slot * SLOT_BYTES + 512 * g + 128 * i),
+                                             "f"(x[j][i] * w[j][g])
+                                             : "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(sfull0 + 8 * slot);
+                        if (++slot == SLOTS) { slot = 0; phase ^= 1; }
+                    }
+                }
+            }
+        done_scales:;
+        } else {
             // -------------------------------------------------- tiles
             const Walk W(ld, p.E, s_off, s_slices);
             TileQueue queue(answer, ready, mapa(taken, 0));
@@ -391,78 +444,61 @@ __global__ void __launch_bounds__(THREADS, 1)
         constexpr int kParts = WIDE / 32;  // 16 columns each
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + group * (WIDE / 2);
         const uint32_t acce = mapa(acce0, 0);
-        const int blocks = (red + BK - 1) / BK;
-        int buf = 0, boxes = 0;
-        uint32_t aphase = 0;
-        float x[AHEAD], w[AHEAD];  // scales of the next blocks: of this thread's row, of the group's features
-        const auto fetch = [&](const Tile& T, int j0) {
-            const int i = 128 * (int)rank + 32 * q + lane, f = T.f0 + group * BK;
-#pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                x[j] = w[j] = 0.0f;
-                if (j0 + j < blocks && f < ld) {
-                    w[j] = p.ws[weight_scale_at<kMode>(p, T.e, f, j0 + j)];
-                    if (i < T.rows) x[j] = p.xs[(j0 + j) * p.M + T.row + i];
-                }
-            }
-        };
-        Tile T = board.take(lane, abort_flag);
-        if (T.e >= 0) fetch(T, 0);
-        while (T.e >= 0) {
+        const uint32_t scales = smem_u32(smem) + SCALE_REGION + 512 * group + 4 * (32 * q + lane);
+        int buf = 0, slot = 0, boxes = 0;
+        uint32_t aphase = 0, sphase = 0;
+        for (;;) {
+            const Tile T = board.take(lane, abort_flag);
+            if (T.e < 0) break;
             uint64_t acc[kParts][8];  // sums of two columns each
 #pragma unroll
             for (int i = 0; i < kParts; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) acc[i][j] = 0;
-            for (int j0 = 0; j0 < blocks; j0 += AHEAD) {
-                float s[AHEAD];
+            // One block at a time: four in a row, unrolled, no longer fit the instruction cache (750 cycles each).
+#pragma unroll 1
+            for (int j = 0; j < blocks; ++j) {
+                // after an expired wait the others return at once; the tile is then not stored
+                mbar_wait(sfull0 + 8 * slot, sphase, abort_flag);
+                float factor;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(factor) : "r"(scales + slot * SLOT_BYTES) : "memory");
+                mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
+                __syncwarp();
+                fence_after();
+                const uint64_t k = f2splat(factor);
+                uint32_t v[2][16];
+                const uint32_t at = lanes + buf * WIDE;
+                tmem_ld16(at, v[0]);
 #pragma unroll
-                for (int j = 0; j < AHEAD; ++j) s[j] = x[j] * w[j];
-                fetch(T, j0 + AHEAD);
-#pragma unroll
-                for (int j = 0; j < AHEAD; ++j) {
-                    if (j0 + j >= blocks) break;
-                    // after an expired wait the others return at once; the tile is then not stored
-                    mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
-                    __syncwarp();
-                    fence_after();
-                    const uint64_t k = f2splat(s[j]);
-                    uint32_t v[2][16];
-                    const uint32_t at = lanes + buf * WIDE;
-                    tmem_ld16(at, v[0]);
-#pragma unroll
-                    for (int i = 0; i < kParts; ++i) {
-                        tmem_wait_ld();
-                        if (i + 1 < kParts) {
-                            tmem_ld16(at + 16 * (i + 1), v[(i + 1) & 1]);  // on its way while this part is added
-                        } else {
-                            fence_before();
-                            __syncwarp();
-                            if (lane == 0) {
-                                if (rank == 0) mbar_arrive(acce0 + 8 * buf);
-                                else arrive_remote_relaxed(acce + 8 * buf);
-                            }
+                for (int i = 0; i < kParts; ++i) {
+                    tmem_wait_ld();
+                    if (i + 1 < kParts) {
+                        tmem_ld16(at + 16 * (i + 1), v[(i + 1) & 1]);  // on its way while this part is added
+                    } else {
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (rank == 0) mbar_arrive(acce0 + 8 * buf);
+                            else arrive_remote_relaxed(acce + 8 * buf);
+                            mbar_arrive(sempty0 + 8 * slot);
                         }
-#pragma unroll
-                        for (int l = 0; l < 8; ++l)
-                            acc[i][l] = f2fma(f2pack(__uint_as_float(v[i & 1][2 * l]), __uint_as_float(v[i & 1][2 * l + 1])), k,
-                                              acc[i][l]);
                     }
-                    buf ^= 1;
-                    aphase ^= buf == 0;
+#pragma unroll
+                    for (int l = 0; l < 8; ++l)
+                        acc[i][l] = f2fma(f2pack(__uint_as_float(v[i & 1][2 * l]), __uint_as_float(v[i & 1][2 * l + 1])), k,
+                                          acc[i][l]);
                 }
+                if (++slot == SLOTS) { slot = 0; sphase ^= 1; }
+                buf ^= 1;
+                aphase ^= buf == 0;
             }
-            const Tile done = T;
-            T = board.take(lane, abort_flag);
-            if (T.e >= 0) fetch(T, 0);
             if (__any_sync(0xffffffffu, *abort_flag)) break;
-
-            const int f0 = done.f0 + group * BK, row = done.row + 128 * (int)rank + 32 * q;
+            const int f0 = T.f0 + group * BK, row = T.row + 128 * (int)rank + 32 * q;
             const int live = (int)min((int64_t)BK, ld - f0);  // features; may be negative: nothing to store
-            const int rows = min(32, done.rows - 128 * (int)rank - 32 * q);
+            const int rows = min(32, T.rows - 128 * (int)rank - 32 * q);
             if (live <= 0 || rows <= 0) continue;
             if (kMode == kFprop && p.bias) {
-                const __nv_bfloat16* bias = p.bias + (int64_t)done.e * p.N + f0;
+                const __nv_bfloat16* bias = p.bias + (int64_t)T.e * p.N + f0;
 #pragma unroll
                 for (int i = 0; i < kParts; ++i)
 #pragma unroll
