@@ -160,7 +160,9 @@ constexpr int ROWS = kFM * CG;   // token rows of a tile, on the MMA's M
 constexpr int WIDE = 256;        // features of a tile, on its N: two blocks of the weight
 constexpr int STAGES = 4;
 constexpr int SLOTS = 8;         // blocks whose scales are on chip
-constexpr int AHEAD = 2;         // and of how many the loads are in flight together
+constexpr int GROUP = 4;         // and that are handed over together; a tile begins at a new group
+constexpr int AHEAD = 2;         // blocks whose scales' loads are in flight together
+static_assert(SLOTS == 2 * GROUP && GROUP % AHEAD == 0, "the ring is two groups");
 constexpr int EPI_FIRST = 4, EPI_WARPS = 8;
 constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
 constexpr int CTL_REGS = 56, EPI_REGS = 224;
@@ -173,11 +175,11 @@ constexpr int EPI_REGION = STAGES * STAGE_BYTES;  // staging of the epilogue, tw
 constexpr int SLOT_BYTES = 2 * kFM * 4;           // a factor for each of this CTA's rows and each block of features
 constexpr int SCALE_REGION = EPI_REGION + 2 * EPI_WARPS * BOX_BYTES;
 constexpr int BAR_REGION = SCALE_REGION + SLOTS * SLOT_BYTES;
-constexpr int BOARD_REGION = BAR_REGION + 320;  // a tile, see Board
+constexpr int BOARD_REGION = BAR_REGION + 256;  // a tile, see Board
 constexpr int TABLE_REGION = BOARD_REGION + 64;
 __host__ __device__ constexpr int smem_bytes(int E) { return 1024 + TABLE_REGION + 8 * (E + 1); }
 static_assert(smem_bytes(MXQ_MAX_EXPERTS) <= 232448, "shared memory over the per-block limit");
-static_assert(BAR_REGION % 1024 == 0 && 8 * (2 * STAGES + 2 * SLOTS + 8) + 16 <= 320, "barrier region");
+static_assert(BAR_REGION % 1024 == 0 && 8 * (2 * STAGES + 4 + 8) + 16 <= 256, "barrier region");
 
 // out[row + i][f0 + c] for i < rows, c < n: rows are of expert e, whose slices have ROWS each
 struct Tile {
@@ -263,8 +265,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_REGION);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, accf0 = empty0 + 8 * STAGES, acce0 = accf0 + 16;
-    const uint32_t sfull0 = acce0 + 16, sempty0 = sfull0 + 8 * SLOTS;
-    const uint32_t bfull = sempty0 + 8 * SLOTS, bempty = bfull + 8, ready = bempty + 8, taken = ready + 8;
+    const uint32_t sfull0 = acce0 + 16, sempty0 = sfull0 + 16, bfull = sempty0 + 16, bempty = bfull + 8, ready = bempty + 8, taken = ready + 8;
     const uint32_t answer = (taken + 8 + 15) & ~15u;
     volatile int* abort_flag = &s_abort;
     if (threadIdx.x == 0) {
@@ -276,10 +277,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf0 + 8 * b, 1);
             mbar_init(acce0 + 8 * b, CG * EPI_WARPS);
-        }
-        for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(sfull0 + 8 * i, 1);
-            mbar_init(sempty0 + 8 * i, EPI_WARPS);
+            mbar_init(sfull0 + 8 * b, 1);
+            mbar_init(sempty0 + 8 * b, EPI_WARPS);
         }
         mbar_init(bfull, 1);
         mbar_init(bempty, 2 + EPI_WARPS + (rank == 0));  // loads, scales, the epilogue; the MMAs
@@ -374,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (warp == 2) {
             // -------------------------------------------------- scales
             const uint32_t at = smem_u32(smem) + SCALE_REGION + 4 * lane;
-            int slot = 0;
+            int group = 0;
             uint32_t phase = 0;
             for (;;) {
                 const Tile T = board.take(lane, abort_flag);
@@ -400,17 +399,23 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < AHEAD; ++j) {
                         if (j0 + j >= blocks) break;
-                        if (!__all_sync(0xffffffffu, mbar_wait(sempty0 + 8 * slot, phase ^ 1, abort_flag))) goto done_scales;
+                        const int in_group = (j0 + j) % GROUP;
+                        if (in_group == 0 && !__all_sync(0xffffffffu, mbar_wait(sempty0 + 8 * group, phase ^ 1, abort_flag)))
+                            goto done_scales;
 #pragma unroll
                         for (int g = 0; g < 2; ++g)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + slot * SLOT_BYTES + 512 * g + 128 * i),
+                                asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + (group * GROUP + in_group) * SLOT_BYTES +
+                                                                             512 * g + 128 * i),
                                              "f"(x[j][i] * w[j][g])
                                              : "memory");
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(sfull0 + 8 * slot);
-                        if (++slot == SLOTS) { slot = 0; phase ^= 1; }
+                        if (in_group == GROUP - 1 || j0 + j == blocks - 1) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(sfull0 + 8 * group);
+                            group ^= 1;
+                            phase ^= group == 0;
+                        }
                     }
                 }
             }
@@ -443,9 +448,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t stage = smem_u32(smem) + EPI_REGION + (warp - EPI_FIRST) * 2 * BOX_BYTES;
         constexpr int kParts = WIDE / 32;  // 16 columns each
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + group * (WIDE / 2);
-        const uint32_t acce = mapa(acce0, 0);
+        const uint32_t acce = mapa(acce0, 0);  // this CTA's own too, for rank 0
         const uint32_t scales = smem_u32(smem) + SCALE_REGION + 512 * group + 4 * (32 * q + lane);
-        int buf = 0, slot = 0, boxes = 0;
+        int buf = 0, group_at = 0, boxes = 0;
         uint32_t aphase = 0, sphase = 0;
         for (;;) {
             const Tile T = board.take(lane, abort_flag);
@@ -459,9 +464,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
             for (int j = 0; j < blocks; ++j) {
                 // after an expired wait the others return at once; the tile is then not stored
-                mbar_wait(sfull0 + 8 * slot, sphase, abort_flag);
+                const int in_group = j % GROUP;
+                const bool group_ends = in_group == GROUP - 1 || j == blocks - 1;
+                if (in_group == 0) mbar_wait(sfull0 + 8 * group_at, sphase, abort_flag);
                 float factor;
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(factor) : "r"(scales + slot * SLOT_BYTES) : "memory");
+                asm volatile("ld.shared.f32 %0, [%1];"
+                             : "=f"(factor)
+                             : "r"(scales + (group_at * GROUP + in_group) * SLOT_BYTES)
+                             : "memory");
                 mbar_wait(accf0 + 8 * buf, aphase, abort_flag);
                 __syncwarp();
                 fence_after();
@@ -477,18 +487,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                     } else {
                         fence_before();
                         __syncwarp();
-                        if (lane == 0) {
-                            if (rank == 0) mbar_arrive(acce0 + 8 * buf);
-                            else arrive_remote_relaxed(acce + 8 * buf);
-                            mbar_arrive(sempty0 + 8 * slot);
-                        }
+                        arrive_relaxed_if(lane == 0, acce + 8 * buf);
                     }
 #pragma unroll
                     for (int l = 0; l < 8; ++l)
                         acc[i][l] = f2fma(f2pack(__uint_as_float(v[i & 1][2 * l]), __uint_as_float(v[i & 1][2 * l + 1])), k,
                                           acc[i][l]);
                 }
-                if (++slot == SLOTS) { slot = 0; sphase ^= 1; }
+                if (group_ends) {
+                    if (lane == 0) mbar_arrive(sempty0 + 8 * group_at);  // behind the arrive above: all lanes have read
+                    group_at ^= 1;
+                    sphase ^= group_at == 0;
+                }
                 buf ^= 1;
                 aphase ^= buf == 0;
             }
