@@ -526,7 +526,7 @@ MXQ_API int mxq_fp8_gemm_dgrad(const void* dyq, const float* dy_scale, const voi
  * be residual or x, n_out may be x. */
 MXQ_API int mxq_norm_residual_fwd(const void* x, const void* residual, const void* post_weight, const void* pre_weight,
                                   const float* gate, int64_t M, int64_t F, double scale, double eps, int flags,
-                                  void* res_out, void* n_out, float* stats, mxq_stream_t stream);
+                                  void* res_out, void* n_out, float* stats, int32_t* d_status, mxq_stream_t stream);
 
 /* The gradients from dres (of r'; NULL: zero) and dn (of n; NULL exactly when
  * pre_weight is), at least one of them. x, res (the forward call's r'), stats,
@@ -541,7 +541,8 @@ MXQ_API int mxq_norm_residual_fwd(const void* x, const void* residual, const voi
 MXQ_API int mxq_norm_residual_bwd(const void* dres, const void* dn, const void* x, const void* res, const float* stats,
                                   const void* post_weight, const void* pre_weight, const float* gate, int64_t M,
                                   int64_t F, double scale, int flags, void* dx, void* dresidual, float* dpost_weight,
-                                  float* dpre_weight, float* dgate, void* ws, size_t ws_bytes, mxq_stream_t stream);
+                                  float* dpre_weight, float* dgate, int32_t* d_status, void* ws, size_t ws_bytes,
+                                  mxq_stream_t stream);
 
 /* ---- Dropout from a counter ----------------------------------------------
  *

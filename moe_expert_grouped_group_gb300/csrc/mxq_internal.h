@@ -146,6 +146,7 @@ struct NormFwd {
     int f32;
     void *res, *n;
     float* stats;  // (2, M)
+    int32_t* status;
 };
 struct NormBwd {
     const void *dres, *dn, *x, *res, *post, *pre;
@@ -156,6 +157,7 @@ struct NormBwd {
     void *dx, *dr;
     float *dpost, *dpre, *dgate;
     float* partials;  // workspace of norm_bwd_workspace(M, F) bytes
+    int32_t* status;
 };
 size_t norm_bwd_workspace(int64_t M, int64_t F);
 cudaError_t run_norm_fwd(const NormFwd& c, cudaStream_t s);

@@ -9,18 +9,23 @@
 //   dx   = a rstd(x) (D w_post - xh mean(D w_post xh))
 //   dgate = c sum_f D w_post xh       (without w_post: dx = a D, xh = x)
 //
-// Bound by HBM: every tensor is read or written once. A row belongs to a team
-// of W warps that keeps it in registers from the loads to the stores; each
-// thread always has the same columns, so that the weights' gradients grow in
-// its registers while the team walks its rows. A team's two sums over the row
-// are the only exchange. All arithmetic is fp32; r', n, dx, dr are rounded
-// once. n comes from r' before its rounding.
+// Bound by HBM: every tensor is read or written once. What it takes is loads in
+// flight all the time: a row's two sums, one after the other, each leave the SM
+// idle for a few hundred cycles. So rows come by bulk copies into a ring of
+// shared memory, two or three rows ahead of the one that is computed.
 //
-// The weights' gradients leave a block as one partial row each, which a second
-// kernel adds up, so that results are the same bits from run to run.
+// A row of more than kWarpWidth columns belongs to a cluster of 1 to 8 CTAs of
+// up to 2048 columns each, eight to a thread; the CTAs' sums meet in each
+// other's shared memory. Shorter rows belong to 8, 16 or 32 lanes of a warp,
+// which hold the next row in registers. A thread always has the same columns,
+// so that the weights' gradients grow in its registers while it walks its
+// rows; they leave a CTA as one partial row each, which a second kernel adds up
+// in a fixed order. All arithmetic is fp32; r', n, dx, dr are rounded once. n
+// comes from r' before its rounding.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "mxq_internal.h"
 #include "mxq_ragged.cuh"
@@ -31,6 +36,12 @@ namespace norm {
 
 using ragged::wait_for_stream;
 
+__device__ __forceinline__ uint4 ld_shared(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
 // Eight consecutive elements as they lie in memory.
 template <class T>
 struct Pack;
@@ -38,6 +49,7 @@ template <>
 struct Pack<__nv_bfloat16> {
     uint4 v;
     __device__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ void load_shared(uint32_t a) { v = ld_shared(a); }
     __device__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
     __device__ void values(float (&f)[8]) const {
         f[0] = bf16lo(v.x), f[1] = bf16hi(v.x), f[2] = bf16lo(v.y), f[3] = bf16hi(v.y);
@@ -55,6 +67,11 @@ struct Pack<float> {
         a = *reinterpret_cast<const float4*>(p);
         b = *reinterpret_cast<const float4*>(p + 4);
     }
+    __device__ void load_shared(uint32_t p) {
+        const uint4 u = ld_shared(p), w = ld_shared(p + 16);
+        a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+        b = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+    }
     __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ void values(float (&f)[8]) const {
         f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
@@ -65,29 +82,110 @@ struct Pack<float> {
     }
 };
 
-constexpr int kMaxWarps = 16, kMaxThreads = 32 * kMaxWarps;
+constexpr int kThreads = 256;      // most threads of a CTA
+constexpr int kWarpWidth = 256;    // widest row of a warp
+constexpr int kWidth = 8 * kThreads;  // and of a CTA
 
-// Where a thread stands: blocks of `teams` teams of W warps; with more than one team a team is one warp.
-struct Team {
-    int W, teams, team, tid;  // tid: thread of the team
-    __device__ explicit Team(int W_) : W(W_), teams(blockDim.x / (32 * W_)), team(threadIdx.x / (32 * W_)) {
-        tid = threadIdx.x - team * 32 * W;
+// Bulk copy into this CTA's shared memory, counted on its barrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"((uint64_t)src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// The rows of kTensors tensors on their way to this CTA: row n of the CTA's walk in stage n mod kStages.
+template <class T, int kTensors, int kStages>
+struct Rows {
+    const T* from[kTensors];  // this CTA's columns of row 0; null: not read
+    int64_t step, M, F;       // rows between two of the walk
+    uint32_t at, full, bytes, total;
+    int width;
+    __device__ uint32_t stage_bytes() const { return kTensors * width * (uint32_t)sizeof(T); }
+    // by one thread
+    __device__ void load(int64_t n, int64_t m) const {
+        if (m >= M) return;
+        const int s = (int)(n % kStages);
+        mbar_expect_tx(full + 8 * s, total);
+#pragma unroll
+        for (int i = 0; i < kTensors; ++i)
+            if (from[i])
+                bulk_load(at + s * stage_bytes() + i * width * (uint32_t)sizeof(T), from[i] + m * F, bytes, full + 8 * s);
     }
-    // The sum of v over the team, the same bits in every thread. Called by all threads of a block alike; buf
-    // alternates between two calls.
-    __device__ float sum(float v, float (&buf)[kMaxWarps]) const {
+    __device__ void get(int64_t n, int i, int f, Pack<T>& p) const {
+        const uint32_t a = at + (uint32_t)(n % kStages) * stage_bytes() + (i * width + f) * (uint32_t)sizeof(T);
+        p.load_shared(a);
+    }
+    __device__ bool wait(int64_t n, volatile int* abort_flag) const {
+        return mbar_wait(full + 8 * (int)(n % kStages), (uint32_t)(n / kStages) & 1, abort_flag);
+    }
+    // After an expired wait, which lets the others return at once: the last rows are waited for again, so that no copy
+    // is in flight when the CTA ends. n: rows of the walk.
+    __device__ void drain(int64_t n) const {
+        volatile int unused = 0;
+        for (int64_t k = n > kStages ? n - kStages : 0; k < n; ++k)
+            mbar_wait(full + 8 * (int)(k % kStages), (uint32_t)(k / kStages) & 1, &unused);
+    }
+};
+
+// Sums over a row, which kC CTAs of W warps share: every warp sends its part to all CTAs, where all threads add the
+// parts in the same order. Two buffers in turn: a warp sends the part after next only when it has the sum after this
+// one, so when all warps have read this one.
+template <int kC>
+struct RowSum {
+    uint32_t at, bar;  // [2][kC * 8] floats; two barriers (kC > 1)
+    int W, rank;
+    uint32_t turn = 0;
+    __device__ RowSum(uint32_t at_, uint32_t bar_, int W_, int rank_) : at(at_), bar(bar_), W(W_), rank(rank_) {}
+    __device__ float sum(float v, volatile int* abort_flag) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const uint32_t side = turn & 1, phase = turn >> 1 & 1, to = at + (side * kC * 8 + rank * W + warp) * 4;
+        ++turn;
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (W == 1) return v;
-        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-        __syncthreads();
-        const int k = threadIdx.x & (kMaxWarps - 1);  // both halves of a warp add the same
-        float s = k < W ? buf[k] : 0.0f;
+        if constexpr (kC == 1) {
+            if (lane == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
+            __syncthreads();
+        } else {
+            if (threadIdx.x == 0) mbar_expect_tx(bar + 8 * side, 4 * kC * W);
+            if (lane < kC)
+                asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                                 ragged::mapa(to, lane)),
+                             "r"(__float_as_uint(v)), "r"(ragged::mapa(bar + 8 * side, lane))
+                             : "memory");
+            ragged::mbar_wait_cluster(bar + 8 * side, phase, abort_flag);
+            __syncwarp();
+        }
+        float s = 0.0f;
 #pragma unroll
-        for (int o = kMaxWarps / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        for (int k = 0; k < (kC * 8 + 31) / 32; ++k)
+            if (lane + 32 * k < kC * W) {
+                float x;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at + (side * kC * 8 + lane + 32 * k) * 4) : "memory");
+                s += x;
+            }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         return s;
     }
 };
+
+// Dynamic shared memory: the ring, then the sums and barriers.
+constexpr int kSumBytes = 2 * 8 * 8 * 4, kTailBytes = kSumBytes + 64;
+constexpr int kMostSmem = 2 * 4 * kWidth * 4 + kTailBytes;  // gradients of fp32: two stages of four tensors
+static_assert(3 * 4 * kWidth * 2 + kTailBytes <= kMostSmem && kMostSmem <= 232448, "shared memory");
+constexpr int kBwdThreads = 640;  // threads of an SM's CTAs in the backward kernel, by their registers
+
+// What a thread does with its eight columns of a row, in the order of the formulas. Weights: 1 without one.
+template <class T>
+__device__ __forceinline__ void weights8(const T* w, int f, bool live, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 1.0f;
+    if (w && live) {
+        Pack<T> k;
+        k.load(w + f);
+        k.values(v);
+    }
+}
 
 template <class T>
 struct Fwd {
@@ -98,81 +196,144 @@ struct Fwd {
     float scale, eps;
     T *res, *n;
     float* stats;
+    int32_t* status;
 };
 
-template <class T, int NV>
-__global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(Fwd<T> p, int W) {
-    __shared__ float buf[2][kMaxWarps];
-    const Team t(W);
-    const int step = 256 * W, f0 = 8 * t.tid;  // a thread's columns: f0 + i * step + 0 .. 7
+// f: the thread's first column; sum(v) adds over the row; `mine`: this thread writes the row's statistics.
+template <class T, class S>
+__device__ __forceinline__ void fwd_row(const Fwd<T>& p, int64_t m, int f, bool live, bool mine, float gate, const Pack<T>& xp,
+                                        const Pack<T>& rp, const float (&w_post)[8], const float (&w_pre)[8], float inv,
+                                        S sum) {
+    float x[8], v[8], rstd = 1.0f, s = 0.0f;
+    xp.values(x);
+    rp.values(v);
+    if (p.post) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
+        rstd = 1.0f / sqrtf(fmaf(sum(s), inv, p.eps));
+        s = 0.0f;
+    }
+    if (p.stats && mine) p.stats[m] = rstd;
+    if (live) {
+        const float a = p.scale * gate;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = fmaf(a, x[j] * rstd * w_post[j], v[j]);
+            s = fmaf(v[j], v[j], s);
+        }
+        if (p.res) Pack<T>::store(p.res + m * p.F + f, v);
+    }
+    rstd = 1.0f;
+    if (p.pre) {
+        rstd = 1.0f / sqrtf(fmaf(sum(s), inv, p.eps));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= rstd * w_pre[j];
+        if (live) Pack<T>::store(p.n + m * p.F + f, v);
+    }
+    if (p.stats && mine) p.stats[p.M + m] = rstd;
+}
+
+// Rows of up to kWarpWidth columns: kLanes lanes each, with the next row in registers.
+template <class T, int kLanes>
+__global__ void __launch_bounds__(kThreads) norm_fwd_lanes_kernel(Fwd<T> p) {
+    const int lane = threadIdx.x % kLanes, f = 8 * lane;
+    const bool live = f < p.F;
     const float inv = 1.0f / (float)p.F;
     wait_for_stream();
-    for (int64_t m = (int64_t)blockIdx.x * t.teams + t.team; m < p.M; m += (int64_t)gridDim.x * t.teams) {
-        const int64_t at = m * p.F;
-        Pack<T> x[NV], r[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            x[i].zero();
-            r[i].zero();
-            if (f0 + i * step < p.F) {
-                x[i].load(p.x + at + f0 + i * step);
-                if (p.residual) r[i].load(p.residual + at + f0 + i * step);
-            }
+    float w_post[8], w_pre[8];
+    weights8(p.post, f, live, w_post);
+    weights8(p.pre, f, live, w_pre);
+    const int64_t step = (int64_t)gridDim.x * (kThreads / kLanes);
+    int64_t m = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+    const auto fetch = [&](int64_t row, Pack<T>& x, Pack<T>& r, float& gate) {
+        x.zero(), r.zero();
+        gate = 1.0f;
+        if (row >= p.M) return;
+        if (live) {
+            x.load(p.x + row * p.F + f);
+            if (p.residual) r.load(p.residual + row * p.F + f);
         }
-        float a = p.scale, f[8], rstd = 1.0f;
-        if (p.gate) a *= p.gate[m];
-        if (p.post) {
-            float s = 0.0f;
+        if (p.gate) gate = p.gate[row];
+    };
+    Pack<T> x, r, nx, nr;
+    float gate, ngate;
+    fetch(m, x, r, gate);
+    // all lanes of a warp take as many turns: they share its shuffles
+    for (int64_t first = m - threadIdx.x % 32 / kLanes; first < p.M; first += step, m += step) {
+        fetch(m + step, nx, nr, ngate);
+        fwd_row(p, m, f, live && m < p.M, lane == 0 && m < p.M, gate, x, r, w_post, w_pre, inv, [](float v) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                x[i].values(f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s = fmaf(f[j], f[j], s);
-            }
-            rstd = 1.0f / sqrtf(fmaf(t.sum(s, buf[0]), inv, p.eps));
-        }
-        if (p.stats && t.tid == 0) p.stats[m] = rstd;
-        float v[NV][8], s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float w[8];
-            x[i].values(f);
-            r[i].values(v[i]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = 1.0f;
-            if (f0 + i * step >= p.F) continue;
-            if (p.post) {
-                Pack<T> k;
-                k.load(p.post + f0 + i * step);
-                k.values(w);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[i][j] = fmaf(a, f[j] * rstd * w[j], v[i][j]);
-                s = fmaf(v[i][j], v[i][j], s);
-            }
-            if (p.res) Pack<T>::store(p.res + at + f0 + i * step, v[i]);
-        }
-        if (p.pre) {
-            rstd = 1.0f / sqrtf(fmaf(t.sum(s, buf[1]), inv, p.eps));
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (f0 + i * step < p.F) {
-                    Pack<T> k;
-                    float w[8];
-                    k.load(p.pre + f0 + i * step);
-                    k.values(w);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = v[i][j] * rstd * w[j];
-                    Pack<T>::store(p.n + at + f0 + i * step, f);
-                }
-        } else {
-            rstd = 1.0f;
-            if (W > 1) __syncthreads();  // buf[0] is read before the next row writes it
-        }
-        if (p.stats && t.tid == 0) p.stats[p.M + m] = rstd;
-        if (!p.post && W > 1) __syncthreads();  // and buf[1]
+            for (int o = kLanes / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            return v;
+        });
+        x = nx, r = nr, gate = ngate;
     }
+}
+
+template <class T>
+constexpr int kStagesOf = sizeof(T) == 2 ? 3 : 2;
+
+template <class T, int kC>
+__global__ void __launch_bounds__(kThreads) norm_fwd_kernel(Fwd<T> p, int width) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int s_abort;
+    constexpr int kS = kStagesOf<T>;
+    const int rank = kC > 1 ? (int)ragged::cta_rank() : 0, W = blockDim.x / 32;
+    const int f0 = rank * width, mine = min(width, p.F - f0), f = 8 * (int)threadIdx.x;
+    const bool live = f < mine;
+    const float inv = 1.0f / (float)p.F;
+    const uint32_t tail = smem_u32(smem) + kS * 2 * width * (uint32_t)sizeof(T), bars = tail + kSumBytes;
+    volatile int* abort_flag = &s_abort;
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int i = 0; i < 2 + kS; ++i) mbar_init(bars + 8 * i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    wait_for_stream();
+    __syncthreads();
+    if (kC > 1) ragged::cluster_sync();
+    const int64_t first = blockIdx.x / kC, step = gridDim.x / kC;
+    const uint32_t bytes = mine * (uint32_t)sizeof(T);
+    const Rows<T, 2, kS> rows{{p.x + f0, p.residual ? p.residual + f0 : nullptr}, step, p.M, p.F, smem_u32(smem), bars + 16,
+                              bytes, bytes * (1 + (p.residual != nullptr)), width};
+    if (threadIdx.x == 0)
+        for (int k = 0; k < kS; ++k) rows.load(k, first + k * step);
+    RowSum<kC> sums(tail, bars, W, rank);
+    float w_post[8], w_pre[8];
+    weights8(p.post, f0 + f, live, w_post);
+    weights8(p.pre, f0 + f, live, w_pre);
+    float next_gate = p.gate && first < p.M ? p.gate[first] : 1.0f;
+    int64_t n = 0;
+    for (int64_t m = first; m < p.M; m += step, ++n) {
+        const float gate = next_gate;
+        if (p.gate && m + step < p.M) next_gate = p.gate[m + step];
+        rows.wait(n, abort_flag);
+        __syncwarp();
+        Pack<T> x, r;
+        x.zero(), r.zero();
+        if (live) {
+            rows.get(n, 0, f, x);
+            if (p.residual) rows.get(n, 1, f, r);
+        }
+        // at a row's first exchange every thread has read the row before
+        bool refill = threadIdx.x == 0 && n > 0;
+        fwd_row(p, m, f0 + f, live, threadIdx.x == 0 && rank == 0, gate, x, r, w_post, w_pre, inv, [&](float v) {
+            v = sums.sum(v, abort_flag);
+            if (refill) rows.load(n - 1 + kS, m + (kS - 1) * step);
+            refill = false;
+            return v;
+        });
+        if (!p.post && !p.pre) {
+            __syncthreads();
+            if (refill) rows.load(n - 1 + kS, m + (kS - 1) * step);
+        }
+    }
+    __syncthreads();
+    if (s_abort && threadIdx.x == 0) {
+        rows.drain(n);
+        if (p.status) atomicOr(p.status, MXQ_STATUS_WAIT_TIMEOUT);
+    }
+    if (kC > 1) ragged::cluster_sync();  // nothing is on its way to a CTA that has ended
 }
 
 template <class T>
@@ -183,262 +344,351 @@ struct Bwd {
     int F;
     float scale;
     T *dx, *dr;
-    float *dgate, *partials;  // partials: (2, blocks, F): of w_post, of w_pre
+    float *dgate, *partials;  // partials: (2, parts, F): of w_post, of w_pre
+    int32_t* status;
 };
 
-// kHold: the row stays in registers from its one read. Otherwise (rows of more than 16 KB a tensor) each of the three
-// passes over the row reads what it needs, the second and third time from L1 or L2. kSums: the weights' gradients
-// grow in shared memory instead of registers.
-template <class T, int NV, bool kHold, bool kSums>
-__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(Bwd<T> p, int W) {
-    __shared__ float buf[2][kMaxWarps];
-    extern __shared__ __align__(16) float sums[];  // kSums: (2, F); teams > 1: (teams, F)
-    const Team t(W);
-    const int step = 256 * W, f0 = 8 * t.tid;
-    const float inv = 1.0f / (float)p.F;
-    constexpr int kRegs = kSums ? 1 : NV, kHeld = kHold ? NV : 1;
-    float d_post[kRegs][8], d_pre[kRegs][8];
-#pragma unroll
-    for (int i = 0; i < kRegs; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d_post[i][j] = d_pre[i][j] = 0.0f;
-    if (kSums)
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (f0 + i * step < p.F) {
-                Pack<float>::store(sums + f0 + i * step, d_post[0]);
-                Pack<float>::store(sums + p.F + f0 + i * step, d_pre[0]);
-            }
-    wait_for_stream();
-    const bool dots = p.post || p.gate;
-    // the values of a tensor's columns i, from registers or from memory
-    const auto values = [&](const Pack<T>(&held)[kHeld], const T* from, int i, float (&f)[8]) {
-        Pack<T> k = held[kHold ? i : 0];
-        if (!kHold) {
-            k.zero();
-            if (from) k.load(from + f0 + i * step);
-        }
-        k.values(f);
-    };
-    const auto weights = [&](const T* w, int i, float (&f)[8]) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = 1.0f;
-        if (w) {
-            Pack<T> k;
-            k.load(w + f0 + i * step);
-            k.values(f);
-        }
-    };
-    const auto add = [&](float (&d)[kRegs][8], int row, int i, const float (&v)[8]) {
-        if constexpr (kSums) {
-            Pack<float> k;
-            float f[8];
-            k.load(sums + row * p.F + f0 + i * step);
-            k.values(f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] += v[j];
-            Pack<float>::store(sums + row * p.F + f0 + i * step, f);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) d[i][j] += v[j];
-        }
-    };
-    for (int64_t m = (int64_t)blockIdx.x * t.teams + t.team; m < p.M; m += (int64_t)gridDim.x * t.teams) {
-        const int64_t at = m * p.F;
-        const T *x_row = dots ? p.x + at : nullptr, *r_row = p.pre ? p.res + at : nullptr;
-        const T *dn_row = p.pre ? p.dn + at : nullptr, *dr_row = p.dres ? p.dres + at : nullptr;
-        Pack<T> x[kHeld], r[kHeld], dn[kHeld], dr[kHeld];
-        if (kHold)
-#pragma unroll
-            for (int i = 0; i < kHeld; ++i) {
-                x[i].zero(), r[i].zero(), dn[i].zero(), dr[i].zero();
-                if (f0 + i * step >= p.F) continue;
-                if (r_row) r[i].load(r_row + f0 + i * step);
-                if (dn_row) dn[i].load(dn_row + f0 + i * step);
-                if (dr_row) dr[i].load(dr_row + f0 + i * step);
-                if (x_row) x[i].load(x_row + f0 + i * step);
-            }
-        const float rstd1 = p.post ? p.stats[m] : 1.0f, rstd2 = p.pre ? p.stats[p.M + m] : 0.0f;
-        const float a = p.gate ? p.scale * p.gate[m] : p.scale;
-        float mean = 0.0f, dot = 0.0f, D[NV][8];
-        if (p.pre) {
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (f0 + i * step >= p.F) continue;
-                float rh[8], g[8], w[8];
-                values(r, r_row, i, rh);
-                values(dn, dn_row, i, g);
-                weights(p.pre, i, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    rh[j] *= g[j] * rstd2;
-                    s = fmaf(rh[j], w[j], s);
-                }
-                add(d_pre, 1, i, rh);
-            }
-            mean = t.sum(s, buf[0]) * inv;
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (f0 + i * step >= p.F) continue;
-            float rh[8], g[8], w[8], xh[8];
-            values(r, r_row, i, rh);
-            values(dn, dn_row, i, g);
-            values(dr, dr_row, i, D[i]);
-            weights(p.pre, i, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) D[i][j] = fmaf(rstd2, fmaf(-rh[j] * rstd2, mean, g[j] * w[j]), D[i][j]);
-            if (p.dr) Pack<T>::store(p.dr + at + f0 + i * step, D[i]);
-            if (!dots) continue;
-            values(x, x_row, i, xh);
-            weights(p.post, i, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                xh[j] *= rstd1 * D[i][j];
-                dot = fmaf(xh[j], w[j], dot);
-                xh[j] *= a;
-            }
-            if (p.post) add(d_post, 0, i, xh);
-        }
-        if (dots) {
-            dot = t.sum(dot, buf[1]);
-            if (p.dgate && t.tid == 0) p.dgate[m] = p.scale * dot;
-        } else if (W > 1) {
-            __syncthreads();  // buf[0] is read before the next row writes it
-        }
-        if (!p.pre && W > 1) __syncthreads();  // and buf[1]
-        if (!p.dx) continue;
-        const float c = p.post ? dot * inv * rstd1 : 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (f0 + i * step >= p.F) continue;
-            float xv[8], w[8];
-            values(x, x_row, i, xv);
-            weights(p.post, i, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) xv[j] = a * rstd1 * fmaf(-xv[j], c, D[i][j] * w[j]);
-            Pack<T>::store(p.dx + at + f0 + i * step, xv);
-        }
+struct RowScalars {
+    float rstd1, rstd2, gate;
+    template <class T>
+    __device__ void load(const Bwd<T>& p, int64_t m) {
+        rstd1 = p.post ? p.stats[m] : 1.0f;
+        rstd2 = p.pre ? p.stats[p.M + m] : 0.0f;
+        gate = p.gate ? p.gate[m] : 1.0f;
     }
-    // this block's part of the weights' gradients
-    const auto leave = [&](const float (&d)[kRegs][8], int row, float* out) {
-        if (t.teams > 1) {
-            __syncthreads();
+};
+
+template <class T, class S>
+__device__ __forceinline__ void bwd_row(const Bwd<T>& p, int64_t m, int f, bool live, bool mine, const RowScalars& c,
+                                        const Pack<T>& rp, const Pack<T>& np, const Pack<T>& dp, const Pack<T>& xp,
+                                        const float (&w_post)[8], const float (&w_pre)[8], float (&d_post)[8],
+                                        float (&d_pre)[8], float inv, S sum) {
+    float rh[8], g[8], D[8], xh[8];
+    const float a = p.scale * c.gate;
+    rp.values(rh);
+    np.values(g);
+    dp.values(D);
+    if (p.pre) {
+        float s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kRegs; ++i)
-                if (f0 + i * step < p.F) Pack<float>::store(sums + t.team * p.F + f0 + i * step, d[i]);
-            __syncthreads();
-            for (int f = threadIdx.x; f < p.F; f += blockDim.x) {
-                float s = 0.0f;
-                for (int k = 0; k < t.teams; ++k) s += sums[k * p.F + f];
-                out[f] = s;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (f0 + i * step >= p.F) continue;
-                float f[8];
-                if constexpr (kSums) {
-                    Pack<float> k;
-                    k.load(sums + row * p.F + f0 + i * step);
-                    k.values(f);
-                    Pack<float>::store(out + f0 + i * step, f);
-                } else {
-                    Pack<float>::store(out + f0 + i * step, d[i]);
-                }
-            }
+        for (int j = 0; j < 8; ++j) {
+            rh[j] *= c.rstd2;
+            d_pre[j] = fmaf(g[j], rh[j], d_pre[j]);
+            g[j] *= w_pre[j];
+            s = fmaf(g[j], rh[j], s);
         }
-    };
-    if (p.post) leave(d_post, 0, p.partials + (int64_t)blockIdx.x * p.F);
-    if (p.pre) leave(d_pre, 1, p.partials + ((int64_t)gridDim.x + blockIdx.x) * p.F);
+        const float mean = sum(s) * inv;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) D[j] = fmaf(c.rstd2, fmaf(-rh[j], mean, g[j]), D[j]);
+    }
+    if (p.dr && live) Pack<T>::store(p.dr + m * p.F + f, D);
+    float dot = 0.0f;
+    if (p.post || p.gate) {
+        xp.values(xh);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            xh[j] *= c.rstd1;
+            const float t = D[j] * xh[j];
+            d_post[j] = fmaf(a, t, d_post[j]);
+            dot = fmaf(t, w_post[j], dot);
+        }
+        dot = sum(dot);
+        if (p.dgate && mine) p.dgate[m] = p.scale * dot;
+    }
+    if (!p.dx || !live) return;
+    if (p.post) {
+        const float mean = dot * inv, k = a * c.rstd1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) D[j] = k * fmaf(-xh[j], mean, D[j] * w_post[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) D[j] *= a;
+    }
+    Pack<T>::store(p.dx + m * p.F + f, D);
 }
 
-// out[f] = the sum of a weight's partial rows: 32 columns a block, row k by warp k mod 8.
-__global__ void __launch_bounds__(256) norm_weights_kernel(const float* partials, int blocks, int F, float* d_post,
-                                                           float* d_pre) {
-    __shared__ float s_sum[8][32];
+template <class T, int kLanes>
+__global__ void __launch_bounds__(kThreads) norm_bwd_lanes_kernel(Bwd<T> p) {
+    constexpr int kTeams = kThreads / kLanes;
+    __shared__ __align__(16) float s_sum[kThreads / 32][kWarpWidth];
+    const int lane = threadIdx.x % kLanes, f = 8 * lane;
+    const bool live = f < p.F, dots = p.post || p.gate;
+    const float inv = 1.0f / (float)p.F;
+    wait_for_stream();
+    float w_post[8], w_pre[8], d_post[8], d_pre[8];
+    weights8(p.post, f, live, w_post);
+    weights8(p.pre, f, live, w_pre);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d_post[j] = d_pre[j] = 0.0f;
+    const int64_t step = (int64_t)gridDim.x * kTeams;
+    int64_t m = (int64_t)blockIdx.x * kTeams + threadIdx.x / kLanes;
+    const auto fetch = [&](int64_t row, Pack<T>(&v)[4], RowScalars& c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i].zero();
+        c.rstd1 = c.rstd2 = c.gate = 0.0f;
+        if (row >= p.M) return;
+        const int64_t at = row * p.F + f;
+        if (live) {
+            if (p.pre) v[0].load(p.res + at), v[1].load(p.dn + at);
+            if (p.dres) v[2].load(p.dres + at);
+            if (dots) v[3].load(p.x + at);
+        }
+        c.load(p, row);
+    };
+    Pack<T> v[4], nv[4];
+    RowScalars c, nc;
+    fetch(m, v, c);
+    for (int64_t first = m - threadIdx.x % 32 / kLanes; first < p.M; first += step, m += step) {
+        fetch(m + step, nv, nc);
+        // rows beyond the last are zeros and have no part in the sums
+        bwd_row(p, m, f, live && m < p.M, lane == 0 && m < p.M, c, v[0], v[1], v[2], v[3], w_post, w_pre, d_post, d_pre, inv,
+                [](float s) {
+#pragma unroll
+                    for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                    return s;
+                });
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = nv[i];
+        c = nc;
+    }
+    // the block's parts of the weights' gradients: over a warp's teams, then over the warps
+    const auto leave = [&](float (&d)[8], float* out) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int o = kLanes; o < 32; o <<= 1) d[j] += __shfl_xor_sync(0xffffffffu, d[j], o);
+        __syncthreads();
+        if (threadIdx.x % 32 < kLanes) Pack<float>::store(&s_sum[threadIdx.x / 32][f], d);
+        __syncthreads();
+        if ((int)threadIdx.x < p.F) {
+            float s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kThreads / 32; ++k) s += s_sum[k][threadIdx.x];
+            out[threadIdx.x] = s;
+        }
+    };
+    if (p.post) leave(d_post, p.partials + (int64_t)blockIdx.x * p.F);
+    if (p.pre) leave(d_pre, p.partials + ((int64_t)gridDim.x + blockIdx.x) * p.F);
+}
+
+template <class T, int kC>
+__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(Bwd<T> p, int width) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int s_abort;
+    constexpr int kS = kStagesOf<T>;
+    const int rank = kC > 1 ? (int)ragged::cta_rank() : 0, W = blockDim.x / 32;
+    const int f0 = rank * width, mine = min(width, p.F - f0), f = 8 * (int)threadIdx.x;
+    const bool live = f < mine, dots = p.post || p.gate;
+    const float inv = 1.0f / (float)p.F;
+    const uint32_t tail = smem_u32(smem) + kS * 4 * width * (uint32_t)sizeof(T), bars = tail + kSumBytes;
+    volatile int* abort_flag = &s_abort;
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int i = 0; i < 2 + kS; ++i) mbar_init(bars + 8 * i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    wait_for_stream();
+    __syncthreads();
+    if (kC > 1) ragged::cluster_sync();
+    const int64_t first = blockIdx.x / kC, step = gridDim.x / kC;
+    const uint32_t bytes = mine * (uint32_t)sizeof(T);
+    const Rows<T, 4, kS> rows{{p.pre ? p.res + f0 : nullptr, p.pre ? p.dn + f0 : nullptr, p.dres ? p.dres + f0 : nullptr,
+                               dots ? p.x + f0 : nullptr},
+                              step, p.M, p.F, smem_u32(smem), bars + 16, bytes,
+                              bytes * (2 * (p.pre != nullptr) + (p.dres != nullptr) + dots), width};
+    if (threadIdx.x == 0)
+        for (int k = 0; k < kS; ++k) rows.load(k, first + k * step);
+    RowSum<kC> sums(tail, bars, W, rank);
+    float w_post[8], w_pre[8], d_post[8], d_pre[8];
+    weights8(p.post, f0 + f, live, w_post);
+    weights8(p.pre, f0 + f, live, w_pre);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d_post[j] = d_pre[j] = 0.0f;
+    RowScalars next;
+    next.rstd1 = next.rstd2 = next.gate = 0.0f;
+    if (first < p.M) next.load(p, first);
+    int64_t n = 0;
+    for (int64_t m = first; m < p.M; m += step, ++n) {
+        const RowScalars c = next;
+        if (m + step < p.M) next.load(p, m + step);
+        rows.wait(n, abort_flag);
+        __syncwarp();
+        Pack<T> v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i].zero();
+            if (live && rows.from[i]) rows.get(n, i, f, v[i]);
+        }
+        // at a row's first exchange every thread has read the row before
+        bool refill = threadIdx.x == 0 && n > 0;
+        bwd_row(p, m, f0 + f, live, threadIdx.x == 0 && rank == 0, c, v[0], v[1], v[2], v[3], w_post, w_pre, d_post, d_pre,
+                inv, [&](float s) {
+                    s = sums.sum(s, abort_flag);
+                    if (refill) rows.load(n - 1 + kS, m + (kS - 1) * step);
+                    refill = false;
+                    return s;
+                });
+        if (!p.pre && !dots) {
+            __syncthreads();
+            if (refill) rows.load(n - 1 + kS, m + (kS - 1) * step);
+        }
+    }
+    __syncthreads();
+    if (s_abort && threadIdx.x == 0) {
+        rows.drain(n);
+        if (p.status) atomicOr(p.status, MXQ_STATUS_WAIT_TIMEOUT);
+    }
+    const int64_t part = blockIdx.x / kC, parts = gridDim.x / kC;
+    if (p.post && live) Pack<float>::store(p.partials + part * p.F + f0 + f, d_post);
+    if (p.pre && live) Pack<float>::store(p.partials + (parts + part) * p.F + f0 + f, d_pre);
+    if (kC > 1) ragged::cluster_sync();  // nothing is on its way to a CTA that has ended
+}
+
+// out[f] = the sum of a weight's partial rows: 32 columns a block, row k by warp k mod 32.
+__global__ void __launch_bounds__(1024) norm_weights_kernel(const float* partials, int parts, int F, float* d_post,
+                                                            float* d_pre) {
+    __shared__ float s_sum[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, f = blockIdx.x * 32 + lane;
     float* out = blockIdx.y ? d_pre : d_post;
     wait_for_stream();
     if (!out) return;
     float s = 0.0f;
-    if (f < F)
-        for (int k = warp; k < blocks; k += 8) s += partials[((int64_t)blockIdx.y * blocks + k) * F + f];
-    s_sum[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && f < F) {
-        for (int k = 1; k < 8; ++k) s += s_sum[k][lane];
-        out[f] = s;
+    if (f < F) {
+        const float* from = partials + (int64_t)blockIdx.y * parts * F + f;
+#pragma unroll 4
+        for (int k = warp; k < parts; k += 32) s += from[(int64_t)k * F];
     }
+    s_sum[lane][warp] = s;
+    __syncthreads();
+    s = s_sum[warp][lane];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0 && blockIdx.x * 32 + warp < F) out[blockIdx.x * 32 + warp] = s;
 }
 
 // ------------------------------------------------------------------ host side
-// A team of W warps with nv vectors of eight columns a thread; teams > 1 share a block when a team is one warp.
+// CTAs that share a row of F columns (0: lanes of a warp do), the columns and threads of each.
 struct Shape {
-    int nv, W, teams;
+    int ctas, width, threads;
 };
 static Shape shape_of(int64_t F) {
+    if (F <= kWarpWidth) return {0, (int)F, kThreads};
     Shape s;
-    s.nv = F > 8192 ? 4 : F > 4096 ? 2 : 1;
-    s.W = (int)((F + 256 * s.nv - 1) / (256 * s.nv));
-    s.teams = s.W == 1 ? 8 : 1;
+    s.ctas = 1;
+    while (s.ctas * kWidth < F) s.ctas *= 2;
+    s.width = (int)((F / 8 + s.ctas - 1) / s.ctas * 8);
+    s.threads = (s.width + 255) / 256 * 32;
     return s;
+}
+
+// As many clusters as the device holds, no more than `clusters`, which is set to their number. The kernel's attribute
+// and its co-residency are set and asked for once per device and number of threads.
+template <auto kKernel, class P>
+static cudaError_t launch_rows(const P& p, const Shape& s, int64_t& clusters, int smem, cudaStream_t st) {
+    static std::atomic<int> cache[64][kThreads / 32 + 1];
+    int dev = 0, most = 0;
+    cudaGetDevice(&dev);
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = s.ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(s.threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (dev >= 64 || (most = cache[dev][s.threads / 32].load(std::memory_order_acquire)) == 0) {
+        const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
+        if (e != cudaSuccess) return e;
+        cfg.gridDim = dim3(s.ctas * ragged::sm_count());
+        // the widest rows of so many threads
+        cfg.dynamicSmemBytes = (smem - kTailBytes) / s.width * (8 * s.threads) + kTailBytes;
+        if (cudaOccupancyMaxActiveClusters(&most, (void*)kKernel, &cfg) != cudaSuccess || most <= 0) {
+            cudaGetLastError();
+            most = std::max(1, ragged::sm_count() / s.ctas);
+        }
+        if (dev < 64) cache[dev][s.threads / 32].store(most, std::memory_order_release);
+        cfg.dynamicSmemBytes = smem;
+    }
+    clusters = std::min<int64_t>(clusters, most);
+    cfg.gridDim = dim3((unsigned)(clusters * s.ctas));
+    cfg.stream = st;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kKernel, p, s.width);
+}
+
+template <class T, int kC>
+static cudaError_t fwd_rows(const Fwd<T>& p, const Shape& s, cudaStream_t st) {
+    int64_t clusters = p.M;
+    return launch_rows<norm_fwd_kernel<T, kC>>(p, s, clusters, kStagesOf<T> * 2 * s.width * (int)sizeof(T) + kTailBytes, st);
 }
 
 template <class T>
 static cudaError_t fwd(const NormFwd& c, cudaStream_t st) {
     const Fwd<T> p{(const T*)c.x, (const T*)c.residual, (const T*)c.post, (const T*)c.pre, c.gate, c.M, (int)c.F,
-                   c.scale, c.eps, (T*)c.res, (T*)c.n, c.stats};
+                   c.scale, c.eps, (T*)c.res, (T*)c.n, c.stats, c.status};
     const Shape s = shape_of(c.F);
-    const unsigned threads = 32 * s.W * s.teams;
-    const int64_t most = (int64_t)ragged::sm_count() * (2048 / threads);
-    const unsigned grid = (unsigned)std::min<int64_t>((c.M + s.teams - 1) / s.teams, most);
-    switch (s.nv) {
-        case 1: return ragged::launch(norm_fwd_kernel<T, 1>, grid, threads, st, 0, p, s.W);
-        case 2: return ragged::launch(norm_fwd_kernel<T, 2>, grid, threads, st, 0, p, s.W);
-        default: return ragged::launch(norm_fwd_kernel<T, 4>, grid, threads, st, 0, p, s.W);
+    if (!s.ctas) {
+        const int lanes = c.F <= 64 ? 8 : c.F <= 128 ? 16 : 32, teams = kThreads / lanes;
+        const unsigned grid = (unsigned)std::min<int64_t>((c.M + teams - 1) / teams, (int64_t)ragged::sm_count() * 4);
+        return lanes == 8    ? ragged::launch(norm_fwd_lanes_kernel<T, 8>, grid, kThreads, st, 0, p)
+               : lanes == 16 ? ragged::launch(norm_fwd_lanes_kernel<T, 16>, grid, kThreads, st, 0, p)
+                             : ragged::launch(norm_fwd_lanes_kernel<T, 32>, grid, kThreads, st, 0, p);
+    }
+    switch (s.ctas) {
+        case 1: return fwd_rows<T, 1>(p, s, st);
+        case 2: return fwd_rows<T, 2>(p, s, st);
+        case 4: return fwd_rows<T, 4>(p, s, st);
+        default: return fwd_rows<T, 8>(p, s, st);
     }
 }
 
-// Blocks of the backward kernel, each of which leaves a partial row per weight: a rule on the shape alone (152 is this
-// GPU's number of SMs), so that a workspace's size does not depend on the current device.
-static int64_t bwd_blocks(int64_t M, int64_t F) {
+// The most blocks (clusters of them, for long rows) of the backward kernel, each of which leaves a partial row per
+// weight: a rule on the shape alone (152 is this GPU's number of SMs), so that a workspace's size does not depend on the
+// current device.
+static int64_t bwd_parts(int64_t M, int64_t F) {
     const Shape s = shape_of(F);
-    const int threads = 32 * s.W * s.teams;
-    return std::max<int64_t>(1, std::min<int64_t>((M + s.teams - 1) / s.teams, 152 * std::max(1, 768 / threads)));
+    if (!s.ctas) {
+        const int teams = kThreads / (F <= 64 ? 8 : F <= 128 ? 16 : 32);
+        return std::max<int64_t>(1, std::min<int64_t>((M + teams - 1) / teams, 152 * 2));
+    }
+    return std::max<int64_t>(1, std::min<int64_t>(M, 152 * kBwdThreads / s.threads / s.ctas));
 }
 
-template <class T, int NV>
-static cudaError_t bwd_rows(const Bwd<T>& p, const Shape& s, unsigned grid, cudaStream_t st) {
-    constexpr bool kHold = NV * sizeof(T) <= 4, kSums = NV == 4;
-    const int smem = kSums ? 8 * p.F : s.teams > 1 ? 4 * s.teams * p.F : 0;
-    if (kSums) {
-        const cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<T, NV, kHold, kSums>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * kNormMaxWidth);
-        if (e != cudaSuccess) return e;
-    }
-    return ragged::launch(norm_bwd_kernel<T, NV, kHold, kSums>, grid, 32 * s.W * s.teams, st, smem, p, s.W);
+template <class T, int kC>
+static cudaError_t bwd_rows(const Bwd<T>& p, const Shape& s, int64_t& parts, cudaStream_t st) {
+    return launch_rows<norm_bwd_kernel<T, kC>>(p, s, parts, kStagesOf<T> * 4 * s.width * (int)sizeof(T) + kTailBytes, st);
 }
 
 template <class T>
 static cudaError_t bwd(const NormBwd& c, cudaStream_t st) {
     const Bwd<T> p{(const T*)c.dres, (const T*)c.dn, (const T*)c.x, (const T*)c.res, (const T*)c.post, (const T*)c.pre,
-                   c.gate, c.stats, c.M, (int)c.F, c.scale, (T*)c.dx, (T*)c.dr, c.dgate, c.partials};
+                   c.gate, c.stats, c.M, (int)c.F, c.scale, (T*)c.dx, (T*)c.dr, c.dgate, c.partials, c.status};
     const Shape s = shape_of(c.F);
-    const unsigned grid = (unsigned)bwd_blocks(c.M, c.F);
-    const cudaError_t e = s.nv == 1   ? bwd_rows<T, 1>(p, s, grid, st)
-                          : s.nv == 2 ? bwd_rows<T, 2>(p, s, grid, st)
-                                      : bwd_rows<T, 4>(p, s, grid, st);
+    int64_t parts = bwd_parts(c.M, c.F);
+    cudaError_t e;
+    if (!s.ctas) {
+        const unsigned grid = (unsigned)parts;
+        e = c.F <= 64    ? ragged::launch(norm_bwd_lanes_kernel<T, 8>, grid, kThreads, st, 0, p)
+            : c.F <= 128 ? ragged::launch(norm_bwd_lanes_kernel<T, 16>, grid, kThreads, st, 0, p)
+                         : ragged::launch(norm_bwd_lanes_kernel<T, 32>, grid, kThreads, st, 0, p);
+    } else {
+        e = s.ctas == 1   ? bwd_rows<T, 1>(p, s, parts, st)
+            : s.ctas == 2 ? bwd_rows<T, 2>(p, s, parts, st)
+            : s.ctas == 4 ? bwd_rows<T, 4>(p, s, parts, st)
+                          : bwd_rows<T, 8>(p, s, parts, st);
+    }
     if (e != cudaSuccess || (!c.dpost && !c.dpre)) return e;
-    return ragged::launch(norm_weights_kernel, dim3((unsigned)((c.F + 31) / 32), 2), 256, st, 0, (const float*)c.partials,
-                          (int)grid, (int)c.F, c.dpost, c.dpre);
+    return ragged::launch(norm_weights_kernel, dim3((unsigned)((c.F + 31) / 32), 2), 1024, st, 0, (const float*)c.partials,
+                          (int)parts, (int)c.F, c.dpost, c.dpre);
 }
 
 }  // namespace norm
 
 size_t norm_bwd_workspace(int64_t M, int64_t F) {
-    return (size_t)(2 * norm::bwd_blocks(M, F)) * (size_t)F * sizeof(float);
+    return (size_t)(2 * norm::bwd_parts(M, F)) * (size_t)F * sizeof(float);
 }
 cudaError_t run_norm_fwd(const NormFwd& c, cudaStream_t s) {
     if (c.M == 0) return cudaSuccess;

@@ -244,7 +244,8 @@ int mxq_dropout(const void* x, const void* residual, int64_t n, const int64_t* d
 
 int mxq_norm_residual_fwd(const void* x, const void* residual, const void* post_weight, const void* pre_weight,
                           const float* gate, int64_t M, int64_t F, double scale, double eps, int flags, void* res_out,
-                          void* n_out, float* stats, mxq_stream_t stream) {
+                          void* n_out, float* stats, int32_t* d_status,
+                          mxq_stream_t stream) {
     if (flags & ~MXQ_OUT_F32) return MXQ_ERR_FLAGS;
     if (M != 0 && (!x || (!res_out && !n_out) || !n_out != !pre_weight)) return MXQ_ERR_NULL;
     if (int r = check_norm(M, F, scale)) return r;
@@ -253,7 +254,7 @@ int mxq_norm_residual_fwd(const void* x, const void* residual, const void* post_
         !aligned16(res_out) || !aligned16(n_out) || !aligned4(stats))
         return MXQ_ERR_ALIGN;
     const cudaError_t e = mxq::run_norm_fwd({x, residual, post_weight, pre_weight, gate, M, F, (float)scale, (float)eps,
-                                             (flags & MXQ_OUT_F32) != 0, res_out, n_out, stats},
+                                             (flags & MXQ_OUT_F32) != 0, res_out, n_out, stats, d_status},
                                             (cudaStream_t)stream);
     return e == cudaSuccess ? MXQ_OK : fail_cuda(e);
 }
@@ -261,7 +262,7 @@ int mxq_norm_residual_fwd(const void* x, const void* residual, const void* post_
 int mxq_norm_residual_bwd(const void* dres, const void* dn, const void* x, const void* res, const float* stats,
                           const void* post_weight, const void* pre_weight, const float* gate, int64_t M, int64_t F,
                           double scale, int flags, void* dx, void* dresidual, float* dpost_weight, float* dpre_weight,
-                          float* dgate, void* ws, size_t ws_bytes, mxq_stream_t stream) {
+                          float* dgate, int32_t* d_status, void* ws, size_t ws_bytes, mxq_stream_t stream) {
     if (flags & ~MXQ_OUT_F32) return MXQ_ERR_FLAGS;
     if (!post_weight != !dpost_weight || !pre_weight != !dpre_weight) return MXQ_ERR_NULL;
     if (M != 0) {
@@ -278,7 +279,7 @@ int mxq_norm_residual_bwd(const void* dres, const void* dn, const void* x, const
     if ((post_weight || pre_weight) && (!ws || ws_bytes < mxq::norm_bwd_workspace(M, F))) return MXQ_ERR_WORKSPACE;
     const cudaError_t e = mxq::run_norm_bwd({dres, dn, x, res, post_weight, pre_weight, gate, stats, M, F, (float)scale,
                                              (flags & MXQ_OUT_F32) != 0, dx, dresidual, dpost_weight, dpre_weight, dgate,
-                                             static_cast<float*>(ws)},
+                                             static_cast<float*>(ws), d_status},
                                             (cudaStream_t)stream);
     return e == cudaSuccess ? MXQ_OK : fail_cuda(e);
 }

@@ -99,9 +99,9 @@ def load(path: str = LIB) -> ctypes.CDLL:
     L.mxq_fp8_quantize_weight.argtypes = [_P, _I64, _I64, _INT, _P, _P, _P]
     L.mxq_fp8_gemm_fprop.argtypes = [_P, _P, _P, _P, _P, _I64, _I64, _I64, _INT, _P, _INT, _P, _P, _P]
     L.mxq_fp8_gemm_dgrad.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _INT, _P, _INT, _P, _P, _P]
-    L.mxq_norm_residual_fwd.argtypes = [_P, _P, _P, _P, _P, _I64, _I64, _F64, _F64, _INT, _P, _P, _P, _P]
+    L.mxq_norm_residual_fwd.argtypes = [_P, _P, _P, _P, _P, _I64, _I64, _F64, _F64, _INT, _P, _P, _P, _P, _P]
     L.mxq_norm_residual_bwd.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _F64, _INT, _P, _P, _P, _P, _P, _P,
-                                        _SZ, _P]
+                                        _P, _SZ, _P]
     L.mxq_status_read.argtypes = [_P, _P, _P]
     L.mxq_probe_mma_stream.argtypes = [_I64, _P, _P]
     L.mxq_probe_mma_stream.restype = _INT
@@ -1049,7 +1049,7 @@ def _norm_row(t, name):
 
 
 def norm_residual_fwd(x, residual=None, post_weight=None, pre_weight=None, gate=None, scale=1.0, eps=1e-6,
-                      res_out=True, stats_out=True, out=None):
+                      res_out=True, stats_out=True, status=None, out=None):
     """r' = residual + scale * gate[m] * N(x; post_weight) and n = N(r'; pre_weight), RMS norms N.
 
     x, residual (M, F) and weights (F,) all bf16 or all fp32, gate (M,) fp32. Returns (r', n, stats): n is
@@ -1074,14 +1074,14 @@ def norm_residual_fwd(x, residual=None, post_weight=None, pre_weight=None, gate=
         xp, _packed(residual, "residual", (M, F), same), _packed(post_weight, "post_weight", (F,), same),
         _packed(pre_weight, "pre_weight", (F,), same), _packed(gate, "gate", (M,), _F32), M, F, scale, eps,
         OUT_F32 if x.dtype is torch.float32 else 0, _packed(r, "r'", (M, F), same), _packed(n, "n", (M, F), same),
-        _packed(stats, "stats", (2, M), _F32), _stream())
+        _packed(stats, "stats", (2, M), _F32), _dev(status, "status", 4, _I32), _stream())
     if rc:
         _check(rc, "mxq_norm_residual_fwd")
     return r, n, stats
 
 
-def norm_residual_bwd(dres, dn, x, res, stats, post_weight=None, pre_weight=None, gate=None, scale=1.0, out=None,
-                      workspace=None):
+def norm_residual_bwd(dres, dn, x, res, stats, post_weight=None, pre_weight=None, gate=None, scale=1.0, status=None,
+                      out=None, workspace=None):
     """The gradients of norm_residual_fwd from dres (of r', may be None) and dn (of n, None exactly without
     pre_weight). x, weights, gate and scale are the forward call's, res its r' and stats its statistics; x
     may be None without post_weight and gate, res without pre_weight. Returns a dict: dx, dresidual (M, F),
@@ -1112,7 +1112,7 @@ def norm_residual_bwd(dres, dn, x, res, stats, post_weight=None, pre_weight=None
         _packed(gate, "gate", (M,), _F32), M, F, scale, OUT_F32 if like.dtype is torch.float32 else 0,
         _packed(o["dx"], "dx", (M, F), same), _packed(o["dresidual"], "dresidual", (M, F), same),
         _packed(o.get("dpost_weight"), "dpost_weight", (F,), _F32), _packed(o.get("dpre_weight"), "dpre_weight", (F,), _F32),
-        _packed(o.get("dgate"), "dgate", (M,), _F32), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+        _packed(o.get("dgate"), "dgate", (M,), _F32), _dev(status, "status", 4, _I32), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
         _stream())
     if rc:
         _check(rc, "mxq_norm_residual_bwd")

@@ -26,8 +26,8 @@ CALLS = {
     "mxq_fp8_quantize_weight": (P, N, K, E, P, P, None),
     "mxq_fp8_gemm_fprop": (P, P, P, P, None, M, N, K, E, P, 0, P, None, None),
     "mxq_fp8_gemm_dgrad": (P, P, P, P, M, N, K, E, P, 0, P, None, None),
-    "mxq_norm_residual_fwd": (P, P, P, P, P, M, F, 1.0, 1e-6, 0, P, P, P, None),
-    "mxq_norm_residual_bwd": (P, P, P, P, P, P, P, P, M, F, 1.0, 0, P, P, P, P, P, P, BIG, None),
+    "mxq_norm_residual_fwd": (P, P, P, P, P, M, F, 1.0, 1e-6, 0, P, P, P, None, None),
+    "mxq_norm_residual_bwd": (P, P, P, P, P, P, P, P, M, F, 1.0, 0, P, P, P, P, P, None, P, BIG, None),
 }
 REQUIRED = {
     "mxq_ragged_gemm_fprop_swiglu": (0, 2, 8, 9),
