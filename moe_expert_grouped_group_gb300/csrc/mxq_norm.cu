@@ -372,16 +372,16 @@ struct RowScalars {
     }
 };
 
-template <class T, class S>
+// get(i): dres (2) and x (3).
+template <class T, class G, class S>
 __device__ __forceinline__ void bwd_row(const Bwd<T>& p, int64_t m, int f, bool live, bool mine, const RowScalars& c,
-                                        const Pack<T>& rp, const Pack<T>& np, const Pack<T>& dp, const Pack<T>& xp,
-                                        const float (&w_post)[8], const float (&w_pre)[8], float (&d_post)[8],
+                                        const Pack<T>& rp, const Pack<T>& np, G get, const float (&w_post)[8], const float (&w_pre)[8], float (&d_post)[8],
                                         float (&d_pre)[8], float inv, S sum) {
     float rh[8], g[8], D[8], xh[8];
     const float a = p.scale * c.gate;
     rp.values(rh);
     np.values(g);
-    dp.values(D);
+    float mean = 0.0f;
     if (p.pre) {
         float s = 0.0f;
 #pragma unroll
@@ -391,14 +391,16 @@ __device__ __forceinline__ void bwd_row(const Bwd<T>& p, int64_t m, int f, bool 
             g[j] *= w_pre[j];
             s = fmaf(g[j], rh[j], s);
         }
-        const float mean = sum(s) * inv;
+        mean = sum(s) * inv;
+    }
+    get(2).values(D);
+    if (p.pre)
 #pragma unroll
         for (int j = 0; j < 8; ++j) D[j] = fmaf(c.rstd2, fmaf(-rh[j], mean, g[j]), D[j]);
-    }
     if (p.dr && live) Pack<T>::store(p.dr + m * p.F + f, D);
     float dot = 0.0f;
     if (p.post || p.gate) {
-        xp.values(xh);
+        get(3).values(xh);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             xh[j] *= c.rstd1;
@@ -455,8 +457,8 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_lanes_kernel(Bwd<T> p) {
     for (int64_t first = m - threadIdx.x % 32 / kLanes; first < p.M; first += step, m += step) {
         fetch(m + step, nv, nc);
         // rows beyond the last are zeros and have no part in the sums
-        bwd_row(p, m, f, live && m < p.M, lane == 0 && m < p.M, c, v[0], v[1], v[2], v[3], w_post, w_pre, d_post, d_pre, inv,
-                [](float s) {
+        bwd_row(p, m, f, live && m < p.M, lane == 0 && m < p.M, c, v[0], v[1],
+                [&](int i) -> const Pack<T>& { return v[i]; }, w_post, w_pre, d_post, d_pre, inv, [](float s) {
 #pragma unroll
                     for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
                     return s;
@@ -524,16 +526,16 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(Bwd<T> p, int width)
         rows.wait(n, abort_flag);
         __syncwarp();
         const RowScalars c{rows.scalar(n, 0, 1.0f), rows.scalar(n, 1, 0.0f), rows.scalar(n, 2, 1.0f)};
-        Pack<T> v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i].zero();
-            if (live && rows.from[i]) rows.get(n, i, f, v[i]);
-        }
+        const auto get = [&](int i) {
+            Pack<T> v;
+            v.zero();
+            if (live && rows.from[i]) rows.get(n, i, f, v);
+            return v;
+        };
         // at a row's first exchange every thread has read the row before
         bool refill = threadIdx.x == 0 && n > 0;
-        bwd_row(p, m, f0 + f, live, threadIdx.x == 0 && rank == 0, c, v[0], v[1], v[2], v[3], w_post, w_pre, d_post, d_pre,
-                inv, [&](float s) {
+        bwd_row(p, m, f0 + f, live, threadIdx.x == 0 && rank == 0, c, get(0), get(1), get, w_post, w_pre, d_post, d_pre, inv,
+                [&](float s) {
                     s = sums.sum(s, abort_flag);
                     if (refill) rows.load(n - 1 + kS, m + (kS - 1) * step);
                     refill = false;
