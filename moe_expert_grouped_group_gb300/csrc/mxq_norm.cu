@@ -14,8 +14,8 @@
 // idle for a few hundred cycles. So rows come by bulk copies into a ring of
 // shared memory, two or three rows ahead of the one that is computed.
 //
-// A row of more than kWarpWidth columns belongs to a cluster of 1 to 8 CTAs of
-// up to 2048 columns each, eight to a thread; the CTAs' sums meet in each
+// A row of more than kWarpWidth columns belongs to a cluster of 1 to 8 CTAs,
+// eight columns to a thread; the CTAs' sums meet in each
 // other's shared memory. Shorter rows belong to 8, 16 or 32 lanes of a warp,
 // which hold the next row in registers. A thread always has the same columns,
 // so that the weights' gradients grow in its registers while it walks its
@@ -82,9 +82,11 @@ struct Pack<float> {
     }
 };
 
-constexpr int kThreads = 256;      // most threads of a CTA
-constexpr int kWarpWidth = 256;    // widest row of a warp
-constexpr int kWidth = 8 * kThreads;  // and of a CTA
+constexpr int kWarpWidth = 256;  // widest row of a warp
+constexpr int kThreads = 256;    // threads of a CTA for such rows
+// Most threads of a CTA for wider ones, with eight columns each, and of one that shares its rows with others.
+constexpr int kFwdThreads = 1024, kBwdThreads = 512, kShareThreads = 256;
+constexpr int kMaxParts = 64;  // warps of a row
 
 // Bulk copy into this CTA's shared memory, counted on its barrier.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -149,13 +151,13 @@ struct Rows {
 // one, so when all warps have read this one.
 template <int kC>
 struct RowSum {
-    uint32_t at, bar;  // [2][kC * 8] floats; two barriers (kC > 1)
+    uint32_t at, bar;  // [2][kMaxParts] floats; two barriers (kC > 1)
     int W, rank;
     uint32_t turn = 0;
     __device__ RowSum(uint32_t at_, uint32_t bar_, int W_, int rank_) : at(at_), bar(bar_), W(W_), rank(rank_) {}
     __device__ float sum(float v, volatile int* abort_flag) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const uint32_t side = turn & 1, phase = turn >> 1 & 1, to = at + (side * kC * 8 + rank * W + warp) * 4;
+        const uint32_t side = turn & 1, phase = turn >> 1 & 1, to = at + (side * kMaxParts + rank * W + warp) * 4;
         ++turn;
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -174,10 +176,10 @@ struct RowSum {
         }
         float s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < (kC * 8 + 31) / 32; ++k)
+        for (int k = 0; k < (kC == 1 ? 1 : 2); ++k)
             if (lane + 32 * k < kC * W) {
                 float x;
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at + (side * kC * 8 + lane + 32 * k) * 4) : "memory");
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at + (side * kMaxParts + lane + 32 * k) * 4) : "memory");
                 s += x;
             }
 #pragma unroll
@@ -187,10 +189,11 @@ struct RowSum {
 };
 
 // Dynamic shared memory: the ring, then the sums, the rows' numbers and the barriers.
-constexpr int kSumBytes = 2 * 8 * 8 * 4, kScalarBytes = 16 * 3, kTailBytes = kSumBytes + kScalarBytes + 64;
-constexpr int kMostSmem = 2 * 4 * kWidth * 4 + kTailBytes;  // gradients of fp32: two stages of four tensors
-static_assert(3 * 4 * kWidth * 2 + kTailBytes <= kMostSmem && kMostSmem <= 232448, "shared memory");
-constexpr int kBwdThreads = 640;  // threads of an SM's CTAs in the backward kernel, by their registers
+constexpr int kStages = 3, kSumBytes = 2 * kMaxParts * 4, kScalarBytes = 16 * kStages, kTailBytes = kSumBytes + kScalarBytes + 64;
+constexpr int smem_bytes(int tensors, int width, int size) { return kStages * tensors * width * size + kTailBytes; }
+constexpr int kMostSmem = std::max(smem_bytes(2, 8 * kFwdThreads, 4), smem_bytes(4, 8 * kBwdThreads, 4));
+static_assert(kMostSmem <= 232448 && (2 + kStages) * 8 <= 64, "shared memory");
+constexpr int kSmThreads = 640;  // threads of an SM's CTAs in the backward kernel, by their registers
 
 // What a thread does with its eight columns of a row, in the order of the formulas. Weights: 1 without one.
 template <class T>
@@ -250,51 +253,42 @@ __device__ __forceinline__ void fwd_row(const Fwd<T>& p, int64_t m, int f, bool 
     if (p.stats && mine) p.stats[p.M + m] = rstd;
 }
 
-// Rows of up to kWarpWidth columns: kLanes lanes each, with the next row in registers.
+// Rows of up to kWarpWidth columns: kLanes lanes each. Many warps hide the loads here; with the next row in registers, as
+// in the backward kernel, there were fewer (65536 x 256: 37 us).
 template <class T, int kLanes>
-__global__ void __launch_bounds__(kThreads) norm_fwd_lanes_kernel(Fwd<T> p) {
+__global__ void __launch_bounds__(kThreads, 6) norm_fwd_lanes_kernel(Fwd<T> p) {
     const int lane = threadIdx.x % kLanes, f = 8 * lane;
     const bool live = f < p.F;
     const float inv = 1.0f / (float)p.F;
     wait_for_stream();
-    float w_post[8], w_pre[8];
-    weights8(p.post, f, live, w_post);
-    weights8(p.pre, f, live, w_pre);
     const int64_t step = (int64_t)gridDim.x * (kThreads / kLanes);
     int64_t m = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-    const auto fetch = [&](int64_t row, Pack<T>& x, Pack<T>& r, float& gate) {
-        x.zero(), r.zero();
-        gate = 1.0f;
-        if (row >= p.M) return;
-        if (live) {
-            x.load(p.x + row * p.F + f);
-            if (p.residual) r.load(p.residual + row * p.F + f);
-        }
-        if (p.gate) gate = p.gate[row];
-    };
-    Pack<T> x, r, nx, nr;
-    float gate, ngate;
-    fetch(m, x, r, gate);
     // all lanes of a warp take as many turns: they share its shuffles
     for (int64_t first = m - threadIdx.x % 32 / kLanes; first < p.M; first += step, m += step) {
-        fetch(m + step, nx, nr, ngate);
-        fwd_row(p, m, f, live && m < p.M, lane == 0 && m < p.M, gate, x, r, w_post, w_pre, inv, [](float v) {
+        Pack<T> x, r;
+        x.zero(), r.zero();
+        const bool mine = live && m < p.M;
+        if (mine) {
+            x.load(p.x + m * p.F + f);
+            if (p.residual) r.load(p.residual + m * p.F + f);
+        }
+        const float gate = p.gate && m < p.M ? p.gate[m] : 1.0f;
+        float w_post[8], w_pre[8];
+        weights8(p.post, f, live, w_post);
+        weights8(p.pre, f, live, w_pre);
+        fwd_row(p, m, f, mine, lane == 0 && m < p.M, gate, x, r, w_post, w_pre, inv, [](float v) {
 #pragma unroll
             for (int o = kLanes / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
             return v;
         });
-        x = nx, r = nr, gate = ngate;
     }
 }
 
-template <class T>
-constexpr int kStagesOf = sizeof(T) == 2 ? 3 : 2;
-
 template <class T, int kC>
-__global__ void __launch_bounds__(kThreads) norm_fwd_kernel(Fwd<T> p, int width) {
+__global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(Fwd<T> p, int width) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_abort;
-    constexpr int kS = kStagesOf<T>;
+    constexpr int kS = kStages;
     const int rank = kC > 1 ? (int)ragged::cta_rank() : 0, W = blockDim.x / 32;
     const int f0 = rank * width, mine = min(width, p.F - f0), f = 8 * (int)threadIdx.x;
     const bool live = f < mine;
@@ -488,10 +482,10 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_lanes_kernel(Bwd<T> p) {
 }
 
 template <class T, int kC>
-__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(Bwd<T> p, int width) {
+__global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(Bwd<T> p, int width) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_abort;
-    constexpr int kS = kStagesOf<T>;
+    constexpr int kS = kStages;
     const int rank = kC > 1 ? (int)ragged::cta_rank() : 0, W = blockDim.x / 32;
     const int f0 = rank * width, mine = min(width, p.F - f0), f = 8 * (int)threadIdx.x;
     const bool live = f < mine, dots = p.post || p.gate;
@@ -584,11 +578,12 @@ __global__ void __launch_bounds__(1024) norm_weights_kernel(const float* partial
 struct Shape {
     int ctas, width, threads;
 };
-static Shape shape_of(int64_t F) {
+static Shape shape_of(int64_t F, int most_threads) {
     if (F <= kWarpWidth) return {0, (int)F, kThreads};
     Shape s;
     s.ctas = 1;
-    while (s.ctas * kWidth < F) s.ctas *= 2;
+    if (F > 8 * most_threads) most_threads = kShareThreads;
+    while (s.ctas * 8 * most_threads < F) s.ctas *= 2;
     s.width = (int)((F / 8 + s.ctas - 1) / s.ctas * 8);
     s.threads = (s.width + 255) / 256 * 32;
     return s;
@@ -598,7 +593,7 @@ static Shape shape_of(int64_t F) {
 // and its co-residency are set and asked for once per device and number of threads.
 template <auto kKernel, class P>
 static cudaError_t launch_rows(const P& p, const Shape& s, int64_t& clusters, int smem, cudaStream_t st) {
-    static std::atomic<int> cache[64][kThreads / 32 + 1];
+    static std::atomic<int> cache[64][kFwdThreads / 32 + 1];
     int dev = 0, most = 0;
     cudaGetDevice(&dev);
     cudaLaunchConfig_t cfg{};
@@ -635,25 +630,23 @@ static cudaError_t launch_rows(const P& p, const Shape& s, int64_t& clusters, in
 template <class T, int kC>
 static cudaError_t fwd_rows(const Fwd<T>& p, const Shape& s, cudaStream_t st) {
     int64_t clusters = p.M;
-    return launch_rows<norm_fwd_kernel<T, kC>>(p, s, clusters, kStagesOf<T> * 2 * s.width * (int)sizeof(T) + kTailBytes, st);
+    return launch_rows<norm_fwd_kernel<T, kC>>(p, s, clusters, smem_bytes(2, s.width, sizeof(T)), st);
 }
 
 template <class T>
 static cudaError_t fwd(const NormFwd& c, cudaStream_t st) {
     const Fwd<T> p{(const T*)c.x, (const T*)c.residual, (const T*)c.post, (const T*)c.pre, c.gate, c.M, (int)c.F,
                    c.scale, c.eps, (T*)c.res, (T*)c.n, c.stats, c.status};
-    const Shape s = shape_of(c.F);
+    const Shape s = shape_of(c.F, kFwdThreads);
     if (!s.ctas) {
         const int lanes = c.F <= 64 ? 8 : c.F <= 128 ? 16 : 32, teams = kThreads / lanes;
-        const unsigned grid = (unsigned)std::min<int64_t>((c.M + teams - 1) / teams, (int64_t)ragged::sm_count() * 4);
+        const unsigned grid = (unsigned)std::min<int64_t>((c.M + teams - 1) / teams, (int64_t)ragged::sm_count() * 8);
         return lanes == 8    ? ragged::launch(norm_fwd_lanes_kernel<T, 8>, grid, kThreads, st, 0, p)
                : lanes == 16 ? ragged::launch(norm_fwd_lanes_kernel<T, 16>, grid, kThreads, st, 0, p)
                              : ragged::launch(norm_fwd_lanes_kernel<T, 32>, grid, kThreads, st, 0, p);
     }
     switch (s.ctas) {
         case 1: return fwd_rows<T, 1>(p, s, st);
-        case 2: return fwd_rows<T, 2>(p, s, st);
-        case 4: return fwd_rows<T, 4>(p, s, st);
         default: return fwd_rows<T, 8>(p, s, st);
     }
 }
@@ -662,24 +655,24 @@ static cudaError_t fwd(const NormFwd& c, cudaStream_t st) {
 // weight: a rule on the shape alone (152 is this GPU's number of SMs), so that a workspace's size does not depend on the
 // current device.
 static int64_t bwd_parts(int64_t M, int64_t F) {
-    const Shape s = shape_of(F);
+    const Shape s = shape_of(F, kBwdThreads);
     if (!s.ctas) {
         const int teams = kThreads / (F <= 64 ? 8 : F <= 128 ? 16 : 32);
         return std::max<int64_t>(1, std::min<int64_t>((M + teams - 1) / teams, 152 * 2));
     }
-    return std::max<int64_t>(1, std::min<int64_t>(M, 152 * kBwdThreads / s.threads / s.ctas));
+    return std::max<int64_t>(1, std::min<int64_t>(M, 152 * std::max(1, kSmThreads / s.threads) / s.ctas));
 }
 
 template <class T, int kC>
 static cudaError_t bwd_rows(const Bwd<T>& p, const Shape& s, int64_t& parts, cudaStream_t st) {
-    return launch_rows<norm_bwd_kernel<T, kC>>(p, s, parts, kStagesOf<T> * 4 * s.width * (int)sizeof(T) + kTailBytes, st);
+    return launch_rows<norm_bwd_kernel<T, kC>>(p, s, parts, smem_bytes(4, s.width, sizeof(T)), st);
 }
 
 template <class T>
 static cudaError_t bwd(const NormBwd& c, cudaStream_t st) {
     const Bwd<T> p{(const T*)c.dres, (const T*)c.dn, (const T*)c.x, (const T*)c.res, (const T*)c.post, (const T*)c.pre,
                    c.gate, c.stats, c.M, (int)c.F, c.scale, (T*)c.dx, (T*)c.dr, c.dgate, c.partials, c.status};
-    const Shape s = shape_of(c.F);
+    const Shape s = shape_of(c.F, kBwdThreads);
     int64_t parts = bwd_parts(c.M, c.F);
     cudaError_t e;
     if (!s.ctas) {
@@ -689,7 +682,6 @@ static cudaError_t bwd(const NormBwd& c, cudaStream_t st) {
                          : ragged::launch(norm_bwd_lanes_kernel<T, 32>, grid, kThreads, st, 0, p);
     } else {
         e = s.ctas == 1   ? bwd_rows<T, 1>(p, s, parts, st)
-            : s.ctas == 2 ? bwd_rows<T, 2>(p, s, parts, st)
             : s.ctas == 4 ? bwd_rows<T, 4>(p, s, parts, st)
                           : bwd_rows<T, 8>(p, s, parts, st);
     }
