@@ -145,11 +145,13 @@ def _ptr(t):
 # The current stream's raw handle without building a torch Stream object (about 3 us a call
 # otherwise, as much as a small kernel); torch's public call where the fast one is missing.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current device likewise (torch.cuda.current_device checks for initialization first, which a CUDA tensor implies).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream():
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -715,20 +717,27 @@ def _try_fast_empty():
         pass
 
 
-def _new(shape, dtype, like):
+def _allocator(like):
+    """The allocation call for tensors beside `like`: (shape, contiguous strides, dtype) -> tensor. Asked for once by a
+    call that makes several."""
     if _fast_empty is None:
         _try_fast_empty()
-    if (_fast_empty and like.get_device() == torch.cuda.current_device()
+    if (_fast_empty and like.get_device() == _current_device()
             and not torch.are_deterministic_algorithms_enabled()):
-        d = len(shape)
-        if d == 2:
-            strides = (shape[1], 1)
-        elif d == 3:
-            strides = (shape[1] * shape[2], shape[2], 1)
-        else:
-            strides = (1,) if d == 1 else torch.empty(shape, device="meta").stride()
-        return _fast_empty(shape, strides, dtype)
-    return torch.empty(shape, dtype=dtype, device=like.device)
+        return _fast_empty
+    device = like.device
+    return lambda shape, strides, dtype: torch.empty(shape, dtype=dtype, device=device)
+
+
+def _new(shape, dtype, like):
+    d = len(shape)
+    if d == 2:
+        strides = (shape[1], 1)
+    elif d == 3:
+        strides = (shape[1] * shape[2], shape[2], 1)
+    else:
+        strides = (1,) if d == 1 else torch.empty(shape, device="meta").stride()
+    return _allocator(like)(shape, strides, dtype)
 
 
 def _rows(t, name, dtypes):
@@ -1056,25 +1065,35 @@ def norm_residual_fwd(x, residual=None, post_weight=None, pre_weight=None, gate=
     None without pre_weight, r' with res_out=False, stats (2, M) fp32 (what the backward call needs) with
     stats_out=False. out: a (r', n, stats) to write to, None where it is to be made; r' may be residual or
     x, n may be x."""
-    xp, (M, F), same = _norm_row(x, "x"), x.shape, (x.dtype,)
+    xp, (M, F), dt = _norm_row(x, "x"), x.shape, x.dtype
+    shape, same, new = (M, F), (dt,), _allocator(x)
     r, n, stats = out if out is not None else (None, None, None)
+    rp = np = sp = None
     if not res_out:
         r = None
     elif r is None:
-        r = _new((M, F), x.dtype, x)
+        r = new(shape, (F, 1), dt)
+        rp = r.data_ptr()
+    else:
+        rp = _packed(r, "r'", shape, same)
     if pre_weight is None:
         n = None
     elif n is None:
-        n = _new((M, F), x.dtype, x)
+        n = new(shape, (F, 1), dt)
+        np = n.data_ptr()
+    else:
+        np = _packed(n, "n", shape, same)
     if not stats_out:
         stats = None
     elif stats is None:
-        stats = _new((2, M), torch.float32, x)
+        stats = new((2, M), (M, 1), torch.float32)
+        sp = stats.data_ptr()
+    else:
+        sp = _packed(stats, "stats", (2, M), _F32)
     rc = lib().mxq_norm_residual_fwd(
-        xp, _packed(residual, "residual", (M, F), same), _packed(post_weight, "post_weight", (F,), same),
+        xp, _packed(residual, "residual", shape, same), _packed(post_weight, "post_weight", (F,), same),
         _packed(pre_weight, "pre_weight", (F,), same), _packed(gate, "gate", (M,), _F32), M, F, scale, eps,
-        OUT_F32 if x.dtype is torch.float32 else 0, _packed(r, "r'", (M, F), same), _packed(n, "n", (M, F), same),
-        _packed(stats, "stats", (2, M), _F32), _dev(status, "status", 4, _I32), _stream())
+        OUT_F32 if dt is torch.float32 else 0, rp, np, sp, _dev(status, "status", 4, _I32), _stream())
     if rc:
         _check(rc, "mxq_norm_residual_fwd")
     return r, n, stats
@@ -1091,29 +1110,39 @@ def norm_residual_bwd(dres, dn, x, res, stats, post_weight=None, pre_weight=None
     if like is None:
         raise MXQError("dres or dn is required")
     _norm_row(like, "dn" if dn is not None else "dres")
-    (M, F), same = like.shape, (like.dtype,)
-    o = dict(out or {})
-    _fill(o, "dx", lambda: _new((M, F), like.dtype, like))
-    _fill(o, "dresidual", lambda: _new((M, F), like.dtype, like))
-    ws = None
+    (M, F), dt = like.shape, like.dtype
+    shape, same, new = (M, F), (dt,), _allocator(like)
+    o = dict(out) if out else {}
+
+    def output(key, want, strides, dtype):
+        t = o.get(key)
+        if t is None:
+            t = o[key] = new(want, strides, dtype)
+            return t.data_ptr()
+        return _packed(t, key, want, (dtype,))
+
+    dxp, drp = output("dx", shape, (F, 1), dt), output("dresidual", shape, (F, 1), dt)
+    post = pre = gp = ws = None
+    ws_bytes = 0
     if post_weight is not None:
-        _fill(o, "dpost_weight", lambda: _new((F,), torch.float32, like))
+        post = output("dpost_weight", (F,), (1,), torch.float32)
     if pre_weight is not None:
-        _fill(o, "dpre_weight", lambda: _new((F,), torch.float32, like))
+        pre = output("dpre_weight", (F,), (1,), torch.float32)
     if gate is not None:
-        _fill(o, "dgate", lambda: _new((M,), torch.float32, like))
-    if post_weight is not None or pre_weight is not None:
-        ws = workspace if workspace is not None else _new((max(16, workspace_bytes(OP_NORM_RESIDUAL_BWD, M, 0, F, 0)),),
-                                                          torch.uint8, like)
+        gp = output("dgate", (M,), (1,), torch.float32)
+    if post is not None or pre is not None:
+        if workspace is None:
+            ws_bytes = workspace_bytes(OP_NORM_RESIDUAL_BWD, M, 0, F, 0)
+            workspace = new((ws_bytes,), (1,), torch.uint8)
+        else:
+            ws_bytes = workspace.numel() * workspace.element_size()
+        ws = _ptr(workspace)
     rc = lib().mxq_norm_residual_bwd(
-        _packed(dres, "dres", (M, F), same), _packed(dn, "dn", (M, F), same), _packed(x, "x", (M, F), same),
-        _packed(res, "res", (M, F), same), _packed(stats, "stats", (2, M), _F32),
+        _packed(dres, "dres", shape, same), _packed(dn, "dn", shape, same), _packed(x, "x", shape, same),
+        _packed(res, "res", shape, same), _packed(stats, "stats", (2, M), _F32),
         _packed(post_weight, "post_weight", (F,), same), _packed(pre_weight, "pre_weight", (F,), same),
-        _packed(gate, "gate", (M,), _F32), M, F, scale, OUT_F32 if like.dtype is torch.float32 else 0,
-        _packed(o["dx"], "dx", (M, F), same), _packed(o["dresidual"], "dresidual", (M, F), same),
-        _packed(o.get("dpost_weight"), "dpost_weight", (F,), _F32), _packed(o.get("dpre_weight"), "dpre_weight", (F,), _F32),
-        _packed(o.get("dgate"), "dgate", (M,), _F32), _dev(status, "status", 4, _I32), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-        _stream())
+        _packed(gate, "gate", (M,), _F32), M, F, scale, OUT_F32 if dt is torch.float32 else 0, dxp, drp, post, pre, gp,
+        _dev(status, "status", 4, _I32), ws, ws_bytes, _stream())
     if rc:
         _check(rc, "mxq_norm_residual_bwd")
     return o
