@@ -35,6 +35,10 @@ constexpr int64_t kTruncDepth = 1 << 15;
 // plain loads behind it.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets the stream's next kernel begin when all blocks of this one have got here: its blocks then set themselves up while
+// this one computes, and wait for its end in wait_for_stream().
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -146,6 +150,13 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, ui
             "%5}], [%2];" ::"r"(dst),
             "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "r"(z)
             : "memory");
+}
+// Asks for a box to be brought into L2. What the stream's previous kernel still writes there is no matter: nothing is
+// read, and the load that follows finds what L2 holds then.
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"((uint64_t)map), "r"(x), "r"(y),
+                 "r"(z)
+                 : "memory");
 }
 // True in one lane of a converged warp, always the same. Behind this predicate (unlike behind a test of the
 // lane's number) the compiler keeps what is equal in all lanes, the MMAs' descriptors, in uniform registers.

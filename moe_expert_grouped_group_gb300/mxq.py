@@ -987,7 +987,8 @@ def fp8_quantize_rows(x, out=None):
     values of a row, x ~ q * scale."""
     xp, M, K, ldx = _rows(x, "x", _BF16)
     if out is None:
-        q, scale = _new((M, K), torch.uint8, x), _new((_blocks(K), M), torch.float32, x)
+        new = _allocator(x)
+        q, scale = new((M, K), (K, 1), torch.uint8), new((_blocks(K), M), (M, 1), torch.float32)
         qp, sp = q.data_ptr(), scale.data_ptr()
     else:
         q, scale = out
@@ -1022,11 +1023,12 @@ def fp8_gemm_fprop(xq, x_scale, wq, w_scale, m_splits, bias=None, out_dtype=None
     wq (E, N, K), w_scale (E, ceil(N/128), ceil(K/128)), bias (E, N); Y (M, N) in bf16 (default) or fp32."""
     M, K = xq.shape
     E, N, Kw = wq.shape
-    _shape(wq, "wq", (E, N, K))
+    if Kw != K:
+        _shape(wq, "wq", (E, N, K))
+    kb = _blocks(K)
     out, op, flag = _out(out, out_dtype, (M, N), xq, torch.bfloat16, torch.float32, OUT_F32)
-    rc = lib().mxq_fp8_gemm_fprop(_dev(xq, "xq", 0, _E4M3), _packed(x_scale, "x_scale", (_blocks(K), M), _F32),
-                                  _dev(wq, "wq", 0, _E4M3),
-                                  _packed(w_scale, "w_scale", (E, _blocks(N), _blocks(K)), _F32),
+    rc = lib().mxq_fp8_gemm_fprop(_dev(xq, "xq", 0, _E4M3), _packed(x_scale, "x_scale", (kb, M), _F32),
+                                  _dev(wq, "wq", 0, _E4M3), _packed(w_scale, "w_scale", (E, _blocks(N), kb), _F32),
                                   _packed(bias, "bias", (E, N), _BF16), M, N, K, E, _grouping(m_splits, E), flag, op,
                                   _dev(status, "status", 4, _I32), _stream())
     if rc:
@@ -1039,11 +1041,12 @@ def fp8_gemm_dgrad(dyq, dy_scale, wq, w_scale, m_splits, out_dtype=None, status=
     w_scale those of fp8_gemm_fprop; dX (M, K) in bf16 (default) or fp32."""
     M, N = dyq.shape
     E, Nw, K = wq.shape
-    _shape(wq, "wq", (E, N, K))
+    if Nw != N:
+        _shape(wq, "wq", (E, N, K))
+    nb = _blocks(N)
     out, op, flag = _out(out, out_dtype, (M, K), dyq, torch.bfloat16, torch.float32, OUT_F32)
-    rc = lib().mxq_fp8_gemm_dgrad(_dev(dyq, "dyq", 0, _E4M3), _packed(dy_scale, "dy_scale", (_blocks(N), M), _F32),
-                                  _dev(wq, "wq", 0, _E4M3),
-                                  _packed(w_scale, "w_scale", (E, _blocks(N), _blocks(K)), _F32), M, N, K, E,
+    rc = lib().mxq_fp8_gemm_dgrad(_dev(dyq, "dyq", 0, _E4M3), _packed(dy_scale, "dy_scale", (nb, M), _F32),
+                                  _dev(wq, "wq", 0, _E4M3), _packed(w_scale, "w_scale", (E, nb, _blocks(K)), _F32), M, N, K, E,
                                   _grouping(m_splits, E), flag, op, _dev(status, "status", 4, _I32), _stream())
     if rc:
         _check(rc, "mxq_fp8_gemm_dgrad")
