@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + group * (WIDE / 2);
         const uint32_t acce = mapa(acce0, 0);  // this CTA's own too, for rank 0
         const uint32_t scales = smem_u32(smem) + SCALE_REGION + 512 * group + 4 * (32 * q + lane);
-        int buf = 0, group_at = 0, boxes = 0;
+        int buf = 0, group_at = 0;
         uint32_t aphase = 0, sphase = 0;
         for (;;) {
             const Tile T = board.take(lane, abort_flag);
@@ -476,24 +476,27 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 fence_after();
                 const uint64_t k = f2splat(factor);
-                uint32_t v[2][16];
-                const uint32_t at = lanes + buf * WIDE;
-                tmem_ld16(at, v[0]);
-#pragma unroll
-                for (int i = 0; i < kParts; ++i) {
-                    tmem_wait_ld();
-                    if (i + 1 < kParts) {
-                        tmem_ld16(at + 16 * (i + 1), v[(i + 1) & 1]);  // on its way while this part is added
-                    } else {
-                        fence_before();
-                        __syncwarp();
-                        arrive_relaxed_if(lane == 0, acce + 8 * buf);
-                    }
+                // Four parts out of TMEM at a time: the accumulator is free when the last has been read, before the last four
+                // are added (two at a time, one on its way while the other is added: 113 us against 110.5).
+                uint32_t v[4][16];
+                const auto load = [&](int i) { tmem_ld16(lanes + buf * WIDE + 16 * i, v[i & 3]); };
+                const auto add = [&](int i) {
 #pragma unroll
                     for (int l = 0; l < 8; ++l)
-                        acc[i][l] = f2fma(f2pack(__uint_as_float(v[i & 1][2 * l]), __uint_as_float(v[i & 1][2 * l + 1])), k,
+                        acc[i][l] = f2fma(f2pack(__uint_as_float(v[i & 3][2 * l]), __uint_as_float(v[i & 3][2 * l + 1])), k,
                                           acc[i][l]);
-                }
+                };
+                static_assert(kParts == 8, "eight parts");
+                load(0), load(1), load(2), load(3);
+                tmem_wait_ld();
+                add(0), load(4), add(1), load(5);
+                tmem_wait_ld();
+                add(2), load(6), add(3), load(7);
+                tmem_wait_ld();
+                fence_before();
+                __syncwarp();
+                arrive_relaxed_if(lane == 0, acce + 8 * buf);
+                add(4), add(5), add(6), add(7);
                 if (group_ends) {
                     if (lane == 0) mbar_arrive(sempty0 + 8 * group_at);  // behind the arrive above: all lanes have read
                     group_at ^= 1;
@@ -521,62 +524,65 @@ __global__ void __launch_bounds__(THREADS, 1)
                             acc[i][4 * h + l] = f2add(acc[i][4 * h + l], f2pack(bf16lo(u[l]), bf16hi(u[l])));
                     }
             }
-            // rows of 128 bytes through shared memory: 64 bf16 or 32 fp32, by TMA where all 32 rows are the slice's
-            const auto store_box = [&](int column, auto put) {
-                const uint32_t box = stage + (boxes & 1) * BOX_BYTES;
-                ++boxes;
-                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            // Rows of 128 bytes through shared memory, 64 bf16 or 32 fp32, two boxes at a time: by TMA where all 32 rows are
+            // the slice's, which nothing waits for.
+            const auto store_boxes = [&](int column, int width, auto put) {
+                if (lane < 2) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 __syncwarp();
-                put(box);
+                put(0, stage);
+                put(1, stage + BOX_BYTES);
                 if (rows == 32) {
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0 && column < live)
+                    if (lane < 2 && column + lane * width < live)
                         asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                                          (uint64_t)&tmOut),
-                                     "r"(f0 + column), "r"(row), "r"(box)
+                                     "r"(f0 + column + lane * width), "r"(row), "r"(stage + lane * BOX_BYTES)
                                      : "memory");
+                    if (lane < 2) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 } else {
                     __syncwarp();
                     const int size = p.out_f32 ? 4 : 2, piece = lane & 7;
-                    uint8_t* o = static_cast<uint8_t*>(p.out) + ((int64_t)row * ld + f0 + column) * size + piece * 16;
-                    if (column * size + piece * 16 < live * size)
-                        for (int m = lane >> 3; m < rows; m += 4)
-                            *reinterpret_cast<uint4*>(o + m * ld * size) = ld_shared(box_piece(box, m, piece));
+                    for (int i = 0; i < 2; ++i) {
+                        const int at = (column + i * width) * size + piece * 16;  // bytes of the row
+                        uint8_t* o = static_cast<uint8_t*>(p.out) + ((int64_t)row * ld + f0) * size + at;
+                        if (at < live * size)
+                            for (int m = lane >> 3; m < rows; m += 4)
+                                *reinterpret_cast<uint4*>(o + m * ld * size) =
+                                    ld_shared(box_piece(stage + i * BOX_BYTES, m, piece));
+                    }
                     __syncwarp();
                 }
-                if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             };
             if (p.out_f32) {
 #pragma unroll
-                for (int i = 0; i < kParts; i += 2)
-                    store_box(16 * i, [&](uint32_t box) {
+                for (int i = 0; i < kParts; i += 4)
+                    store_boxes(16 * i, 32, [&](int half, uint32_t box) {
 #pragma unroll
                         for (int h = 0; h < 8; ++h) {
-                            const float2 a = f2unpack(acc[i + (h >> 2)][2 * (h & 3)]), b = f2unpack(acc[i + (h >> 2)][2 * (h & 3) + 1]);
+                            const int part = i + 2 * half + (h >> 2);
+                            const float2 a = f2unpack(acc[part][2 * (h & 3)]), b = f2unpack(acc[part][2 * (h & 3) + 1]);
                             st_shared(box_piece(box, lane, h), make_uint4(__float_as_uint(a.x), __float_as_uint(a.y),
                                                                           __float_as_uint(b.x), __float_as_uint(b.y)));
                         }
                     });
             } else {
+                store_boxes(0, 64, [&](int half, uint32_t box) {
 #pragma unroll
-                for (int i = 0; i < kParts; i += 4)
-                    store_box(16 * i, [&](uint32_t box) {
+                    for (int h = 0; h < 8; ++h) {
+                        uint32_t u[4];
 #pragma unroll
-                        for (int h = 0; h < 8; ++h) {
-                            uint32_t u[4];
-#pragma unroll
-                            for (int l = 0; l < 4; ++l) {
-                                const float2 a = f2unpack(acc[i + (h >> 1)][4 * (h & 1) + l]);
-                                u[l] = bf16x2_bits(a.x, a.y);
-                            }
-                            st_shared(box_piece(box, lane, h), make_uint4(u[0], u[1], u[2], u[3]));
+                        for (int l = 0; l < 4; ++l) {
+                            const float2 a = f2unpack(acc[4 * half + (h >> 1)][4 * (h & 1) + l]);
+                            u[l] = bf16x2_bits(a.x, a.y);
                         }
-                    });
+                        st_shared(box_piece(box, lane, h), make_uint4(u[0], u[1], u[2], u[3]));
+                    }
+                });
             }
         }
         // the last boxes are written before the block leaves its shared memory
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (lane < 2) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
     }
     fence_before();
