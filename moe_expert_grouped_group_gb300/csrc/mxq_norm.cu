@@ -589,10 +589,10 @@ static Shape shape_of(int64_t F, int most_threads) {
     return s;
 }
 
-// As many clusters as the device holds, no more than `clusters`, which is set to their number. The kernel's attribute
-// and its co-residency are set and asked for once per device and number of threads.
+// `waves` times as many clusters as the device holds, no more than `clusters`, which is set to their number. The kernel's
+// attribute and its co-residency are set and asked for once per device and number of threads.
 template <auto kKernel, class P>
-static cudaError_t launch_rows(const P& p, const Shape& s, int64_t& clusters, int smem, cudaStream_t st) {
+static cudaError_t launch_rows(const P& p, const Shape& s, int64_t& clusters, int waves, int smem, cudaStream_t st) {
     static std::atomic<int> cache[64][kFwdThreads / 32 + 1];
     int dev = 0, most = 0;
     cudaGetDevice(&dev);
@@ -620,7 +620,7 @@ static cudaError_t launch_rows(const P& p, const Shape& s, int64_t& clusters, in
         if (dev < 64) cache[dev][s.threads / 32].store(most, std::memory_order_release);
         cfg.dynamicSmemBytes = smem;
     }
-    clusters = std::min<int64_t>(clusters, most);
+    clusters = std::min<int64_t>(clusters, (int64_t)waves * most);
     cfg.gridDim = dim3((unsigned)(clusters * s.ctas));
     cfg.stream = st;
     cfg.numAttrs = 2;
@@ -630,7 +630,10 @@ static cudaError_t launch_rows(const P& p, const Shape& s, int64_t& clusters, in
 template <class T, int kC>
 static cudaError_t fwd_rows(const Fwd<T>& p, const Shape& s, cudaStream_t st) {
     int64_t clusters = p.M;
-    return launch_rows<norm_fwd_kernel<T, kC>>(p, s, clusters, smem_bytes(2, s.width, sizeof(T)), st);
+    // Blocks that start as others end even out short rows (bf16, us, with one wave and with four: 40961 x 2048 122 and 118,
+    // 83968 x 1024 128 and 123; 8192 x 8192 100 and 107).
+    const int waves = s.threads <= 256 ? 4 : 1;
+    return launch_rows<norm_fwd_kernel<T, kC>>(p, s, clusters, kC == 1 ? waves : 1, smem_bytes(2, s.width, sizeof(T)), st);
 }
 
 template <class T>
@@ -647,7 +650,8 @@ static cudaError_t fwd(const NormFwd& c, cudaStream_t st) {
     }
     switch (s.ctas) {
         case 1: return fwd_rows<T, 1>(p, s, st);
-        default: return fwd_rows<T, 8>(p, s, st);
+        case 8: return fwd_rows<T, 8>(p, s, st);
+        default: return cudaErrorInvalidConfiguration;  // no such width
     }
 }
 
@@ -665,7 +669,7 @@ static int64_t bwd_parts(int64_t M, int64_t F) {
 
 template <class T, int kC>
 static cudaError_t bwd_rows(const Bwd<T>& p, const Shape& s, int64_t& parts, cudaStream_t st) {
-    return launch_rows<norm_bwd_kernel<T, kC>>(p, s, parts, smem_bytes(4, s.width, sizeof(T)), st);
+    return launch_rows<norm_bwd_kernel<T, kC>>(p, s, parts, 1, smem_bytes(4, s.width, sizeof(T)), st);
 }
 
 template <class T>
@@ -683,7 +687,8 @@ static cudaError_t bwd(const NormBwd& c, cudaStream_t st) {
     } else {
         e = s.ctas == 1   ? bwd_rows<T, 1>(p, s, parts, st)
             : s.ctas == 4 ? bwd_rows<T, 4>(p, s, parts, st)
-                          : bwd_rows<T, 8>(p, s, parts, st);
+            : s.ctas == 8 ? bwd_rows<T, 8>(p, s, parts, st)
+                          : cudaErrorInvalidConfiguration;  // no such width
     }
     if (e != cudaSuccess || (!c.dpost && !c.dpre)) return e;
     return ragged::launch(norm_weights_kernel, dim3((unsigned)((c.F + 31) / 32), 2), 1024, st, 0, (const float*)c.partials,
