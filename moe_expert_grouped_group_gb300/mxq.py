@@ -1102,13 +1102,14 @@ def norm_residual_fwd(x, residual=None, post_weight=None, pre_weight=None, gate=
     return r, n, stats
 
 
-def norm_residual_bwd(dres, dn, x, res, stats, post_weight=None, pre_weight=None, gate=None, scale=1.0, status=None,
-                      out=None, workspace=None):
+def norm_residual_bwd(dres, dn, x, res, stats, post_weight=None, pre_weight=None, gate=None, scale=1.0, dx_out=True,
+                      dresidual_out=True, status=None, out=None, workspace=None):
     """The gradients of norm_residual_fwd from dres (of r', may be None) and dn (of n, None exactly without
     pre_weight). x, weights, gate and scale are the forward call's, res its r' and stats its statistics; x
     may be None without post_weight and gate, res without pre_weight. Returns a dict: dx, dresidual (M, F),
-    dpost_weight, dpre_weight (F,) fp32, dgate (M,) fp32, those of arguments that were given. out: tensors
-    to write to, by the same names; dresidual may be dres."""
+    dpost_weight, dpre_weight (F,) fp32, dgate (M,) fp32, those of arguments that were given and not left out
+    by dx_out or dresidual_out (one of the two is needed). out: tensors to write to, by the same names;
+    dresidual may be dres."""
     like = dn if dn is not None else dres
     if like is None:
         raise MXQError("dres or dn is required")
@@ -1124,7 +1125,8 @@ def norm_residual_bwd(dres, dn, x, res, stats, post_weight=None, pre_weight=None
             return t.data_ptr()
         return _packed(t, key, want, (dtype,))
 
-    dxp, drp = output("dx", shape, (F, 1), dt), output("dresidual", shape, (F, 1), dt)
+    dxp = output("dx", shape, (F, 1), dt) if dx_out else None
+    drp = output("dresidual", shape, (F, 1), dt) if dresidual_out else None
     post = pre = gp = ws = None
     ws_bytes = 0
     if post_weight is not None:
