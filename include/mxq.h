@@ -492,7 +492,8 @@ MXQ_API int mxq_fp8_quantize_weight(const void* w_bf16, int64_t N, int64_t K, in
  * xq[m,k] wq[e,n,k]) (+ bias[e,n]); y (M, N) bf16, or fp32 with MXQ_OUT_F32;
  * bias (E, N) bf16 or NULL. A block's 128 products are summed by the tensor core
  * (truncating, up to 2^-23 of their magnitudes for every 32), blocks in fp32 by
- * fused multiply-adds with the product of the two scales rounded to fp32.
+ * fused multiply-adds with the product of the two scales rounded to fp32 (which
+ * loses bits below 2^-126).
  * K % 16 == 0, N % 8 == 0. */
 MXQ_API int mxq_fp8_gemm_fprop(const void* xq, const float* x_scale, const void* wq, const float* w_scale,
                                const void* bias_bf16, int64_t M, int64_t N, int64_t K, int E,

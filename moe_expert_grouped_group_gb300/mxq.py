@@ -763,6 +763,12 @@ def _shape(t, name, want):
         raise MXQError(f"{name}: shape {tuple(t.shape)}, expected {want}")
 
 
+def _here(t, name):
+    """The kernels run on the current device, whose stream they get: tensors elsewhere are refused."""
+    if t.get_device() != _current_device():
+        raise MXQError(f"{name}: on device {t.get_device()}, the current one is {_current_device()}")
+
+
 def _packed(t, name, want, dtypes):
     """Pointer of a tensor of shape `want` that may be passed: its own bytes would not tell a transposed
     one. Dimensions of one do not count, and a flat tensor of as many elements is the same memory."""
@@ -862,6 +868,7 @@ def ragged_gemm_fprop_swiglu(x, w, m_splits, bias=None, y_out=False, status=None
     slice of wider ones; w (E, 2F, K), gate first; bias (E, 2F). Returns h (M, F) or, with y_out, h and
     [g | u] (M, 2F). out: what is returned, to write to."""
     xp, M, K, ldx = _rows(x, "x", _BF16)
+    _here(x, "x")
     E, F2, Kw = w.shape
     _shape(w, "w", (E, F2, K))
     if F2 & 1:
@@ -884,6 +891,7 @@ def ragged_gemm_dgrad_swiglu(dy, w, y1, m_splits, h_out=False, status=None, out=
     backward, on bf16, any expert counts. dy (M, N), its rows possibly a slice of wider ones; w (E, N, F).
     Returns [dg | du] (M, 2F) or, with h_out, it and h = silu(g) * u (M, F). out: what is returned, to write to."""
     dyp, M, N, lddy = _rows(dy, "dy", _BF16)
+    _here(dy, "dy")
     E, Nw, F = w.shape
     _shape(w, "w", (E, N, F))
     if out is None:
@@ -986,6 +994,7 @@ def fp8_quantize_rows(x, out=None):
     """bf16 rows (M, K) -> (E4M3 codes (M, K) uint8, fp32 scales (ceil(K/128), M)): one scale for 128
     values of a row, x ~ q * scale."""
     xp, M, K, ldx = _rows(x, "x", _BF16)
+    _here(x, "x")
     if out is None:
         new = _allocator(x)
         q, scale = new((M, K), (K, 1), torch.uint8), new((_blocks(K), M), (M, 1), torch.float32)
@@ -1004,6 +1013,7 @@ def fp8_quantize_weight(w, out=None):
     wp = _dev(w, "w", 0, _BF16)
     if w is None or w.dim() != 3:
         raise MXQError("w: expected a 3-D tensor (E, N, K)")
+    _here(w, "w")
     E, N, K = w.shape
     want = (E, _blocks(N), _blocks(K))
     if out is None:
@@ -1027,7 +1037,9 @@ def fp8_gemm_fprop(xq, x_scale, wq, w_scale, m_splits, bias=None, out_dtype=None
         _shape(wq, "wq", (E, N, K))
     kb = _blocks(K)
     out, op, flag = _out(out, out_dtype, (M, N), xq, torch.bfloat16, torch.float32, OUT_F32)
-    rc = lib().mxq_fp8_gemm_fprop(_dev(xq, "xq", 0, _E4M3), _packed(x_scale, "x_scale", (kb, M), _F32),
+    xp = _dev(xq, "xq", 0, _E4M3)
+    _here(xq, "xq")
+    rc = lib().mxq_fp8_gemm_fprop(xp, _packed(x_scale, "x_scale", (kb, M), _F32),
                                   _dev(wq, "wq", 0, _E4M3), _packed(w_scale, "w_scale", (E, _blocks(N), kb), _F32),
                                   _packed(bias, "bias", (E, N), _BF16), M, N, K, E, _grouping(m_splits, E), flag, op,
                                   _dev(status, "status", 4, _I32), _stream())
@@ -1045,7 +1057,9 @@ def fp8_gemm_dgrad(dyq, dy_scale, wq, w_scale, m_splits, out_dtype=None, status=
         _shape(wq, "wq", (E, N, K))
     nb = _blocks(N)
     out, op, flag = _out(out, out_dtype, (M, K), dyq, torch.bfloat16, torch.float32, OUT_F32)
-    rc = lib().mxq_fp8_gemm_dgrad(_dev(dyq, "dyq", 0, _E4M3), _packed(dy_scale, "dy_scale", (nb, M), _F32),
+    dyp = _dev(dyq, "dyq", 0, _E4M3)
+    _here(dyq, "dyq")
+    rc = lib().mxq_fp8_gemm_dgrad(dyp, _packed(dy_scale, "dy_scale", (nb, M), _F32),
                                   _dev(wq, "wq", 0, _E4M3), _packed(w_scale, "w_scale", (E, nb, _blocks(K)), _F32), M, N, K, E,
                                   _grouping(m_splits, E), flag, op, _dev(status, "status", 4, _I32), _stream())
     if rc:
@@ -1057,6 +1071,7 @@ def _norm_row(t, name):
     p = _dev(t, name, 0, _BF16_F32)
     if p is None or t.dim() != 2:
         raise MXQError(f"{name}: expected a 2-D tensor (M, F)")
+    _here(t, name)
     return p
 
 

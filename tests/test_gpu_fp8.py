@@ -150,6 +150,56 @@ def test_wrong_counts_write_nothing(mxq, counts):
         assert mxq.status_read(status) & bit and (out == 7.0).all()
 
 
+def test_many_experts(mxq):
+    """As many experts as a call takes, most without rows: few rows on average, and tiles of a pair of SMs."""
+    E, N, K = 1024, 24, 144
+    for per, some in ((1, 7), (40, 331)):
+        counts = [0] * E
+        for e in range(0, E, some):
+            counts[e] = E * per // len(range(0, E, some))
+        x, xs, w, ws = make(E, counts, N, K, False)
+        y = mxq.fp8_gemm_fprop(x, xs, w, ws, splits(counts))
+        ref, mag = fprop64(row_values(x, xs), weight_values(w, ws), counts)
+        assert ((y.double() - ref).abs() <= fp8_tolerance(K, BF16) * mag).all()
+    with pytest.raises(mxq.MXQError):
+        mxq.fp8_gemm_fprop(x[:0], xs[:, :0].contiguous(), w.repeat(2, 1, 1), ws.repeat(2, 1, 1), splits(counts + counts))
+
+
+def test_offsets_beyond_32_bits(mxq):
+    """Rows, results and weights of more than 2^31 elements: the last ones."""
+    M = (1 << 18) + 3
+    ms = splits([M - 5, 5])
+    x = normal(1, 16, 8208).repeat(-(-M // 16), 1)[:M]
+    w = normal(2, 2, 16, 8208, std=0.02)
+    q, s = mxq.fp8_quantize_rows(x)
+    tail_q, tail_s = quantize_rows(x[-16:])
+    same_codes(q[-16:], tail_q)
+    same_scales(s[:, -16:].contiguous(), tail_s)
+    wq, ws = mxq.fp8_quantize_weight(w)
+    y = mxq.fp8_gemm_fprop(q, s, wq, ws, ms)
+    ref, mag = fprop64(row_values(tail_q, tail_s), weight_values(wq.view(E4M3), ws), [11, 5])
+    assert ((y[-16:].double() - ref).abs() <= fp8_tolerance(8208, BF16) * mag).all()
+    del x, q, s, y
+    d = normal(3, 16, 16).repeat(-(-M // 16), 1)[:M].contiguous()  # dX (M, 8208)
+    q, s = mxq.fp8_quantize_rows(d)
+    for dtype in (BF16, F32):
+        dx = mxq.fp8_gemm_dgrad(q, s, wq, ws, ms, out_dtype=dtype)
+        ref, mag = dgrad64(row_values(q[-16:].view(E4M3), s[:, -16:]), weight_values(wq.view(E4M3), ws), [11, 5])
+        assert ((dx[-16:].double() - ref).abs() <= fp8_tolerance(16, dtype) * mag).all()
+        del dx
+    w = normal(4, 3, 1, 1, std=0.02).expand(3, 32768, 32768).contiguous()
+    w[2, -128:, -128:] = normal(5, 128, 128)
+    wq, ws = mxq.fp8_quantize_weight(w)
+    tail_q, tail_s = quantize_weight(w[2:, -128:, -128:])
+    same_codes(wq[2:, -128:, -128:].contiguous(), tail_q)
+    same_scales(ws[2:, -1:, -1:].contiguous(), tail_s)
+    xq, xs = mxq.fp8_quantize_rows(normal(6, 3, 32768))
+    y = mxq.fp8_gemm_fprop(xq, xs, wq, ws, splits([1, 1, 1]))
+    v = row_values(xq.view(E4M3), xs)[2]
+    values = weight_values(wq[2:, -128:].view(E4M3), ws[2:, -1:])[0]
+    assert ((y[2, -128:].double() - values @ v).abs() <= fp8_tolerance(32768, BF16) * (values.abs() @ v.abs())).all()
+
+
 def test_no_rows(mxq):
     ms = splits([0, 0])
     w, ws = mxq.fp8_quantize_weight(normal(1, 2, 32, 48))

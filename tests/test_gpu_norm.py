@@ -156,12 +156,27 @@ def test_non_finite_rows(mxq):
     assert got[1][[3, 6]].isnan().all() and got[1][5, 100].isnan() and (got[1][5, :100] == 0).all()
 
 
-def test_no_rows(mxq):
-    a = make(5, 0, 64, F32)
+@pytest.mark.parametrize("F", [64, 512, 4104, 9000])
+def test_no_rows(mxq, F):
+    a = make(5, 0, F, F32)
     r, n, stats = mxq.norm_residual_fwd(**a)
-    assert r.shape == n.shape == (0, 64) and stats.shape == (2, 0)
+    assert r.shape == n.shape == (0, F) and stats.shape == (2, 0)
     g = mxq.norm_residual_bwd(r, n, a["x"], r, stats, a["post_weight"], a["pre_weight"], a["gate"])
     assert (g["dpost_weight"] == 0).all() and (g["dpre_weight"] == 0).all() and g["dgate"].shape == (0,)
+
+
+def test_one_output(mxq):
+    """dx or dresidual left out: the other's bits are the same; neither is refused."""
+    a = make(5, 40, 512, BF16)
+    r, n, stats = mxq.norm_residual_fwd(**a)
+    dres, dn = make(1, 40, 512, BF16)["x"], make(2, 40, 512, BF16)["x"]
+    args = (dres, dn, a["x"], r, stats, a["post_weight"], a["pre_weight"], a["gate"])
+    g = mxq.norm_residual_bwd(*args)
+    for left_out in ("dx", "dresidual"):
+        h = mxq.norm_residual_bwd(*args, **{left_out + "_out": False})
+        assert left_out not in h and set(h) | {left_out} == set(g) and all(torch.equal(h[k], g[k]) for k in h)
+    with pytest.raises(mxq.MXQError):
+        mxq.norm_residual_bwd(*args, dx_out=False, dresidual_out=False)
 
 
 def test_graph_and_bits(mxq):

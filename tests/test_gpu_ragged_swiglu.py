@@ -145,6 +145,37 @@ def test_wrong_counts_write_nothing(mxq, counts):
         assert mxq.status_read(status) & bit and (h == 7.0).all() and (d == 7.0).all()
 
 
+def test_many_experts(mxq):
+    E, F, K = 1024, 24, 72
+    w, w2 = normal(1, E, 2 * F, K, std=0.1), normal(2, E, K, F, std=0.1)
+    for per, some in ((1, 7), (40, 331)):
+        counts = [0] * E
+        for e in range(0, E, some):
+            counts[e] = E * per // len(range(0, E, some))
+        M = sum(counts)
+        x, y = normal(3, M, K), normal(4, M, 2 * F)
+        h, eh, _, _ = fprop_reference(x, w, counts, None)
+        check(mxq.ragged_gemm_fprop_swiglu(x, w, splits(counts)), h, eh, "h")
+        d, ed, _ = dgrad_reference(x, w2, y, counts)
+        check(mxq.ragged_gemm_dgrad_swiglu(x, w2, y, splits(counts)), d, ed, "dy1")
+
+
+def test_offsets_beyond_32_bits(mxq):
+    """[g | u] and its gradient of more than 2^31 elements: the last rows."""
+    M, F, K = (1 << 18) + 3, 4104, 16
+    x = normal(1, 16, K).repeat(-(-M // 16), 1)[:M].contiguous()
+    w = normal(2, 2, 2 * F, K, std=0.3)
+    h, y = mxq.ragged_gemm_fprop_swiglu(x, w, splits([M - 5, 5]), y_out=True)
+    ref, eh, ry, ey = fprop_reference(x[-16:], w, [11, 5], None)
+    check(h[-16:], ref, eh, "h")
+    check(y[-16:], ry, ey, "y")
+    w2 = normal(3, 2, K, F, std=0.3)
+    d, h2 = mxq.ragged_gemm_dgrad_swiglu(x, w2, y, splits([M - 5, 5]), h_out=True)
+    ref, ed, rh = dgrad_reference(x[-16:], w2, y[-16:], [11, 5])
+    check(d[-16:], ref, ed, "dy1")
+    check(h2[-16:], rh, APPROX * rh.abs(), "h")
+
+
 def test_no_rows(mxq):
     ms = splits([0, 0])
     x, y = torch.empty(0, 64, dtype=BF16, device="cuda"), torch.empty(0, 48, dtype=BF16, device="cuda")
