@@ -42,6 +42,32 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t at) {
     return v;
 }
 
+// Eight fp32 values, two to a packed instruction. The backward rows compute that way, which leaves registers for half as
+// many rows again on an SM (41k x 2048: 157 us against 178). The forward rows get no room by it, and a packed instruction
+// takes as long as two: 120 us against 103.
+struct V8 {
+    uint64_t p[4];
+    V8() = default;
+    explicit __device__ V8(const float (&f)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = f2pack(f[2 * i], f[2 * i + 1]);
+    }
+    __device__ void split(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = f2unpack(p[i]);
+            f[2 * i] = v.x, f[2 * i + 1] = v.y;
+        }
+    }
+    __device__ void fill(float v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = f2splat(v);
+    }
+    __device__ float sum() const {
+        const float2 s = f2unpack(f2add(f2add(p[0], p[1]), f2add(p[2], p[3])));
+        return s.x + s.y;
+    }
+};
 // Eight consecutive elements as they lie in memory.
 template <class T>
 struct Pack;
@@ -82,6 +108,19 @@ struct Pack<float> {
     }
 };
 
+template <class T>
+__device__ __forceinline__ V8 packed(const Pack<T>& k) {
+    float f[8];
+    k.values(f);
+    return V8(f);
+}
+template <class T>
+__device__ __forceinline__ void store8(T* p, const V8& v) {
+    float f[8];
+    v.split(f);
+    Pack<T>::store(p, f);
+}
+
 constexpr int kWarpWidth = 256;  // widest row of a warp
 constexpr int kThreads = 256;    // threads of a CTA for such rows
 // Most threads of a CTA for wider ones, with eight columns each, and of one that shares its rows with others.
@@ -100,8 +139,9 @@ __device__ __forceinline__ void async_load(uint32_t dst, const float* src) {
 }
 
 // The rows of kTensors tensors on their way to this CTA, and what there is one number of for a row (its statistics, its
-// gate): row n of the CTA's walk in stage n mod kStages. The numbers come the same way as the rows: read by every thread
-// one row ahead into registers, they were waited for at once (gradients of 84k x 1024: 300 us against 174).
+// gate): row n of the CTA's walk in stage n mod kStages
+// (32 bits: no memory holds more rows). The numbers come the same way as the rows: read by every thread one row ahead into
+// registers, they were waited for at once (gradients of 84k x 1024: 300 us against 174).
 template <class T, int kTensors, int kStages>
 struct Rows {
     const T* from[kTensors];  // this CTA's columns of row 0; null: not read
@@ -111,7 +151,7 @@ struct Rows {
     int width;
     __device__ uint32_t stage_bytes() const { return kTensors * width * (uint32_t)sizeof(T); }
     // by one thread
-    __device__ void load(int64_t n, int64_t m) const {
+    __device__ void load(uint32_t n, int64_t m) const {
         if (m >= M) return;
         const int s = (int)(n % kStages);
         mbar_expect_tx(full + 8 * s, total);
@@ -124,17 +164,17 @@ struct Rows {
             if (scalars[i]) async_load(scalars_at + 16 * s + 4 * i, scalars[i] + m);
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full + 8 * s) : "memory");
     }
-    __device__ float scalar(int64_t n, int i, float none) const {
+    __device__ float scalar(uint32_t n, int i, float none) const {
         float v = none;
         if (scalars[i])
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(scalars_at + 16 * (int)(n % kStages) + 4 * i) : "memory");
         return v;
     }
-    __device__ void get(int64_t n, int i, int f, Pack<T>& p) const {
+    __device__ void get(uint32_t n, int i, int f, Pack<T>& p) const {
         const uint32_t a = at + (uint32_t)(n % kStages) * stage_bytes() + (i * width + f) * (uint32_t)sizeof(T);
         p.load_shared(a);
     }
-    __device__ bool wait(int64_t n, volatile int* abort_flag) const {
+    __device__ bool wait(uint32_t n, volatile int* abort_flag) const {
         return mbar_wait(full + 8 * (int)(n % kStages), (uint32_t)(n / kStages) & 1, abort_flag);
     }
     // After an expired wait, which lets the others return at once: the last rows are waited for again, so that no copy
@@ -193,7 +233,7 @@ constexpr int kStages = 3, kSumBytes = 2 * kMaxParts * 4, kScalarBytes = 16 * kS
 constexpr int smem_bytes(int tensors, int width, int size) { return kStages * tensors * width * size + kTailBytes; }
 constexpr int kMostSmem = std::max(smem_bytes(2, 8 * kFwdThreads, 4), smem_bytes(4, 8 * kBwdThreads, 4));
 static_assert(kMostSmem <= 232448 && (2 + kStages) * 8 <= 64, "shared memory");
-constexpr int kSmThreads = 640;  // threads of an SM's CTAs in the backward kernel, by their registers
+constexpr int kSmThreads = 768;  // threads of an SM's CTAs in the backward kernel, by their registers
 
 // What a thread does with its eight columns of a row, in the order of the formulas. Weights: 1 without one.
 template <class T>
@@ -205,6 +245,13 @@ __device__ __forceinline__ void weights8(const T* w, int f, bool live, float (&v
         k.load(w + f);
         k.values(v);
     }
+}
+
+template <class T>
+__device__ __forceinline__ V8 packed_weights8(const T* w, int f, bool live) {
+    float v[8];
+    weights8(w, f, live, v);
+    return V8(v);
 }
 
 template <class T>
@@ -224,13 +271,15 @@ template <class T, class S>
 __device__ __forceinline__ void fwd_row(const Fwd<T>& p, int64_t m, int f, bool live, bool mine, float gate, const Pack<T>& xp,
                                         const Pack<T>& rp, const float (&w_post)[8], const float (&w_pre)[8], float inv,
                                         S sum) {
+    // rsqrtf is off by two units of the last place at most; 1 / sqrtf took every thread of a row through two long
+    // sequences (41k x 2048: 118 us against 104)
     float x[8], v[8], rstd = 1.0f, s = 0.0f;
     xp.values(x);
     rp.values(v);
     if (p.post) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
-        rstd = 1.0f / sqrtf(fmaf(sum(s), inv, p.eps));
+        rstd = rsqrtf(fmaf(sum(s), inv, p.eps));
         s = 0.0f;
     }
     if (p.stats && mine) p.stats[m] = rstd;
@@ -245,7 +294,7 @@ __device__ __forceinline__ void fwd_row(const Fwd<T>& p, int64_t m, int f, bool 
     }
     rstd = 1.0f;
     if (p.pre) {
-        rstd = 1.0f / sqrtf(fmaf(sum(s), inv, p.eps));
+        rstd = rsqrtf(fmaf(sum(s), inv, p.eps));
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= rstd * w_pre[j];
         if (live) Pack<T>::store(p.n + m * p.F + f, v);
@@ -254,9 +303,9 @@ __device__ __forceinline__ void fwd_row(const Fwd<T>& p, int64_t m, int f, bool 
 }
 
 // Rows of up to kWarpWidth columns: kLanes lanes each. Many warps hide the loads here; with the next row in registers, as
-// in the backward kernel, there were fewer (65536 x 256: 37 us).
+// in the backward kernel, there were fewer (65536 x 256: 37 us against 30). 64 registers, not 40: 25 us.
 template <class T, int kLanes>
-__global__ void __launch_bounds__(kThreads, 6) norm_fwd_lanes_kernel(Fwd<T> p) {
+__global__ void __launch_bounds__(kThreads, 4) norm_fwd_lanes_kernel(Fwd<T> p) {
     const int lane = threadIdx.x % kLanes, f = 8 * lane;
     const bool live = f < p.F;
     const float inv = 1.0f / (float)p.F;
@@ -313,7 +362,7 @@ __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(Fwd<T> p, int wid
     float w_post[8], w_pre[8];
     weights8(p.post, f0 + f, live, w_post);
     weights8(p.pre, f0 + f, live, w_pre);
-    int64_t n = 0;
+    uint32_t n = 0;
     for (int64_t m = first; m < p.M; m += step, ++n) {
         rows.wait(n, abort_flag);
         __syncwarp();
@@ -369,52 +418,57 @@ struct RowScalars {
 // get(i): dres (2) and x (3).
 template <class T, class G, class S>
 __device__ __forceinline__ void bwd_row(const Bwd<T>& p, int64_t m, int f, bool live, bool mine, const RowScalars& c,
-                                        const Pack<T>& rp, const Pack<T>& np, G get, const float (&w_post)[8], const float (&w_pre)[8], float (&d_post)[8],
-                                        float (&d_pre)[8], float inv, S sum) {
-    float rh[8], g[8], D[8], xh[8];
+                                        const Pack<T>& rp, const Pack<T>& np, G get, const V8& w_post, const V8& w_pre,
+                                        V8& d_post, V8& d_pre, float inv, S sum) {
+    V8 rh = packed(rp), g = packed(np), s;
     const float a = p.scale * c.gate;
-    rp.values(rh);
-    np.values(g);
+    const uint64_t k2 = f2splat(c.rstd2);
     float mean = 0.0f;
     if (p.pre) {
-        float s = 0.0f;
+        s.fill(0.0f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            rh[j] *= c.rstd2;
-            d_pre[j] = fmaf(g[j], rh[j], d_pre[j]);
-            g[j] *= w_pre[j];
-            s = fmaf(g[j], rh[j], s);
+        for (int i = 0; i < 4; ++i) {
+            rh.p[i] = f2mul(rh.p[i], k2);
+            d_pre.p[i] = f2fma(g.p[i], rh.p[i], d_pre.p[i]);
+            g.p[i] = f2mul(g.p[i], w_pre.p[i]);
+            s.p[i] = f2mul(g.p[i], rh.p[i]);
         }
-        mean = sum(s) * inv;
+        mean = sum(s.sum()) * inv;
     }
-    get(2).values(D);
-    if (p.pre)
+    V8 D = packed(get(2));
+    if (p.pre) {
+        const uint64_t minus = f2splat(-mean);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) D[j] = fmaf(c.rstd2, fmaf(-rh[j], mean, g[j]), D[j]);
-    if (p.dr && live) Pack<T>::store(p.dr + m * p.F + f, D);
+        for (int i = 0; i < 4; ++i) D.p[i] = f2fma(k2, f2fma(rh.p[i], minus, g.p[i]), D.p[i]);
+    }
+    if (p.dr && live) store8(p.dr + m * p.F + f, D);
     float dot = 0.0f;
+    V8 xh;
+    xh.fill(0.0f);
     if (p.post || p.gate) {
-        get(3).values(xh);
+        xh = packed(get(3));
+        const uint64_t k1 = f2splat(c.rstd1), ka = f2splat(a);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            xh[j] *= c.rstd1;
-            const float t = D[j] * xh[j];
-            d_post[j] = fmaf(a, t, d_post[j]);
-            dot = fmaf(t, w_post[j], dot);
+        for (int i = 0; i < 4; ++i) {
+            xh.p[i] = f2mul(xh.p[i], k1);
+            const uint64_t t = f2mul(D.p[i], xh.p[i]);
+            d_post.p[i] = f2fma(ka, t, d_post.p[i]);
+            s.p[i] = f2mul(t, w_post.p[i]);
         }
-        dot = sum(dot);
+        dot = sum(s.sum());
         if (p.dgate && mine) p.dgate[m] = p.scale * dot;
     }
     if (!p.dx || !live) return;
     if (p.post) {
-        const float mean = dot * inv, k = a * c.rstd1;
+        const uint64_t minus = f2splat(-dot * inv), k = f2splat(a * c.rstd1);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) D[j] = k * fmaf(-xh[j], mean, D[j] * w_post[j]);
+        for (int i = 0; i < 4; ++i) D.p[i] = f2mul(k, f2fma(xh.p[i], minus, f2mul(D.p[i], w_post.p[i])));
     } else {
+        const uint64_t k = f2splat(a);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) D[j] *= a;
+        for (int i = 0; i < 4; ++i) D.p[i] = f2mul(k, D.p[i]);
     }
-    Pack<T>::store(p.dx + m * p.F + f, D);
+    store8(p.dx + m * p.F + f, D);
 }
 
 template <class T, int kLanes>
@@ -425,11 +479,9 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_lanes_kernel(Bwd<T> p) {
     const bool live = f < p.F, dots = p.post || p.gate;
     const float inv = 1.0f / (float)p.F;
     wait_for_stream();
-    float w_post[8], w_pre[8], d_post[8], d_pre[8];
-    weights8(p.post, f, live, w_post);
-    weights8(p.pre, f, live, w_pre);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) d_post[j] = d_pre[j] = 0.0f;
+    const V8 w_post = packed_weights8(p.post, f, live), w_pre = packed_weights8(p.pre, f, live);
+    V8 d_post, d_pre;
+    d_post.fill(0.0f), d_pre.fill(0.0f);
     const int64_t step = (int64_t)gridDim.x * kTeams;
     int64_t m = (int64_t)blockIdx.x * kTeams + threadIdx.x / kLanes;
     const auto fetch = [&](int64_t row, Pack<T>(&v)[4], RowScalars& c) {
@@ -462,13 +514,13 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_lanes_kernel(Bwd<T> p) {
         c = nc;
     }
     // the block's parts of the weights' gradients: over a warp's teams, then over the warps
-    const auto leave = [&](float (&d)[8], float* out) {
+    const auto leave = [&](V8& d, float* out) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int o = kLanes; o < 32; o <<= 1) d[j] += __shfl_xor_sync(0xffffffffu, d[j], o);
+            for (int o = kLanes; o < 32; o <<= 1) d.p[i] = f2add(d.p[i], __shfl_xor_sync(0xffffffffu, d.p[i], o));
         __syncthreads();
-        if (threadIdx.x % 32 < kLanes) Pack<float>::store(&s_sum[threadIdx.x / 32][f], d);
+        if (threadIdx.x % 32 < kLanes) store8(&s_sum[threadIdx.x / 32][f], d);
         __syncthreads();
         if ((int)threadIdx.x < p.F) {
             float s = 0.0f;
@@ -510,12 +562,10 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(Bwd<T> p, int wid
     if (threadIdx.x == 0)
         for (int k = 0; k < kS; ++k) rows.load(k, first + k * step);
     RowSum<kC> sums(tail, bars, W, rank);
-    float w_post[8], w_pre[8], d_post[8], d_pre[8];
-    weights8(p.post, f0 + f, live, w_post);
-    weights8(p.pre, f0 + f, live, w_pre);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) d_post[j] = d_pre[j] = 0.0f;
-    int64_t n = 0;
+    const V8 w_post = packed_weights8(p.post, f0 + f, live), w_pre = packed_weights8(p.pre, f0 + f, live);
+    V8 d_post, d_pre;
+    d_post.fill(0.0f), d_pre.fill(0.0f);
+    uint32_t n = 0;
     for (int64_t m = first; m < p.M; m += step, ++n) {
         rows.wait(n, abort_flag);
         __syncwarp();
@@ -546,8 +596,8 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(Bwd<T> p, int wid
         if (p.status) atomicOr(p.status, MXQ_STATUS_WAIT_TIMEOUT);
     }
     const int64_t part = blockIdx.x / kC, parts = gridDim.x / kC;
-    if (p.post && live) Pack<float>::store(p.partials + part * p.F + f0 + f, d_post);
-    if (p.pre && live) Pack<float>::store(p.partials + (parts + part) * p.F + f0 + f, d_pre);
+    if (p.post && live) store8(p.partials + part * p.F + f0 + f, d_post);
+    if (p.pre && live) store8(p.partials + (parts + part) * p.F + f0 + f, d_pre);
     if (kC > 1) ragged::cluster_sync();  // nothing is on its way to a CTA that has ended
 }
 
@@ -630,8 +680,8 @@ static cudaError_t launch_rows(const P& p, const Shape& s, int64_t& clusters, in
 template <class T, int kC>
 static cudaError_t fwd_rows(const Fwd<T>& p, const Shape& s, cudaStream_t st) {
     int64_t clusters = p.M;
-    // Blocks that start as others end even out short rows (bf16, us, with one wave and with four: 40961 x 2048 122 and 118,
-    // 83968 x 1024 128 and 123; 8192 x 8192 100 and 107).
+    // Blocks that start as others end even out short rows (bf16, us, with one wave and with four: 40961 x 2048 109 and 103,
+    // 83968 x 1024 114 and 112; 8192 x 8192 93 and 100).
     const int waves = s.threads <= 256 ? 4 : 1;
     return launch_rows<norm_fwd_kernel<T, kC>>(p, s, clusters, kC == 1 ? waves : 1, smem_bytes(2, s.width, sizeof(T)), st);
 }
