@@ -3,7 +3,8 @@
 //   fprop  Y[m,:]  = X[m,:]  . W[e(m)]^T (+ b[e(m)])
 //   dgrad  dX[m,:] = dY[m,:] . W[e(m)]
 //   wgrad  dW[e]   = dY_e^T . X_e
-// fp32 sums, one rounding to bf16 (or none, fp32 outputs).
+// fp32 sums, one rounding to bf16 (or none, fp32 outputs). Two more modes have
+// SwiGLU in their epilogue, FC1's product and FC2's dgrad (mxq_ragged_swiglu.cuh).
 //
 // Which operand is which. The output's contiguous dimension is put on the
 // MMA's M (TMEM lanes), its rows on the MMA's N (accumulator columns): W and

@@ -1,5 +1,6 @@
 // mxq_ragged.cuh -- what the ragged grouped products (mxq_ragged.cu and
-// mxq_ragged_few.cu, bf16; mxq_ragged_int8.cu; mxq_ragged_vec.cu) share: the
+// mxq_ragged_few.cu, bf16; mxq_ragged_int8.cu; mxq_ragged_vec.cu;
+// mxq_ragged_fp8.cu) share: the
 // tables of a ragged grouping, the tile walk and queue, split sums, the bf16
 // epilogue, the tcgen05 wrappers for 16-bit floating operands, the launchers.
 #pragma once

@@ -1,4 +1,4 @@
-// mxq_ragged_few.cu -- bf16 fprop and dgrad for experts with few rows (the
+// mxq_ragged_few.cu -- bf16 fprop (with SwiGLU too) and dgrad for experts with few rows (the
 // steps of serving, short tails of training): the products of mxq_ragged.cu on
 // one-SM tiles of 128 features by up to 32 rows.
 //

@@ -13,7 +13,15 @@
 // accumulator holds one block (four MMAs of 32 k, kind::f8f6f4), and the
 // epilogue's warps add it to sums in registers, one fused multiply-add an
 // element, while the MMAs fill the other accumulator. That is the bottleneck:
-// everything an accumulator holds leaves TMEM once a block.
+// everything an accumulator holds leaves TMEM once a block. Stamped in one CTA
+// (16384 x 2048 by 4096 x 2048), a block takes its epilogue warps 730 to 760
+// cycles: 150 for two barriers and the factor, 330 from the first load to the
+// last with half of the FMAs, 210 for the other half; its MMAs take 512 at the
+// pipe's rate. A tile's end takes 2300 more, of 14000: 780 to the staged rows, 620 for
+// the proxy fence and the boxes, 900 to the next tile's first sums. Loads that
+// run on from one block into the next (two at a time 128 us for the product,
+// four 120 to 124, against 112), the next factor read a block ahead (112.5, but
+// dgrad 117 against 107) and FMAs one at a time (118) were slower.
 //
 // Which operand is which. In the pair kernel the tokens are on the MMA's M: a
 // thread of the epilogue has one token, so one factor for a block and 128

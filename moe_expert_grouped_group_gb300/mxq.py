@@ -763,10 +763,25 @@ def _shape(t, name, want):
         raise MXQError(f"{name}: shape {tuple(t.shape)}, expected {want}")
 
 
-def _here(t, name):
+def _outputs(out):
+    """The tensors of an `out` argument, one or a tuple of them."""
+    return () if out is None else out if isinstance(out, (tuple, list)) else (out,)
+
+
+@functools.lru_cache(maxsize=1)
+def _several_devices():
+    return torch.cuda.device_count() > 1
+
+
+def _here(t, name, *others):
     """The kernels run on the current device, whose stream they get: tensors elsewhere are refused."""
-    if t.get_device() != _current_device():
-        raise MXQError(f"{name}: on device {t.get_device()}, the current one is {_current_device()}")
+    here = _current_device()
+    if t.get_device() != here:
+        raise MXQError(f"{name}: on device {t.get_device()}, the current one is {here}")
+    if _several_devices():
+        for o in others:
+            if o is not None and o.get_device() != here:
+                raise MXQError(f"an argument beside {name} is on device {o.get_device()}, the current one is {here}")
 
 
 def _packed(t, name, want, dtypes):
@@ -868,7 +883,7 @@ def ragged_gemm_fprop_swiglu(x, w, m_splits, bias=None, y_out=False, status=None
     slice of wider ones; w (E, 2F, K), gate first; bias (E, 2F). Returns h (M, F) or, with y_out, h and
     [g | u] (M, 2F). out: what is returned, to write to."""
     xp, M, K, ldx = _rows(x, "x", _BF16)
-    _here(x, "x")
+    _here(x, "x", w, m_splits, bias, status, *_outputs(out))
     E, F2, Kw = w.shape
     _shape(w, "w", (E, F2, K))
     if F2 & 1:
@@ -891,7 +906,7 @@ def ragged_gemm_dgrad_swiglu(dy, w, y1, m_splits, h_out=False, status=None, out=
     backward, on bf16, any expert counts. dy (M, N), its rows possibly a slice of wider ones; w (E, N, F).
     Returns [dg | du] (M, 2F) or, with h_out, it and h = silu(g) * u (M, F). out: what is returned, to write to."""
     dyp, M, N, lddy = _rows(dy, "dy", _BF16)
-    _here(dy, "dy")
+    _here(dy, "dy", w, y1, m_splits, status, *_outputs(out))
     E, Nw, F = w.shape
     _shape(w, "w", (E, N, F))
     if out is None:
@@ -994,7 +1009,7 @@ def fp8_quantize_rows(x, out=None):
     """bf16 rows (M, K) -> (E4M3 codes (M, K) uint8, fp32 scales (ceil(K/128), M)): one scale for 128
     values of a row, x ~ q * scale."""
     xp, M, K, ldx = _rows(x, "x", _BF16)
-    _here(x, "x")
+    _here(x, "x", *_outputs(out))
     if out is None:
         new = _allocator(x)
         q, scale = new((M, K), (K, 1), torch.uint8), new((_blocks(K), M), (M, 1), torch.float32)
@@ -1013,7 +1028,7 @@ def fp8_quantize_weight(w, out=None):
     wp = _dev(w, "w", 0, _BF16)
     if w is None or w.dim() != 3:
         raise MXQError("w: expected a 3-D tensor (E, N, K)")
-    _here(w, "w")
+    _here(w, "w", *_outputs(out))
     E, N, K = w.shape
     want = (E, _blocks(N), _blocks(K))
     if out is None:
@@ -1038,7 +1053,7 @@ def fp8_gemm_fprop(xq, x_scale, wq, w_scale, m_splits, bias=None, out_dtype=None
     kb = _blocks(K)
     out, op, flag = _out(out, out_dtype, (M, N), xq, torch.bfloat16, torch.float32, OUT_F32)
     xp = _dev(xq, "xq", 0, _E4M3)
-    _here(xq, "xq")
+    _here(xq, "xq", x_scale, wq, w_scale, m_splits, bias, status, out)
     rc = lib().mxq_fp8_gemm_fprop(xp, _packed(x_scale, "x_scale", (kb, M), _F32),
                                   _dev(wq, "wq", 0, _E4M3), _packed(w_scale, "w_scale", (E, _blocks(N), kb), _F32),
                                   _packed(bias, "bias", (E, N), _BF16), M, N, K, E, _grouping(m_splits, E), flag, op,
@@ -1058,7 +1073,7 @@ def fp8_gemm_dgrad(dyq, dy_scale, wq, w_scale, m_splits, out_dtype=None, status=
     nb = _blocks(N)
     out, op, flag = _out(out, out_dtype, (M, K), dyq, torch.bfloat16, torch.float32, OUT_F32)
     dyp = _dev(dyq, "dyq", 0, _E4M3)
-    _here(dyq, "dyq")
+    _here(dyq, "dyq", dy_scale, wq, w_scale, m_splits, status, out)
     rc = lib().mxq_fp8_gemm_dgrad(dyp, _packed(dy_scale, "dy_scale", (nb, M), _F32),
                                   _dev(wq, "wq", 0, _E4M3), _packed(w_scale, "w_scale", (E, nb, _blocks(K)), _F32), M, N, K, E,
                                   _grouping(m_splits, E), flag, op, _dev(status, "status", 4, _I32), _stream())
@@ -1067,11 +1082,11 @@ def fp8_gemm_dgrad(dyq, dy_scale, wq, w_scale, m_splits, out_dtype=None, status=
     return out
 
 
-def _norm_row(t, name):
+def _norm_row(t, name, *others):
     p = _dev(t, name, 0, _BF16_F32)
     if p is None or t.dim() != 2:
         raise MXQError(f"{name}: expected a 2-D tensor (M, F)")
-    _here(t, name)
+    _here(t, name, *others)
     return p
 
 
@@ -1083,7 +1098,8 @@ def norm_residual_fwd(x, residual=None, post_weight=None, pre_weight=None, gate=
     None without pre_weight, r' with res_out=False, stats (2, M) fp32 (what the backward call needs) with
     stats_out=False. out: a (r', n, stats) to write to, None where it is to be made; r' may be residual or
     x, n may be x."""
-    xp, (M, F), dt = _norm_row(x, "x"), x.shape, x.dtype
+    xp = _norm_row(x, "x", residual, post_weight, pre_weight, gate, status, *_outputs(out))
+    (M, F), dt = x.shape, x.dtype
     shape, same, new = (M, F), (dt,), _allocator(x)
     r, n, stats = out if out is not None else (None, None, None)
     rp = np = sp = None
@@ -1128,7 +1144,8 @@ def norm_residual_bwd(dres, dn, x, res, stats, post_weight=None, pre_weight=None
     like = dn if dn is not None else dres
     if like is None:
         raise MXQError("dres or dn is required")
-    _norm_row(like, "dn" if dn is not None else "dres")
+    _norm_row(like, "dn" if dn is not None else "dres", dres, x, res, stats, post_weight, pre_weight, gate, status, workspace,
+              *(out.values() if out else ()))
     (M, F), dt = like.shape, like.dtype
     shape, same, new = (M, F), (dt,), _allocator(like)
     o = dict(out) if out else {}

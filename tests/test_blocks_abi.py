@@ -105,3 +105,21 @@ def test_norm_gradients_are_the_definitions(post, pre, gated):
         h = 1e-5  # the difference's own error is of order h^2 and of the rounding over h
         diff = (loss({**t, k: t[k] + h * d}) - loss({**t, k: t[k] - h * d})) / (2 * h)
         assert abs(diff - (got[names[k]] * d).sum()) <= 1e-7 * (1 + (got[names[k]] * d).abs().sum())
+
+
+def test_tensors_of_another_device(monkeypatch):
+    from moe_expert_grouped_group_gb300 import mxq
+
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def get_device(self):
+            return self.device
+
+    monkeypatch.setattr(mxq, "_current_device", lambda: 1)
+    monkeypatch.setattr(mxq, "_several_devices", lambda: True)
+    mxq._here(On(1), "x", None, On(1), *mxq._outputs(None), *mxq._outputs((On(1), None)))
+    for args in ((On(0),), (On(1), On(0)), (On(1), None, *mxq._outputs(On(0))), (On(1), *mxq._outputs((On(1), On(0))))):
+        with pytest.raises(mxq.MXQError, match="on device 0, the current one is 1"):
+            mxq._here(args[0], "x", *args[1:])
