@@ -680,11 +680,12 @@ struct SplitSum {
 // cluster holds one tile more than it works on.
 struct TileQueue {
     uint32_t answer, ready, taken;  // 16 bytes; barrier of this CTA; barrier of rank 0 (cluster address)
+    uint32_t ctas;                  // of a cluster: 1 or 2
     uint32_t phase = 0;
     enum Result { kDone = 0, kTile = 1, kAbort = 2 };
 
-    __device__ TileQueue(uint32_t answer_, uint32_t ready_, uint32_t taken_)
-        : answer(answer_), ready(ready_), taken(taken_) {}
+    __device__ TileQueue(uint32_t answer_, uint32_t ready_, uint32_t taken_, uint32_t ctas_ = 2)
+        : answer(answer_), ready(ready_), taken(taken_), ctas(ctas_) {}
 
     // The next tile of this cluster, for a whole warp.
     __device__ Result next(int64_t& tile, int lane, volatile int* abort_flag) {
@@ -705,11 +706,18 @@ struct TileQueue {
         fence_async_smem();  // read before the next answer is written
         __syncwarp();
         if (lane == 0) arrive_remote(taken);
-        tile = first / 2;
+        tile = first / ctas;
         return valid ? kTile : kDone;
     }
     // Asks for the next cluster; the answer goes to `answer` and `ready` of both CTAs.
     __device__ void ask() const {
+        if (ctas == 1) {
+            asm volatile(
+                "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+                "r"(ready)
+                : "memory");
+            return;
+        }
         asm volatile(
             "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 "
             "[%0], [%1];" ::"r"(answer),

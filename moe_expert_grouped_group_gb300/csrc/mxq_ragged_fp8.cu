@@ -21,18 +21,20 @@
 // the proxy fence and the boxes, 900 to the next tile's first sums. Loads that
 // run on from one block into the next (two at a time 128 us for the product,
 // four 120 to 124, against 112), the next factor read a block ahead (112.5, but
-// dgrad 117 against 107) and FMAs one at a time (118) were slower.
+// dgrad 117 against 107) and FMAs one at a time (118) were slower. Without any
+// loads and FMAs the same kernel takes 95 us (dgrad 96): the rest is the MMAs,
+// their feed and the tiles' ends, as in the MXFP8 product of this shape.
 //
-// Which operand is which. In the pair kernel the tokens are on the MMA's M: a
+// Which operand is which. In the kernel for tiles of one SM (128 rows) or a
+// pair (256) the tokens are on the MMA's M: a
 // thread of the epilogue has one token, so one factor for a block and 128
 // features, and reads TMEM 32 lanes at a time. With the features on M, as in
 // the bf16 products, the factor differs from column to column: 256 factors a
 // block from shared memory cost more than the FMAs (a warp's 128 columns with
 // them 743 cycles, without 316), and fragment loads, which need few factors,
-// take TMEM twice as long (560). The price is that a tile has 256 rows whatever
-// the expert has; experts so small that it matters are bound by their weights'
-// bytes. Experts with few rows on average go to the kernel below, whose tokens
-// are on N.
+// take TMEM twice as long (560). The price is that a tile has 128 or 256 rows
+// whatever the expert has. Experts with few rows on average go to the kernel
+// below, whose tokens are on N.
 //
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -160,13 +162,10 @@ __device__ __forceinline__ void add_scaled(Sums& s, const uint32_t (&v)[16], flo
         s[i] = f2fma(f2pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), k[i >> 1], s[i]);
 }
 
-// ------------------------------------------------------------ pairs of SMs
-namespace pair {
+// ------------------------------------------------- pairs of SMs, and single ones
+namespace wide {
 
-constexpr int CG = 2;
-constexpr int ROWS = kFM * CG;   // token rows of a tile, on the MMA's M
-constexpr int WIDE = 256;        // features of a tile, on its N: two blocks of the weight
-constexpr int STAGES = 4;
+constexpr int WIDE = 256;        // features of a tile, on the MMA's N: two blocks of the weight
 constexpr int SLOTS = 8;         // blocks whose scales are on chip
 constexpr int GROUP = 4;         // and that are handed over together; a tile begins at a new group
 constexpr int AHEAD = 2;         // blocks whose scales' loads are in flight together
@@ -176,26 +175,33 @@ constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
 constexpr int CTL_REGS = 56, EPI_REGS = 224;
 static_assert(EPI_FIRST * CTL_REGS + EPI_WARPS * EPI_REGS <= THREADS / 32 * (65536 / THREADS / 8 * 8),
               "the warps' registers are those that the block starts with");
-constexpr int A_BYTES = kFM * BK, STAGE_BYTES = A_BYTES + WIDE / CG * BK;
 constexpr int TMEM_COLS = 2 * WIDE;
-constexpr int BOX_BYTES = 32 * 128;               // 32 rows of 128 bytes
-constexpr int EPI_REGION = STAGES * STAGE_BYTES;  // staging of the epilogue, two boxes a warp
-constexpr int SLOT_BYTES = 2 * kFM * 4;           // a factor for each of this CTA's rows and each block of features
-constexpr int SCALE_REGION = EPI_REGION + 2 * EPI_WARPS * BOX_BYTES;
-constexpr int BAR_REGION = SCALE_REGION + SLOTS * SLOT_BYTES;
-constexpr int BOARD_REGION = BAR_REGION + 256;  // a tile, see Board
-constexpr int TABLE_REGION = BOARD_REGION + 64;
-__host__ __device__ constexpr int smem_bytes(int E) { return 1024 + TABLE_REGION + 8 * (E + 1); }
-static_assert(smem_bytes(MXQ_MAX_EXPERTS) <= 232448, "shared memory over the per-block limit");
-static_assert(BAR_REGION % 1024 == 0 && 8 * (2 * STAGES + 4 + 8) + 16 <= 256, "barrier region");
+constexpr int BOX_BYTES = 32 * 128;      // 32 rows of 128 bytes
+constexpr int SLOT_BYTES = 2 * kFM * 4;  // a factor for each of this CTA's rows and each block of features
 
-// out[row + i][f0 + c] for i < rows, c < n: rows are of expert e, whose slices have ROWS each
+// Shared memory of a CTA. CG of them share a tile: each has 128 of its rows, and the codes of a CG-th of its features.
+template <int CG>
+struct Layout {
+    static constexpr int ROWS = kFM * CG;  // token rows of a tile, on the MMA's M
+    static constexpr int STAGES = CG == 2 ? 4 : 3;
+    static constexpr int A_BYTES = kFM * BK, STAGE_BYTES = A_BYTES + WIDE / CG * BK;
+    static constexpr int EPI_REGION = STAGES * STAGE_BYTES;  // staging of the epilogue, two boxes a warp
+    static constexpr int SCALE_REGION = EPI_REGION + 2 * EPI_WARPS * BOX_BYTES;
+    static constexpr int BAR_REGION = SCALE_REGION + SLOTS * SLOT_BYTES;
+    static constexpr int BOARD_REGION = BAR_REGION + 256;  // a tile, see Board
+    static constexpr int TABLE_REGION = BOARD_REGION + 64;
+    __host__ __device__ static constexpr int smem_bytes(int E) { return 1024 + TABLE_REGION + 8 * (E + 1); }
+    static_assert(1024 + TABLE_REGION + 8 * (MXQ_MAX_EXPERTS + 1) <= 232448, "shared memory over the per-block limit");
+    static_assert(BAR_REGION % 1024 == 0 && 8 * (2 * STAGES + 4 + 8) + 16 <= 256, "barrier region");
+};
+
 struct Tile {
     int e, f0, row, rows, n;
 };
 
 // Slices of an expert run fastest, so that the CTAs of one wave share its weight (a tile's number is below 2^31: the
 // outputs of more would not fit the device).
+template <int kRows>
 struct Walk {
     int feats, E;
     int64_t width, total;
@@ -211,8 +217,8 @@ struct Walk {
         const uint32_t count = slices[T.e + 1] - slices[T.e], r = (uint32_t)(t - (int64_t)slices[T.e] * feats);
         const int f = (int)(r / count), i = (int)(r - f * count);
         T.f0 = f * WIDE;
-        T.row = off[T.e] + i * ROWS;
-        T.rows = min(ROWS, off[T.e + 1] - T.row);
+        T.row = off[T.e] + i * kRows;
+        T.rows = min(kRows, off[T.e + 1] - T.row);
         T.n = width - T.f0 > WIDE / 2 ? WIDE : WIDE / 2;
         return T;
     }
@@ -258,20 +264,22 @@ struct Board {
 // 16-byte piece i (of 8) of a row of 128 bytes under the 128-byte swizzle
 __device__ __forceinline__ uint32_t box_piece(uint32_t box, int row, int i) { return box + row * 128 + ((i ^ (row & 7)) << 4); }
 
-template <int kMode>
+template <int kMode, int CG>
 __global__ void __launch_bounds__(THREADS, 1)
     ragged_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmOut, Params p) {
+    using L = Layout<CG>;
+    constexpr int ROWS = L::ROWS, STAGES = L::STAGES, A_BYTES = L::A_BYTES, STAGE_BYTES = L::STAGE_BYTES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align<1024>(smem_raw);
-    int32_t* s_off = reinterpret_cast<int32_t*>(smem + TABLE_REGION);
+    int32_t* s_off = reinterpret_cast<int32_t*>(smem + L::TABLE_REGION);
     int32_t* s_slices = s_off + p.E + 1;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cta_rank();
+    const uint32_t rank = CG == 1 ? 0 : cta_rank();
 
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_REGION);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_REGION);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, accf0 = empty0 + 8 * STAGES, acce0 = accf0 + 16;
     const uint32_t sfull0 = acce0 + 16, sempty0 = sfull0 + 16, bfull = sempty0 + 16, bempty = bfull + 8, ready = bempty + 8, taken = ready + 8;
     const uint32_t answer = (taken + 8 + 15) & ~15u;
@@ -311,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int red = (int)(kMode == kFprop ? p.K : p.N);      // terms of a sum
     const int64_t ld = kMode == kFprop ? p.N : p.K;          // features
     const int blocks = (red + BK - 1) / BK;
-    Board board(smem_u32(smem) + BOARD_REGION, bfull, bempty);
+    Board board(smem_u32(smem) + L::BOARD_REGION, bfull, bempty);
 
     if (warp < EPI_FIRST) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTL_REGS));
@@ -327,13 +335,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int r = 0; r < red; r += BK) {
                     if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag)) goto done_producer;
                     __syncwarp();
-                    const uint32_t own = full0 + 8 * stage, fb = mapa(own, 0);
+                    const uint32_t own = full0 + 8 * stage, fb = CG == 1 ? own : mapa(own, 0);
                     const uint32_t a = smem_u32(smem) + stage * STAGE_BYTES, b = a + A_BYTES;
                     if (elect_one()) {
                         if (rank == 0) mbar_expect_tx(own, CG * STAGE_BYTES);
                         load_2d<CG>(a, &tmA, fb, r, m);
-                        if (kMode == kFprop) load_3d<CG>(b, &tmB, fb, r, f, T.e);
-                        else load_3d<CG>(b, &tmB, fb, f, r, T.e);
+#pragma unroll
+                        for (int g = 0; g < 2 / CG; ++g) {  // 128 features each
+                            if (kMode == kFprop) load_3d<CG>(b + g * kFM * BK, &tmB, fb, r, f + g * kFM, T.e);
+                            else load_3d<CG>(b + g * kFM * BK, &tmB, fb, f + g * kFM, r, T.e);
+                        }
                     }
                     __syncwarp();
                     ++fills;
@@ -349,8 +360,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 int stage = 0, buf = 0;
                 uint32_t phase = 0, aphase = 0;
                 const uint32_t base = smem_u32(smem);
-                // MN-major B: one 128-byte chunk of features, 8-row groups of the reduction 1024 bytes apart
-                const uint64_t ad0 = smem_desc(base, 16, 1024), bd0 = smem_desc(base + A_BYTES, 16, 1024);
+                // MN-major B: 128-byte chunks of features (one, or two for a single CTA), 8-row groups of the reduction 1024
+                // bytes apart
+                const uint64_t ad0 = smem_desc(base, 16, 1024);
+                const uint64_t bd0 = smem_desc(base + A_BYTES, kMode == kDgrad ? kFM * BK : 16, 1024);
                 constexpr uint32_t a_step = 32 / 16, b_step = (kMode == kDgrad ? 4096 : 32) / 16;  // 32 of the sum
                 for (;;) {
                     const Tile T = board.take(lane, abort_flag);
@@ -380,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         } else if (warp == 2) {
             // -------------------------------------------------- scales
-            const uint32_t at = smem_u32(smem) + SCALE_REGION + 4 * lane;
+            const uint32_t at = smem_u32(smem) + L::SCALE_REGION + 4 * lane;
             int group = 0;
             uint32_t phase = 0;
             for (;;) {
@@ -430,8 +443,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         done_scales:;
         } else {
             // -------------------------------------------------- tiles
-            const Walk W(ld, p.E, s_off, s_slices);
-            TileQueue queue(answer, ready, mapa(taken, 0));
+            const Walk<ROWS> W(ld, p.E, s_off, s_slices);
+            TileQueue queue(answer, ready, mapa(taken, 0), CG);
             int64_t t = blockIdx.x / CG;
             for (uint32_t asked = 0;; asked ^= 1) {
                 if (t < W.total && !board.put(W.get(t), lane, abort_flag)) break;
@@ -453,11 +466,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
         // two groups of four warps: a group has one of the tile's two blocks of features
         const int q = warp & 3, group = (warp - EPI_FIRST) >> 2;
-        const uint32_t stage = smem_u32(smem) + EPI_REGION + (warp - EPI_FIRST) * 2 * BOX_BYTES;
+        const uint32_t stage = smem_u32(smem) + L::EPI_REGION + (warp - EPI_FIRST) * 2 * BOX_BYTES;
         constexpr int kParts = WIDE / 32;  // 16 columns each
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + group * (WIDE / 2);
         const uint32_t acce = mapa(acce0, 0);  // this CTA's own too, for rank 0
-        const uint32_t scales = smem_u32(smem) + SCALE_REGION + 512 * group + 4 * (32 * q + lane);
+        const uint32_t scales = smem_u32(smem) + L::SCALE_REGION + 512 * group + 4 * (32 * q + lane);
         int buf = 0, group_at = 0;
         uint32_t aphase = 0, sphase = 0;
         for (;;) {
@@ -603,7 +616,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-}  // namespace pair
+}  // namespace wide
 
 // ------------------------------------------------------------ few rows
 // One-SM tiles of 128 features by up to 32 rows: what is left is reading W once. As in the bf16 kernel for few rows
@@ -936,9 +949,10 @@ static Params params(const Fp8Call& c) {
             c.status, (c.N + BK - 1) / BK, (c.K + BK - 1) / BK};
 }
 
-template <int kMode>
-static cudaError_t run_pair(const Fp8Call& c, cudaStream_t s) {
-    using namespace pair;
+template <int kMode, int CG>
+static cudaError_t run_wide(const Fp8Call& c, cudaStream_t s) {
+    using namespace wide;
+    using L = Layout<CG>;
     const int64_t red = kMode == kDgrad ? c.N : c.K, width = kMode == kFprop ? c.N : c.K, size = c.out_f32 ? 4 : 2;
     const int64_t da[2] = {red, c.M}, sa[1] = {red}, db[3] = {c.K, c.N, c.E}, sb[2] = {c.K, c.K * c.N};
     const int64_t dd[2] = {width, c.M}, sd[1] = {size * width};
@@ -948,9 +962,9 @@ static cudaError_t run_pair(const Fp8Call& c, cudaStream_t s) {
         !encode_tmap(&out, c.out, (int)size, 2, dd, sd, boxd))
         return cudaErrorInvalidValue;
     // no fewer than the device counts
-    const int64_t tiles = (c.M / ROWS + std::min<int64_t>(c.E, c.M)) * ((width + WIDE - 1) / WIDE);
-    return launch_persistent<CG, true, ragged_fp8_kernel<kMode>>(THREADS, smem_bytes(MXQ_MAX_EXPERTS), smem_bytes(c.E),
-                                                                 tiles, s, a, b, out, params(c));
+    const int64_t tiles = (c.M / L::ROWS + std::min<int64_t>(c.E, c.M)) * ((width + WIDE - 1) / WIDE);
+    return launch_persistent<CG, true, ragged_fp8_kernel<kMode, CG>>(THREADS, L::smem_bytes(MXQ_MAX_EXPERTS),
+                                                                     L::smem_bytes(c.E), tiles, s, a, b, out, params(c));
 }
 
 template <int kMode, int kSplit>
@@ -979,12 +993,21 @@ static cudaError_t run_few(const Fp8Call& c, cudaStream_t s) {
 }  // namespace f8
 
 cudaError_t run_fp8(const Fp8Call& c, cudaStream_t s) {
-    // One-SM tiles up to as many rows as one holds, on average. W of 2048 x 4096, us, fprop and dgrad, one SM against
-    // pairs: 8 experts of 32 rows each 13.6 and 12.7 against 19.5 and 17.5, of 48 24.1 and 22.6 against 20.2 and 18.0; 64
-    // experts of 32 88 and 86 against 110 and 104, of 48 149 and 143 against 114 and 106. Dirichlet(0.3) shares, 32 rows on
-    // average, fprop: 18.6 against 19.9 (8 experts), 110 against 91 (64).
-    if (c.M <= (int64_t)kFewRows * c.E) return c.mode == kFprop ? f8::run_few<kFprop>(c, s) : f8::run_few<kDgrad>(c, s);
-    return c.mode == kFprop ? f8::run_pair<kFprop>(c, s) : f8::run_pair<kDgrad>(c, s);
+    // By the rows of an expert on average: the counts are on the device. W of 2048 x 4096, us, fprop and dgrad.
+    // Up to 16, or as many as one tile of the kernel for few rows holds, that kernel; against tiles of 128 rows: one expert
+    // of 32 rows 8.2 and 7.8 against 11.5 and 15.8; 8 experts of 16 13.5 and 12.6 against 12.9 and 16.7, of 32 18.8 and 22.7
+    // against 13.4 and 17.0 (Dirichlet(100) shares); 64 experts of 16 85 and 84 against 86 and 89, of 24 in Dirichlet(0.3)
+    // shares 100 and 94 against 74 and 73.
+    // Up to 128 tiles of one SM, against pairs: 8 experts of 48 rows 13.3 and 16.8 against 20.5 and 18.0, of 128 in flat
+    // Dirichlet shares 21 and 18.5 against 27 and 29; 64 experts of 48 88.8 and 91 against 114 and 107, of 128 even rows 96
+    // and 98 against 119 and 113. Beyond, the counts decide: 64 experts of 208 rows 132 and 128 against 123 and 117 even,
+    // 136 and 137 against 158 and 144 in flat Dirichlet shares; 48 experts of 208 (1424 x 2064) 60 against 56; 8 of 2048 even
+    // 116 and 107 against 111 and 98.
+    const bool fprop = c.mode == kFprop;
+    if (c.M <= std::max<int64_t>((int64_t)16 * c.E, f8::few::WIDE))
+        return fprop ? f8::run_few<kFprop>(c, s) : f8::run_few<kDgrad>(c, s);
+    if (c.M <= (int64_t)128 * c.E) return fprop ? f8::run_wide<kFprop, 1>(c, s) : f8::run_wide<kDgrad, 1>(c, s);
+    return fprop ? f8::run_wide<kFprop, 2>(c, s) : f8::run_wide<kDgrad, 2>(c, s);
 }
 
 cudaError_t run_fp8_quantize_rows(const void* x, int64_t M, int64_t K, int64_t ld, void* q, float* scale, cudaStream_t s) {

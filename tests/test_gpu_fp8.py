@@ -102,6 +102,14 @@ SHAPES = [
     ([129, 0, 257, 64, 1], 400, 528),
     ([511, 130], 1040, 656),
     ([255, 256, 1000], 2064, 1424),
+    # tiles of one SM: whole and ragged ones, several of an expert, experts without rows, last blocks of both kinds of width
+    ([128], 256, 128),
+    ([33], 24, 16),
+    ([100, 0, 60], 144, 144),
+    ([17] * 8, 272, 1040),
+    ([127, 128, 129], 656, 272),
+    ([1, 300, 0, 40], 2064, 1424),
+    ([129], 144, 272),
 ]
 
 
@@ -151,9 +159,9 @@ def test_wrong_counts_write_nothing(mxq, counts):
 
 
 def test_many_experts(mxq):
-    """As many experts as a call takes, most without rows: few rows on average, and tiles of a pair of SMs."""
+    """As many experts as a call takes, most without rows: few rows on average, and tiles of one SM and of a pair."""
     E, N, K = 1024, 24, 144
-    for per, some in ((1, 7), (40, 331)):
+    for per, some in ((1, 7), (40, 331), (140, 331)):
         counts = [0] * E
         for e in range(0, E, some):
             counts[e] = E * per // len(range(0, E, some))
