@@ -123,10 +123,10 @@ def test_captured_and_concurrent(mxq, fp8):
             assert all(torch.equal(a[k], w[k]) for k in w)
 
 
-# single rows, a few rows of an expert (its weights are asked for before the counts are known), tiles of a pair of SMs
+# single rows, a few rows of an expert (its weights are asked for before the counts are known), tiles of one SM and of a pair
 @pytest.mark.gpu
-@pytest.mark.parametrize("counts,other", [([1, 2, 0], [0, 0, 3]), ([17, 0, 20], [5, 30, 2]), ([150, 3, 90], [1, 240, 2])],
-                         ids=str)
+@pytest.mark.parametrize("counts,other", [([1, 2, 0], [0, 0, 3]), ([17, 0, 20], [5, 30, 2]), ([150, 3, 90], [1, 240, 2]),
+                                          ([400, 3, 90], [1, 490, 2])], ids=str)
 def test_early_launch_products(mxq, producer, counts, other):  # noqa: F811
     E, M, N, K = len(counts), sum(counts), 144, 528
 
