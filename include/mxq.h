@@ -474,7 +474,8 @@ MXQ_API int mxq_int8_gemm_fprop(const void* xq, const float* x_scale, const void
  * (ceil(width / 128), M), a row's neighbours side by side; those of a weight
  * (E, ceil(N / 128), ceil(K / 128)). A block at an edge covers what there is.
  * Scales need no alignment but a float's. Any fp32 scales may be given, also
- * those of a checkpoint. Grouping as in the bf16 products. */
+ * those of a checkpoint, where the product of a row's and a weight's is within
+ * fp32's range (see fprop). Grouping as in the bf16 products. */
 
 /* Quantizes the rows of x (M, K), row stride ldx: with a the largest magnitude
  * of a block, at least 2^-100, scale = a / 448 and q = the E4M3 value nearest to
@@ -492,8 +493,10 @@ MXQ_API int mxq_fp8_quantize_weight(const void* w_bf16, int64_t N, int64_t K, in
  * xq[m,k] wq[e,n,k]) (+ bias[e,n]); y (M, N) bf16, or fp32 with MXQ_OUT_F32;
  * bias (E, N) bf16 or NULL. A block's 128 products are summed by the tensor core
  * (truncating, up to 2^-23 of their magnitudes for every 32), blocks in fp32 by
- * fused multiply-adds with the product of the two scales rounded to fp32 (which
- * loses bits below 2^-126).
+ * fused multiply-adds with the product of the two scales rounded to fp32. That
+ * product loses bits below 2^-126 and is to be below 2^128: beyond, the row's
+ * results in the 128 features (here and in the dgrad) are infinite or NaN,
+ * whatever the codes are.
  * K % 16 == 0, N % 8 == 0. */
 MXQ_API int mxq_fp8_gemm_fprop(const void* xq, const float* x_scale, const void* wq, const float* w_scale,
                                const void* bias_bf16, int64_t M, int64_t N, int64_t K, int E,

@@ -1045,7 +1045,8 @@ def fp8_quantize_weight(w, out=None):
 
 def fp8_gemm_fprop(xq, x_scale, wq, w_scale, m_splits, bias=None, out_dtype=None, status=None, out=None):
     """Y = X W_e^T (+ b_e) on E4M3 codes with a scale per block. xq (M, K), x_scale (ceil(K/128), M),
-    wq (E, N, K), w_scale (E, ceil(N/128), ceil(K/128)), bias (E, N); Y (M, N) in bf16 (default) or fp32."""
+    wq (E, N, K), w_scale (E, ceil(N/128), ceil(K/128)), bias (E, N); Y (M, N) in bf16 (default) or fp32. A row's
+    scale times a weight's is to be below 2^128 (infinite or NaN results otherwise); below 2^-126 it loses bits."""
     M, K = xq.shape
     E, N, Kw = wq.shape
     if Kw != K:
