@@ -1134,14 +1134,17 @@ def norm_residual_fwd(x, residual=None, post_weight=None, pre_weight=None, gate=
     return r, n, stats
 
 
+_NORM_GRADIENTS = {"dx", "dresidual", "dpost_weight", "dpre_weight", "dgate"}
+
+
 def norm_residual_bwd(dres, dn, x, res, stats, post_weight=None, pre_weight=None, gate=None, scale=1.0, dx_out=True,
                       dresidual_out=True, status=None, out=None, workspace=None):
     """The gradients of norm_residual_fwd from dres (of r', may be None) and dn (of n, None exactly without
     pre_weight). x, weights, gate and scale are the forward call's, res its r' and stats its statistics; x
     may be None without post_weight and gate, res without pre_weight. Returns a dict: dx, dresidual (M, F),
     dpost_weight, dpre_weight (F,) fp32, dgate (M,) fp32, those of arguments that were given and not left out
-    by dx_out or dresidual_out (one of the two is needed). out: tensors to write to, by the same names;
-    dresidual may be dres."""
+    by dx_out or dresidual_out (one of the two is needed). out: tensors to write to, by the same names (one
+    of a gradient that is not returned is left as it is); dresidual may be dres."""
     like = dn if dn is not None else dres
     if like is None:
         raise MXQError("dres or dn is required")
@@ -1149,13 +1152,16 @@ def norm_residual_bwd(dres, dn, x, res, stats, post_weight=None, pre_weight=None
               *(out.values() if out else ()))
     (M, F), dt = like.shape, like.dtype
     shape, same, new = (M, F), (dt,), _allocator(like)
-    o = dict(out) if out else {}
+    if out and not out.keys() <= _NORM_GRADIENTS:
+        raise MXQError(f"out: {sorted(out.keys() - _NORM_GRADIENTS)}, expected some of {sorted(_NORM_GRADIENTS)}")
+    o = {}
 
     def output(key, want, strides, dtype):
-        t = o.get(key)
+        t = out.get(key) if out else None
         if t is None:
             t = o[key] = new(want, strides, dtype)
             return t.data_ptr()
+        o[key] = t
         return _packed(t, key, want, (dtype,))
 
     dxp = output("dx", shape, (F, 1), dt) if dx_out else None
