@@ -768,6 +768,17 @@ def _outputs(out):
     return () if out is None else out if isinstance(out, (tuple, list)) else (out,)
 
 
+def _pair(out, both):
+    """The tensors of a call's `out` argument, None where one is to be made or (the second) not wanted."""
+    if out is None:
+        return None, None
+    if not both:
+        return out, None
+    if not isinstance(out, (tuple, list)) or len(out) != 2:
+        raise MXQError("out: expected a pair of tensors")
+    return out
+
+
 @functools.lru_cache(maxsize=1)
 def _several_devices():
     return torch.cuda.device_count() > 1
@@ -881,7 +892,7 @@ def ragged_gemm_wgrad(dy, x, m_splits, accumulate=False, out_dtype=None, status=
 def ragged_gemm_fprop_swiglu(x, w, m_splits, bias=None, y_out=False, status=None, out=None):
     """h = silu(g) * u of [g | u] = X W1_e^T (+ b_e) on bf16, any expert counts. x (M, K), its rows possibly a
     slice of wider ones; w (E, 2F, K), gate first; bias (E, 2F). Returns h (M, F) or, with y_out, h and
-    [g | u] (M, 2F). out: what is returned, to write to."""
+    [g | u] (M, 2F). out: what is returned, to write to, None in a pair where it is to be made."""
     xp, M, K, ldx = _rows(x, "x", _BF16)
     _here(x, "x", w, m_splits, bias, status, *_outputs(out))
     E, F2, Kw = w.shape
@@ -889,10 +900,11 @@ def ragged_gemm_fprop_swiglu(x, w, m_splits, bias=None, y_out=False, status=None
     if F2 & 1:
         raise MXQError(f"w: shape {tuple(w.shape)}, expected (E, 2F, K)")
     F = F2 >> 1
-    if out is None:
-        h, y = _new((M, F), torch.bfloat16, x), _new((M, F2), torch.bfloat16, x) if y_out else None
-    else:
-        h, y = out if y_out else (out, None)
+    h, y = _pair(out, y_out)
+    if h is None:
+        h = _new((M, F), torch.bfloat16, x)
+    if y_out and y is None:
+        y = _new((M, F2), torch.bfloat16, x)
     rc = lib().mxq_ragged_gemm_fprop_swiglu(xp, ldx, _dev(w, "w", 0, _BF16), _packed(bias, "bias", (E, F2), _BF16), M, F, K,
                                             E, _grouping(m_splits, E), _packed(h, "h", (M, F), _BF16),
                                             _packed(y, "y", (M, F2), _BF16), _dev(status, "status", 4, _I32), _stream())
@@ -904,15 +916,17 @@ def ragged_gemm_fprop_swiglu(x, w, m_splits, bias=None, y_out=False, status=None
 def ragged_gemm_dgrad_swiglu(dy, w, y1, m_splits, h_out=False, status=None, out=None):
     """The gradient [dg | du] of y1 = [g | u] (M, 2F) from FC2's output gradient: dh = dY W2_e, then the SwiGLU
     backward, on bf16, any expert counts. dy (M, N), its rows possibly a slice of wider ones; w (E, N, F).
-    Returns [dg | du] (M, 2F) or, with h_out, it and h = silu(g) * u (M, F). out: what is returned, to write to."""
+    Returns [dg | du] (M, 2F) or, with h_out, it and h = silu(g) * u (M, F). out: what is returned, to write to,
+    None in a pair where it is to be made."""
     dyp, M, N, lddy = _rows(dy, "dy", _BF16)
     _here(dy, "dy", w, y1, m_splits, status, *_outputs(out))
     E, Nw, F = w.shape
     _shape(w, "w", (E, N, F))
-    if out is None:
-        d, h = _new((M, 2 * F), torch.bfloat16, dy), _new((M, F), torch.bfloat16, dy) if h_out else None
-    else:
-        d, h = out if h_out else (out, None)
+    d, h = _pair(out, h_out)
+    if d is None:
+        d = _new((M, 2 * F), torch.bfloat16, dy)
+    if h_out and h is None:
+        h = _new((M, F), torch.bfloat16, dy)
     rc = lib().mxq_ragged_gemm_dgrad_swiglu(dyp, lddy, _dev(w, "w", 0, _BF16), _packed(y1, "y1", (M, 2 * F), _BF16), M, N, F,
                                             E, _grouping(m_splits, E), _packed(d, "dy1", (M, 2 * F), _BF16),
                                             _packed(h, "h", (M, F), _BF16), _dev(status, "status", 4, _I32), _stream())
