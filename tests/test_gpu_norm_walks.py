@@ -1,0 +1,65 @@
+"""Norms and their gradients where every CTA, cluster or team of lanes walks several rows: its ring of stages goes round
+more than twice, the sums' buffers are used again, and what is held from one row to the next is another row's."""
+import pytest
+import torch
+
+from ._blocks import U, norm_bwd
+from .test_gpu_norm import BF16, F32, check_fwd, close, dbl, make, mxq  # noqa: F401 (mxq is a fixture)
+
+pytestmark = pytest.mark.gpu
+# roundings of a row's sum: 8 in a thread, 5 of a warp, at most 2 + 5 over a row's 64 warps; a dozen for the rest
+ROW = 32
+
+# rows, columns: lanes of a warp (three widths), one CTA to a row (two to 32 warps), a cluster of eight
+FORWARD = [(120001, 64), (60001, 120), (30001, 256), (130001, 512), (20001, 2056), (5000, 4096), (2001, 8192), (3001, 9000),
+           (1501, 16384)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,F", FORWARD)
+def test_forward(mxq, M, F, dtype):  # noqa: F811
+    for form in (dict(), dict(gate=False), dict(post=False), dict(pre=False, residual=False)):
+        a = make(M + F, M, F, dtype, **form)
+        check_fwd(a, 0.5, 1e-5, *mxq.norm_residual_fwd(**a, scale=0.5, eps=1e-5))
+
+
+# lanes of a warp, one CTA to a row, clusters of four and of eight
+BACKWARD = [(60001, 64), (30001, 128), (20001, 256), (9001, 1000), (6001, 2048), (3001, 4096), (1023, 7168), (900, 8192),
+            (600, 9000), (700, 16384)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,F", BACKWARD)
+def test_backward(mxq, M, F, dtype):  # noqa: F811
+    for form in (dict(), dict(gate=False), dict(post=False), dict(pre=False)):
+        a = make(M + F, M, F, dtype, **form)
+        res, _, stats = mxq.norm_residual_fwd(**a, scale=0.5)
+        dres, dn = make(1, M, F, dtype)["x"], make(2, M, F, dtype)["x"] if a["pre_weight"] is not None else None
+        args = (a["x"], res, stats, a["post_weight"], a["pre_weight"], a["gate"], 0.5)
+        got = mxq.norm_residual_bwd(dres, dn, *args)
+        ref, mag = norm_bwd(dbl(dres), dbl(dn), *[dbl(v) if torch.is_tensor(v) else v for v in args])
+        assert set(ref) == set(got)
+        # a weight's gradient: the rows of one walk after another (19 walks at least, clusters of eight on 152 SMs; 152
+        # without clusters), eight warps' parts, then at most 608 partial rows, 32 at once
+        walks = 19 if F > 4096 else 152
+        rows = -(-M // walks) + 8 + 19 + 5
+        for k in ref:
+            close(got[k], ref[k], (2 * ROW + (rows if k.endswith("weight") else 0)) * U * mag[k], (k, form))
+
+
+def test_long_axis_distinct_rows(mxq):  # noqa: F811
+    """Rows past 2^31 elements that differ from each other, in values that every step keeps exact but for single units of
+    fp32, which the rounding to bf16 takes off: a row in another's place shows."""
+    M, F = (1 << 18) + 3, 8200
+    c = 1.0 + (torch.arange(M, device="cuda") % 127) / 128.0  # 127 rows before one comes again: no walk's stride
+    w = torch.full((F,), 2.0, dtype=BF16, device="cuda")
+    x = torch.ones(M, F, dtype=BF16, device="cuda")
+    r, n, stats = mxq.norm_residual_fwd(x, post_weight=w, pre_weight=w, gate=c)
+    assert (r == (2.0 * c).to(BF16)[:, None]).all() and (n == 2.0).all()
+    torch.testing.assert_close(stats, torch.stack([torch.ones_like(c), 0.5 / c]), rtol=1e-5, atol=0.0)
+    del x
+    # t = dn w is the same in a row, so what the norm adds to dres is 0
+    dres = (3.0 - c).to(BF16)[:, None].expand(M, F).contiguous()
+    g = mxq.norm_residual_bwd(dres, n, None, r, torch.stack([torch.ones_like(c), 0.5 / c]), pre_weight=w, dx_out=False)
+    assert torch.equal(g["dresidual"], dres)
+    torch.testing.assert_close(g["dpre_weight"], torch.full((F,), 2.0 * M, device="cuda"), rtol=1e-5, atol=0.0)
