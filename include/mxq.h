@@ -519,7 +519,8 @@ MXQ_API int mxq_fp8_gemm_dgrad(const void* dyq, const float* dy_scale, const voi
  * Tensors (M, F) and weights (F) are all bf16, or all fp32 with MXQ_OUT_F32;
  * gate (M), stats (2, M) and the gradients of the weights and of gate are fp32.
  * Arithmetic is fp32, each result rounded once; n is made from r' before its
- * rounding. F % 8 == 0, F <= 16384, M <= 2^28. scale is finite, eps > 0
+ * rounding. A row whose squares' sum is beyond fp32's range (values past 2^63, or
+ * an infinity) has 1 / sqrt = 0, so that its finite values' norms are 0. F % 8 == 0, F <= 16384, M <= 2^28. scale is finite, eps > 0
  * (MXQ_ERR_VALUE otherwise). An infinity or NaN stays in its row (the weights'
  * gradients are sums over rows). */
 

@@ -40,9 +40,9 @@ def test_backward(mxq, M, F, dtype):  # noqa: F811
         ref, mag = norm_bwd(dbl(dres), dbl(dn), *[dbl(v) if torch.is_tensor(v) else v for v in args])
         assert set(ref) == set(got)
         # a weight's gradient: the rows of one walk after another (19 walks at least, clusters of eight on 152 SMs; 152
-        # without clusters), eight warps' parts, then at most 608 partial rows, 32 at once
+        # without clusters), eight warps' parts, then at most 912 partial rows, 32 at once
         walks = 19 if F > 4096 else 152
-        rows = -(-M // walks) + 8 + 19 + 5
+        rows = -(-M // walks) + 8 + 29 + 5
         for k in ref:
             close(got[k], ref[k], (2 * ROW + (rows if k.endswith("weight") else 0)) * U * mag[k], (k, form))
 
@@ -63,3 +63,21 @@ def test_long_axis_distinct_rows(mxq):  # noqa: F811
     g = mxq.norm_residual_bwd(dres, n, None, r, torch.stack([torch.ones_like(c), 0.5 / c]), pre_weight=w, dx_out=False)
     assert torch.equal(g["dresidual"], dres)
     torch.testing.assert_close(g["dpre_weight"], torch.full((F,), 2.0 * M, device="cuda"), rtol=1e-5, atol=0.0)
+
+
+@pytest.mark.parametrize("F", [256, 2048, 9000])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_squares_beyond_range(mxq, F, dtype):  # noqa: F811
+    """A row whose squares' sum is beyond fp32's range counts as infinitely large, its norm as 0; the other rows keep their
+    bits, and the gradients through such a row stay finite."""
+    a = make(5, 9, F, dtype)
+    clean = mxq.norm_residual_fwd(**a)
+    a["x"][3], a["residual"][6, 1] = 2.0 ** 70, 2.0 ** 70
+    got = r, n, stats = mxq.norm_residual_fwd(**a)
+    keep = [0, 1, 2, 4, 5, 7, 8]
+    assert all(torch.equal(c[keep], g[keep]) for c, g in zip(clean[:2], got))
+    assert torch.equal(r[3], a["residual"][3]) and (n[6] == 0).all() and stats[0, 3] == 0 and stats[1, 6] == 0
+    dres, dn = make(1, 9, F, dtype)["x"], make(2, 9, F, dtype)["x"]
+    g = mxq.norm_residual_bwd(dres, dn, a["x"], r, stats, a["post_weight"], a["pre_weight"], a["gate"])
+    assert all(v.isfinite().all() for v in g.values()) and (g["dx"][3] == 0).all()
+    assert torch.equal(g["dresidual"][6], dres[6])
