@@ -99,11 +99,11 @@ __device__ __forceinline__ int64_t weight_scale_at(const Params& p, int e, int f
     return kMode == kFprop ? (e * p.ws_rows + i) * p.ws_cols + j : (e * p.ws_rows + j) * p.ws_cols + i;
 }
 
-// The scales of the tiles' columns, block by block, through a ring of slots in shared memory. A slot keeps its columns in
+// In the kernel for few rows: the scales of the tiles' columns, block by block, through a ring of slots in shared memory. A slot keeps its columns in
 // the order in which matrix fragments want them: of 16 columns, the four that a thread holds (8b + 2c and the next, b = 0
 // and 1) side by side.
-template <int kWide, int kSlots>
 struct Scales {
+    static constexpr int kWide = kFewRows, kSlots = 16;
     static constexpr int kBytes = kSlots * kWide * 4, kBatch = 4, kPer = kWide / 32;
     uint32_t at, full, empty;
     int slot = 0;
@@ -630,16 +630,15 @@ __global__ void __launch_bounds__(THREADS, 1)
 // fill the SMs the sum is split over a cluster. An accumulator is 32 columns, so there are four.
 namespace few {
 
-constexpr int STAGES = 8, SLOTS = 16, BUFS = 4;
+constexpr int STAGES = 8, SLOTS = Scales::kSlots, BUFS = 4;
 constexpr int WIDE = kFewRows, STEP = 16;
 constexpr int A_BYTES = kFM * BK, STAGE_BYTES = A_BYTES + WIDE * BK;
 constexpr int EPI_FIRST = 4, EPI_WARPS = 4;  // warp 3 is idle
 constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
 constexpr int TMEM_COLS = BUFS * WIDE;
-using Ring = Scales<WIDE, SLOTS>;
 constexpr int PART_REGION = STAGES * STAGE_BYTES;
 constexpr int SCALE_REGION = PART_REGION + kPartBytes;
-constexpr int BAR_REGION = SCALE_REGION + Ring::kBytes;
+constexpr int BAR_REGION = SCALE_REGION + Scales::kBytes;
 constexpr int TABLE_REGION = BAR_REGION + 512;
 __host__ __device__ constexpr int smem_bytes(int E) { return 1024 + TABLE_REGION + 8 * (E + 1); }
 static_assert(smem_bytes(MXQ_MAX_EXPERTS) <= 232448, "shared memory over the per-block limit");
@@ -715,7 +714,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_after();
     const uint32_t tmem = s_tmem;
     const Walk<kMode, kFM, WIDE, STEP> W(p.N, p.K, p.E, s_off, s_slices, nullptr);
-    Ring ring(smem_u32(smem) + SCALE_REGION, sfull0, sempty0);
+    Scales ring(smem_u32(smem) + SCALE_REGION, sfull0, sempty0);
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
@@ -777,7 +776,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------ scales
         for (int64_t t = first; t < W.total; t += stride) {
             const Tile T = W.get(t);
-            if (!ring.template produce<kMode>(p, T, T.f0, jb, je, lane, abort_flag)) break;
+            if (!ring.produce<kMode>(p, T, T.f0, jb, je, lane, abort_flag)) break;
         }
     } else if (warp >= EPI_FIRST) {
         // ------------------------------------------------------ epilogue
@@ -922,7 +921,7 @@ __global__ void __launch_bounds__(256, 6) fp8_quantize_rows_kernel(const uint16_
 }
 
 // Weights: a block of 256 threads holds one 128 x 128 block in registers, 16 bytes of eight rows a thread. Bound by HBM
-// (128 x 2048 x 7168: 843 us, 6.68 TB/s) when the compiler has the registers of three blocks to an SM and issues a thread's
+// (128 x 2048 x 7168: 843 us, 6.68 TB/s, two bytes read for one written: a plain copy, one for one, reaches 6.67) when the compiler has the registers of three blocks to an SM and issues a thread's
 // eight loads together; with those of four, what it takes by itself, 1009 us, of six 1095.
 __global__ void __launch_bounds__(256, 3) fp8_quantize_weight_kernel(const uint16_t* w, int64_t N, int64_t K, int64_t across,
                                                                   int64_t down, uint8_t* q, float* scale) {
