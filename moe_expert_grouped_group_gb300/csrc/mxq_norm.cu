@@ -12,12 +12,12 @@
 // Bound by HBM: every tensor is read or written once. What it takes is loads in
 // flight all the time: a row's two sums, one after the other, each leave the SM
 // idle for a few hundred cycles. So rows come by bulk copies into a ring of
-// shared memory, two or three rows ahead of the one that is computed.
+// shared memory, two rows ahead of the one that is computed.
 //
 // A row of more than kWarpWidth columns belongs to a cluster of 1 to 8 CTAs,
 // eight columns to a thread; the CTAs' sums meet in each
 // other's shared memory. Shorter rows belong to 8, 16 or 32 lanes of a warp,
-// which hold the next row in registers. A thread always has the same columns,
+// which in the backward kernel hold the next row in registers. A thread always has the same columns,
 // so that the weights' gradients grow in its registers while it walks its
 // rows; they leave a CTA as one partial row each, which a second kernel adds up
 // in a fixed order. All arithmetic is fp32; r', n, dx, dr are rounded once. n
