@@ -81,3 +81,23 @@ def test_squares_beyond_range(mxq, F, dtype):  # noqa: F811
     g = mxq.norm_residual_bwd(dres, dn, a["x"], r, stats, a["post_weight"], a["pre_weight"], a["gate"])
     assert all(v.isfinite().all() for v in g.values()) and (g["dx"][3] == 0).all()
     assert torch.equal(g["dresidual"][6], dres[6])
+
+
+@pytest.mark.parametrize("M,F", [(20001, 256), (9001, 1000), (3001, 4096), (1023, 7168), (3001, 9000)])
+def test_in_place_walks(mxq, M, F):  # noqa: F811
+    """r' over the residual or x, n over x, dr over dr', while the rows behind are on their way: the bits of the calls with
+    outputs of their own."""
+    a = make(5, M, F, BF16)
+    r, n, stats = mxq.norm_residual_fwd(**a)
+    b = {k: v.clone() for k, v in a.items()}
+    r2, n2, stats2 = mxq.norm_residual_fwd(**b, out=(b["residual"], b["x"], None))
+    assert r2 is b["residual"] and n2 is b["x"]
+    assert torch.equal(r, r2) and torch.equal(n, n2) and torch.equal(stats, stats2)
+    x = a["x"].clone()
+    r2, n2, _ = mxq.norm_residual_fwd(**{**a, "x": x}, out=(x, None, None))
+    assert r2 is x and torch.equal(r, r2) and torch.equal(n, n2)
+    dres, dn = make(1, M, F, BF16)["x"], make(2, M, F, BF16)["x"]
+    args = (dn, a["x"], r, stats, a["post_weight"], a["pre_weight"], a["gate"])
+    want = mxq.norm_residual_bwd(dres, *args)
+    got = mxq.norm_residual_bwd(dres, *args, out={"dresidual": dres})
+    assert got["dresidual"] is dres and all(torch.equal(want[k], got[k]) for k in want)
